@@ -9,4 +9,7 @@ from .attention import (MASK_CAUSAL, MASK_DOCUMENT_CAUSAL, MASK_NONE,  # noqa: F
                         FP8_TILES, FP8_V_TRANSPOSED, fp8_inputs, forward_fp8, fwd_fp8_into,
                         quantize_fp8, decode_paged, decode_paged_into, decode_split_keys,
                         decode_workspace_size, selftest_wait_timeout, check_doc_offsets)
+from .paged import (CACHE_BF16, CACHE_E4M3, cache_read, cache_read_into, cache_write,  # noqa: F401
+                    prefill_paged, prefill_paged_into, prefill_split_keys,
+                    prefill_workspace_size)
 from ._lib import AttnError  # noqa: F401

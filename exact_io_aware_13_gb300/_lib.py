@@ -29,11 +29,21 @@ class ScoreParams(ctypes.Structure):
                 ("dropout_seed", ctypes.c_uint64)]
 
 
+class PagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("kv_exp", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("kind", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("max_pages_per_seq", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
 _F = ctypes.c_float
 _MP = ctypes.POINTER(MaskParams)
 _SP = ctypes.POINTER(ScoreParams)
+_CP = ctypes.POINTER(PagedCache)
 
 _FWD_ARGS = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _MP, _I, _SP, _P]
 _BWD_ARGS = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _MP, _I, _SP,
@@ -55,6 +65,14 @@ SIGNATURES = {
                                                      _P]),
     "attn_decode_workspace_size": (ctypes.c_size_t, [_I] * 7),
     "attn_decode_split_keys": (_I, [_I, _I, _I, _I, ctypes.c_longlong, _I]),
+    "attn_cache_write": (_I, [_CP, _P, _L, _L, _P, _L, _L, _P, _P, _I, _I, _P]),
+    "attn_cache_read": (_I, [_CP, _P, _P, _P, _P, _I, _I, _P]),
+    "attn_prefill_paged": (_I, [_CP, _P, _L, _L, _P, _P, _P, _P] + [_I] * 6 +
+                           [_F, _I, _MP, _I, _SP, _P, ctypes.c_size_t, _P]),
+    "attn_prefill_workspace_size": (ctypes.c_size_t, [_I] * 5),
+    "attn_prefill_split_keys": (_I, [_I] * 6 + [_L, _I]),
+    "attn_decode_paged_e4m3": (_I, [_CP, _P, _P, _P, _P] + [_I] * 5 +
+                               [_F, _I, _MP, _I, _SP, _P, ctypes.c_size_t, _P]),
     "attn_check_doc_offsets": (_I, [_P, _I, _I, _P]),
     "attn_device_status": (_I, [_P]),
     "attn_selftest_wait_timeout": (_I, [_P]),

@@ -330,13 +330,16 @@ def decode_workspace_size(B: int, Hq: int, Hkv: int, Nq: int, d: int, max_seq_le
 def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspace, *,
                       max_seq_len: int, split_keys: int, scale: float,
                       mask_kind: int = MASK_NONE, window: int = 0, score_kind: int = SCORE_NONE,
-                      softcap: float = 0.0, stream=None) -> None:
+                      softcap: float = 0.0, kv_exp=None, stream=None) -> None:
     """attn_decode_paged on caller-owned tensors (see include/attn.h for the layouts):
     q [B, Hq, Nq, d], caches [pages, Hkv, page_size, d], page_table int32 [B, max_pages],
-    seq_lens int32 [B]; writes o and lse."""
-    _check_tensors(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspace)
-    _check_dtypes((q, _BF16, "q"), (k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache"),
-                  (o, _BF16, "o"), (lse, _F32, "lse"))
+    seq_lens int32 [B]; writes o and lse. With kv_exp (uint8 [pages, Hkv, page_size, 2]) the
+    caches hold e4m3 codes as uint8, as paged.cache_write fills them, and
+    attn_decode_paged_e4m3 runs."""
+    kind = _BF16 if kv_exp is None else _U8
+    _check_tensors(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspace, kv_exp)
+    _check_dtypes((q, _BF16, "q"), (k_cache, kind, "k_cache"), (v_cache, kind, "v_cache"),
+                  (o, _BF16, "o"), (lse, _F32, "lse"), (kv_exp, _U8, "kv_exp"))
     if q.dim() != 4 or tuple(o.shape) != tuple(q.shape) or tuple(lse.shape) != tuple(q.shape[:-1]):
         raise ValueError("q, o must be [B, Hq, Nq, d] and lse [B, Hq, Nq]")
     B, Hq, Nq, d = q.shape
@@ -347,8 +350,20 @@ def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspa
         raise ValueError("page_table and seq_lens must be int32")
     if page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.shape != (B,):
         raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
+    if kv_exp is not None and tuple(kv_exp.shape) != (num_pages, Hkv, page_size, 2):
+        raise ValueError("kv_exp must be [pages, Hkv, page_size, 2]")
     mp, sp, _keep = _params(mask_kind, window, None, softcap)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if kv_exp is not None:
+        cache = _lib.PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), kv_exp.data_ptr(),
+                                page_table.data_ptr(), 1, num_pages, Hkv, page_size, d,
+                                page_table.shape[1])
+        _lib.check(_lib.load().attn_decode_paged_e4m3(
+            ctypes.byref(cache), _ptr(q), _ptr(seq_lens), _ptr(o), _ptr(lse), B, Hq, Nq,
+            int(max_seq_len), int(split_keys), ctypes.c_float(scale), mask_kind, mp, score_kind,
+            sp, _ptr(workspace), ctypes.c_size_t(ws_bytes), _stream(stream)),
+            "attn_decode_paged_e4m3")
+        return
     st = _lib.load().attn_decode_paged(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(o),
         _ptr(lse), B, Hq, Hkv, Nq, d, num_pages, page_size, page_table.shape[1],
@@ -360,10 +375,10 @@ def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspa
 def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, max_seq_len: Optional[int] = None,
                  split_keys: Optional[int] = None, total_kv_tokens: Optional[int] = None,
                  scale: Optional[float] = None, mask_kind: int = MASK_NONE, window: int = 0,
-                 score_kind: int = SCORE_NONE, softcap: float = 0.0, stream=None):
+                 score_kind: int = SCORE_NONE, softcap: float = 0.0, kv_exp=None, stream=None):
     """Allocating wrapper of decode_paged_into: returns (o, lse). max_seq_len defaults to
     the page table's capacity; split_keys to the library's choice for total_kv_tokens
-    (default B * max_seq_len)."""
+    (default B * max_seq_len). kv_exp selects an e4m3 cache."""
     B, Hq, Nq, d = q.shape
     Hkv, page_size = k_cache.shape[1], k_cache.shape[2]
     if max_seq_len is None:
@@ -379,5 +394,5 @@ def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, max_seq_len: Opti
     decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, ws,
                       max_seq_len=max_seq_len, split_keys=split_keys, scale=scale,
                       mask_kind=mask_kind, window=window, score_kind=score_kind, softcap=softcap,
-                      stream=stream)
+                      kv_exp=kv_exp, stream=stream)
     return o, lse

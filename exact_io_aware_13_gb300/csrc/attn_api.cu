@@ -391,6 +391,92 @@ size_t decode_lse_plane(long long n_chunks, long long rows) {
   return round256((size_t)(n_chunks * rows) * sizeof(float));
 }
 
+// ---------------------------------------------------------------- paged cache
+// Checks of a cache description and of the ragged batch over it; fills `p`. max_new and
+// max_seq_len are the caller's bounds (already clamped to what T and the table allow).
+attn_status check_cache(const attn_paged_cache* c, int B, int T, int max_new, int max_seq_len,
+                        PagedProblem* p) {
+  if (!c) return ATTN_ERR_ARG;
+  if (c->kind != ATTN_CACHE_BF16 && c->kind != ATTN_CACHE_E4M3) return ATTN_ERR_ARG;
+  if (B < 0 || T < 0 || max_new < 0 || max_seq_len < 0 || c->num_pages < 0 || c->Hkv < 0 ||
+      c->max_pages_per_seq < 0)
+    return ATTN_ERR_SHAPE;
+  if (c->d != 64 && c->d != 128) return ATTN_ERR_SHAPE;
+  if (!decode_page_size_ok(c->page_size)) return ATTN_ERR_SHAPE;
+  if ((long long)max_seq_len > (long long)c->max_pages_per_seq * c->page_size)
+    return ATTN_ERR_SHAPE;
+  if ((long long)c->num_pages * c->Hkv > 0x7fffffffLL ||
+      (long long)c->num_pages * c->Hkv * c->page_size > 0x7fffffffLL)
+    return ATTN_ERR_SHAPE;
+  if ((c->kind == ATTN_CACHE_E4M3) != (c->kv_exp != nullptr)) return ATTN_ERR_ARG;
+  *p = PagedProblem{};
+  p->k_cache = c->k; p->v_cache = c->v; p->kv_exp = c->kv_exp; p->page_table = c->page_table;
+  p->num_pages = c->num_pages; p->Hkv = c->Hkv; p->page_size = c->page_size; p->d = c->d;
+  p->max_pages = c->max_pages_per_seq;
+  p->B = B; p->T = T;
+  p->max_new = std::min(max_new, T);
+  p->max_seq_len = max_seq_len;
+  return ATTN_OK;
+}
+
+// Pointers of the cache and of the batch, once the sizes show that there is work.
+attn_status check_cache_pointers(const PagedProblem& p, const int32_t* offsets,
+                                 const int32_t* seq_lens) {
+  if (!offsets || !seq_lens) return ATTN_ERR_ARG;
+  if (p.max_seq_len > 0 && (!p.k_cache || !p.v_cache || !p.page_table)) return ATTN_ERR_ARG;
+  if (!aligned16(p.k_cache) || !aligned16(p.v_cache) || !aligned16(p.kv_exp) ||
+      !aligned4(p.page_table) || !aligned4(offsets) || !aligned4(seq_lens))
+    return ATTN_ERR_ALIGN;
+  return ATTN_OK;
+}
+
+bool stride_ok(long long s) { return s >= 0 && s % 8 == 0; }
+
+int table_capacity(const attn_paged_cache* c) {
+  if (!c || c->max_pages_per_seq <= 0 || c->page_size <= 0) return 0;
+  return (int)std::min<long long>((long long)c->max_pages_per_seq * c->page_size, 0x7fffffffLL);
+}
+
+// Score and mask arguments of the paged attention calls (as attn_decode_paged takes them).
+attn_status check_paged_scores(float scale, int mask_kind, const attn_mask_params* mp,
+                               int score_kind, const attn_score_params* sp, PagedAttention* a) {
+  if (!std::isfinite(scale)) return ATTN_ERR_ARG;
+  if (mask_kind != ATTN_MASK_NONE && mask_kind != ATTN_MASK_CAUSAL &&
+      mask_kind != ATTN_MASK_SLIDING_WINDOW)
+    return ATTN_ERR_ARG;
+  if (score_kind & ~(ATTN_SCORE_ALIBI | ATTN_SCORE_SOFTCAP)) return ATTN_ERR_ARG;
+  a->scale = scale;
+  a->mask_kind = mask_kind;
+  a->score_kind = score_kind;
+  if (score_kind & ATTN_SCORE_SOFTCAP) {
+    if (!sp || !(sp->softcap > 0.f) || !std::isfinite(sp->softcap)) return ATTN_ERR_ARG;
+    a->softcap = sp->softcap;
+  }
+  if (mask_kind == ATTN_MASK_SLIDING_WINDOW) {
+    if (!mp || mp->window < 0) return ATTN_ERR_ARG;
+    a->window = mp->window;
+  }
+  return ATTN_OK;
+}
+
+// Splits of the keys and the workspace that holds their partial results.
+attn_status set_splits(PagedAttention* a, int split_keys, size_t need, void* workspace,
+                       size_t workspace_bytes) {
+  const long long n = decode_chunks(a->p.max_seq_len, split_keys);
+  const long long rows = (long long)a->p.T * a->Hq;
+  if (rows > 0x7fffffffLL || n > 0x7fffffffLL / 2) return ATTN_ERR_SHAPE;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_ALIGN;
+  a->chunk = split_keys;
+  a->n_chunks = (int)n;
+  if (n > 1) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a->part_lse = reinterpret_cast<float*>(ws);
+    a->part_o = reinterpret_cast<float*>(ws + decode_lse_plane(n, rows));
+  }
+  return ATTN_OK;
+}
+
 }  // namespace
 }  // namespace attn
 
@@ -636,6 +722,155 @@ attn_status attn_decode_paged(const void* q, const void* k_cache, const void* v_
   return from_cuda(launch_decode_tc(p, tk, tv, out, dev->num_sms, st));
 }
 
+attn_status attn_cache_write(const attn_paged_cache* cache, const void* k,
+                             long long k_token_stride, long long k_head_stride, const void* v,
+                             long long v_token_stride, long long v_head_stride,
+                             const int32_t* offsets, const int32_t* seq_lens, int B, int T,
+                             void* stream) {
+  PagedProblem p;
+  attn_status s = check_cache(cache, B, T, T, table_capacity(cache), &p);
+  if (s != ATTN_OK) return s;
+  if (!stride_ok(k_token_stride) || !stride_ok(k_head_stride) || !stride_ok(v_token_stride) ||
+      !stride_ok(v_head_stride))
+    return ATTN_ERR_ALIGN;
+  if (B == 0 || T == 0 || p.Hkv == 0) return ATTN_OK;
+  if (!k || !v) return ATTN_ERR_ARG;
+  if ((s = check_cache_pointers(p, offsets, seq_lens)) != ATTN_OK) return s;
+  if (!aligned16(k) || !aligned16(v)) return ATTN_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != ATTN_OK) return s;
+  p.status = dev->status;
+  p.offsets = offsets;
+  p.seq_lens = seq_lens;
+  const RowView kr{static_cast<const __nv_bfloat16*>(k), k_token_stride, k_head_stride};
+  const RowView vr{static_cast<const __nv_bfloat16*>(v), v_token_stride, v_head_stride};
+  return from_cuda(launch_cache_write(p, kr, vr, static_cast<cudaStream_t>(stream)));
+}
+
+attn_status attn_cache_read(const attn_paged_cache* cache, void* k, void* v,
+                            const int32_t* offsets, const int32_t* seq_lens, int B, int T,
+                            void* stream) {
+  PagedProblem p;
+  attn_status s = check_cache(cache, B, T, T, table_capacity(cache), &p);
+  if (s != ATTN_OK) return s;
+  if (B == 0 || T == 0 || p.Hkv == 0) return ATTN_OK;
+  if (!k || !v) return ATTN_ERR_ARG;
+  if ((s = check_cache_pointers(p, offsets, seq_lens)) != ATTN_OK) return s;
+  if (!aligned16(k) || !aligned16(v)) return ATTN_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != ATTN_OK) return s;
+  p.status = dev->status;
+  p.offsets = offsets;
+  p.seq_lens = seq_lens;
+  return from_cuda(launch_cache_read(p, static_cast<__nv_bfloat16*>(k),
+                                     static_cast<__nv_bfloat16*>(v),
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+int attn_prefill_split_keys(int B, int T, int Hq, int Hkv, int max_new, int max_seq_len,
+                            long long total_kv_tokens, int num_sms) {
+  const long long whole = std::max(128LL, ((long long)max_seq_len + 127) / 128 * 128);
+  const long long one = std::min(whole, 0x7fffff80LL);
+  if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || max_new <= 0 || max_seq_len <= 0 ||
+      total_kv_tokens <= 0 || Hq % Hkv != 0)
+    return (int)one;
+  const long long G = Hq / Hkv;
+  const long long units = std::min((long long)T * G / 256 + B,
+                                   (long long)B * ((max_new * G + 255) / 256)) * Hkv;
+  const long long target = num_sms > 0 ? num_sms : 148;
+  if (units >= target) return (int)one;
+  // each unit walks its sequence's keys: total_kv_tokens / B of them on average
+  const long long keys = (total_kv_tokens / B * units + target - 1) / target;
+  return (int)std::min(std::max(512LL, (keys + 127) / 128 * 128), one);
+}
+
+size_t attn_prefill_workspace_size(int T, int Hq, int d, int max_seq_len, int split_keys) {
+  if (T <= 0 || Hq <= 0 || d <= 0 || max_seq_len <= 0 || split_keys <= 0) return 0;
+  const long long n = decode_chunks(max_seq_len, split_keys);
+  if (n <= 1) return 0;
+  const long long rows = (long long)T * Hq;
+  return decode_lse_plane(n, rows) + round256((size_t)(n * rows) * d * sizeof(float));
+}
+
+attn_status attn_prefill_paged(const attn_paged_cache* cache, const void* q,
+                               long long q_token_stride, long long q_head_stride, void* o,
+                               float* lse, const int32_t* offsets, const int32_t* seq_lens,
+                               int B, int T, int Hq, int max_new, int max_seq_len,
+                               int split_keys, float scale, int mask_kind,
+                               const attn_mask_params* mask_params, int score_kind,
+                               const attn_score_params* score_params, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  PagedAttention a{};
+  attn_status s = check_cache(cache, B, T, max_new, max_seq_len, &a.p);
+  if (s != ATTN_OK) return s;
+  const int d = a.p.d, Hkv = a.p.Hkv;
+  if (Hq < 0 || (Hkv == 0 ? Hq != 0 : (Hq % Hkv) != 0)) return ATTN_ERR_SHAPE;
+  if (!stride_ok(q_token_stride) || !stride_ok(q_head_stride)) return ATTN_ERR_ALIGN;
+  if (split_keys <= 0 || split_keys % 128 != 0) return ATTN_ERR_ARG;
+  if ((s = check_paged_scores(scale, mask_kind, mask_params, score_kind, score_params, &a)) !=
+      ATTN_OK)
+    return s;
+  if (B == 0 || T == 0 || Hq == 0) return ATTN_OK;
+  if (!q || !o || !lse) return ATTN_ERR_ARG;
+  if ((s = check_cache_pointers(a.p, offsets, seq_lens)) != ATTN_OK) return s;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return ATTN_ERR_ALIGN;
+  a.Hq = Hq;
+  a.G = Hq / Hkv;
+  const size_t need = attn_prefill_workspace_size(T, Hq, d, max_seq_len, split_keys);
+  if ((s = set_splits(&a, split_keys, need, workspace, workspace_bytes)) != ATTN_OK) return s;
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != ATTN_OK) return s;
+  a.p.status = dev->status;
+  a.p.offsets = offsets;
+  a.p.seq_lens = seq_lens;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.q_token = q_token_stride; a.q_head = q_head_stride;
+  a.o_token = (long long)Hq * d; a.o_head = d;
+  a.l_token = Hq; a.l_head = 1;
+  return from_cuda(launch_paged_attention(a, dev->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+attn_status attn_decode_paged_e4m3(const attn_paged_cache* cache, const void* q,
+                                   const int32_t* seq_lens, void* o, float* lse, int B, int Hq,
+                                   int Nq, int max_seq_len, int split_keys, float scale,
+                                   int mask_kind, const attn_mask_params* mask_params,
+                                   int score_kind, const attn_score_params* score_params,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  if (!cache || cache->kind != ATTN_CACHE_E4M3) return ATTN_ERR_ARG;
+  if (B < 0 || Nq < 0 || Hq < 0 || (long long)B * Nq > 0x7fffffffLL) return ATTN_ERR_SHAPE;
+  PagedAttention a{};
+  attn_status s = check_cache(cache, B, B * Nq, Nq, max_seq_len, &a.p);
+  if (s != ATTN_OK) return s;
+  const int d = a.p.d, Hkv = a.p.Hkv;
+  if (Hkv == 0 ? Hq != 0 : (Hq % Hkv) != 0) return ATTN_ERR_SHAPE;
+  if (split_keys <= 0 || split_keys % 64 != 0) return ATTN_ERR_ARG;
+  if ((s = check_paged_scores(scale, mask_kind, mask_params, score_kind, score_params, &a)) !=
+      ATTN_OK)
+    return s;
+  if (B == 0 || Nq == 0 || Hq == 0) return ATTN_OK;
+  if (!q || !o || !lse) return ATTN_ERR_ARG;
+  if ((s = check_cache_pointers(a.p, seq_lens, seq_lens)) != ATTN_OK) return s;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return ATTN_ERR_ALIGN;
+  a.Hq = Hq;
+  a.G = Hq / Hkv;
+  const size_t need = attn_decode_workspace_size(B, Hq, Hkv, Nq, d, max_seq_len, split_keys);
+  if ((s = set_splits(&a, split_keys, need, workspace, workspace_bytes)) != ATTN_OK) return s;
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != ATTN_OK) return s;
+  a.p.status = dev->status;
+  a.p.seq_lens = seq_lens;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.q_batch = a.o_batch = (long long)Hq * Nq * d;
+  a.q_head = a.o_head = (long long)Nq * d;
+  a.q_token = a.o_token = d;
+  a.l_batch = (long long)Hq * Nq; a.l_head = Nq; a.l_token = 1;
+  return from_cuda(launch_paged_attention(a, dev->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
 attn_status attn_classify_tiles(int mask_kind, const attn_mask_params* mask_params, int Nq,
                                 int Nkv, int32_t* classes, void* stream) {
   Problem p;
@@ -693,13 +928,13 @@ const char* attn_strerror(attn_status status) {
     case ATTN_ERR_ARG: return "invalid argument (null pointer, unknown kind or bad parameter)";
     case ATTN_ERR_SHAPE:
       return "unsupported shape (d must be 64 or 128, or 256 for attn_fwd; Hq a multiple of Hkv)";
-    case ATTN_ERR_ALIGN: return "tensor pointer not 16-byte aligned";
+    case ATTN_ERR_ALIGN: return "tensor pointer or row stride not 16-byte aligned";
     case ATTN_ERR_ARCH: return "current device is not an sm_103 (GB300) GPU";
-    case ATTN_ERR_WORKSPACE: return "workspace missing or smaller than attn_bwd_workspace_size";
+    case ATTN_ERR_WORKSPACE: return "workspace missing or smaller than the call's workspace size";
     case ATTN_ERR_LAUNCH: return "CUDA launch or driver call failed";
     case ATTN_ERR_DEVICE_TIMEOUT: return "a kernel gave up a bounded wait";
     case ATTN_ERR_DEVICE_INPUT:
-      return "a kernel met an out-of-range device input (sequence length or page index)";
+      return "a kernel met an out-of-range device input (offsets, sequence length or page index)";
   }
   return "unknown status";
 }

@@ -1,0 +1,238 @@
+// Writing new tokens into the paged cache and reading them back.
+//
+// Writing to an e4m3 cache takes, per (token, kv head) and for K and V apart, the smallest
+// power of two 2^e with amax <= 448 * 2^e and stores e4m3(x * 2^-e). With amax = m * 2^x,
+// 1 <= m < 2, and 448 = 1.75 * 2^8, that is e = x - 8 for m <= 1.75, else x - 7. The scale
+// is a power of two because a floating-point code loses nothing by it, and because
+// code * 2^e is then exact in bf16 and in the attention kernels' fp16 operands.
+//
+// Both directions move each byte once and compute next to nothing: they are bound by HBM
+// for long batches and by the chain of dependent loads (offsets, lengths, page table) for
+// a decode step. A warp owns one packed row's slice of kChunksPerWarp 16-byte pieces, all
+// of them in flight at once; the row's values are fetched before its slot is known.
+#include "paged.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kWarps = 8;          // warps per CTA, each with its own row slice
+constexpr int kPieces = 4;         // bf16 pieces of 16 bytes per lane
+constexpr int kChunksPerWarp = 32 * kPieces;
+
+// Largest finite magnitude of 8 bf16 values, as bf16 bits (their order is the numbers').
+__device__ __forceinline__ uint32_t finite_amax8(const uint4& w) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = u[i] & 0x7FFFu, hi = (u[i] >> 16) & 0x7FFFu;
+    m = max(m, lo < 0x7F80u ? lo : 0u);
+    m = max(m, hi < 0x7F80u ? hi : 0u);
+  }
+  return m;
+}
+
+// Biased exponent byte of the scale of a row whose largest magnitude has these bf16 bits.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+  if (amax == 0) return 0;
+  const int field = (int)(amax >> 7);  // x + 127; 0 for a subnormal, whose e is below -127
+  const int e = (amax & 0x7Fu) <= 0x60u ? field - 8 : field - 7;
+  return (uint32_t)(e < 0 ? 0 : e);
+}
+
+// Eight bf16 values times inv (a power of two) to eight e4m3 codes, lowest element first.
+__device__ __forceinline__ uint2 encode8(const uint4& w, float inv) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo = __uint_as_float(u[i] << 16), hi = __uint_as_float(u[i] & 0xFFFF0000u);
+    // an infinity would saturate to the largest finite code
+    lo = isinf(lo) ? __uint_as_float(0x7FC00000u) : lo * inv;
+    hi = isinf(hi) ? __uint_as_float(0x7FC00000u) : hi * inv;
+    c[i] = pack_e4m3x2(lo, hi);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+struct CopyArgs {
+  PagedProblem p;
+  RowView in[2];            // write: K and V rows
+  __nv_bfloat16* out[2];    // read: contiguous [T, Hkv, d]
+  int slices;               // warps per row
+};
+
+// The packed row, slice and sequence of a warp; false when there is nothing to do. A
+// position outside the sequence or the page table is reported, not followed.
+struct WarpRow {
+  int t, c0, b, pos;
+};
+__device__ __forceinline__ bool locate(const CopyArgs& a, int lane, WarpRow& r) {
+  const PagedProblem& p = a.p;
+  r.b = find_sequence(p, r.t, lane);
+  const Span s = load_span(p, r.b);
+  const int i = r.t - s.row0;
+  if (i < 0 || i >= s.n) return false;  // a row of no sequence, or bad inputs
+  r.pos = s.L - s.n + i;
+  if (r.pos < 0) {
+    if (lane == 0) atomicOr(p.status, DEV_BAD_INPUT);
+    return false;
+  }
+  return true;
+}
+
+template <int D, bool kE4m3>
+__global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(const CopyArgs a) {
+  constexpr int kPer = D / 8;  // 16-byte pieces per (head, K or V) row: 8 or 16 lanes
+  const PagedProblem& p = a.p;
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0) report_bad_spans(p);
+  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  WarpRow r;
+  r.t = (int)(unit / a.slices);
+  if (r.t >= p.T) return;
+  r.c0 = (int)(unit % a.slices) * kChunksPerWarp;
+  const int per_tensor = p.Hkv * kPer;
+  uint4 w[kPieces];
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) {  // K heads, then V heads
+    const int c = r.c0 + j * 32 + lane;
+    const bool is_v = c >= per_tensor;
+    const int cc = is_v ? c - per_tensor : c;
+    const RowView& in = a.in[is_v];
+    w[j] = make_uint4(0, 0, 0, 0);
+    if (c < 2 * per_tensor)
+      w[j] = __ldg(reinterpret_cast<const uint4*>(in.p + (long long)r.t * in.token_stride +
+                                                  (long long)(cc / kPer) * in.head_stride) + cc % kPer);
+  }
+  if (!locate(a, lane, r)) return;
+  const long long row0 = cache_row(p, r.b, r.pos, 0);
+  if (row0 < 0) {
+    if (lane == 0) atomicOr(p.status, DEV_BAD_INPUT);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) {
+    const int c = r.c0 + j * 32 + lane;
+    const bool is_v = c >= per_tensor;
+    const int cc = is_v ? c - per_tensor : c;
+    const int head = cc / kPer, piece = cc % kPer;
+    const long long row = row0 + (long long)head * p.page_size;
+    void* base = is_v ? p.v_cache : p.k_cache;
+    if constexpr (!kE4m3) {
+      if (c < 2 * per_tensor) reinterpret_cast<uint4*>(base)[row * kPer + piece] = w[j];
+    } else {
+      uint32_t m = finite_amax8(w[j]);  // the kPer lanes of one head's row agree on it
+#pragma unroll
+      for (int off = kPer / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+      const uint32_t byte = scale_byte(m);
+      const float inv = __uint_as_float((254u - byte) << 23);  // 2^-(byte - 127)
+      if (c < 2 * per_tensor) {
+        reinterpret_cast<uint2*>(base)[row * kPer + piece] = encode8(w[j], inv);
+        if (piece == 0) p.kv_exp[row * 2 + is_v] = (uint8_t)byte;
+      }
+    }
+  }
+}
+
+template <int D, bool kE4m3>
+__global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(const CopyArgs a) {
+  constexpr int kPer = D / 8;
+  const PagedProblem& p = a.p;
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0) report_bad_spans(p);
+  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  WarpRow r;
+  r.t = (int)(unit / a.slices);
+  if (r.t >= p.T) return;
+  r.c0 = (int)(unit % a.slices) * kChunksPerWarp;
+  if (!locate(a, lane, r)) return;
+  const long long row0 = cache_row(p, r.b, r.pos, 0);
+  if (row0 < 0) {
+    if (lane == 0) atomicOr(p.status, DEV_BAD_INPUT);
+    return;
+  }
+  const int per_tensor = p.Hkv * kPer;
+  uint4 w[kPieces];
+  uint32_t byte[kPieces];
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) {
+    const int c = r.c0 + j * 32 + lane;
+    const bool is_v = c >= per_tensor;
+    const int cc = is_v ? c - per_tensor : c;
+    const long long row = row0 + (long long)(cc / kPer) * p.page_size;
+    const void* base = is_v ? p.v_cache : p.k_cache;
+    w[j] = make_uint4(0, 0, 0, 0);
+    byte[j] = 127;
+    if (c >= 2 * per_tensor) continue;
+    if constexpr (kE4m3) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(base) + row * kPer + cc % kPer);
+      w[j].x = v.x;
+      w[j].y = v.y;
+      byte[j] = __ldg(p.kv_exp + row * 2 + is_v);
+    } else {
+      w[j] = __ldg(reinterpret_cast<const uint4*>(base) + row * kPer + cc % kPer);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) {
+    const int c = r.c0 + j * 32 + lane;
+    if (c >= 2 * per_tensor) continue;
+    const bool is_v = c >= per_tensor;
+    const int cc = is_v ? c - per_tensor : c;
+    if constexpr (kE4m3) {
+      const float s = exp_byte_scale(byte[j]);
+      const uint32_t codes[4] = {w[j].x, w[j].x >> 16, w[j].y, w[j].y >> 16};
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(codes[i]));
+        u[i] = pack_bf16x2(f.x * s, f.y * s);
+      }
+      w[j] = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    reinterpret_cast<uint4*>(a.out[is_v])[((long long)r.t * p.Hkv) * kPer + cc] = w[j];
+  }
+}
+
+cudaError_t launch_copy(const CopyArgs& args, bool write, cudaStream_t st) {
+  const PagedProblem& p = args.p;
+  CopyArgs a = args;
+  const int chunks = 2 * p.Hkv * (p.d / 8);
+  if (p.T == 0 || chunks == 0) return cudaSuccess;
+  a.slices = ceil_div(chunks, kChunksPerWarp);
+  const long long blocks = ((long long)p.T * a.slices + kWarps - 1) / kWarps;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const unsigned g = (unsigned)blocks, t = kWarps * 32;
+  const bool e = p.kv_exp != nullptr;
+  if (write) {
+    if (p.d == 64) e ? cache_write_kernel<64, true><<<g, t, 0, st>>>(a) : cache_write_kernel<64, false><<<g, t, 0, st>>>(a);
+    else e ? cache_write_kernel<128, true><<<g, t, 0, st>>>(a) : cache_write_kernel<128, false><<<g, t, 0, st>>>(a);
+  } else {
+    if (p.d == 64) e ? cache_read_kernel<64, true><<<g, t, 0, st>>>(a) : cache_read_kernel<64, false><<<g, t, 0, st>>>(a);
+    else e ? cache_read_kernel<128, true><<<g, t, 0, st>>>(a) : cache_read_kernel<128, false><<<g, t, 0, st>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const PagedProblem& p, const RowView& k, const RowView& v,
+                               cudaStream_t st) {
+  CopyArgs a{};
+  a.p = p;
+  a.in[0] = k;
+  a.in[1] = v;
+  return launch_copy(a, true, st);
+}
+
+cudaError_t launch_cache_read(const PagedProblem& p, __nv_bfloat16* k, __nv_bfloat16* v,
+                              cudaStream_t st) {
+  CopyArgs a{};
+  a.p = p;
+  a.out[0] = k;
+  a.out[1] = v;
+  return launch_copy(a, false, st);
+}
+
+}  // namespace attn

@@ -1,0 +1,186 @@
+"""The paged cache: writing new tokens (bf16 or e4m3), reading them back, and attention of
+ragged chunks of new tokens over it. Argument checks and marshalling for the C ABI
+(include/attn.h states layouts, scales and bad-input rules); decode over the cache is
+attention.decode_paged.
+
+A call's rows are packed: offsets int32 [B + 1] cuts them into sequences, and sequence b's
+rows are its newest tokens, row i of n at position seq_lens[b] - n + i. An e4m3 cache is two
+uint8 tensors of codes plus kv_exp uint8 [pages, Hkv, page_size, 2], the biased exponents of
+each token's K and V scale; passing kv_exp selects it.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import _lib
+from .attention import (MASK_NONE, SCORE_NONE, _BF16, _F32, _U8, _check_dtypes, _check_tensors,
+                        _params, _ptr, _stream)
+
+CACHE_BF16, CACHE_E4M3 = 0, 1
+
+
+def _cache(k_cache, v_cache, page_table, kv_exp, B: int) -> _lib.PagedCache:
+    _check_tensors(k_cache, v_cache, page_table, kv_exp)
+    kind = _BF16 if kv_exp is None else _U8
+    _check_dtypes((k_cache, kind, "k_cache"), (v_cache, kind, "v_cache"), (kv_exp, _U8, "kv_exp"),
+                  (page_table, torch.int32, "page_table"))
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be [pages, Hkv, page_size, d]")
+    pages, Hkv, page_size, d = k_cache.shape
+    if kv_exp is not None and tuple(kv_exp.shape) != (pages, Hkv, page_size, 2):
+        raise ValueError(f"kv_exp must have shape {(pages, Hkv, page_size, 2)}, got "
+                         f"{tuple(kv_exp.shape)}")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, max_pages]")
+    return _lib.PagedCache(k_cache.data_ptr(), v_cache.data_ptr(),
+                           None if kv_exp is None else kv_exp.data_ptr(), page_table.data_ptr(),
+                           CACHE_BF16 if kv_exp is None else CACHE_E4M3, pages, Hkv, page_size, d,
+                           page_table.shape[1])
+
+
+def _check_batch(offsets, seq_lens) -> int:
+    _check_tensors(offsets, seq_lens)
+    _check_dtypes((offsets, torch.int32, "offsets"), (seq_lens, torch.int32, "seq_lens"))
+    if seq_lens.dim() != 1 or offsets.dim() != 1 or offsets.shape[0] != seq_lens.shape[0] + 1:
+        raise ValueError("offsets must be [B + 1] and seq_lens [B]")
+    return seq_lens.shape[0]
+
+
+def _rows(t, H: int, d: int, name: str):
+    """Pointer and element strides of packed rows [T, H, d], d contiguous."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if t.dtype != _BF16:
+        raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != d:
+        raise ValueError(f"{name} must be [T, {H}, {d}], got {tuple(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name} must be contiguous along d")
+    return (_ptr(t), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if H > 1 else 0)
+
+
+def cache_write(k, v, k_cache, v_cache, page_table, offsets, seq_lens, *, kv_exp=None,
+                stream=None) -> None:
+    """Write the new tokens' K and V rows (bf16 [T, Hkv, d], any token and head stride that
+    is a multiple of 8) into the cache: as they are, or with kv_exp as e4m3 codes under the
+    smallest power-of-two scale that holds each row."""
+    B = _check_batch(offsets, seq_lens)
+    cache = _cache(k_cache, v_cache, page_table, kv_exp, B)
+    kp, kt, kh = _rows(k, cache.Hkv, cache.d, "k")
+    vp, vt, vh = _rows(v, cache.Hkv, cache.d, "v")
+    if v.shape[0] != k.shape[0]:
+        raise ValueError("k and v disagree on the number of tokens")
+    _lib.check(_lib.load().attn_cache_write(ctypes.byref(cache), kp, kt, kh, vp, vt, vh,
+                                            _ptr(offsets), _ptr(seq_lens), B, k.shape[0],
+                                            _stream(stream)), "attn_cache_write")
+
+
+def cache_read_into(k_cache, v_cache, page_table, offsets, seq_lens, k, v, *, kv_exp=None,
+                    stream=None) -> None:
+    """Read the newest tokens of each sequence into k and v (bf16 [T, Hkv, d], contiguous);
+    rows behind offsets[B] keep what they held."""
+    B = _check_batch(offsets, seq_lens)
+    cache = _cache(k_cache, v_cache, page_table, kv_exp, B)
+    _check_tensors(k, v)
+    _check_dtypes((k, _BF16, "k"), (v, _BF16, "v"))
+    if k.dim() != 3 or tuple(k.shape[1:]) != (cache.Hkv, cache.d) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [T, {cache.Hkv}, {cache.d}]")
+    _lib.check(_lib.load().attn_cache_read(ctypes.byref(cache), _ptr(k), _ptr(v), _ptr(offsets),
+                                           _ptr(seq_lens), B, k.shape[0], _stream(stream)),
+               "attn_cache_read")
+
+
+def cache_read(k_cache, v_cache, page_table, offsets, seq_lens, n_tokens: int, *, kv_exp=None,
+               stream=None):
+    """Allocating wrapper of cache_read_into for n_tokens = offsets[B] rows: (k, v)."""
+    shape = (int(n_tokens), k_cache.shape[1], k_cache.shape[3])
+    k = torch.empty(shape, dtype=_BF16, device=k_cache.device)
+    v = torch.empty(shape, dtype=_BF16, device=k_cache.device)
+    cache_read_into(k_cache, v_cache, page_table, offsets, seq_lens, k, v, kv_exp=kv_exp,
+                    stream=stream)
+    return k, v
+
+
+_SMS: dict = {}
+
+
+def _num_sms() -> int:
+    """SM count of the current device (0 without one), looked up once per device."""
+    if not torch.cuda.is_available():
+        return 0
+    dev = torch.cuda.current_device()
+    if dev not in _SMS:
+        _SMS[dev] = torch.cuda.get_device_properties(dev).multi_processor_count
+    return _SMS[dev]
+
+
+def prefill_split_keys(B: int, T: int, Hq: int, Hkv: int, max_new: int, max_seq_len: int,
+                       total_kv_tokens: int, num_sms: Optional[int] = None) -> int:
+    """The library's split size for a prefill_paged call (keys per chunk)."""
+    return int(_lib.load().attn_prefill_split_keys(
+        int(B), int(T), int(Hq), int(Hkv), int(max_new), int(max_seq_len), int(total_kv_tokens),
+        _num_sms() if num_sms is None else int(num_sms)))
+
+
+def prefill_workspace_size(T: int, Hq: int, d: int, max_seq_len: int, split_keys: int) -> int:
+    return int(_lib.load().attn_prefill_workspace_size(int(T), int(Hq), int(d), int(max_seq_len),
+                                                       int(split_keys)))
+
+
+def prefill_paged_into(q, k_cache, v_cache, page_table, offsets, seq_lens, o, lse, workspace, *,
+                       max_new: int, max_seq_len: int, split_keys: int, scale: float,
+                       kv_exp=None, mask_kind: int = MASK_NONE, window: int = 0,
+                       score_kind: int = SCORE_NONE, softcap: float = 0.0, stream=None) -> None:
+    """attn_prefill_paged on caller-owned tensors: q bf16 [T, Hq, d] (any token and head
+    stride that is a multiple of 8), o bf16 [T, Hq, d] and lse fp32 [T, Hq] contiguous. Rows
+    behind offsets[B] keep what they held."""
+    B = _check_batch(offsets, seq_lens)
+    cache = _cache(k_cache, v_cache, page_table, kv_exp, B)
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, d]")
+    T, Hq, d = q.shape
+    qp, qt, qh = _rows(q, Hq, cache.d, "q")
+    _check_tensors(o, lse, workspace)
+    _check_dtypes((o, _BF16, "o"), (lse, _F32, "lse"))
+    if o.shape != q.shape or lse.shape != q.shape[:2]:
+        raise ValueError("o must be [T, Hq, d] and lse [T, Hq]")
+    mp, sp, _keep = _params(mask_kind, window, None, softcap)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _lib.check(_lib.load().attn_prefill_paged(
+        ctypes.byref(cache), qp, qt, qh, _ptr(o), _ptr(lse), _ptr(offsets), _ptr(seq_lens), B, T,
+        Hq, int(max_new), int(max_seq_len), int(split_keys), scale, mask_kind, mp, score_kind, sp,
+        _ptr(workspace), ws_bytes, _stream(stream)), "attn_prefill_paged")
+
+
+def prefill_paged(q, k_cache, v_cache, page_table, offsets, seq_lens, *, kv_exp=None,
+                  max_new: Optional[int] = None, max_seq_len: Optional[int] = None,
+                  split_keys: Optional[int] = None, total_kv_tokens: Optional[int] = None,
+                  scale: Optional[float] = None, mask_kind: int = MASK_NONE, window: int = 0,
+                  score_kind: int = SCORE_NONE, softcap: float = 0.0, stream=None):
+    """Allocating wrapper of prefill_paged_into: (o, lse) of the chunks' rows. max_new (the
+    longest chunk) defaults to T, max_seq_len to the page table's capacity, split_keys to
+    the library's choice (total_kv_tokens, the sum of seq_lens when the caller knows it,
+    lets it weigh long sequences against short ones)."""
+    T, Hq, d = q.shape
+    B = seq_lens.shape[0]
+    if max_seq_len is None:
+        max_seq_len = page_table.shape[1] * k_cache.shape[2]
+    if max_new is None:
+        max_new = T
+    if split_keys is None:
+        split_keys = prefill_split_keys(B, T, Hq, k_cache.shape[1], max_new, max_seq_len,
+                                        total_kv_tokens or B * max_seq_len)
+    if scale is None:
+        scale = float(d) ** -0.5
+    o = torch.empty((T, Hq, d), dtype=_BF16, device=q.device)
+    lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
+    nbytes = prefill_workspace_size(T, Hq, d, max_seq_len, split_keys)
+    ws = torch.empty((nbytes,), dtype=_U8, device=q.device) if nbytes else None
+    prefill_paged_into(q, k_cache, v_cache, page_table, offsets, seq_lens, o, lse, ws,
+                       max_new=max_new, max_seq_len=max_seq_len, split_keys=split_keys,
+                       scale=scale, kv_exp=kv_exp, mask_kind=mask_kind, window=window,
+                       score_kind=score_kind, softcap=softcap, stream=stream)
+    return o, lse

@@ -323,6 +323,120 @@ int attn_decode_split_keys(int B, int Hq, int Hkv, int Nq, long long total_kv_to
                            int num_sms);
 
 /*
+ * ---- The paged cache as a whole: writing it, reading it back, attending chunks of new
+ * tokens to it, and decode over an 8-bit cache ("FlashAttention/es", "Variantes y
+ * sucesores": PagedAttention). One HOST struct describes a cache; its tensors are DEVICE
+ * memory in attn_decode_paged's layout:
+ *   k, v        [num_pages, Hkv, page_size, d]: page p, kv head g, slot s; bf16
+ *               (ATTN_CACHE_BF16) or e4m3 codes, one byte each (ATTN_CACHE_E4M3)
+ *   kv_exp      ATTN_CACHE_E4M3 only (NULL otherwise): uint8 [num_pages, Hkv, page_size, 2],
+ *               the biased exponents of the K and of the V scale of each token and kv head:
+ *               the value of a code is code * 2^(exp - 127)
+ *   page_table  int32 [B, max_pages_per_seq], as in attn_decode_paged
+ * d: 64 or 128; page_size: 8, 16, 32 or a multiple of 64; k, v, kv_exp 16-byte aligned.
+ *
+ * The calls take the packed rows of a ragged batch: offsets is int32 [B + 1] (DEVICE),
+ * offsets[0] = 0, non-decreasing, offsets[B] <= T. Rows offsets[b] .. offsets[b+1] - 1 are
+ * the n_b newest tokens of sequence b (n_b may be 0): row i of them sits at position
+ * seq_lens[b] - n_b + i, where seq_lens int32 [B] (DEVICE) counts these tokens too. Rows of
+ * a call behind offsets[B] belong to no sequence: they are neither read nor written.
+ * Input rows may be strided views: element (t, h, c) of such a tensor is at
+ * t * token_stride + h * head_stride + c (strides in elements, non-negative multiples of
+ * 8; base 16-byte aligned), so the q, k and v slices of a fused projection need no copy.
+ * Bad DEVICE inputs (offsets that break the rule above, a length above the page table's
+ * capacity or max_seq_len, a page index outside [0, num_pages), for cache_write and
+ * cache_read a position below 0) are skipped, never followed, and reported by
+ * attn_device_status as ATTN_ERR_DEVICE_INPUT; the results of that call are then
+ * unspecified. The calls allocate nothing, take any B and T (0 included) and are
+ * deterministic.
+ */
+enum { ATTN_CACHE_BF16 = 0, ATTN_CACHE_E4M3 = 1 };
+
+typedef struct {
+  void* k;
+  void* v;
+  uint8_t* kv_exp;
+  const int32_t* page_table;
+  int32_t kind;                /* ATTN_CACHE_* */
+  int32_t num_pages, Hkv, page_size, d;
+  int32_t max_pages_per_seq;
+} attn_paged_cache;
+
+/*
+ * Writes the K and V rows of the new tokens (bf16 [T, Hkv, d], strided) into the cache. A
+ * bf16 cache takes them as they are. An e4m3 cache takes, per token and kv head and for K
+ * and V apart, the smallest e with amax <= 448 * 2^e (amax: the largest finite magnitude of
+ * the d values; e clamped to [-127, 127], -127 for a row of zeros), the codes
+ * e4m3(x * 2^-e) rounded to nearest even, and the byte e + 127. A power-of-two scale costs
+ * a floating-point code no precision, and code * 2^e is exact in bf16. NaN and infinities
+ * become the NaN code. Slots of different new tokens must differ (two sequences may share
+ * pages of older tokens, not the slot of a token that this call writes).
+ */
+attn_status attn_cache_write(const attn_paged_cache* cache, const void* k,
+                             long long k_token_stride, long long k_head_stride, const void* v,
+                             long long v_token_stride, long long v_head_stride,
+                             const int32_t* offsets, const int32_t* seq_lens, int B, int T,
+                             void* stream);
+
+/*
+ * Reads the newest tokens back: k, v bf16 [T, Hkv, d] (contiguous) receive the cached rows
+ * (an e4m3 cache: code * 2^e, rounded to bf16, which is exact for what attn_cache_write
+ * wrote down to bf16's smallest normal value). With n_b = seq_lens[b] this is the whole
+ * sequence.
+ */
+attn_status attn_cache_read(const attn_paged_cache* cache, void* k, void* v,
+                            const int32_t* offsets, const int32_t* seq_lens, int B, int T,
+                            void* stream);
+
+/*
+ * Attention of a ragged batch of chunks of new tokens over the cache (chunked prefill; the
+ * new tokens' own K and V are in the cache already, see attn_cache_write).
+ *   q    bf16 [T, Hq, d], strided;  o bf16 [T, Hq, d];  lse fp32 [T, Hq] (natural log)
+ * Masks, ALiBi, soft-cap and their positions are those of attn_decode_paged. A row without
+ * an allowed key gets O = 0 and lse = -inf. max_new bounds every n_b and max_seq_len
+ * (<= max_pages_per_seq * page_size) every seq_lens[b]; tighter bounds launch fewer CTAs.
+ * split_keys (a positive multiple of 128, see attn_prefill_split_keys) cuts the keys into
+ * chunks computed by separate CTAs and merged by their log-sum-exp; with
+ * max_seq_len <= split_keys no merge runs and no workspace is needed. workspace: DEVICE
+ * memory of attn_prefill_workspace_size bytes, 256-byte aligned, not shared with a
+ * concurrent call (two captured graphs that may run at the same time need one each).
+ * An e4m3 cache is attended to as the values its codes stand for.
+ */
+attn_status attn_prefill_paged(const attn_paged_cache* cache, const void* q,
+                               long long q_token_stride, long long q_head_stride, void* o,
+                               float* lse, const int32_t* offsets, const int32_t* seq_lens,
+                               int B, int T, int Hq, int max_new, int max_seq_len,
+                               int split_keys, float scale, int mask_kind,
+                               const attn_mask_params* mask_params, int score_kind,
+                               const attn_score_params* score_params, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * Workspace bytes of attn_prefill_paged: with n = ceil(max_seq_len / split_keys) and
+ * R = T * Hq rows, round256(4 n R) + round256(4 n R d) when n > 1, else 0.
+ */
+size_t attn_prefill_workspace_size(int T, int Hq, int d, int max_seq_len, int split_keys);
+
+/*
+ * A split_keys for attn_prefill_paged: all keys in one chunk when the row tiles alone fill
+ * the SMs, else chunks of at least 512 keys, as many as fill them over total_kv_tokens (the
+ * sum of seq_lens, or B * max_seq_len when unknown). Pure function of its arguments.
+ */
+int attn_prefill_split_keys(int B, int T, int Hq, int Hkv, int max_new, int max_seq_len,
+                            long long total_kv_tokens, int num_sms);
+
+/*
+ * attn_decode_paged over an ATTN_CACHE_E4M3 cache: same queries, outputs, masks, score
+ * modifications, split_keys and workspace (attn_decode_workspace_size).
+ */
+attn_status attn_decode_paged_e4m3(const attn_paged_cache* cache, const void* q,
+                                   const int32_t* seq_lens, void* o, float* lse, int B, int Hq,
+                                   int Nq, int max_seq_len, int split_keys, float scale,
+                                   int mask_kind, const attn_mask_params* mask_params,
+                                   int score_kind, const attn_score_params* score_params,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Block-sparsity classifier ("El FlexAttention de PyTorch con FlashAttention-4 es
  * un cambio radical", "Limitaciones actuales", names block sparsity): writes
  * classes[r * ceil(Nkv/128) + c] = EMPTY / PARTIAL / FULL for query tile r and key
