@@ -423,7 +423,9 @@ attn_status check_cache(const attn_paged_cache* c, int B, int T, int max_new, in
 attn_status check_cache_pointers(const PagedProblem& p, const int32_t* offsets,
                                  const int32_t* seq_lens) {
   if (!offsets || !seq_lens) return ATTN_ERR_ARG;
-  if (p.max_seq_len > 0 && (!p.k_cache || !p.v_cache || !p.page_table)) return ATTN_ERR_ARG;
+  if (p.max_seq_len > 0 &&
+      (!p.k_cache || !p.v_cache || !p.page_table || p.num_pages == 0 || p.Hkv == 0))
+    return ATTN_ERR_ARG;
   if (!aligned16(p.k_cache) || !aligned16(p.v_cache) || !aligned16(p.kv_exp) ||
       !aligned4(p.page_table) || !aligned4(offsets) || !aligned4(seq_lens))
     return ATTN_ERR_ALIGN;
@@ -457,6 +459,35 @@ attn_status check_paged_scores(float scale, int mask_kind, const attn_mask_param
     a->window = mp->window;
   }
   return ATTN_OK;
+}
+
+// Tensor map over the rows of d codes of an e4m3 cache, boxes of box_rows whole rows,
+// swizzled over the row's 128 or 64 bytes.
+attn_status make_map_codes(CUtensorMap* map, const void* base, int rows, int d,
+                           unsigned box_rows) {
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)d};
+  cuuint32_t box[2] = {(cuuint32_t)d, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+// The maps of the kernel that will run, then the launch.
+attn_status run_paged_attention(const PagedAttention& a, cudaStream_t st) {
+  const PagedProblem& p = a.p;
+  const int rows = p.num_pages * p.Hkv * p.page_size;
+  PagedMaps maps{};  // without cached tokens nothing is loaded through them
+  if (paged_few_rows(a) && p.max_seq_len > 0) {
+    const unsigned box = (unsigned)std::min(p.page_size, 32);
+    attn_status s = make_map_codes(&maps.k, p.k_cache, rows, p.d, box);
+    if (s == ATTN_OK) s = make_map_codes(&maps.v, p.v_cache, rows, p.d, box);
+    if (s != ATTN_OK) return s;
+  }
+  return from_cuda(launch_paged_attention(a, maps, st));
 }
 
 // Splits of the keys and the workspace that holds their partial results.
@@ -829,7 +860,7 @@ attn_status attn_prefill_paged(const attn_paged_cache* cache, const void* q,
   a.q_token = q_token_stride; a.q_head = q_head_stride;
   a.o_token = (long long)Hq * d; a.o_head = d;
   a.l_token = Hq; a.l_head = 1;
-  return from_cuda(launch_paged_attention(a, dev->num_sms, static_cast<cudaStream_t>(stream)));
+  return run_paged_attention(a, static_cast<cudaStream_t>(stream));
 }
 
 attn_status attn_decode_paged_e4m3(const attn_paged_cache* cache, const void* q,
@@ -868,7 +899,7 @@ attn_status attn_decode_paged_e4m3(const attn_paged_cache* cache, const void* q,
   a.q_head = a.o_head = (long long)Nq * d;
   a.q_token = a.o_token = d;
   a.l_batch = (long long)Hq * Nq; a.l_head = Nq; a.l_token = 1;
-  return from_cuda(launch_paged_attention(a, dev->num_sms, static_cast<cudaStream_t>(stream)));
+  return run_paged_attention(a, static_cast<cudaStream_t>(stream));
 }
 
 attn_status attn_classify_tiles(int mask_kind, const attn_mask_params* mask_params, int Nq,

@@ -195,6 +195,18 @@ struct PagedAttention {
   float* part_o;              // [n_chunks, T * Hq, d] fp32 when n_chunks > 1
   float* part_lse;            // [n_chunks, T * Hq]
 };
-cudaError_t launch_paged_attention(const PagedAttention& a, int num_sms, cudaStream_t st);
+// Tensor maps over an e4m3 cache for the row kernel: rows of d codes, boxes of
+// min(page_size, 32) rows, 128-byte (d = 128) or 64-byte swizzle.
+struct PagedMaps {
+  CUtensorMap k, v;
+};
+// Few query rows per kv head over an e4m3 cache take the row kernel.
+constexpr int kPagedRowsMax = 32;
+inline bool paged_few_rows(const PagedAttention& a) {
+  return a.p.kv_exp != nullptr && (long long)a.p.max_new * a.G <= kPagedRowsMax;
+}
+cudaError_t launch_paged_rows(const PagedAttention& a, const PagedMaps& maps, cudaStream_t st);
+cudaError_t launch_paged_attention(const PagedAttention& a, const PagedMaps& maps,
+                                   cudaStream_t st);
 
 }  // namespace attn

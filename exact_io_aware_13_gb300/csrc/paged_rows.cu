@@ -1,0 +1,473 @@
+// Few query rows per kv head over an e4m3 paged cache (decode, speculative tokens, chunks
+// of a handful of tokens): each warp streams key tiles of its own.
+//
+// The recurrence is the forward's ("FlashAttention/es", "El algoritmo FlashAttention"). The
+// work is reading 2 (d + 1) bytes per key and kv head once, with 4 d FLOPs per row on top,
+// so the kernel is built around the stream:
+//   * a CTA (4 warps) takes one key chunk of one (sequence, kv head); warp w takes its
+//     32-key tiles w, w + 4, ... through a ring of its own, filled by TMA (codes, one box
+//     per page piece) and bulk copies (exponents). A warp waits for nobody, and no thread
+//     waits between a tile's arrival and the request for the next one but for its own work;
+//   * codes become fp16 in registers (exact, one conversion for two values) and feed
+//     mma.sync m16n8k16 with the KEYS (S^T = K Q^T) or the head dimension (O^T = V^T P^T) as
+//     the 16-row side and 8 query rows as the other: with a few query rows per kv head a
+//     128-row tile would be empty for the most part. The tensor pipe is not what bounds
+//     this: 8 rows at the full HBM rate need about a tenth of the warp-level MMA rate;
+//   * MMA slots are permuted so that a thread's fragment bytes are contiguous 16-byte pieces:
+//     the head dimension of S^T = K Q^T (K and Q alike), the keys (the order of P^T's columns
+//     is the order of V^T's), and the head dimension of O^T (undone when O is written).
+//     With the 128-byte swizzle every such shared-memory read is free of bank conflicts;
+//   * P^T's fragment is S^T's, transposed by movmatrix: no shared memory in between.
+//
+// Number ranges (fp16 operands, fp32 sums). Q: each row times a power of two that brings its
+// largest magnitude to [2^14, 2^15) - exact but for elements below 2^-29 of it, which lose
+// bits below 2^-39 of it. P: 2^(s - m + 11) <= 2^15 (the running maximum m may lag by 2^4),
+// so weights keep fp16's 11 bits down to 2^-25 of the largest. The V scales are powers of
+// two: P is multiplied by 2^(e_j - E) <= 1, E the largest V exponent so far, and O carries
+// 2^E; the row sum keeps the plain weights.
+#include "paged.cuh"
+#include "paged_out.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kTile = 32;        // keys per ring stage
+constexpr float kPOffset = 11.0f;  // P is scaled by 2^11
+constexpr float kLag = 4.0f;       // O is rescaled when the maximum grows by more than 2^4
+
+// Ring stages per warp. 8.1 KB each at d = 128.
+constexpr int kStages = 3;
+
+template <int D>
+struct Layout {
+  static constexpr int kCodes = kTile * D;                    // one K or V tile
+  static constexpr int kStage = 2 * kCodes;                   // swizzled: 1024-byte aligned
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kExp = kRing;                          // exponents [warp][stage][32][2]
+  static constexpr int kBars = kExp + kWarps * kStages * kTile * 2;
+  static constexpr int kAlloc = kBars + kWarps * kStages * 8 + 16 + 1024;
+};
+
+// Fragment row g (0..7) of a key tile holds key kappa(g): rows g and g + 1 differ in bit 2
+// of the key, so the eight lanes of a 16-byte shared-memory phase hit eight swizzled pieces.
+__device__ __forceinline__ int kappa(int g) { return (g >> 1) | ((g & 1) << 2); }
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  unsigned short v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+
+// Address of 16-byte piece `piece` of row `row` of a swizzled tile of D-byte rows.
+template <int D>
+__device__ __forceinline__ uint32_t piece_addr(uint32_t tile, int row, int piece) {
+  return D == 128 ? tile + row * 128 + ((piece ^ (row & 7)) << 4)
+                  : tile + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32)
+    paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const PagedAttention a) {
+  using L = Layout<D>;
+  constexpr int kSteps = D / 16;   // MMA steps over the head dimension; also 16-row O tiles
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const PagedProblem& p = a.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  if (blockIdx.x == 0) report_bad_spans(p);
+  const int cc = (int)(blockIdx.x % a.n_chunks);
+  const int bh = (int)(blockIdx.x / a.n_chunks);
+  const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
+  const Span sp = load_span(p, b);
+  const int rows = sp.n * a.G;  // packed row i * G + g of query token i, head hk * G + g
+  if (rows == 0) return;
+  // Keys of the chunk that any row sees: the first token's lower end, the last one's upper.
+  int lo0, hi0, lo1, hi1;
+  decode_row_keys(a.mask_kind, a.window, sp.L, sp.n, 0, lo0, hi0);
+  decode_row_keys(a.mask_kind, a.window, sp.L, sp.n, sp.n - 1, lo1, hi1);
+  const int k_lo = imax(lo0, cc * a.chunk);
+  const int k_hi = imin(hi1, (int)imin64((long long)(cc + 1) * a.chunk, sp.L));
+  if (k_hi <= k_lo && a.n_chunks > 1) return;  // the merge reads no such chunk
+  const int tb = k_lo / kTile, te = k_hi > k_lo ? ceil_div(k_hi, kTile) : tb;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  int* abort_flag = reinterpret_cast<int*>(smem + L::kBars + kWarps * kStages * 8);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(bars + i), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const WaitCtx wc{abort_flag, p.status};
+  const uint32_t ring = smem_u32(smem) + warp * kStages * L::kStage;
+  const uint32_t exps = smem_u32(smem + L::kExp) + warp * kStages * kTile * 2;
+  const uint32_t full = smem_u32(bars) + warp * kStages * 8;
+
+  // Requests tile t0 / 32 into stage s: lane q fetches the q-th page piece of it.
+  const int R = imin(p.page_size, kTile), pieces = kTile / R;
+  auto request = [&](int tile, int s) {
+    const int key = tile * kTile + lane * R;
+    const bool in_seq = lane < pieces && key < sp.L;
+    long long row = -1;
+    if (in_seq) {
+      row = cache_row(p, b, key, hk);
+      if (row < 0) atomicOr(p.status, DEV_BAD_INPUT);
+    }
+    const uint32_t bar = full + s * 8;
+    const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0));
+    if (lane == 0) mbar_arrive_expect_tx(bar, n * R * (2 * D + 2));
+    __syncwarp();
+    if (row >= 0) {
+      const uint32_t kt = ring + s * L::kStage + lane * R * D;
+      tma_load_2d(kt, &tm_k, bar, 0, (int)row);
+      tma_load_2d(kt + L::kCodes, &tm_v, bar, 0, (int)row);
+      bulk_load(exps + (s * kTile + lane * R) * 2, p.kv_exp + row * 2, R * 2, bar);
+    }
+  };
+  int issued = tb + warp;  // next tile to request
+  for (int s = 0; s < kStages && issued < te; ++s, issued += kWarps) request(issued, s);
+
+  // Q fragments: thread (g, c) holds, of row nt * 8 + g, the head dimensions 16 c + 4 s .. + 3
+  // (and 64 + ... for steps 4-7) of step s, the pieces it reads of K.
+  uint32_t qf[NT][kSteps][2];
+  float k1[NT][2], slope[NT][2];
+  int lo[NT][2], hi[NT][2], pos[NT][2];
+  const float unit = (a.score_kind & ATTN_SCORE_SOFTCAP) ? 1.0f / a.softcap : kPagedLog2e;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = nt * 8 + g;
+    uint32_t w[kSteps][2];
+    uint32_t top = 0;
+    const bool ok = r < rows;
+    const int i = ok ? r / a.G : 0, h = hk * a.G + (ok ? r - i * a.G : 0);
+    const long long t = p.offsets ? sp.row0 + i : i;
+    const __nv_bfloat16* q = a.q + (p.offsets ? 0 : b) * a.q_batch + t * a.q_token + h * a.q_head;
+#pragma unroll
+    for (int v = 0; v < kSteps / 2; ++v) {  // 16-byte loads: two steps each
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (ok) x = __ldg(reinterpret_cast<const uint4*>(q + (v >> 1) * 64 + c * 16 + (v & 1) * 8));
+      w[2 * v][0] = x.x; w[2 * v][1] = x.y;
+      w[2 * v + 1][0] = x.z; w[2 * v + 1][1] = x.w;
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) top = max(top, max(w[s][e] & 0x7FFFu, (w[s][e] >> 16) & 0x7FFFu));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // top = m 2^x, 1 <= m < 2; the row times 2^(14 - x). Rows below 2^-112 keep x = -112.
+    const int x = imax((int)(top >> 7) - 127, -112);
+    const float up = __uint_as_float((uint32_t)(14 - x + 127) << 23);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        qf[nt][s][e] = pack_f16x2(__uint_as_float(w[s][e] << 16) * up,
+                                  __uint_as_float(w[s][e] & 0xFFFF0000u) * up);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {  // the softmax's rows of this thread: nt * 8 + 2 c + e
+      const int rr = nt * 8 + 2 * c + e;
+      const int xr = __shfl_sync(0xffffffffu, x, (2 * c + e) * 4);
+      const int ii = rr / a.G, hh = hk * a.G + rr - ii * a.G;
+      // 2^(xr - 14) is a normal number: xr >= -112
+      k1[nt][e] = a.scale * unit * __uint_as_float((uint32_t)(xr - 14 + 127) << 23);
+      slope[nt][e] = (a.score_kind & ATTN_SCORE_ALIBI) ? alibi_slope(hh, a.Hq) * unit : 0.f;
+      lo[nt][e] = hi[nt][e] = 0;
+      if (rr < rows) decode_row_keys(a.mask_kind, a.window, sp.L, sp.n, ii, lo[nt][e], hi[nt][e]);
+      pos[nt][e] = sp.L - sp.n + ii;
+    }
+  }
+
+  float o[NT][kSteps][4];  // O^T: (dims of fragment rows g, g + 8) x (query rows 2 c, 2 c + 1)
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[nt][s][e] = 0.f;
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+  }
+  int E = 0;  // largest V exponent byte so far
+  const bool plain = !(a.score_kind & (ATTN_SCORE_ALIBI | ATTN_SCORE_SOFTCAP));
+  const float cap = a.softcap * kPagedLog2e;
+
+  bool live = true;
+  int s = 0;
+  uint32_t parity = 0;
+  for (int tile = tb + warp; tile < te; tile += kWarps) {
+    live = __all_sync(0xffffffffu, mbar_wait(full + s * 8, parity, wc));
+    if (!live) break;
+    const int t0 = tile * kTile;
+    const uint32_t kt = ring + s * L::kStage, vt = kt + L::kCodes, et = exps + s * kTile * 2;
+    const int valid = imin(kTile, sp.L - t0);
+    if (valid < kTile) {  // slots behind the sequence: their V must not reach the sums
+      for (int e = lane; e < (kTile - valid) * (D / 16); e += 32) {
+        const int row = valid + e / (D / 16), piece = e % (D / 16);
+        const uint32_t at = piece_addr<D>(vt, row, piece);
+        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+      }
+      __syncwarp();
+    }
+    const uint32_t e_lane = lds16(et + lane * 2) >> 8;  // V exponent of key t0 + lane
+    const int Et = (int)__reduce_max_sync(0xffffffffu, lane < valid ? e_lane : 0u);
+    // Whether every row sees every key of the tile (warp-uniform)
+    const bool masked = t0 < lo1 || t0 + kTile > hi0 || rows < NT * 8;
+
+    // ---- S^T = K Q^T for the two 16-key halves
+    float x[2][NT][4];
+    float ks[2][2];
+    int ve[2][2];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int row = hf * 16 + kappa(g);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[hf][nt][e] = 0.f;
+#pragma unroll
+      for (int half = 0; half < D / 64; ++half) {
+        const uint4 u = lds128(piece_addr<D>(kt, row, half * 4 + c));
+        const uint4 v = lds128(piece_addr<D>(kt, row + 8, half * 4 + c));
+        const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {
+          const uint32_t a0 = e4m3x2_to_f16x2(uw[st]), a2 = e4m3x2_to_f16x2(uw[st] >> 16);
+          const uint32_t a1 = e4m3x2_to_f16x2(vw[st]), a3 = e4m3x2_to_f16x2(vw[st] >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_16816(x[hf][nt], a0, a1, a2, a3, qf[nt][half * 4 + st][0], qf[nt][half * 4 + st][1]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t w = lds16(et + (row + 8 * e) * 2);
+        ks[hf][e] = exp_byte_scale(w & 255u);
+        ve[hf][e] = (int)(w >> 8);
+      }
+    }
+    // ---- scores in log2 units, row maxima
+    float mt[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mt[nt][0] = mt[nt][1] = -INFINITY;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = t0 + hf * 16 + kappa(g) + 8 * e;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float y = x[hf][nt][2 * e + r] * ks[hf][e] * k1[nt][r];
+            if (!plain) {
+              y -= slope[nt][r] * (float)(pos[nt][r] - j);
+              if (a.score_kind & ATTN_SCORE_SOFTCAP) y = cap * tanhf(y);
+            }
+            if (masked) y = (j >= lo[nt][r] && j < hi[nt][r]) ? y : -INFINITY;
+            x[hf][nt][2 * e + r] = y;
+            mt[nt][r] = fmaxf(mt[nt][r], y);
+          }
+      }
+    bool grow = Et > E;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
+          mt[nt][r] = fmaxf(mt[nt][r], __shfl_xor_sync(0xffffffffu, mt[nt][r], off));
+        grow |= mt[nt][r] > m[nt][r] + kLag;
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+      const int En = imax(E, Et);
+      const float fe = En - E > 126 ? 0.f : __uint_as_float((uint32_t)(127 - (En - E)) << 23);
+      E = En;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float mn = fmaxf(m[nt][r], mt[nt][r]);
+          const float f = mn == -INFINITY ? 1.f : ex2_approx(m[nt][r] - mn);
+          m[nt][r] = mn;
+          l[nt][r] *= f;
+#pragma unroll
+          for (int st = 0; st < kSteps; ++st) {
+            o[nt][st][r] *= f * fe;
+            o[nt][st][2 + r] *= f * fe;
+          }
+        }
+    }
+    // ---- P^T (fp16) and O^T += V^T P^T
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int down = E - ve[hf][e];  // V scale relative to 2^E; slots behind the sequence: any
+        const float wj = down >= 0 && down <= 126 ? __uint_as_float((uint32_t)(127 - down) << 23) : 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float pr[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float off = m[nt][r] == -INFINITY ? 0.f : kPOffset - m[nt][r];
+            pr[r] = ex2_approx(x[hf][nt][2 * e + r] + off);
+            l[nt][r] += pr[r];
+          }
+          pf[nt][e] = transpose_8x8(pack_f16x2(pr[0] * wj, pr[1] * wj));
+        }
+      }
+      // keys of the transposed fragment's slots 2 c, 2 c + 1: c, c + 4 (and + 8)
+      uint32_t w[4][D / 32];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = hf * 16 + c + 4 * k;
+        if constexpr (D == 128) {
+          const uint4 v = lds128(piece_addr<D>(vt, row, kappa(g)));
+          w[k][0] = v.x; w[k][1] = v.y; w[k][2] = v.z; w[k][3] = v.w;
+        } else {
+          const uint2 v = lds64(piece_addr<D>(vt, row, g >> 1) + (g & 1) * 8);
+          w[k][0] = v.x; w[k][1] = v.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb) {  // two head dimensions of the word: one O tile
+          const uint32_t sel = hb ? 0x7362u : 0x5140u;
+          const uint32_t u = prmt(w[0][i], w[1][i], sel), v = prmt(w[2][i], w[3][i], sel);
+          const uint32_t a0 = e4m3x2_to_f16x2(u), a1 = e4m3x2_to_f16x2(u >> 16);
+          const uint32_t a2 = e4m3x2_to_f16x2(v), a3 = e4m3x2_to_f16x2(v >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_16816(o[nt][2 * i + hb], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+        }
+    }
+    __syncwarp();  // every lane has read the stage
+    if (issued < te) {
+      request(issued, s);
+      issued += kWarps;
+    }
+    if (++s == kStages) {
+      s = 0;
+      parity ^= 1;
+    }
+  }
+  if (!live)  // leave no copy in flight into this CTA's shared memory
+    for (int i = 0; i < kStages; ++i) drain_wait(full + i * 8, i < s ? parity ^ 1 : parity);
+
+  // ---- merge of the warps: factors 2^(m_w - M) 2^E_w, fixed order
+  __syncthreads();
+  constexpr int kRows = NT * 8;
+  float* sm_m = reinterpret_cast<float*>(smem);            // [warp][row]
+  float* sm_l = sm_m + kWarps * kRows;
+  float* sm_o = sm_l + kWarps * kRows;                     // [warp][row][D + 4]
+  static_assert((2 * kWarps * kRows + kWarps * kRows * (D + 4)) * 4 <= L::kRing, "merge space");
+  const float vs = exp_byte_scale((uint32_t)E);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float sum = l[nt][r];
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      const int rr = nt * 8 + 2 * c + r;
+      if (g == 0) {
+        sm_m[warp * kRows + rr] = m[nt][r];
+        sm_l[warp * kRows + rr] = sum;
+      }
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        const int dim = D == 128 ? 16 * kappa(g) + 2 * st : 8 * g + 2 * st;
+        float2* dst = reinterpret_cast<float2*>(sm_o + (warp * kRows + rr) * (D + 4) + dim);
+        *dst = make_float2(o[nt][st][r] * vs, o[nt][st][2 + r] * vs);
+      }
+    }
+  __syncthreads();
+  const bool ok = *abort_flag == 0;
+  for (int rr = warp; rr < rows; rr += kWarps) {
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * kRows + rr]);
+    float sum = 0.f, acc[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = sm_m[w * kRows + rr];
+      const float f = mw == -INFINITY || !ok ? 0.f : ex2_approx(mw - M);
+      sum = fmaf(f, sm_l[w * kRows + rr], sum);
+      const float* src = sm_o + (w * kRows + rr) * (D + 4) + lane * (D / 32);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) acc[e] = f > 0.f ? fmaf(f, src[e], acc[e]) : acc[e];
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[e] *= inv;
+    const float l2 = sum > 0.f ? M - kPOffset + log2f(sum) : -INFINITY;
+    const int i = rr / a.G;
+    store_row<D>(a, b, sp.row0 + i, i, hk * a.G + rr - i * a.G, cc, lane, acc, l2);
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch_nt(const PagedAttention& a, const PagedMaps& maps, cudaStream_t st) {
+  auto kern = paged_rows_kernel<D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kAlloc);
+  if (e != cudaSuccess) return e;
+  const long long grid = (long long)a.p.B * a.p.Hkv * a.n_chunks;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  kern<<<(unsigned)grid, kWarps * 32, Layout<D>::kAlloc, st>>>(maps.k, maps.v, a);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const PagedAttention& a, const PagedMaps& maps, cudaStream_t st) {
+  const int rows = a.p.max_new * a.G;
+  if (rows <= 8) return launch_nt<D, 1>(a, maps, st);
+  if (rows <= 16) return launch_nt<D, 2>(a, maps, st);
+  return launch_nt<D, 4>(a, maps, st);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_rows(const PagedAttention& a, const PagedMaps& maps, cudaStream_t st) {
+  return a.p.d == 64 ? launch_d<64>(a, maps, st) : launch_d<128>(a, maps, st);
+}
+
+}  // namespace attn
