@@ -486,6 +486,11 @@ attn_status run_paged_attention(const PagedAttention& a, cudaStream_t st) {
     attn_status s = make_map_codes(&maps.k, p.k_cache, rows, p.d, box);
     if (s == ATTN_OK) s = make_map_codes(&maps.v, p.v_cache, rows, p.d, box);
     if (s != ATTN_OK) return s;
+  } else if (!p.kv_exp && p.max_seq_len > 0) {
+    const unsigned box = (unsigned)std::min(p.page_size, 64);
+    attn_status s = make_map(&maps.k, p.k_cache, 1, rows, p.d, box);
+    if (s == ATTN_OK) s = make_map(&maps.v, p.v_cache, 1, rows, p.d, box);
+    if (s != ATTN_OK) return s;
   }
   return from_cuda(launch_paged_attention(a, maps, st));
 }

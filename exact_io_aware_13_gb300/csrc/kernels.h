@@ -195,8 +195,9 @@ struct PagedAttention {
   float* part_o;              // [n_chunks, T * Hq, d] fp32 when n_chunks > 1
   float* part_lse;            // [n_chunks, T * Hq]
 };
-// Tensor maps over an e4m3 cache for the row kernel: rows of d codes, boxes of
-// min(page_size, 32) rows, 128-byte (d = 128) or 64-byte swizzle.
+// Tensor maps over the cache's rows. Row kernel (e4m3): whole rows of d codes, boxes of
+// min(page_size, 32) rows, swizzled over the row. Tile kernel, bf16: boxes of 64 columns and
+// min(page_size, 64) rows, 128-byte swizzle (e4m3 tiles are plain bulk copies).
 struct PagedMaps {
   CUtensorMap k, v;
 };
@@ -206,6 +207,8 @@ inline bool paged_few_rows(const PagedAttention& a) {
   return a.p.kv_exp != nullptr && (long long)a.p.max_new * a.G <= kPagedRowsMax;
 }
 cudaError_t launch_paged_rows(const PagedAttention& a, const PagedMaps& maps, cudaStream_t st);
+cudaError_t launch_paged_tiles_bf16(const PagedAttention& a, const PagedMaps& maps, cudaStream_t st);
+cudaError_t launch_paged_tiles_e4m3(const PagedAttention& a, cudaStream_t st);
 cudaError_t launch_paged_attention(const PagedAttention& a, const PagedMaps& maps,
                                    cudaStream_t st);
 

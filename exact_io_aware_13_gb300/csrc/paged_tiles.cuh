@@ -1,0 +1,803 @@
+// Attention of packed rows over the paged cache on the fifth-generation tensor cores:
+// chunks of new tokens (prefill), and decode with more rows per kv head than
+// paged_rows.cu takes.
+//
+// The algorithm is the forward kernel's (fwd_tc.cu: tiled online softmax, two 128-row query
+// tiles against 128-key tiles, S and O in tensor memory, P written over S). What differs:
+//   * rows are packed: row r of a (sequence, kv head) is query token r / G, query head
+//     hk * G + r % G, so every key tile serves the whole group and a short chunk still fills
+//     the 128 rows of an MMA. A CTA takes 256 consecutive packed rows of one (sequence, kv
+//     head) against one key chunk; the softmax warps bring their Q rows into swizzled shared
+//     memory themselves (any strides, any G);
+//   * key tiles come from pages: the loader issues one TMA box (bf16) or bulk copy (e4m3)
+//     per page piece, its page-table entries fetched one tile ahead;
+//   * masks are aligned at the bottom right (decode_row_keys), slots behind the sequence are
+//     masked in S and cleared in V;
+//   * the key axis may be cut into chunks: fp32 partial rows, merged by their log-sum-exp.
+//
+// e4m3 cache: a fourth warpgroup converts code tiles to fp16 operand tiles. The scales are
+// powers of two, so a K tile becomes code * 2^(e_j - E), E the tile's largest exponent:
+// exact down to 2^15 between scales, and off by at most 2^-25 of the largest scale below;
+// 2^E multiplies the tile's scores with the softmax scale. A V tile is scaled the same way
+// with E_V, and P by 2^(E_V - E_ref), E_ref the largest E_V so far, which O carries (row sums
+// keep the plain weights). E_V is taken no smaller than E_ref - 8, so that P keeps its
+// range. P = 2^(s - m + 11) in fp16, m lagging by at most 2^4; Q rows are scaled by a power
+// of two into [2^14, 2^15). The conversions cost the fourth warpgroup about 25 instructions
+// per 16 values and hide behind the MMAs and the softmax.
+#pragma once
+
+#include "paged.cuh"
+
+namespace attn {
+namespace pt {
+
+constexpr int BM = 128;
+constexpr int BN = 128;
+constexpr int kQTiles = 2;
+constexpr int kUnitRows = kQTiles * BM;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kRelayWarp = 10, kConvWarp = 12;
+constexpr int kInfo = 4;             // slots of the converters' per-tile scales
+constexpr uint32_t kNbP = 1, kNbPCount = 160;
+constexpr uint32_t kNbKv = 3;
+constexpr float kPOffset = 11.0f;    // e4m3: P is scaled by 2^11 (fp16)
+constexpr int kMaxDown = 8;          // e4m3: a V tile's exponent is at least E_ref - 8
+
+template <bool kE4m3>
+struct Shape {
+  static constexpr int kThreads = kE4m3 ? 512 : 384;
+  static constexpr int kStages = kE4m3 ? 3 : 4;       // operand tiles in the ring
+  static constexpr int kCodeStages = kE4m3 ? 3 : 0;   // code tiles waiting for conversion
+  static constexpr uint32_t kNbKvCount = kE4m3 ? 160 : 64;
+  // Registers: softmax threads hold 128 scores and the row state, the others little. The
+  // launch gives kThreads x kRegsLaunch; the split must not exceed it (launch_variant checks
+  // what the compiler used).
+  static constexpr int kRegsLaunch = kE4m3 ? 128 : 168;
+  static constexpr int kRegsSoftmax = kE4m3 ? 208 : 232;
+  static constexpr int kRegsOther = kE4m3 ? 48 : 40;
+  static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * kRegsLaunch,
+                "register pool");
+  static constexpr float kLag = kE4m3 ? 4.0f : 8.0f;  // O is rescaled beyond this growth (log2)
+};
+
+template <int D, bool kE4m3>
+struct Layout {
+  using S = Shape<kE4m3>;
+  static constexpr int kChunk = BM * 128;             // 128 rows of 128 bytes
+  static constexpr int kSlabs = D / 64;
+  static constexpr int kTile = BM * D * 2;
+  static constexpr int kQ = 0;
+  static constexpr int kRing = kQ + kQTiles * kTile;
+  static constexpr int kCodes = kRing + S::kStages * kTile;
+  static constexpr int kCodeTile = BN * D;
+  static constexpr int kExp = kCodes + S::kCodeStages * kCodeTile;   // [kInfo][128][2]
+  static constexpr int kRowScale = kExp + (kE4m3 ? kInfo * BN * 2 : 0);
+  static constexpr int kBars = kRowScale + (kE4m3 ? kUnitRows * 4 : 0);
+  static constexpr int kAlloc = kBars + 512 + 1024;
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
+};
+static_assert(Layout<128, true>::kAlloc <= 232448 && Layout<128, false>::kAlloc <= 232448,
+              "shared memory");
+
+struct Bars {
+  uint64_t q_full;
+  uint64_t kv_full[4];
+  uint64_t kv_empty[4];
+  uint64_t s_full[kQTiles];
+  uint64_t o_full[kQTiles];
+  uint64_t code_full[4];
+  uint64_t code_empty[4];
+  uint64_t info_full[kInfo];
+  int4 info[kInfo];     // E_K, E_V, E_ref of key tile j (slot j % kInfo)
+  uint32_t tmem_base;
+  int abort_flag;
+  // the CTA's work
+  int b, hk, unit, cc;  // b < 0: none
+  Span span;
+};
+static_assert(sizeof(Bars) <= 512, "barrier space");
+
+// Instruction descriptor of tcgen05.mma kind::f16 with fp16 A and B, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// 2^-n as an fp16 pair, n >= 0 (subnormal down to 2^-24, then 0).
+__device__ __forceinline__ uint32_t pow2_f16x2(int n) {
+  const uint32_t h = n <= 14 ? (uint32_t)(15 - n) << 10 : (n <= 24 ? 1u << (24 - n) : 0u);
+  return h | (h << 16);
+}
+
+// CTA -> (sequence, kv head, key chunk, row unit): sequence b owns units_b * Hkv * chunks_b
+// consecutive CTAs, the units of one (kv head, chunk) together, so that CTAs running at the
+// same time read the same keys from L2; the last units (the longest rows under causal
+// masks) come first. One warp, all lanes.
+__device__ __forceinline__ void find_work(const PagedAttention& a, Bars* bars, int lane) {
+  const PagedProblem& p = a.p;
+  long long at = blockIdx.x, base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    Span s{0, 0, 0};
+    if (b < p.B) s = load_span(p, b);
+    const int units = (int)(((long long)s.n * a.G + kUnitRows - 1) / kUnitRows);
+    // (with several chunks the merge writes the rows of an empty sequence)
+    const int chunks = a.n_chunks == 1 ? 1 : (int)(((long long)s.L + a.chunk - 1) / a.chunk);
+    const long long mine = (long long)units * p.Hkv * chunks;
+    long long incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
+    }
+    const long long first = base + incl - mine;
+    const bool hit = at >= first && at < first + mine;
+    if (hit) {
+      const int rem = (int)(at - first);
+      const int u = rem % units, hc = rem / units;
+      bars->unit = units - 1 - u;
+      bars->cc = hc % chunks;
+      bars->hk = hc / chunks;
+      bars->b = b;
+      bars->span = s;
+    }
+    if (__any_sync(0xffffffffu, hit)) return;
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) bars->b = -1;
+}
+
+// Key tiles of one query tile, and the range in which every one of its rows sees every key.
+struct TileKeys {
+  int lo, hi;            // tiles [lo, hi) of BN keys
+  int full_lo, full_hi;  // keys
+};
+
+template <int D, bool kAlibi, bool kSoftcap, bool kE4m3>
+__global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
+    paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const PagedAttention a) {
+  using S = Shape<kE4m3>;
+  using L = Layout<D, kE4m3>;
+  constexpr int kStages = S::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
+  const PagedProblem& p = a.p;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (blockIdx.x == 0) report_bad_spans(p);
+  if (warp == 0) find_work(a, bars, lane);
+  if (threadIdx.x == 32) {
+    mbar_init(smem_u32(&bars->q_full), 8);  // one arrival per softmax warp
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&bars->kv_full[s]), 1);
+      mbar_init(smem_u32(&bars->kv_empty[s]), 1);
+    }
+    for (int s = 0; s < S::kCodeStages; ++s) {
+      mbar_init(smem_u32(&bars->code_full[s]), 1);
+      mbar_init(smem_u32(&bars->code_empty[s]), 4);  // one arrival per converter warp
+    }
+    for (int s = 0; s < kInfo; ++s) mbar_init(smem_u32(&bars->info_full[s]), 1);
+    for (int t = 0; t < kQTiles; ++t) {
+      mbar_init(smem_u32(&bars->s_full[t]), 1);
+      mbar_init(smem_u32(&bars->o_full[t]), 1);
+    }
+    bars->abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const int b = bars->b;
+  if (b < 0) return;
+  const int hk = bars->hk, cc = bars->cc;
+  const Span sp = bars->span;
+  const int rows = sp.n * a.G - bars->unit * kUnitRows;  // packed rows from this unit on
+  const int row_base = bars->unit * kUnitRows;
+  const int c0 = a.n_chunks == 1 ? 0 : cc * a.chunk;
+  const int c1 = a.n_chunks == 1 ? sp.L : (int)imin64((long long)c0 + a.chunk, sp.L);
+
+  TileKeys tk[kQTiles];
+  int lo = 1 << 30, hi = 0;
+#pragma unroll
+  for (int t = 0; t < kQTiles; ++t) {
+    tk[t] = TileKeys{0, 0, 0, 0};
+    const int r0 = t * BM;
+    if (r0 >= rows) continue;
+    int la, ha, lb, hb;
+    decode_row_keys(a.mask_kind, a.window, sp.L, sp.n, (row_base + r0) / a.G, la, ha);
+    decode_row_keys(a.mask_kind, a.window, sp.L, sp.n, (row_base + imin(r0 + BM, rows) - 1) / a.G, lb, hb);
+    tk[t].full_lo = imax(lb, c0);
+    tk[t].full_hi = imin(ha, c1);
+    const int k_lo = imax(la, c0), k_hi = imin(hb, c1);
+    if (k_hi <= k_lo) continue;
+    tk[t].lo = k_lo / BN;
+    tk[t].hi = (k_hi + BN - 1) / BN;
+    lo = imin(lo, tk[t].lo);
+    hi = imax(hi, tk[t].hi);
+  }
+
+  // Element offsets of packed row r of this unit.
+  const int batch = p.offsets ? 0 : b, tok0 = p.offsets ? sp.row0 : 0;
+  auto o_row = [&](int r) {
+    const int pr = row_base + r, i = pr / a.G, h = hk * a.G + pr - i * a.G;
+    return a.o + batch * a.o_batch + (tok0 + i) * a.o_token + h * a.o_head;
+  };
+  auto lse_row = [&](int r) {
+    const int pr = row_base + r, i = pr / a.G, h = hk * a.G + pr - i * a.G;
+    return a.lse + batch * a.l_batch + (tok0 + i) * a.l_token + h * a.l_head;
+  };
+  auto part_row = [&](int r) {
+    const int pr = row_base + r, i = pr / a.G, h = hk * a.G + pr - i * a.G;
+    return ((long long)cc * p.T + sp.row0 + i) * a.Hq + h;
+  };
+
+  if (hi <= lo) {  // no row sees a key of this chunk
+    if (a.n_chunks > 1) return;  // the merge reads no such chunk
+    for (int r = threadIdx.x; r < imin(kUnitRows, rows); r += S::kThreads) {
+      uint4* dst = reinterpret_cast<uint4*>(o_row(r));
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
+      *lse_row(r) = -INFINITY;
+    }
+    return;
+  }
+  const int n_kv = hi - lo;
+
+  WaitCtx wc{&bars->abort_flag, p.status};
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&bars->tmem_base), L::kTmemCols);
+    tmem_relinquish();
+    tc_fence_before_sync();
+  }
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp >= 8) {
+    setmaxnreg_dec<S::kRegsOther>();
+    if (warp == kLoadWarp) {
+      // ------------------------------------------------------------ loader
+      // Lane q fetches the q-th page piece of a tile.
+      const int ps = p.page_size;
+      const int R = kE4m3 && ps % 128 == 0 ? 128 : imin(ps, 64);
+      const int pieces = BN / R;
+      auto rows_of = [&](int j) -> int {  // cache row of this lane's piece, or -1
+        const int key = j * BN + lane * R;
+        if (lane >= pieces || key >= sp.L) return -1;
+        const long long r = cache_row(p, b, key, hk);
+        if (r < 0) atomicOr(p.status, DEV_BAD_INPUT);
+        return (int)r;
+      };
+      constexpr int kDepth = kE4m3 ? S::kCodeStages : kStages;
+      uint64_t* full = kE4m3 ? bars->code_full : bars->kv_full;
+      uint64_t* empty = kE4m3 ? bars->code_empty : bars->kv_empty;
+      int row = rows_of(lo), next = n_kv > 1 ? rows_of(lo + 1) : -1;
+      bool live = true;
+      int issued = 0;
+      for (int u = 0; u < 2 * n_kv && live; ++u) {
+        const int s = u % kDepth;
+        live = __all_sync(0xffffffffu,
+                          mbar_wait(smem_u32(&empty[s]), ((u / kDepth) & 1) ^ 1, wc));
+        if (!live) break;
+        const uint32_t bar = smem_u32(&full[s]);
+        const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0));
+        const bool is_v = u & 1;
+        if (lane == 0)
+          mbar_arrive_expect_tx(bar, kE4m3 ? n * R * (D + (is_v ? 0 : 2)) : n * R * D * 2);
+        __syncwarp();
+        if (row >= 0) {
+          if constexpr (kE4m3) {
+            const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache);
+            bulk_load(smem_u32(smem + L::kCodes + s * L::kCodeTile + lane * R * D),
+                      src + (size_t)row * D, R * D, bar);
+            if (!is_v)  // the exponents of K and V come with K
+              bulk_load(smem_u32(smem + L::kExp + (((u >> 1) % kInfo) * BN + lane * R) * 2),
+                        p.kv_exp + (size_t)row * 2, R * 2, bar);
+          } else {
+#pragma unroll
+            for (int c = 0; c < L::kSlabs; ++c)
+              tma_load_3d(smem_u32(smem + L::kRing + s * L::kTile + c * L::kChunk) + lane * R * 128,
+                          is_v ? &tm_v : &tm_k, bar, c * 64, row, 0);
+          }
+        }
+        ++issued;
+        if (is_v) {
+          const int j = lo + (u >> 1);
+          row = next;
+          next = j + 2 < hi ? rows_of(j + 2) : -1;
+        }
+      }
+      // Do not leave while copies into this CTA's shared memory are in flight.
+      for (int u = imax(0, issued - kDepth); u < issued; ++u)
+        drain_wait(smem_u32(&full[u % kDepth]), (u / kDepth) & 1);
+    } else if (!kE4m3 && warp == kRelayWarp) {
+      // ------------------------------------------------------------ relay (bf16)
+      // After a ring use's bytes have landed (and the V rows behind the sequence are
+      // cleared), arrive on its named barrier for the MMA warp. After an abort, rendezvous.
+      bool live = true;
+      for (int u = 0; u < 2 * n_kv; ++u) {
+        const int s = u % kStages;
+        if (live)
+          live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->kv_full[s]), (u / kStages) & 1, wc));
+        const int valid = sp.L - (lo + (u >> 1)) * BN;
+        if (live && (u & 1) && valid < BN) {
+          for (int e = lane; e < (BN - valid) * 8 * L::kSlabs; e += 32) {
+            const int slab = e / ((BN - valid) * 8), rem = e - slab * (BN - valid) * 8;
+            *reinterpret_cast<uint4*>(smem + L::kRing + s * L::kTile + slab * L::kChunk +
+                                      (valid + rem / 8) * 128 + (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (live) nb_arrive(kNbKv + s, S::kNbKvCount);
+        else nb_sync(kNbKv + s, S::kNbKvCount);
+      }
+    } else if (kE4m3 && warp >= kConvWarp) {
+      // ------------------------------------------------------------ converters (e4m3)
+      const int cw = warp - kConvWarp;
+      bool live = true;
+      int e_ref = 0, e_k = 0, e_v = 0;
+      for (int u = 0; u < 2 * n_kv; ++u) {
+        const int cs = u % S::kCodeStages, s = u % kStages, jj = u >> 1;
+        const bool is_v = u & 1;
+        if (live)
+          live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->code_full[cs]),
+                                                   (u / S::kCodeStages) & 1, wc));
+        if (live)
+          live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->kv_empty[s]),
+                                                   ((u / kStages) & 1) ^ 1, wc));
+        if (!live) {
+          nb_sync(kNbKv + s, S::kNbKvCount);
+          continue;
+        }
+        const int valid = imin(BN, sp.L - (lo + jj) * BN);
+        const uint8_t* ex = smem + L::kExp + (jj % kInfo) * BN * 2;
+        if (!is_v) {  // the tile's exponents: lane reads rows 4 lane .. + 3 (K low, V high byte)
+          const uint2 w = *reinterpret_cast<const uint2*>(ex + lane * 8);
+          uint32_t mk = 0, mv = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t pair = ((e & 2) ? w.y : w.x) >> ((e & 1) * 16);
+            if (4 * lane + e < valid) {
+              mk = max(mk, pair & 255u);
+              mv = max(mv, (pair >> 8) & 255u);
+            }
+          }
+          e_k = (int)__reduce_max_sync(0xffffffffu, mk);
+          e_v = (int)__reduce_max_sync(0xffffffffu, mv);
+          e_ref = imax(e_ref, e_v);
+          e_v = imax(e_v, e_ref - kMaxDown);
+          if (cw == 0 && lane == 0) {
+            bars->info[jj % kInfo] = make_int4(e_k, e_v, e_ref, 0);
+            mbar_arrive(smem_u32(&bars->info_full[jj % kInfo]));
+          }
+        }
+        const int top = is_v ? e_v : e_k;
+        const uint8_t* codes = smem + L::kCodes + cs * L::kCodeTile;
+        uint8_t* dst = smem + L::kRing + s * L::kTile;
+        // A warp converts 32 rows, 512 codes at a time: eight lanes in a row take two rows
+        // and four pieces, whose swizzled halves hit eight different 16-byte columns.
+        constexpr int kRowsPerIter = 512 / D;  // 4 or 8
+#pragma unroll
+        for (int it = 0; it < 32 / kRowsPerIter; ++it) {
+          const int row = cw * 32 + it * kRowsPerIter +
+                          (D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) & 1) * 2 : lane >> 2);
+          const int piece = (lane & 3) + (D == 128 ? ((lane >> 3) & 1) * 4 : 0);
+          const uint4 w = *reinterpret_cast<const uint4*>(codes + row * D + piece * 16);
+          const int e = ex[row * 2 + is_v];
+          const uint32_t f = pow2_f16x2(imax(0, top - e));
+          const uint32_t cw4[4] = {w.x, w.y, w.z, w.w};
+          uint32_t h[8];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            h[2 * q] = row < valid ? mul_f16x2(e4m3x2_to_f16x2(cw4[q]), f) : 0u;
+            h[2 * q + 1] = row < valid ? mul_f16x2(e4m3x2_to_f16x2(cw4[q] >> 16), f) : 0u;
+          }
+          uint8_t* line = dst + (piece >> 2) * L::kChunk + row * 128;
+          const int ch = (piece & 3) * 2;
+          *reinterpret_cast<uint4*>(line + ((ch ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(line + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->code_empty[cs]));
+        nb_arrive(kNbKv + s, S::kNbKvCount);
+      }
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------ MMA issuer
+      // As in the forward kernel: the whole warp walks the schedule and waits on named
+      // barriers; one elected lane issues. If Q never arrives it issues nothing.
+      constexpr uint32_t idS = kE4m3 ? idesc_f16_f32(BM, BN, false) : idesc_bf16_f32(BM, BN, false, false);
+      constexpr uint32_t idO = kE4m3 ? idesc_f16_f32(BM, D, true) : idesc_bf16_f32(BM, D, false, true);
+      const uint32_t q_base = smem_u32(smem + L::kQ);
+      const uint32_t ring = smem_u32(smem + L::kRing);
+      int np[kQTiles] = {0, 0};
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->q_full), 0, wc));
+      tc_fence_after_sync();
+      const bool issuer = elect_one();
+      auto commit = [&](uint64_t* bar) {
+        if (ok) mma_commit_if(issuer, smem_u32(bar));
+      };
+      auto sync_stage = [&](int u) {
+        nb_sync(kNbKv + u % kStages, S::kNbKvCount);
+        tc_fence_after_sync();
+      };
+      auto issue_s = [&](int t, int u) {
+        if (!ok) return;
+        const uint64_t dq = smem_desc_sw128(q_base + t * L::kTile, 16, 1024);
+        const uint64_t dk = smem_desc_sw128(ring + (u % kStages) * L::kTile, 16, 1024);
+        const uint32_t col = t == 0 ? L::kColS0 : L::kColS1;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * L::kChunk + (kk & 3) * 32) >> 4;
+          mma_ss_if(issuer, tmem + col, dq + off, dk + off, idS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit_if(issuer, smem_u32(&bars->s_full[t]));
+      };
+      auto issue_pv = [&](int t, int u) {
+        if (!ok) return;
+        const uint32_t colS = t == 0 ? L::kColS0 : L::kColS1;
+        const uint32_t colO = t == 0 ? L::kColO0 : L::kColO1;
+        const uint64_t dv = smem_desc_sw128(ring + (u % kStages) * L::kTile, L::kChunk, 1024);
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_ts_if(issuer, tmem + colO, tmem + colS + kk * 8, dv + ((kk * 16 * 128) >> 4), idO,
+                    (np[t] > 0 || kk > 0) ? 1u : 0u);
+      };
+      sync_stage(0);
+#pragma unroll
+      for (int t = 0; t < kQTiles; ++t)
+        if (lo >= tk[t].lo && lo < tk[t].hi) issue_s(t, 0);
+      commit(&bars->kv_empty[0]);
+      for (int jj = 0; jj < n_kv; ++jj) {
+        const int j = lo + jj;
+        const int uv = 2 * jj + 1, uk = 2 * jj + 2;
+        const bool next = jj + 1 < n_kv;
+        sync_stage(uv);
+#pragma unroll
+        for (int t = 0; t < kQTiles; ++t) {
+          if (j >= tk[t].lo && j < tk[t].hi) {
+            nb_sync(kNbP + t, kNbPCount);
+            tc_fence_after_sync();
+            issue_pv(t, uv);
+            ++np[t];
+          }
+          if (next) {
+            if (t == 0) sync_stage(uk);
+            if (j + 1 >= tk[t].lo && j + 1 < tk[t].hi) issue_s(t, uk);
+          }
+        }
+        commit(&bars->kv_empty[uv % kStages]);
+        if (next) commit(&bars->kv_empty[uk % kStages]);
+      }
+#pragma unroll
+      for (int t = 0; t < kQTiles; ++t) commit(&bars->o_full[t]);
+    }
+  } else {
+    setmaxnreg_inc<S::kRegsSoftmax>();
+    // ------------------------------------------------------------ softmax warpgroups
+    const int t = warp >> 2;
+    const int wrow = t * BM + (warp & 3) * 32;  // this warp's first row in the unit
+    const int row = (warp & 3) * 32 + lane;     // TMEM lane = row in the tile
+    const int r = t * BM + row;                 // row in the unit
+    const bool has_row = r < rows;
+    float* row_scale = reinterpret_cast<float*>(smem + L::kRowScale);
+    {
+      // This warp's 32 Q rows into swizzled shared memory (rows past the end: zeros). e4m3:
+      // scaled by a power of two to fp16, the factor that undoes it kept per row.
+      constexpr int kPer = D / 8, kRowsPerIter = 32 / kPer;
+      const int piece = lane % kPer;
+#pragma unroll
+      for (int it0 = 0; it0 < 32 / kRowsPerIter; it0 += 8) {  // eight loads in flight
+        uint4 w[8];
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const int rr = wrow + (it0 + it) * kRowsPerIter + lane / kPer;
+          const int pr = row_base + rr, i = pr / a.G, h = hk * a.G + pr - i * a.G;
+          w[it] = make_uint4(0, 0, 0, 0);
+          if (rr < rows)
+            w[it] = __ldg(reinterpret_cast<const uint4*>(a.q + batch * a.q_batch +
+                                                         (tok0 + i) * a.q_token + h * a.q_head) + piece);
+        }
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const int rr = wrow + (it0 + it) * kRowsPerIter + lane / kPer;
+          if constexpr (kE4m3) {
+            uint32_t u[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
+#pragma unroll
+            for (int off = kPer / 2; off > 0; off >>= 1)
+              top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const int x = imax((int)(top >> 7) - 127, -112);
+            const float up = __uint_as_float((uint32_t)(14 - x + 127) << 23);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              u[e] = pack_f16x2(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xFFFF0000u) * up);
+            w[it] = make_uint4(u[0], u[1], u[2], u[3]);
+            if (piece == 0) row_scale[rr] = __uint_as_float((uint32_t)(x - 14 + 127) << 23);
+          }
+          const int rt = rr - t * BM;
+          *reinterpret_cast<uint4*>(smem + L::kQ + t * L::kTile + (piece >> 3) * L::kChunk + rt * 128 +
+                                    (((piece & 7) ^ (rt & 7)) << 4)) = w[it];
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->q_full));
+    }
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + (t == 0 ? L::kColS0 : L::kColS1);
+    const uint32_t tO = tmem + lane_base + (t == 0 ? L::kColO0 : L::kColO1);
+    const int pr = row_base + imin(r, rows - 1);
+    const int qi = pr / a.G, h = hk * a.G + pr - qi * a.G;
+    const int pos = sp.L - sp.n + qi;
+    int row_lo, row_hi;  // allowed keys of this row in this chunk
+    decode_row_keys(a.mask_kind, a.window, sp.L, sp.n, qi, row_lo, row_hi);
+    row_lo = imax(row_lo, c0);
+    row_hi = imin(row_hi, c1);
+    const float slope = kAlibi ? alibi_slope(h, a.Hq) : 0.f;
+    const float unit = kSoftcap ? 1.0f / a.softcap : kPagedLog2e;
+    const float k1 = a.scale * unit * (kE4m3 ? row_scale[r] : 1.f);
+    const float kb = slope * unit;
+    const float capA = kSoftcap ? a.softcap * kPagedLog2e : 0.f;
+    const bool raw_ok = !kAlibi && !kSoftcap && a.scale > 0.f;
+    float m_run = -INFINITY, l_run = 0.f;
+    int n = 0, e_ref = 0;
+    bool live = true;
+    for (int j = tk[t].lo; j < tk[t].hi; ++j, ++n) {
+      if (live) live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->s_full[t]), n & 1, wc));
+      int4 info = make_int4(127, 127, 127, 0);
+      if (kE4m3 && live) {
+        const int jj = j - lo;
+        live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->info_full[jj % kInfo]), (jj / kInfo) & 1, wc));
+        info = bars->info[jj % kInfo];
+      }
+      if (!live) {  // aborted: keep the barrier schedule with the MMA warp, do nothing else
+        nb_sync(kNbP + t, kNbPCount);
+        continue;
+      }
+      tc_fence_after_sync();
+      uint32_t x[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, x[c]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) reg_fence32(x[c]);
+      const int k0 = j * BN;
+      const float k1j = kE4m3 ? k1 * exp_byte_scale((uint32_t)info.x) : k1;
+      const bool masked = k0 < tk[t].full_lo || k0 + BN > tk[t].full_hi;  // warp-uniform
+      const bool fast = raw_ok && !masked;
+      float mx[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx[e] = -INFINITY;
+      if (fast) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(x[c][e]));
+      } else {
+        const int c_lo = row_lo - k0, c_hi = row_hi - k0;  // allowed columns [c_lo, c_hi)
+        const float base = kAlibi ? (float)(k0 - pos) * kb : 0.f;
+        const uint64_t k1j2 = f32x2(k1j, k1j);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const int col = c * 32 + e;
+            const uint64_t x2 = f32x2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+            uint64_t s2 = kAlibi ? fma_f32x2(x2, k1j2,
+                                             f32x2(fmaf((float)col, kb, base),
+                                                   fmaf((float)(col + 1), kb, base)))
+                                 : mul_f32x2(x2, k1j2);
+            float v0, v1;
+            f32x2_split(s2, v0, v1);
+            if (kSoftcap) {
+              v0 = tanh_approx(v0);
+              v1 = tanh_approx(v1);
+            }
+            if (masked) {
+              v0 = (col >= c_lo && col < c_hi) ? v0 : -INFINITY;
+              v1 = (col + 1 >= c_lo && col + 1 < c_hi) ? v1 : -INFINITY;
+            }
+            mx[e & 7] = fmaxf(mx[e & 7], v0);
+            mx[(e + 1) & 7] = fmaxf(mx[(e + 1) & 7], v1);
+            x[c][e] = __float_as_uint(v0);
+            x[c][e + 1] = __float_as_uint(v1);
+          }
+      }
+      float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                       fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+      if (fast) mt *= k1j;
+      else if (kSoftcap) mt *= capA;
+      const float m_new = fmaxf(m_run, mt);
+      const bool e_grow = kE4m3 && n > 0 && info.z > e_ref;
+      const bool warp_grow = __any_sync(0xffffffffu, m_new > m_run + S::kLag || e_grow);
+      float corr = 1.f;
+      if (warp_grow) {
+        corr = m_new == -INFINITY ? 1.f : ex2_approx(m_run - m_new);
+        m_run = m_new;
+        l_run *= corr;
+        if (kE4m3) {  // O also moves to the new reference exponent
+          const int up = info.z - e_ref;
+          corr = up > 126 ? 0.f : corr * __uint_as_float((uint32_t)(127 - up) << 23);
+        }
+      }
+      if (kE4m3) e_ref = info.z;
+      float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+      if (kE4m3) neg_m += kPOffset + (float)(info.y - info.z);
+      const float mul = fast ? k1j : (kSoftcap ? capA : 1.f);
+      uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+      const uint64_t mul2 = f32x2(mul, mul), negm2 = f32x2(neg_m, neg_m), one2 = f32x2(1.f, 1.f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t ph[8];
+#pragma unroll
+          for (int e8 = 0; e8 < 8; ++e8) {
+            const int e = hf * 8 + e8;
+            float a0, a1;
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])),
+                                  mul2, negm2), a0, a1);
+            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+            acc2[e & 3] = fma_f32x2(f32x2(p0, p1), one2, acc2[e & 3]);
+            ph[e8] = kE4m3 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          }
+          tmem_st8(tS + c * 16 + hf * 8, ph);
+        }
+      }
+      float acc[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f32x2_split(acc2[e], acc[2 * e], acc[2 * e + 1]);
+      const float sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+      // the row sum keeps the plain weights (0 <= E_ref - E_V <= kMaxDown)
+      l_run = kE4m3 ? fmaf(sum, __uint_as_float((uint32_t)(127 + info.z - info.y) << 23), l_run) : l_run + sum;
+      if (warp_grow && n > 0) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + c * 32, o);
+          tmem_wait_ld();
+          reg_fence32(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+          tmem_st32(tO + c * 32, o);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before_sync();
+      nb_arrive(kNbP + t, kNbPCount);
+    }
+    // ---------------------------------------------------------- epilogue
+    // Every tile waits for the CTA's last MMA: the staging below writes over Q.
+    const bool mma_done = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->o_full[t]), 0, wc));
+    const bool have_o = n > 0 && mma_done;
+    tc_fence_after_sync();
+    float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+    if (kE4m3) inv *= exp_byte_scale((uint32_t)e_ref);
+    const float l2 = l_run > 0.f ? m_run + log2f(l_run) - (kE4m3 ? kPOffset : 0.f) : -INFINITY;
+    if (a.n_chunks > 1) {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (have_o) {
+          tmem_ld32(tO + c * 32, o);
+          tmem_wait_ld();
+          reg_fence32(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (!has_row) continue;
+        float4* dst = reinterpret_cast<float4*>(a.part_o + part_row(r) * D + c * 32);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                               __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+      }
+      if (has_row) a.part_lse[part_row(r)] = l2;
+    } else {
+      uint8_t* otile = smem + t * L::kTile;
+      {
+        uint32_t o[D];
+        if (have_o) {  // warp-uniform
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
+            tmem_ld32(tO + c * 32, *reinterpret_cast<uint32_t(*)[32]>(o + c * 32));
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(o + c * 32));
+        } else {
+#pragma unroll
+          for (int e = 0; e < D; ++e) o[e] = 0u;
+        }
+#pragma unroll
+        for (int gc = 0; gc < D / 8; ++gc) {
+          uint4 w;
+          w.x = pack_bf16x2(__uint_as_float(o[8 * gc + 0]) * inv, __uint_as_float(o[8 * gc + 1]) * inv);
+          w.y = pack_bf16x2(__uint_as_float(o[8 * gc + 2]) * inv, __uint_as_float(o[8 * gc + 3]) * inv);
+          w.z = pack_bf16x2(__uint_as_float(o[8 * gc + 4]) * inv, __uint_as_float(o[8 * gc + 5]) * inv);
+          w.w = pack_bf16x2(__uint_as_float(o[8 * gc + 6]) * inv, __uint_as_float(o[8 * gc + 7]) * inv);
+          *reinterpret_cast<uint4*>(otile + (gc >> 3) * L::kChunk + row * 128 + (((gc & 7) ^ (row & 7)) << 4)) = w;
+        }
+      }
+      __syncwarp();
+      constexpr int kPer = D / 8, kRowsPerStore = 32 / kPer;
+      const int gc = lane % kPer;
+#pragma unroll 4
+      for (int k = 0; k < 32 / kRowsPerStore; ++k) {
+        const int rt = (warp & 3) * 32 + k * kRowsPerStore + lane / kPer;
+        const uint4 w = *reinterpret_cast<const uint4*>(otile + (gc >> 3) * L::kChunk + rt * 128 +
+                                                       (((gc & 7) ^ (rt & 7)) << 4));
+        if (t * BM + rt < rows) reinterpret_cast<uint4*>(o_row(t * BM + rt))[gc] = w;
+      }
+      if (has_row) *lse_row(r) = l2 * kPagedLn2;
+    }
+  }
+  __syncwarp();
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+template <int D, bool kAlibi, bool kSoftcap, bool kE4m3>
+cudaError_t launch_variant(const PagedAttention& a, const PagedMaps& maps, unsigned grid,
+                           cudaStream_t st) {
+  using S = Shape<kE4m3>;
+  auto kern = paged_tiles_kernel<D, kAlibi, kSoftcap, kE4m3>;
+  const int smem = Layout<D, kE4m3>::kAlloc;
+  // The register split of setmaxnreg waits for ever unless the launch brings kRegsLaunch
+  // registers a thread: refuse to launch a build in which it does not.
+  static const bool regs_ok = [&] {
+    cudaFuncAttributes attr;
+    return cudaFuncGetAttributes(&attr, kern) == cudaSuccess && attr.numRegs >= S::kRegsLaunch;
+  }();
+  if (!regs_ok) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, S::kThreads, smem, st>>>(maps.k, maps.v, a);
+  return cudaGetLastError();
+}
+
+template <bool kE4m3>
+cudaError_t launch_tiles(const PagedAttention& a, const PagedMaps& maps, cudaStream_t st) {
+  const PagedProblem& p = a.p;
+  // Row units: at most T G / 256 full ones and one more per sequence.
+  const long long per_seq = ((long long)p.max_new * a.G + kUnitRows - 1) / kUnitRows;
+  const long long units = imin64((long long)p.T * a.G / kUnitRows + p.B, per_seq * p.B);
+  const long long grid = units * p.Hkv * a.n_chunks;
+  if (grid == 0) return cudaSuccess;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const unsigned g = (unsigned)grid;
+  const bool al = a.score_kind & ATTN_SCORE_ALIBI, sc = a.score_kind & ATTN_SCORE_SOFTCAP;
+  if (p.d == 64) {
+    if (al && sc) return launch_variant<64, true, true, kE4m3>(a, maps, g, st);
+    if (al) return launch_variant<64, true, false, kE4m3>(a, maps, g, st);
+    if (sc) return launch_variant<64, false, true, kE4m3>(a, maps, g, st);
+    return launch_variant<64, false, false, kE4m3>(a, maps, g, st);
+  }
+  if (al && sc) return launch_variant<128, true, true, kE4m3>(a, maps, g, st);
+  if (al) return launch_variant<128, true, false, kE4m3>(a, maps, g, st);
+  if (sc) return launch_variant<128, false, true, kE4m3>(a, maps, g, st);
+  return launch_variant<128, false, false, kE4m3>(a, maps, g, st);
+}
+
+}  // namespace pt
+}  // namespace attn
