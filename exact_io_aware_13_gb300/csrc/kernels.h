@@ -197,12 +197,12 @@ struct PagedAttention {
 };
 // Tensor maps over the cache's rows. Row kernel (e4m3): whole rows of d codes, boxes of
 // min(page_size, 32) rows, swizzled over the row. Tile kernel, bf16: boxes of 64 columns and
-// min(page_size, 64) rows, 128-byte swizzle (e4m3 tiles are plain bulk copies).
+// min(page_size, 64) rows, 128-byte swizzle (e4m3 tiles take plain loads).
 struct PagedMaps {
   CUtensorMap k, v;
 };
 // Few query rows per kv head over an e4m3 cache take the row kernel.
-constexpr int kPagedRowsMax = 32;
+constexpr int kPagedRowsMax = 16;
 inline bool paged_few_rows(const PagedAttention& a) {
   return a.p.kv_exp != nullptr && (long long)a.p.max_new * a.G <= kPagedRowsMax;
 }

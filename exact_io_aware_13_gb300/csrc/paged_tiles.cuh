@@ -9,8 +9,8 @@
 //     the 128 rows of an MMA. A CTA takes 256 consecutive packed rows of one (sequence, kv
 //     head) against one key chunk; the softmax warps bring their Q rows into swizzled shared
 //     memory themselves (any strides, any G);
-//   * key tiles come from pages: the loader issues one TMA box (bf16) or bulk copy (e4m3)
-//     per page piece, its page-table entries fetched one tile ahead;
+//   * key tiles come from pages: the loader issues one TMA box per page piece, its
+//     page-table entries fetched one tile ahead (bf16; e4m3 below);
 //   * masks are aligned at the bottom right (decode_row_keys), slots behind the sequence are
 //     masked in S and cleared in V;
 //   * the key axis may be cut into chunks: fp32 partial rows, merged by their log-sum-exp.
@@ -22,8 +22,7 @@
 // with E_V, and P by 2^(E_V - E_ref), E_ref the largest E_V so far, which O carries (row sums
 // keep the plain weights). E_V is taken no smaller than E_ref - 8, so that P keeps its
 // range. P = 2^(s - m + 11) in fp16, m lagging by at most 2^4; Q rows are scaled by a power
-// of two into [2^14, 2^15). The conversions cost the fourth warpgroup about 25 instructions
-// per 16 values and hide behind the MMAs and the softmax.
+// of two into [2^14, 2^15).
 #pragma once
 
 #include "paged.cuh"
@@ -53,8 +52,10 @@ struct Shape {
   // what the compiler used).
   static constexpr int kRegsLaunch = kE4m3 ? 128 : 168;
   static constexpr int kRegsSoftmax = kE4m3 ? 208 : 232;
-  static constexpr int kRegsOther = kE4m3 ? 48 : 40;
-  static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * kRegsLaunch,
+  static constexpr int kRegsOther = 40;
+  static constexpr int kRegsConvert = 56;
+  static_assert(256 * kRegsSoftmax + 128 * kRegsOther + (kE4m3 ? 128 * kRegsConvert : 0) <=
+                    kThreads * kRegsLaunch,
                 "register pool");
   static constexpr float kLag = kE4m3 ? 4.0f : 8.0f;  // O is rescaled beyond this growth (log2)
 };
@@ -79,21 +80,36 @@ struct Layout {
 static_assert(Layout<128, true>::kAlloc <= 232448 && Layout<128, false>::kAlloc <= 232448,
               "shared memory");
 
+// Key tiles of one query tile, and the range in which every one of its rows sees every key.
+struct TileKeys {
+  int lo, hi;            // tiles [lo, hi) of BN keys
+  int full_lo, full_hi;  // keys
+};
+
+// A CTA's work, found by warp 0 and kept in shared memory: held in every thread's registers
+// it would not fit the few that the loader and the converters have.
+struct Cta {
+  int b, hk, cc;         // sequence (< 0: nothing to do), kv head, key chunk
+  int row_base, rows;    // first packed row, packed rows from there on
+  int c0, c1;            // keys of the chunk
+  int lo, hi;            // key tiles of both query tiles together
+  Span span;
+  TileKeys tk[kQTiles];
+};
+
 struct Bars {
   uint64_t q_full;
   uint64_t kv_full[4];
   uint64_t kv_empty[4];
   uint64_t s_full[kQTiles];
   uint64_t o_full[kQTiles];
-  uint64_t code_full[4];
-  uint64_t code_empty[4];
+  uint64_t code_full[3];
+  uint64_t code_empty[3];
   uint64_t info_full[kInfo];
   int4 info[kInfo];     // E_K, E_V, E_ref of key tile j (slot j % kInfo)
   uint32_t tmem_base;
   int abort_flag;
-  // the CTA's work
-  int b, hk, unit, cc;  // b < 0: none
-  Span span;
+  Cta cta;
 };
 static_assert(sizeof(Bars) <= 512, "barrier space");
 
@@ -112,19 +128,16 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// 2^-n as an fp16 pair, n >= 0 (subnormal down to 2^-24, then 0).
-__device__ __forceinline__ uint32_t pow2_f16x2(int n) {
-  const uint32_t h = n <= 14 ? (uint32_t)(15 - n) << 10 : (n <= 24 ? 1u << (24 - n) : 0u);
-  return h | (h << 16);
-}
 
 // CTA -> (sequence, kv head, key chunk, row unit): sequence b owns units_b * Hkv * chunks_b
 // consecutive CTAs, the units of one (kv head, chunk) together, so that CTAs running at the
 // same time read the same keys from L2; the last units (the longest rows under causal
 // masks) come first. One warp, all lanes.
-__device__ __forceinline__ void find_work(const PagedAttention& a, Bars* bars, int lane) {
+__device__ __forceinline__ void find_work(const PagedAttention& a, Cta* w, int lane) {
   const PagedProblem& p = a.p;
   long long at = blockIdx.x, base = 0;
+  if (lane == 0) w->b = -1;
+  __syncwarp();
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
     Span s{0, 0, 0};
@@ -144,23 +157,41 @@ __device__ __forceinline__ void find_work(const PagedAttention& a, Bars* bars, i
     if (hit) {
       const int rem = (int)(at - first);
       const int u = rem % units, hc = rem / units;
-      bars->unit = units - 1 - u;
-      bars->cc = hc % chunks;
-      bars->hk = hc / chunks;
-      bars->b = b;
-      bars->span = s;
+      w->b = b;
+      w->hk = hc / chunks;
+      w->cc = hc % chunks;
+      w->row_base = (units - 1 - u) * kUnitRows;
+      w->rows = s.n * a.G - w->row_base;
+      w->c0 = a.n_chunks == 1 ? 0 : w->cc * a.chunk;
+      w->c1 = a.n_chunks == 1 ? s.L : (int)imin64((long long)w->c0 + a.chunk, s.L);
+      w->span = s;
+      w->lo = 1 << 30;
+      w->hi = 0;
+      for (int t = 0; t < kQTiles; ++t) {
+        TileKeys k{0, 0, 0, 0};
+        const int r0 = t * BM;
+        if (r0 < w->rows) {
+          int la, ha, lb, hb;  // keys of the tile's first and last token
+          decode_row_keys(a.mask_kind, a.window, s.L, s.n, (w->row_base + r0) / a.G, la, ha);
+          decode_row_keys(a.mask_kind, a.window, s.L, s.n,
+                          (w->row_base + imin(r0 + BM, w->rows) - 1) / a.G, lb, hb);
+          k.full_lo = imax(lb, w->c0);
+          k.full_hi = imin(ha, w->c1);
+          const int k_lo = imax(la, w->c0), k_hi = imin(hb, w->c1);
+          if (k_hi > k_lo) {
+            k.lo = k_lo / BN;
+            k.hi = (k_hi + BN - 1) / BN;
+            w->lo = imin(w->lo, k.lo);
+            w->hi = imax(w->hi, k.hi);
+          }
+        }
+        w->tk[t] = k;
+      }
     }
     if (__any_sync(0xffffffffu, hit)) return;
     base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  if (lane == 0) bars->b = -1;
 }
-
-// Key tiles of one query tile, and the range in which every one of its rows sees every key.
-struct TileKeys {
-  int lo, hi;            // tiles [lo, hi) of BN keys
-  int full_lo, full_hi;  // keys
-};
 
 template <int D, bool kAlibi, bool kSoftcap, bool kE4m3>
 __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
@@ -178,7 +209,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
   const int lane = threadIdx.x & 31;
 
   if (blockIdx.x == 0) report_bad_spans(p);
-  if (warp == 0) find_work(a, bars, lane);
+  if (warp == 0) find_work(a, &bars->cta, lane);
   if (threadIdx.x == 32) {
     mbar_init(smem_u32(&bars->q_full), 8);  // one arrival per softmax warp
     for (int s = 0; s < kStages; ++s) {
@@ -198,61 +229,38 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     fence_barrier_init();
   }
   __syncthreads();
-  const int b = bars->b;
-  if (b < 0) return;
-  const int hk = bars->hk, cc = bars->cc;
-  const Span sp = bars->span;
-  const int rows = sp.n * a.G - bars->unit * kUnitRows;  // packed rows from this unit on
-  const int row_base = bars->unit * kUnitRows;
-  const int c0 = a.n_chunks == 1 ? 0 : cc * a.chunk;
-  const int c1 = a.n_chunks == 1 ? sp.L : (int)imin64((long long)c0 + a.chunk, sp.L);
+  const Cta& w = bars->cta;
+  if (w.b < 0) return;
 
-  TileKeys tk[kQTiles];
-  int lo = 1 << 30, hi = 0;
-#pragma unroll
-  for (int t = 0; t < kQTiles; ++t) {
-    tk[t] = TileKeys{0, 0, 0, 0};
-    const int r0 = t * BM;
-    if (r0 >= rows) continue;
-    int la, ha, lb, hb;
-    decode_row_keys(a.mask_kind, a.window, sp.L, sp.n, (row_base + r0) / a.G, la, ha);
-    decode_row_keys(a.mask_kind, a.window, sp.L, sp.n, (row_base + imin(r0 + BM, rows) - 1) / a.G, lb, hb);
-    tk[t].full_lo = imax(lb, c0);
-    tk[t].full_hi = imin(ha, c1);
-    const int k_lo = imax(la, c0), k_hi = imin(hb, c1);
-    if (k_hi <= k_lo) continue;
-    tk[t].lo = k_lo / BN;
-    tk[t].hi = (k_hi + BN - 1) / BN;
-    lo = imin(lo, tk[t].lo);
-    hi = imax(hi, tk[t].hi);
-  }
-
-  // Element offsets of packed row r of this unit.
-  const int batch = p.offsets ? 0 : b, tok0 = p.offsets ? sp.row0 : 0;
-  auto o_row = [&](int r) {
-    const int pr = row_base + r, i = pr / a.G, h = hk * a.G + pr - i * a.G;
-    return a.o + batch * a.o_batch + (tok0 + i) * a.o_token + h * a.o_head;
+  // Packed row r of this unit: its token (index among the new ones, packed row) and head.
+  struct Row {
+    int i, t, h;
   };
-  auto lse_row = [&](int r) {
-    const int pr = row_base + r, i = pr / a.G, h = hk * a.G + pr - i * a.G;
-    return a.lse + batch * a.l_batch + (tok0 + i) * a.l_token + h * a.l_head;
+  auto row_of = [&](int r) {
+    const int pr = w.row_base + r, i = pr / a.G;
+    return Row{i, w.span.row0 + i, w.hk * a.G + pr - i * a.G};
   };
-  auto part_row = [&](int r) {
-    const int pr = row_base + r, i = pr / a.G, h = hk * a.G + pr - i * a.G;
-    return ((long long)cc * p.T + sp.row0 + i) * a.Hq + h;
+  auto q_row = [&](const Row& x) {
+    return a.q + (p.offsets ? 0 : w.b) * a.q_batch + (p.offsets ? x.t : x.i) * a.q_token + x.h * a.q_head;
+  };
+  auto o_row = [&](const Row& x) {
+    return a.o + (p.offsets ? 0 : w.b) * a.o_batch + (p.offsets ? x.t : x.i) * a.o_token + x.h * a.o_head;
+  };
+  auto lse_row = [&](const Row& x) {
+    return a.lse + (p.offsets ? 0 : w.b) * a.l_batch + (p.offsets ? x.t : x.i) * a.l_token + x.h * a.l_head;
   };
 
-  if (hi <= lo) {  // no row sees a key of this chunk
+  if (w.hi <= w.lo) {  // no row sees a key of this chunk
     if (a.n_chunks > 1) return;  // the merge reads no such chunk
-    for (int r = threadIdx.x; r < imin(kUnitRows, rows); r += S::kThreads) {
-      uint4* dst = reinterpret_cast<uint4*>(o_row(r));
+    for (int r = threadIdx.x; r < imin(kUnitRows, w.rows); r += S::kThreads) {
+      const Row x = row_of(r);
+      uint4* dst = reinterpret_cast<uint4*>(o_row(x));
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
-      *lse_row(r) = -INFINITY;
+      *lse_row(x) = -INFINITY;
     }
     return;
   }
-  const int n_kv = hi - lo;
 
   WaitCtx wc{&bars->abort_flag, p.status};
   if (warp == kMmaWarp) {
@@ -264,33 +272,130 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
 
-  if (warp >= 8) {
+  if (kE4m3 && warp >= kConvWarp) {
+    setmaxnreg_dec<S::kRegsConvert>();
+    // ------------------------------------------------------------ converters (e4m3)
+    // A warp converts 32 of a tile's rows, 512 codes at a time. The eight lanes of a
+    // shared-memory phase read 128 contiguous bytes of codes; at d = 128 those are one row,
+    // whose pieces q and q + 4 go to the same 16-byte columns of the two operand slabs, so
+    // lanes with q >= 4 convert and write their second eight codes first.
+    constexpr int kRowsPerIter = 512 / D;            // 4 or 8
+    constexpr int kPieces = D / 16;
+    const int cw = warp - kConvWarp;
+    const int lo = w.lo, n_kv = w.hi - w.lo, L_seq = w.span.L;
+    const int sub = lane / kPieces, piece = lane % kPieces;
+    const bool swap = D == 128 ? piece >= 4 : sub & 1;
+    bool live = true;
+    int e_ref = 0, e_k = 0, e_v = 0;
+    for (int u = 0; u < 2 * n_kv; ++u) {
+      const int cs = u % 3, s = u % kStages, jj = u >> 1;
+      const bool is_v = u & 1;
+      if (live)
+        live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->code_full[cs]), (u / 3) & 1, wc));
+      const int valid = imin(BN, L_seq - (lo + jj) * BN);
+      const uint8_t* ex = smem + L::kExp + (jj % kInfo) * BN * 2;
+      if (live && !is_v) {  // the tile's exponents: lane reads rows 4 lane .. + 3 (K low byte)
+        const uint2 x = *reinterpret_cast<const uint2*>(ex + lane * 8);
+        uint32_t mk = 0, mv = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t pair = ((e & 2) ? x.y : x.x) >> ((e & 1) * 16);
+          if (4 * lane + e < valid) {
+            mk = max(mk, pair & 255u);
+            mv = max(mv, (pair >> 8) & 255u);
+          }
+        }
+        e_k = (int)__reduce_max_sync(0xffffffffu, mk);
+        e_v = (int)__reduce_max_sync(0xffffffffu, mv);
+        e_ref = imax(e_ref, e_v);
+        e_v = imax(e_v, e_ref - kMaxDown);
+      }
+      if (live)
+        live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->kv_empty[s]),
+                                                 ((u / kStages) & 1) ^ 1, wc));
+      if (!live) {
+        nb_sync(kNbKv + s, S::kNbKvCount);
+        continue;
+      }
+      if (!is_v && cw == 0 && lane == 0) {
+        bars->info[jj % kInfo] = make_int4(e_k, e_v, e_ref, 0);
+        mbar_arrive(smem_u32(&bars->info_full[jj % kInfo]));
+      }
+      const int row0 = cw * 32 + sub;
+      const uint8_t* src = smem + L::kCodes + cs * L::kCodeTile + row0 * D + piece * 16;
+      const uint8_t* ex_row = ex + row0 * 2 + is_v;
+      uint8_t* dst = smem + L::kRing + s * L::kTile + (piece >> 2) * L::kChunk + row0 * 128;
+      const int bias = 127 - (is_v ? e_v : e_k);
+      const int ch = (piece & 3) * 2 + swap;
+      constexpr int kIters = 32 / kRowsPerIter;
+#pragma unroll
+      for (int it0 = 0; it0 < kIters; it0 += 4) {
+        uint4 c[4];
+        int e[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          c[q] = *reinterpret_cast<const uint4*>(src + (it0 + q) * 512);
+          e[q] = ex_row[(it0 + q) * kRowsPerIter * 2];
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          // 2^(e_j - E) as an fp16 pair (0 below fp16's range)
+          const float ff = __uint_as_float((uint32_t)imax(bias + e[q], 0) << 23);
+          const uint32_t f = pack_f16x2(ff, ff);
+          const uint32_t c4[4] = {swap ? c[q].z : c[q].x, swap ? c[q].w : c[q].y,
+                                  swap ? c[q].x : c[q].z, swap ? c[q].y : c[q].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            h[2 * i] = mul_f16x2(e4m3x2_to_f16x2(c4[i]), f);
+            h[2 * i + 1] = mul_f16x2(e4m3x2_to_f16x2(c4[i] >> 16), f);
+          }
+          const int it = it0 + q, r7 = (row0 + it * kRowsPerIter) & 7;
+          uint8_t* line = dst + it * kRowsPerIter * 128;
+          *reinterpret_cast<uint4*>(line + ((ch ^ r7) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(line + ((ch ^ 1 ^ r7) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+      }
+      if (valid < BN) {  // rows behind the sequence hold anything, NaN codes included: clear
+        __syncwarp();
+        for (int e = lane; e < 32 * 8 * L::kSlabs; e += 32) {
+          const int slab = e / 256, row = cw * 32 + (e % 256) / 8;
+          if (row >= valid)
+            *reinterpret_cast<uint4*>(smem + L::kRing + s * L::kTile + slab * L::kChunk + row * 128 +
+                                      (e % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->code_empty[cs]));
+      nb_arrive(kNbKv + s, S::kNbKvCount);
+    }
+  } else if (warp >= 8) {
     setmaxnreg_dec<S::kRegsOther>();
     if (warp == kLoadWarp) {
       // ------------------------------------------------------------ loader
-      // Lane q fetches the q-th page piece of a tile.
+      // Lane q fetches the q-th page piece of a tile: TMA boxes (bf16) or bulk copies (codes).
       const int ps = p.page_size;
-      const int R = kE4m3 && ps % 128 == 0 ? 128 : imin(ps, 64);
-      const int pieces = BN / R;
+      const int R = kE4m3 && ps % 128 == 0 ? 128 : imin(ps, 64), pieces = BN / R;
+      const int lo = w.lo, hi = w.hi, n_kv = hi - lo;
       auto rows_of = [&](int j) -> int {  // cache row of this lane's piece, or -1
         const int key = j * BN + lane * R;
-        if (lane >= pieces || key >= sp.L) return -1;
-        const long long r = cache_row(p, b, key, hk);
+        if (lane >= pieces || key >= w.span.L) return -1;
+        const long long r = cache_row(p, w.b, key, w.hk);
         if (r < 0) atomicOr(p.status, DEV_BAD_INPUT);
         return (int)r;
       };
-      constexpr int kDepth = kE4m3 ? S::kCodeStages : kStages;
-      uint64_t* full = kE4m3 ? bars->code_full : bars->kv_full;
-      uint64_t* empty = kE4m3 ? bars->code_empty : bars->kv_empty;
+      constexpr int kDepth = kE4m3 ? 3 : kStages;
+      const uint32_t full = smem_u32(kE4m3 ? bars->code_full : bars->kv_full);
+      const uint32_t empty = smem_u32(kE4m3 ? bars->code_empty : bars->kv_empty);
       int row = rows_of(lo), next = n_kv > 1 ? rows_of(lo + 1) : -1;
       bool live = true;
       int issued = 0;
       for (int u = 0; u < 2 * n_kv && live; ++u) {
         const int s = u % kDepth;
-        live = __all_sync(0xffffffffu,
-                          mbar_wait(smem_u32(&empty[s]), ((u / kDepth) & 1) ^ 1, wc));
+        live = __all_sync(0xffffffffu, mbar_wait(empty + s * 8, ((u / kDepth) & 1) ^ 1, wc));
         if (!live) break;
-        const uint32_t bar = smem_u32(&full[s]);
+        const uint32_t bar = full + s * 8;
         const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0));
         const bool is_v = u & 1;
         if (lane == 0)
@@ -299,10 +404,10 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
         if (row >= 0) {
           if constexpr (kE4m3) {
             const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache);
-            bulk_load(smem_u32(smem + L::kCodes + s * L::kCodeTile + lane * R * D),
+            bulk_load(smem_u32(smem + L::kCodes + s * L::kCodeTile) + lane * R * D,
                       src + (size_t)row * D, R * D, bar);
             if (!is_v)  // the exponents of K and V come with K
-              bulk_load(smem_u32(smem + L::kExp + (((u >> 1) % kInfo) * BN + lane * R) * 2),
+              bulk_load(smem_u32(smem + L::kExp + ((u >> 1) % kInfo) * BN * 2) + lane * R * 2,
                         p.kv_exp + (size_t)row * 2, R * 2, bar);
           } else {
 #pragma unroll
@@ -320,17 +425,18 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       }
       // Do not leave while copies into this CTA's shared memory are in flight.
       for (int u = imax(0, issued - kDepth); u < issued; ++u)
-        drain_wait(smem_u32(&full[u % kDepth]), (u / kDepth) & 1);
+        drain_wait(full + (u % kDepth) * 8, (u / kDepth) & 1);
     } else if (!kE4m3 && warp == kRelayWarp) {
       // ------------------------------------------------------------ relay (bf16)
       // After a ring use's bytes have landed (and the V rows behind the sequence are
       // cleared), arrive on its named barrier for the MMA warp. After an abort, rendezvous.
       bool live = true;
+      const int lo = w.lo, n_kv = w.hi - lo;
       for (int u = 0; u < 2 * n_kv; ++u) {
         const int s = u % kStages;
         if (live)
           live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->kv_full[s]), (u / kStages) & 1, wc));
-        const int valid = sp.L - (lo + (u >> 1)) * BN;
+        const int valid = w.span.L - (lo + (u >> 1)) * BN;
         if (live && (u & 1) && valid < BN) {
           for (int e = lane; e < (BN - valid) * 8 * L::kSlabs; e += 32) {
             const int slab = e / ((BN - valid) * 8), rem = e - slab * (BN - valid) * 8;
@@ -343,77 +449,6 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
         if (live) nb_arrive(kNbKv + s, S::kNbKvCount);
         else nb_sync(kNbKv + s, S::kNbKvCount);
       }
-    } else if (kE4m3 && warp >= kConvWarp) {
-      // ------------------------------------------------------------ converters (e4m3)
-      const int cw = warp - kConvWarp;
-      bool live = true;
-      int e_ref = 0, e_k = 0, e_v = 0;
-      for (int u = 0; u < 2 * n_kv; ++u) {
-        const int cs = u % S::kCodeStages, s = u % kStages, jj = u >> 1;
-        const bool is_v = u & 1;
-        if (live)
-          live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->code_full[cs]),
-                                                   (u / S::kCodeStages) & 1, wc));
-        if (live)
-          live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->kv_empty[s]),
-                                                   ((u / kStages) & 1) ^ 1, wc));
-        if (!live) {
-          nb_sync(kNbKv + s, S::kNbKvCount);
-          continue;
-        }
-        const int valid = imin(BN, sp.L - (lo + jj) * BN);
-        const uint8_t* ex = smem + L::kExp + (jj % kInfo) * BN * 2;
-        if (!is_v) {  // the tile's exponents: lane reads rows 4 lane .. + 3 (K low, V high byte)
-          const uint2 w = *reinterpret_cast<const uint2*>(ex + lane * 8);
-          uint32_t mk = 0, mv = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t pair = ((e & 2) ? w.y : w.x) >> ((e & 1) * 16);
-            if (4 * lane + e < valid) {
-              mk = max(mk, pair & 255u);
-              mv = max(mv, (pair >> 8) & 255u);
-            }
-          }
-          e_k = (int)__reduce_max_sync(0xffffffffu, mk);
-          e_v = (int)__reduce_max_sync(0xffffffffu, mv);
-          e_ref = imax(e_ref, e_v);
-          e_v = imax(e_v, e_ref - kMaxDown);
-          if (cw == 0 && lane == 0) {
-            bars->info[jj % kInfo] = make_int4(e_k, e_v, e_ref, 0);
-            mbar_arrive(smem_u32(&bars->info_full[jj % kInfo]));
-          }
-        }
-        const int top = is_v ? e_v : e_k;
-        const uint8_t* codes = smem + L::kCodes + cs * L::kCodeTile;
-        uint8_t* dst = smem + L::kRing + s * L::kTile;
-        // A warp converts 32 rows, 512 codes at a time: eight lanes in a row take two rows
-        // and four pieces, whose swizzled halves hit eight different 16-byte columns.
-        constexpr int kRowsPerIter = 512 / D;  // 4 or 8
-#pragma unroll
-        for (int it = 0; it < 32 / kRowsPerIter; ++it) {
-          const int row = cw * 32 + it * kRowsPerIter +
-                          (D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) & 1) * 2 : lane >> 2);
-          const int piece = (lane & 3) + (D == 128 ? ((lane >> 3) & 1) * 4 : 0);
-          const uint4 w = *reinterpret_cast<const uint4*>(codes + row * D + piece * 16);
-          const int e = ex[row * 2 + is_v];
-          const uint32_t f = pow2_f16x2(imax(0, top - e));
-          const uint32_t cw4[4] = {w.x, w.y, w.z, w.w};
-          uint32_t h[8];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            h[2 * q] = row < valid ? mul_f16x2(e4m3x2_to_f16x2(cw4[q]), f) : 0u;
-            h[2 * q + 1] = row < valid ? mul_f16x2(e4m3x2_to_f16x2(cw4[q] >> 16), f) : 0u;
-          }
-          uint8_t* line = dst + (piece >> 2) * L::kChunk + row * 128;
-          const int ch = (piece & 3) * 2;
-          *reinterpret_cast<uint4*>(line + ((ch ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(line + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->code_empty[cs]));
-        nb_arrive(kNbKv + s, S::kNbKvCount);
-      }
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------ MMA issuer
       // As in the forward kernel: the whole warp walks the schedule and waits on named
@@ -423,6 +458,8 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       const uint32_t q_base = smem_u32(smem + L::kQ);
       const uint32_t ring = smem_u32(smem + L::kRing);
       int np[kQTiles] = {0, 0};
+      const int lo = w.lo, n_kv = w.hi - lo;
+      const int t_lo[kQTiles] = {w.tk[0].lo, w.tk[1].lo}, t_hi[kQTiles] = {w.tk[0].hi, w.tk[1].hi};
       const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->q_full), 0, wc));
       tc_fence_after_sync();
       const bool issuer = elect_one();
@@ -458,7 +495,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       sync_stage(0);
 #pragma unroll
       for (int t = 0; t < kQTiles; ++t)
-        if (lo >= tk[t].lo && lo < tk[t].hi) issue_s(t, 0);
+        if (lo >= t_lo[t] && lo < t_hi[t]) issue_s(t, 0);
       commit(&bars->kv_empty[0]);
       for (int jj = 0; jj < n_kv; ++jj) {
         const int j = lo + jj;
@@ -467,7 +504,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
         sync_stage(uv);
 #pragma unroll
         for (int t = 0; t < kQTiles; ++t) {
-          if (j >= tk[t].lo && j < tk[t].hi) {
+          if (j >= t_lo[t] && j < t_hi[t]) {
             nb_sync(kNbP + t, kNbPCount);
             tc_fence_after_sync();
             issue_pv(t, uv);
@@ -475,7 +512,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
           }
           if (next) {
             if (t == 0) sync_stage(uk);
-            if (j + 1 >= tk[t].lo && j + 1 < tk[t].hi) issue_s(t, uk);
+            if (j + 1 >= t_lo[t] && j + 1 < t_hi[t]) issue_s(t, uk);
           }
         }
         commit(&bars->kv_empty[uv % kStages]);
@@ -491,7 +528,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     const int wrow = t * BM + (warp & 3) * 32;  // this warp's first row in the unit
     const int row = (warp & 3) * 32 + lane;     // TMEM lane = row in the tile
     const int r = t * BM + row;                 // row in the unit
-    const bool has_row = r < rows;
+    const bool has_row = r < w.rows;
     float* row_scale = reinterpret_cast<float*>(smem + L::kRowScale);
     {
       // This warp's 32 Q rows into swizzled shared memory (rows past the end: zeros). e4m3:
@@ -500,21 +537,18 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       const int piece = lane % kPer;
 #pragma unroll
       for (int it0 = 0; it0 < 32 / kRowsPerIter; it0 += 8) {  // eight loads in flight
-        uint4 w[8];
+        uint4 v[8];
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
           const int rr = wrow + (it0 + it) * kRowsPerIter + lane / kPer;
-          const int pr = row_base + rr, i = pr / a.G, h = hk * a.G + pr - i * a.G;
-          w[it] = make_uint4(0, 0, 0, 0);
-          if (rr < rows)
-            w[it] = __ldg(reinterpret_cast<const uint4*>(a.q + batch * a.q_batch +
-                                                         (tok0 + i) * a.q_token + h * a.q_head) + piece);
+          v[it] = make_uint4(0, 0, 0, 0);
+          if (rr < w.rows) v[it] = __ldg(reinterpret_cast<const uint4*>(q_row(row_of(rr))) + piece);
         }
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
           const int rr = wrow + (it0 + it) * kRowsPerIter + lane / kPer;
           if constexpr (kE4m3) {
-            uint32_t u[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
+            uint32_t u[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
             uint32_t top = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
@@ -526,12 +560,12 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               u[e] = pack_f16x2(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xFFFF0000u) * up);
-            w[it] = make_uint4(u[0], u[1], u[2], u[3]);
+            v[it] = make_uint4(u[0], u[1], u[2], u[3]);
             if (piece == 0) row_scale[rr] = __uint_as_float((uint32_t)(x - 14 + 127) << 23);
           }
           const int rt = rr - t * BM;
           *reinterpret_cast<uint4*>(smem + L::kQ + t * L::kTile + (piece >> 3) * L::kChunk + rt * 128 +
-                                    (((piece & 7) ^ (rt & 7)) << 4)) = w[it];
+                                    (((piece & 7) ^ (rt & 7)) << 4)) = v[it];
         }
       }
       fence_proxy_async_smem();
@@ -541,14 +575,15 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + (t == 0 ? L::kColS0 : L::kColS1);
     const uint32_t tO = tmem + lane_base + (t == 0 ? L::kColO0 : L::kColO1);
-    const int pr = row_base + imin(r, rows - 1);
-    const int qi = pr / a.G, h = hk * a.G + pr - qi * a.G;
-    const int pos = sp.L - sp.n + qi;
+    const Row me = row_of(imin(r, w.rows - 1));
+    const int pos = w.span.L - w.span.n + me.i;
     int row_lo, row_hi;  // allowed keys of this row in this chunk
-    decode_row_keys(a.mask_kind, a.window, sp.L, sp.n, qi, row_lo, row_hi);
-    row_lo = imax(row_lo, c0);
-    row_hi = imin(row_hi, c1);
-    const float slope = kAlibi ? alibi_slope(h, a.Hq) : 0.f;
+    decode_row_keys(a.mask_kind, a.window, w.span.L, w.span.n, me.i, row_lo, row_hi);
+    row_lo = imax(row_lo, w.c0);
+    row_hi = imin(row_hi, w.c1);
+    const TileKeys tk = w.tk[t];
+    const int lo = w.lo;
+    const float slope = kAlibi ? alibi_slope(me.h, a.Hq) : 0.f;
     const float unit = kSoftcap ? 1.0f / a.softcap : kPagedLog2e;
     const float k1 = a.scale * unit * (kE4m3 ? row_scale[r] : 1.f);
     const float kb = slope * unit;
@@ -557,7 +592,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     float m_run = -INFINITY, l_run = 0.f;
     int n = 0, e_ref = 0;
     bool live = true;
-    for (int j = tk[t].lo; j < tk[t].hi; ++j, ++n) {
+    for (int j = tk.lo; j < tk.hi; ++j, ++n) {
       if (live) live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->s_full[t]), n & 1, wc));
       int4 info = make_int4(127, 127, 127, 0);
       if (kE4m3 && live) {
@@ -578,7 +613,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       for (int c = 0; c < 4; ++c) reg_fence32(x[c]);
       const int k0 = j * BN;
       const float k1j = kE4m3 ? k1 * exp_byte_scale((uint32_t)info.x) : k1;
-      const bool masked = k0 < tk[t].full_lo || k0 + BN > tk[t].full_hi;  // warp-uniform
+      const bool masked = k0 < tk.full_lo || k0 + BN > tk.full_hi;  // warp-uniform
       const bool fast = raw_ok && !masked;
       float mx[8];
 #pragma unroll
@@ -690,6 +725,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     if (kE4m3) inv *= exp_byte_scale((uint32_t)e_ref);
     const float l2 = l_run > 0.f ? m_run + log2f(l_run) - (kE4m3 ? kPOffset : 0.f) : -INFINITY;
     if (a.n_chunks > 1) {
+      const long long part = ((long long)w.cc * p.T + me.t) * a.Hq + me.h;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -702,13 +738,13 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
         if (!has_row) continue;
-        float4* dst = reinterpret_cast<float4*>(a.part_o + part_row(r) * D + c * 32);
+        float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + c * 32);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
                                __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
       }
-      if (has_row) a.part_lse[part_row(r)] = l2;
+      if (has_row) a.part_lse[part] = l2;
     } else {
       uint8_t* otile = smem + t * L::kTile;
       {
@@ -726,12 +762,12 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
         }
 #pragma unroll
         for (int gc = 0; gc < D / 8; ++gc) {
-          uint4 w;
-          w.x = pack_bf16x2(__uint_as_float(o[8 * gc + 0]) * inv, __uint_as_float(o[8 * gc + 1]) * inv);
-          w.y = pack_bf16x2(__uint_as_float(o[8 * gc + 2]) * inv, __uint_as_float(o[8 * gc + 3]) * inv);
-          w.z = pack_bf16x2(__uint_as_float(o[8 * gc + 4]) * inv, __uint_as_float(o[8 * gc + 5]) * inv);
-          w.w = pack_bf16x2(__uint_as_float(o[8 * gc + 6]) * inv, __uint_as_float(o[8 * gc + 7]) * inv);
-          *reinterpret_cast<uint4*>(otile + (gc >> 3) * L::kChunk + row * 128 + (((gc & 7) ^ (row & 7)) << 4)) = w;
+          uint4 v;
+          v.x = pack_bf16x2(__uint_as_float(o[8 * gc + 0]) * inv, __uint_as_float(o[8 * gc + 1]) * inv);
+          v.y = pack_bf16x2(__uint_as_float(o[8 * gc + 2]) * inv, __uint_as_float(o[8 * gc + 3]) * inv);
+          v.z = pack_bf16x2(__uint_as_float(o[8 * gc + 4]) * inv, __uint_as_float(o[8 * gc + 5]) * inv);
+          v.w = pack_bf16x2(__uint_as_float(o[8 * gc + 6]) * inv, __uint_as_float(o[8 * gc + 7]) * inv);
+          *reinterpret_cast<uint4*>(otile + (gc >> 3) * L::kChunk + row * 128 + (((gc & 7) ^ (row & 7)) << 4)) = v;
         }
       }
       __syncwarp();
@@ -740,11 +776,11 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
 #pragma unroll 4
       for (int k = 0; k < 32 / kRowsPerStore; ++k) {
         const int rt = (warp & 3) * 32 + k * kRowsPerStore + lane / kPer;
-        const uint4 w = *reinterpret_cast<const uint4*>(otile + (gc >> 3) * L::kChunk + rt * 128 +
+        const uint4 v = *reinterpret_cast<const uint4*>(otile + (gc >> 3) * L::kChunk + rt * 128 +
                                                        (((gc & 7) ^ (rt & 7)) << 4));
-        if (t * BM + rt < rows) reinterpret_cast<uint4*>(o_row(t * BM + rt))[gc] = w;
+        if (t * BM + rt < w.rows) reinterpret_cast<uint4*>(o_row(row_of(t * BM + rt)))[gc] = v;
       }
-      if (has_row) *lse_row(r) = l2 * kPagedLn2;
+      if (has_row) *lse_row(me) = l2 * kPagedLn2;
     }
   }
   __syncwarp();
