@@ -202,7 +202,7 @@ struct PagedMaps {
   CUtensorMap k, v;
 };
 // Few query rows per kv head over an e4m3 cache take the row kernel.
-constexpr int kPagedRowsMax = 16;
+constexpr int kPagedRowsMax = 32;
 inline bool paged_few_rows(const PagedAttention& a) {
   return a.p.kv_exp != nullptr && (long long)a.p.max_new * a.G <= kPagedRowsMax;
 }

@@ -35,12 +35,29 @@ __global__ void __launch_bounds__(kWarps * 32) paged_merge_kernel(const PagedAtt
 #pragma unroll
   for (int e = 0; e < kC; ++e) acc[e] = 0.f;
   if (M > -INFINITY)
-    for (int c = ca; c < cb; ++c) {
-      const float w = ex2_approx(a.part_lse[c * rows + row] - M);
-      W += w;
-      const float* src = a.part_o + (c * rows + row) * D + lane * kC;
+    for (int c0 = ca; c0 < cb; c0 += 4) {  // four chunks' loads in flight
+      float l2[4], v[4][kC];
 #pragma unroll
-      for (int e = 0; e < kC; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+      for (int k = 0; k < 4; ++k) {
+        const bool in = c0 + k < cb;
+        const long long at = imin(c0 + k, cb - 1) * rows + row;
+        l2[k] = in ? a.part_lse[at] : -INFINITY;
+        const float* src = a.part_o + at * D + lane * kC;
+        if constexpr (kC == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(src);
+          v[k][0] = f.x; v[k][1] = f.y; v[k][2] = f.z; v[k][3] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(src);
+          v[k][0] = f.x; v[k][1] = f.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float w = ex2_approx(l2[k] - M);
+        W += w;
+#pragma unroll
+        for (int e = 0; e < kC; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+      }
     }
   const float inv = W > 0.f ? 1.f / W : 0.f;
 #pragma unroll

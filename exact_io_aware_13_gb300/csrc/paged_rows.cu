@@ -6,8 +6,9 @@
 // so the kernel is built around the stream:
 //   * a CTA (4 warps) takes one key chunk of one (sequence, kv head); warp w takes its
 //     32-key tiles w, w + 4, ... through a ring of its own, filled by TMA (codes, one box
-//     per page piece) and bulk copies (exponents). A warp waits for nobody, and no thread
-//     waits between a tile's arrival and the request for the next one but for its own work;
+//     per page piece) and bulk copies (exponents), and waits for nobody. With 17 to 32 rows
+//     two warps share each tile and take 16 rows each (one warp's O would not fit its
+//     registers);
 //   * codes become fp16 in registers (exact, one conversion for two values) and feed
 //     mma.sync m16n8k16 with the KEYS (S^T = K Q^T) or the head dimension (O^T = V^T P^T) as
 //     the 16-row side and 8 query rows as the other: with a few query rows per kv head a
@@ -36,17 +37,17 @@ constexpr int kTile = 32;        // keys per ring stage
 constexpr float kPOffset = 11.0f;  // P is scaled by 2^11
 constexpr float kLag = 4.0f;       // O is rescaled when the maximum grows by more than 2^4
 
-// Ring stages per warp. 8.1 KB each at d = 128.
-constexpr int kStages = 3;
+// Key tiles of a CTA in its rings, 8.1 KB each at d = 128: three CTAs fit an SM.
+constexpr int kRingTiles = 8;
 
 template <int D>
 struct Layout {
   static constexpr int kCodes = kTile * D;                    // one K or V tile
   static constexpr int kStage = 2 * kCodes;                   // swizzled: 1024-byte aligned
-  static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kExp = kRing;                          // exponents [warp][stage][32][2]
-  static constexpr int kBars = kExp + kWarps * kStages * kTile * 2;
-  static constexpr int kAlloc = kBars + kWarps * kStages * 8 + 16 + 1024;
+  static constexpr int kRing = kRingTiles * kStage;
+  static constexpr int kExp = kRing;                          // exponents [tile][32][2]
+  static constexpr int kBars = kExp + kRingTiles * kTile * 2;
+  static constexpr int kAlloc = kBars + kRingTiles * 8 + 16 + 1024;
 };
 
 // Fragment row g (0..7) of a key tile holds key kappa(g): rows g and g + 1 differ in bit 2
@@ -88,14 +89,23 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
   return v;
 }
 
-// Address of 16-byte piece `piece` of row `row` of a swizzled tile of D-byte rows.
+// Offset of 16-byte piece `piece` of row `row` in a swizzled tile of D-byte rows. Rows 8
+// apart have the same swizzle.
 template <int D>
-__device__ __forceinline__ uint32_t piece_addr(uint32_t tile, int row, int piece) {
-  return D == 128 ? tile + row * 128 + ((piece ^ (row & 7)) << 4)
-                  : tile + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+__device__ __forceinline__ uint32_t piece_offset(int row, int piece) {
+  return D == 128 ? row * 128 + ((piece ^ (row & 7)) << 4)
+                  : row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+}
+// Four e4m3 codes to two half2 words.
+__device__ __forceinline__ void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
-template <int D, int NT>
+// NT: 8-row groups per warp; RG: warps that share a key tile, each with NT * 8 rows.
+template <int D, int NT, int RG>
 __global__ void __launch_bounds__(kWarps * 32)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PagedAttention a) {
@@ -107,6 +117,8 @@ __global__ void __launch_bounds__(kWarps * 32)
   const PagedProblem& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
+  constexpr int kKeyGroups = kWarps / RG, kStages = kRingTiles / kKeyGroups;
+  const int kg = warp / RG, rg = warp % RG, row0 = rg * NT * 8;  // key group, first row
   if (blockIdx.x == 0) report_bad_spans(p);
   const int cc = (int)(blockIdx.x % a.n_chunks);
   const int bh = (int)(blockIdx.x / a.n_chunks);
@@ -124,27 +136,34 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int tb = k_lo / kTile, te = k_hi > k_lo ? ceil_div(k_hi, kTile) : tb;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
-  int* abort_flag = reinterpret_cast<int*>(smem + L::kBars + kWarps * kStages * 8);
+  int* abort_flag = reinterpret_cast<int*>(smem + L::kBars + kRingTiles * 8);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(bars + i), 1);
+    for (int i = 0; i < kRingTiles; ++i) mbar_init(smem_u32(bars + i), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
   __syncthreads();
   const WaitCtx wc{abort_flag, p.status};
-  const uint32_t ring = smem_u32(smem) + warp * kStages * L::kStage;
-  const uint32_t exps = smem_u32(smem + L::kExp) + warp * kStages * kTile * 2;
-  const uint32_t full = smem_u32(bars) + warp * kStages * 8;
+  const uint32_t ring = smem_u32(smem) + kg * kStages * L::kStage;
+  const uint32_t exps = smem_u32(smem + L::kExp) + kg * kStages * kTile * 2;
+  const uint32_t full = smem_u32(bars) + kg * kStages * 8;
 
-  // Requests tile t0 / 32 into stage s: lane q fetches the q-th page piece of it.
+  // Requests the key group's next tile into stage s: lane q fetches its q-th page piece. The
+  // group's tiles are kKeyGroups * 32 keys apart, which is a whole number of pages or leads
+  // at most one page on, so the page and slot of the lane's piece advance without a division.
   const int R = imin(p.page_size, kTile), pieces = kTile / R;
-  auto request = [&](int tile, int s) {
-    const int key = tile * kTile + lane * R;
-    const bool in_seq = lane < pieces && key < sp.L;
-    long long row = -1;
-    if (in_seq) {
-      row = cache_row(p, b, key, hk);
-      if (row < 0) atomicOr(p.status, DEV_BAD_INPUT);
+  constexpr int kStride = kKeyGroups * kTile;
+  const bool whole = p.page_size <= kStride;       // then it divides kStride
+  const int page_step = whole ? kStride / p.page_size : 0;
+  int key = (tb + kg) * kTile + lane * R;
+  int page_idx = key / p.page_size, slot = key - page_idx * p.page_size;
+  const int32_t* table = p.page_table + (size_t)b * p.max_pages;
+  auto request = [&](int s) {
+    int row = -1;
+    if (lane < pieces && key < sp.L) {
+      const int page = __ldg(table + page_idx);
+      if (page >= 0 && page < p.num_pages) row = (page * p.Hkv + hk) * p.page_size + slot;
+      else atomicOr(p.status, DEV_BAD_INPUT);
     }
     const uint32_t bar = full + s * 8;
     const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0));
@@ -152,13 +171,23 @@ __global__ void __launch_bounds__(kWarps * 32)
     __syncwarp();
     if (row >= 0) {
       const uint32_t kt = ring + s * L::kStage + lane * R * D;
-      tma_load_2d(kt, &tm_k, bar, 0, (int)row);
-      tma_load_2d(kt + L::kCodes, &tm_v, bar, 0, (int)row);
-      bulk_load(exps + (s * kTile + lane * R) * 2, p.kv_exp + row * 2, R * 2, bar);
+      tma_load_2d(kt, &tm_k, bar, 0, row);
+      tma_load_2d(kt + L::kCodes, &tm_v, bar, 0, row);
+      bulk_load(exps + (s * kTile + lane * R) * 2, p.kv_exp + (size_t)row * 2, R * 2, bar);
+    }
+    key += kStride;
+    page_idx += page_step;
+    if (!whole) {
+      slot += kStride;
+      if (slot >= p.page_size) {
+        slot -= p.page_size;
+        ++page_idx;
+      }
     }
   };
-  int issued = tb + warp;  // next tile to request
-  for (int s = 0; s < kStages && issued < te; ++s, issued += kWarps) request(issued, s);
+  int issued = tb + kg;  // next tile to request
+  if (rg == 0)
+    for (int s = 0; s < kStages && issued < te; ++s, issued += kKeyGroups) request(s);
 
   // Q fragments: thread (g, c) holds, of row nt * 8 + g, the head dimensions 16 c + 4 s .. + 3
   // (and 64 + ... for steps 4-7) of step s, the pieces it reads of K.
@@ -168,7 +197,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const float unit = (a.score_kind & ATTN_SCORE_SOFTCAP) ? 1.0f / a.softcap : kPagedLog2e;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = nt * 8 + g;
+    const int r = row0 + nt * 8 + g;
     uint32_t w[kSteps][2];
     uint32_t top = 0;
     const bool ok = r < rows;
@@ -199,7 +228,7 @@ __global__ void __launch_bounds__(kWarps * 32)
                                   __uint_as_float(w[s][e] & 0xFFFF0000u) * up);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {  // the softmax's rows of this thread: nt * 8 + 2 c + e
-      const int rr = nt * 8 + 2 * c + e;
+      const int rr = row0 + nt * 8 + 2 * c + e;
       const int xr = __shfl_sync(0xffffffffu, x, (2 * c + e) * 4);
       const int ii = rr / a.G, hh = hk * a.G + rr - ii * a.G;
       // 2^(xr - 14) is a normal number: xr >= -112
@@ -226,27 +255,40 @@ __global__ void __launch_bounds__(kWarps * 32)
   const bool plain = !(a.score_kind & (ATTN_SCORE_ALIBI | ATTN_SCORE_SOFTCAP));
   const float cap = a.softcap * kPagedLog2e;
 
+  // This lane's offsets in the tiles: K pieces c and 4 + c of key row kappa(g), V pieces of
+  // key rows c and c + 4.
+  uint32_t koff[D / 64], voff[2];
+#pragma unroll
+  for (int half = 0; half < D / 64; ++half) koff[half] = piece_offset<D>(kappa(g), half * 4 + c);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    voff[k] = L::kCodes + (D == 128 ? piece_offset<D>(c + 4 * k, kappa(g))
+                                    : piece_offset<D>(c + 4 * k, g >> 1) + (g & 1) * 8);
+
   bool live = true;
   int s = 0;
   uint32_t parity = 0;
-  for (int tile = tb + warp; tile < te; tile += kWarps) {
-    live = __all_sync(0xffffffffu, mbar_wait(full + s * 8, parity, wc));
-    if (!live) break;
+  for (int tile = tb + kg; tile < te; tile += kKeyGroups) {
+    if (live) live = __all_sync(0xffffffffu, mbar_wait(full + s * 8, parity, wc));
+    if (!live) {  // keep the barriers of the warps that share the tile paired
+      if (RG > 1) nb_sync(1 + kg, RG * 32);
+      continue;
+    }
     const int t0 = tile * kTile;
     const uint32_t kt = ring + s * L::kStage, vt = kt + L::kCodes, et = exps + s * kTile * 2;
     const int valid = imin(kTile, sp.L - t0);
     if (valid < kTile) {  // slots behind the sequence: their V must not reach the sums
       for (int e = lane; e < (kTile - valid) * (D / 16); e += 32) {
         const int row = valid + e / (D / 16), piece = e % (D / 16);
-        const uint32_t at = piece_addr<D>(vt, row, piece);
+        const uint32_t at = vt + piece_offset<D>(row, piece);
         asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
       }
-      __syncwarp();
+      __syncwarp();  // (warps that share the tile write the same zeros before they read it)
     }
     const uint32_t e_lane = lds16(et + lane * 2) >> 8;  // V exponent of key t0 + lane
     const int Et = (int)__reduce_max_sync(0xffffffffu, lane < valid ? e_lane : 0u);
     // Whether every row sees every key of the tile (warp-uniform)
-    const bool masked = t0 < lo1 || t0 + kTile > hi0 || rows < NT * 8;
+    const bool masked = t0 < lo1 || t0 + kTile > hi0;
 
     // ---- S^T = K Q^T for the two 16-key halves
     float x[2][NT][4];
@@ -254,20 +296,20 @@ __global__ void __launch_bounds__(kWarps * 32)
     int ve[2][2];
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      const int row = hf * 16 + kappa(g);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[hf][nt][e] = 0.f;
 #pragma unroll
       for (int half = 0; half < D / 64; ++half) {
-        const uint4 u = lds128(piece_addr<D>(kt, row, half * 4 + c));
-        const uint4 v = lds128(piece_addr<D>(kt, row + 8, half * 4 + c));
+        const uint4 u = lds128(kt + koff[half] + hf * 16 * D);
+        const uint4 v = lds128(kt + koff[half] + (hf * 16 + 8) * D);
         const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int st = 0; st < 4; ++st) {
-          const uint32_t a0 = e4m3x2_to_f16x2(uw[st]), a2 = e4m3x2_to_f16x2(uw[st] >> 16);
-          const uint32_t a1 = e4m3x2_to_f16x2(vw[st]), a3 = e4m3x2_to_f16x2(vw[st] >> 16);
+          uint32_t a0, a1, a2, a3;
+          decode4(uw[st], a0, a2);
+          decode4(vw[st], a1, a3);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             mma_16816(x[hf][nt], a0, a1, a2, a3, qf[nt][half * 4 + st][0], qf[nt][half * 4 + st][1]);
@@ -275,7 +317,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint32_t w = lds16(et + (row + 8 * e) * 2);
+        const uint32_t w = lds16(et + (hf * 16 + kappa(g) + 8 * e) * 2);
         ks[hf][e] = exp_byte_scale(w & 255u);
         ve[hf][e] = (int)(w >> 8);
       }
@@ -293,7 +335,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float y = x[hf][nt][2 * e + r] * ks[hf][e] * k1[nt][r];
+            float y = x[hf][nt][2 * e + r] * (ks[hf][e] * k1[nt][r]);
             if (!plain) {
               y -= slope[nt][r] * (float)(pos[nt][r] - j);
               if (a.score_kind & ATTN_SCORE_SOFTCAP) y = cap * tanhf(y);
@@ -356,12 +398,12 @@ __global__ void __launch_bounds__(kWarps * 32)
       uint32_t w[4][D / 32];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int row = hf * 16 + c + 4 * k;
+        const uint32_t at = kt + voff[k & 1] + (hf * 16 + 8 * (k >> 1)) * D;
         if constexpr (D == 128) {
-          const uint4 v = lds128(piece_addr<D>(vt, row, kappa(g)));
+          const uint4 v = lds128(at);
           w[k][0] = v.x; w[k][1] = v.y; w[k][2] = v.z; w[k][3] = v.w;
         } else {
-          const uint2 v = lds64(piece_addr<D>(vt, row, g >> 1) + (g & 1) * 8);
+          const uint2 v = lds64(at);
           w[k][0] = v.x; w[k][1] = v.y;
         }
       }
@@ -371,17 +413,20 @@ __global__ void __launch_bounds__(kWarps * 32)
         for (int hb = 0; hb < 2; ++hb) {  // two head dimensions of the word: one O tile
           const uint32_t sel = hb ? 0x7362u : 0x5140u;
           const uint32_t u = prmt(w[0][i], w[1][i], sel), v = prmt(w[2][i], w[3][i], sel);
-          const uint32_t a0 = e4m3x2_to_f16x2(u), a1 = e4m3x2_to_f16x2(u >> 16);
-          const uint32_t a2 = e4m3x2_to_f16x2(v), a3 = e4m3x2_to_f16x2(v >> 16);
+          uint32_t a0, a1, a2, a3;
+          decode4(u, a0, a1);
+          decode4(v, a2, a3);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             mma_16816(o[nt][2 * i + hb], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
         }
     }
-    __syncwarp();  // every lane has read the stage
-    if (issued < te) {
-      request(issued, s);
-      issued += kWarps;
+    // every thread has read the stage
+    if (RG > 1) nb_sync(1 + kg, RG * 32);
+    else __syncwarp();
+    if (rg == 0 && issued < te) {
+      request(s);
+      issued += kKeyGroups;
     }
     if (++s == kStages) {
       s = 0;
@@ -391,13 +436,13 @@ __global__ void __launch_bounds__(kWarps * 32)
   if (!live)  // leave no copy in flight into this CTA's shared memory
     for (int i = 0; i < kStages; ++i) drain_wait(full + i * 8, i < s ? parity ^ 1 : parity);
 
-  // ---- merge of the warps: factors 2^(m_w - M) 2^E_w, fixed order
+  // ---- merge of the key groups: factors 2^(m_k - M) 2^E_k, fixed order
   __syncthreads();
-  constexpr int kRows = NT * 8;
-  float* sm_m = reinterpret_cast<float*>(smem);            // [warp][row]
-  float* sm_l = sm_m + kWarps * kRows;
-  float* sm_o = sm_l + kWarps * kRows;                     // [warp][row][D + 4]
-  static_assert((2 * kWarps * kRows + kWarps * kRows * (D + 4)) * 4 <= L::kRing, "merge space");
+  constexpr int kRows = NT * 8 * RG;
+  float* sm_m = reinterpret_cast<float*>(smem);            // [key group][row]
+  float* sm_l = sm_m + kKeyGroups * kRows;
+  float* sm_o = sm_l + kKeyGroups * kRows;                 // [key group][row][D + 4]
+  static_assert((2 + D + 4) * kKeyGroups * kRows * 4 <= L::kRing, "merge space");
   const float vs = exp_byte_scale((uint32_t)E);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -406,16 +451,16 @@ __global__ void __launch_bounds__(kWarps * 32)
       float sum = l[nt][r];
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      const int rr = nt * 8 + 2 * c + r;
+      const int rr = kg * kRows + row0 + nt * 8 + 2 * c + r;
       if (g == 0) {
-        sm_m[warp * kRows + rr] = m[nt][r];
-        sm_l[warp * kRows + rr] = sum;
+        sm_m[rr] = m[nt][r];
+        sm_l[rr] = sum;
       }
 #pragma unroll
       for (int st = 0; st < kSteps; ++st) {
         const int dim = D == 128 ? 16 * kappa(g) + 2 * st : 8 * g + 2 * st;
-        float2* dst = reinterpret_cast<float2*>(sm_o + (warp * kRows + rr) * (D + 4) + dim);
-        *dst = make_float2(o[nt][st][r] * vs, o[nt][st][2 + r] * vs);
+        *reinterpret_cast<float2*>(sm_o + rr * (D + 4) + dim) =
+            make_float2(o[nt][st][r] * vs, o[nt][st][2 + r] * vs);
       }
     }
   __syncthreads();
@@ -423,16 +468,16 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int rr = warp; rr < rows; rr += kWarps) {
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * kRows + rr]);
+    for (int k = 0; k < kKeyGroups; ++k) M = fmaxf(M, sm_m[k * kRows + rr]);
     float sum = 0.f, acc[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float mw = sm_m[w * kRows + rr];
-      const float f = mw == -INFINITY || !ok ? 0.f : ex2_approx(mw - M);
-      sum = fmaf(f, sm_l[w * kRows + rr], sum);
-      const float* src = sm_o + (w * kRows + rr) * (D + 4) + lane * (D / 32);
+    for (int k = 0; k < kKeyGroups; ++k) {
+      const float mk = sm_m[k * kRows + rr];
+      const float f = mk == -INFINITY || !ok ? 0.f : ex2_approx(mk - M);
+      sum = fmaf(f, sm_l[k * kRows + rr], sum);
+      const float* src = sm_o + (k * kRows + rr) * (D + 4) + lane * (D / 32);
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) acc[e] = f > 0.f ? fmaf(f, src[e], acc[e]) : acc[e];
     }
@@ -445,9 +490,9 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, int RG>
 cudaError_t launch_nt(const PagedAttention& a, const PagedMaps& maps, cudaStream_t st) {
-  auto kern = paged_rows_kernel<D, NT>;
+  auto kern = paged_rows_kernel<D, NT, RG>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kAlloc);
   if (e != cudaSuccess) return e;
   const long long grid = (long long)a.p.B * a.p.Hkv * a.n_chunks;
@@ -459,9 +504,9 @@ cudaError_t launch_nt(const PagedAttention& a, const PagedMaps& maps, cudaStream
 template <int D>
 cudaError_t launch_d(const PagedAttention& a, const PagedMaps& maps, cudaStream_t st) {
   const int rows = a.p.max_new * a.G;
-  if (rows <= 8) return launch_nt<D, 1>(a, maps, st);
-  if (rows <= 16) return launch_nt<D, 2>(a, maps, st);
-  return launch_nt<D, 4>(a, maps, st);
+  if (rows <= 8) return launch_nt<D, 1, 1>(a, maps, st);
+  if (rows <= 16) return launch_nt<D, 2, 1>(a, maps, st);
+  return launch_nt<D, 2, 2>(a, maps, st);
 }
 
 }  // namespace

@@ -51,8 +51,8 @@ struct Shape {
   // launch gives kThreads x kRegsLaunch; the split must not exceed it (launch_variant checks
   // what the compiler used).
   static constexpr int kRegsLaunch = kE4m3 ? 128 : 168;
-  static constexpr int kRegsSoftmax = kE4m3 ? 208 : 232;
-  static constexpr int kRegsOther = 40;
+  static constexpr int kRegsSoftmax = kE4m3 ? 184 : 208;
+  static constexpr int kRegsOther = 88;
   static constexpr int kRegsConvert = 56;
   static_assert(256 * kRegsSoftmax + 128 * kRegsOther + (kE4m3 ? 128 * kRegsConvert : 0) <=
                     kThreads * kRegsLaunch,
@@ -71,8 +71,7 @@ struct Layout {
   static constexpr int kCodes = kRing + S::kStages * kTile;
   static constexpr int kCodeTile = BN * D;
   static constexpr int kExp = kCodes + S::kCodeStages * kCodeTile;   // [kInfo][128][2]
-  static constexpr int kRowScale = kExp + (kE4m3 ? kInfo * BN * 2 : 0);
-  static constexpr int kBars = kRowScale + (kE4m3 ? kUnitRows * 4 : 0);
+  static constexpr int kBars = kExp + (kE4m3 ? kInfo * BN * 2 : 0);
   static constexpr int kAlloc = kBars + 512 + 1024;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
@@ -529,10 +528,10 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     const int row = (warp & 3) * 32 + lane;     // TMEM lane = row in the tile
     const int r = t * BM + row;                 // row in the unit
     const bool has_row = r < w.rows;
-    float* row_scale = reinterpret_cast<float*>(smem + L::kRowScale);
+    float row_scale = 1.f;  // e4m3: undoes the power of two that this thread's row was scaled by
     {
       // This warp's 32 Q rows into swizzled shared memory (rows past the end: zeros). e4m3:
-      // scaled by a power of two to fp16, the factor that undoes it kept per row.
+      // scaled by a power of two to fp16.
       constexpr int kPer = D / 8, kRowsPerIter = 32 / kPer;
       const int piece = lane % kPer;
 #pragma unroll
@@ -561,7 +560,10 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
             for (int e = 0; e < 4; ++e)
               u[e] = pack_f16x2(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xFFFF0000u) * up);
             v[it] = make_uint4(u[0], u[1], u[2], u[3]);
-            if (piece == 0) row_scale[rr] = __uint_as_float((uint32_t)(x - 14 + 127) << 23);
+            const int row_in_iter = lane % kRowsPerIter;
+            const int xl = __shfl_sync(0xffffffffu, x, row_in_iter * kPer);
+            if (lane / kRowsPerIter == it0 + it)
+              row_scale = __uint_as_float((uint32_t)(xl - 14 + 127) << 23);
           }
           const int rt = rr - t * BM;
           *reinterpret_cast<uint4*>(smem + L::kQ + t * L::kTile + (piece >> 3) * L::kChunk + rt * 128 +
@@ -585,7 +587,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     const int lo = w.lo;
     const float slope = kAlibi ? alibi_slope(me.h, a.Hq) : 0.f;
     const float unit = kSoftcap ? 1.0f / a.softcap : kPagedLog2e;
-    const float k1 = a.scale * unit * (kE4m3 ? row_scale[r] : 1.f);
+    const float k1 = a.scale * unit * row_scale;
     const float kb = slope * unit;
     const float capA = kSoftcap ? a.softcap * kPagedLog2e : 0.f;
     const bool raw_ok = !kAlibi && !kSoftcap && a.scale > 0.f;
@@ -593,9 +595,16 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     int n = 0, e_ref = 0;
     bool live = true;
     for (int j = tk.lo; j < tk.hi; ++j, ++n) {
-      if (live) live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->s_full[t]), n & 1, wc));
       int4 info = make_int4(127, 127, 127, 0);
-      if (kE4m3 && live) {
+      if (kE4m3 && n > 0 && live) {
+        // The tile's scales are there long before its scores; having seen tile j - 1's, this
+        // thread cannot be a whole turn of the slots behind, which the parity would not show.
+        const int jj = j - lo;
+        live = mbar_wait(smem_u32(&bars->info_full[jj % kInfo]), (jj / kInfo) & 1, wc);
+        info = bars->info[jj % kInfo];
+      }
+      live = __all_sync(0xffffffffu, live && mbar_wait(smem_u32(&bars->s_full[t]), n & 1, wc));
+      if (kE4m3 && n == 0 && live) {  // the first tile: its scores show that the turn is right
         const int jj = j - lo;
         live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->info_full[jj % kInfo]), (jj / kInfo) & 1, wc));
         info = bars->info[jj % kInfo];
