@@ -70,7 +70,7 @@ SIGNATURES = {
     "attn_prefill_paged": (_I, [_CP, _P, _L, _L, _P, _P, _P, _P] + [_I] * 6 +
                            [_F, _I, _MP, _I, _SP, _P, ctypes.c_size_t, _P]),
     "attn_prefill_workspace_size": (ctypes.c_size_t, [_I] * 5),
-    "attn_prefill_split_keys": (_I, [_I] * 6 + [_L, _I]),
+    "attn_prefill_split_keys": (_I, [_I] * 7 + [_L, _I]),
     "attn_decode_paged_e4m3": (_I, [_CP, _P, _P, _P, _P] + [_I] * 5 +
                                [_F, _I, _MP, _I, _SP, _P, ctypes.c_size_t, _P]),
     "attn_check_doc_offsets": (_I, [_P, _I, _I, _P]),

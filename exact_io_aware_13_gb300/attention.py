@@ -20,13 +20,13 @@ TILE = 128
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+def _stream(stream) -> int:
+    if stream is None:  # the raw handle: a Stream object per call costs 3 us
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _params(mask_kind: int, window: int, doc_offsets: Optional[torch.Tensor],
@@ -94,8 +94,8 @@ def _check_tensors(*ts):
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError("tensors must be contiguous CUDA tensors")
         if index is None:
-            index = t.device.index
-        elif t.device.index != index:
+            index = t.get_device()
+        elif t.get_device() != index:
             raise ValueError("tensors must all be on one device")
     if index is not None and index != torch.cuda.current_device():
         raise ValueError(f"tensors are on cuda:{index}, the current device is "
@@ -311,12 +311,24 @@ def forward_fp8(q, k, v, *, scale: Optional[float] = None, mask_kind: int = MASK
 
 
 # ---------------------------------------------------------------- paged decode
+_SM_COUNT: dict = {}
+
+
+def _num_sms() -> int:
+    """SM count of the current device (0 without one), looked up once per device."""
+    if not _SM_COUNT and not torch.cuda.is_available():
+        return 0
+    dev = torch.cuda.current_device()
+    if dev not in _SM_COUNT:
+        _SM_COUNT[dev] = torch.cuda.get_device_properties(dev).multi_processor_count
+    return _SM_COUNT[dev]
+
+
 def decode_split_keys(B: int, Hq: int, Hkv: int, Nq: int, total_kv_tokens: int,
                       num_sms: Optional[int] = None) -> int:
     """The library's split size for a decode call (keys per chunk)."""
     if num_sms is None:
-        num_sms = (torch.cuda.get_device_properties(torch.cuda.current_device())
-                   .multi_processor_count if torch.cuda.is_available() else 0)
+        num_sms = _num_sms()
     return int(_lib.load().attn_decode_split_keys(int(B), int(Hq), int(Hkv), int(Nq),
                                                   int(total_kv_tokens), int(num_sms)))
 

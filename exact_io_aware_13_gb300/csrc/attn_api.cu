@@ -803,21 +803,28 @@ attn_status attn_cache_read(const attn_paged_cache* cache, void* k, void* v,
                                      static_cast<cudaStream_t>(stream)));
 }
 
-int attn_prefill_split_keys(int B, int T, int Hq, int Hkv, int max_new, int max_seq_len,
-                            long long total_kv_tokens, int num_sms) {
+int attn_prefill_split_keys(int cache_kind, int B, int T, int Hq, int Hkv, int max_new,
+                            int max_seq_len, long long total_kv_tokens, int num_sms) {
   const long long whole = std::max(128LL, ((long long)max_seq_len + 127) / 128 * 128);
   const long long one = std::min(whole, 0x7fffff80LL);
   if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || max_new <= 0 || max_seq_len <= 0 ||
       total_kv_tokens <= 0 || Hq % Hkv != 0)
     return (int)one;
-  const long long G = Hq / Hkv;
-  const long long units = std::min((long long)T * G / 256 + B,
-                                   (long long)B * ((max_new * G + 255) / 256)) * Hkv;
-  const long long target = num_sms > 0 ? num_sms : 148;
-  if (units >= target) return (int)one;
-  // each unit walks its sequence's keys: total_kv_tokens / B of them on average
-  const long long keys = (total_kv_tokens / B * units + target - 1) / target;
-  return (int)std::min(std::max(512LL, (keys + 127) / 128 * 128), one);
+  const long long G = Hq / Hkv, rows = std::min(max_new, T) * G;
+  if (cache_kind == ATTN_CACHE_E4M3 && rows <= kPagedRowsMax) {
+    // The row kernel: ten chunks per SM, as for decode. 8 new tokens of 16 sequences of 2000
+    // to 32768 (Hq = 32, Hkv = 8, d = 128): 306 us at 2048 keys, 388 at 512, 846 unsplit.
+    const long long keys = attn_decode_split_keys(B, Hq, Hkv, 1, total_kv_tokens, num_sms);
+    return (int)std::min((keys + 127) / 128 * 128, one);
+  }
+  // The tile kernel, one CTA per SM: unsplit when the 256-row units fill the SMs (24 short
+  // turns, 180 units: 36 us, 62 us in chunks of 1024), else four chunks per SM (the batch
+  // above over bf16, 128 units: 288 us at 4096 keys, 345 at 2048, 337 unsplit).
+  const long long units = std::min((long long)T * G / 256 + B, B * ((rows + 255) / 256));
+  const long long sms = num_sms > 0 ? num_sms : 148;
+  if (units * Hkv >= sms) return (int)one;
+  const long long keys = (total_kv_tokens / B * units * Hkv + 4 * sms - 1) / (4 * sms);
+  return (int)std::min(std::max(1024LL, (keys + 127) / 128 * 128), one);
 }
 
 size_t attn_prefill_workspace_size(int T, int Hq, int d, int max_seq_len, int split_keys) {

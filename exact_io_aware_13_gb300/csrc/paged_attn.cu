@@ -8,17 +8,20 @@ namespace {
 
 constexpr int kWarps = 8;
 
-// Merge of the key chunks' partial results, one warp per row, in chunk order:
+// Merge of the key chunks' partial results, in a fixed order:
 //   M = max_c L2_c, w_c = 2^(L2_c - M), O = sum_c w_c O_c / sum_c w_c, L = M + log2 sum_c w_c.
-// Only chunks that hold keys of the row were written.
-template <int D>
+// Only chunks that hold keys of the row were written. A row takes one warp, or with many
+// chunks and few rows eight (each a contiguous part of them, joined through shared memory):
+// a lone warp's loads for 98 chunks of a 131072-token sequence took 25 us one after the other.
+template <int D, int kPerRow>
 __global__ void __launch_bounds__(kWarps * 32) paged_merge_kernel(const PagedAttention a) {
   constexpr int kC = D / 32;
+  __shared__ float sm[kPerRow > 1 ? kWarps : 1][D + 4];
   const PagedProblem& p = a.p;
-  const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kPerRow;
+  const long long unit = ((long long)blockIdx.x * kWarps + warp) / kPerRow;
   const int t = (int)(unit / a.Hq), h = (int)(unit % a.Hq);
-  if (t >= p.T) return;
+  if (t >= p.T) return;  // (with eight warps per row a CTA has one row)
   const int b = find_sequence(p, t, lane);
   const Span s = load_span(p, b);
   const int i = t - s.row0;
@@ -26,22 +29,23 @@ __global__ void __launch_bounds__(kWarps * 32) paged_merge_kernel(const PagedAtt
   int lo, hi;
   decode_row_keys(a.mask_kind, a.window, s.L, s.n, i, lo, hi);
   const int ca = hi > lo ? lo / a.chunk : 0, cb = hi > lo ? (hi - 1) / a.chunk + 1 : 0;
+  const int each = (cb - ca + kPerRow - 1) / kPerRow;
+  const int c_begin = imin(ca + part * each, cb), c_end = imin(c_begin + each, cb);
   const long long rows = (long long)p.T * a.Hq, row = (long long)t * a.Hq + h;
   float M = -INFINITY;
-  for (int c = ca + lane; c < cb; c += 32) M = fmaxf(M, a.part_lse[c * rows + row]);
+  for (int c = c_begin + lane; c < c_end; c += 32) M = fmaxf(M, a.part_lse[c * rows + row]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   float W = 0.f, acc[kC];
 #pragma unroll
   for (int e = 0; e < kC; ++e) acc[e] = 0.f;
   if (M > -INFINITY)
-    for (int c0 = ca; c0 < cb; c0 += 4) {  // four chunks' loads in flight
+    for (int c0 = c_begin; c0 < c_end; c0 += 4) {  // four chunks' loads in flight
       float l2[4], v[4][kC];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const bool in = c0 + k < cb;
-        const long long at = imin(c0 + k, cb - 1) * rows + row;
-        l2[k] = in ? a.part_lse[at] : -INFINITY;
+        const long long at = imin(c0 + k, c_end - 1) * rows + row;
+        l2[k] = c0 + k < c_end ? a.part_lse[at] : -INFINITY;
         const float* src = a.part_o + at * D + lane * kC;
         if constexpr (kC == 4) {
           const float4 f = *reinterpret_cast<const float4*>(src);
@@ -59,6 +63,28 @@ __global__ void __launch_bounds__(kWarps * 32) paged_merge_kernel(const PagedAtt
         for (int e = 0; e < kC; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
       }
     }
+  if constexpr (kPerRow > 1) {
+#pragma unroll
+    for (int e = 0; e < kC; ++e) sm[warp][lane * kC + e] = acc[e];
+    if (lane == 0) {
+      sm[warp][D] = M;
+      sm[warp][D + 1] = W;
+    }
+    __syncthreads();
+    if (part != 0) return;
+#pragma unroll
+    for (int k = 0; k < kPerRow; ++k) M = fmaxf(M, sm[k][D]);
+    W = 0.f;
+#pragma unroll
+    for (int e = 0; e < kC; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPerRow; ++k) {
+      const float mk = sm[k][D], f = mk == -INFINITY ? 0.f : ex2_approx(mk - M);
+      W = fmaf(f, sm[k][D + 1], W);
+#pragma unroll
+      for (int e = 0; e < kC; ++e) acc[e] = fmaf(f, sm[k][lane * kC + e], acc[e]);
+    }
+  }
   const float inv = W > 0.f ? 1.f / W : 0.f;
 #pragma unroll
   for (int e = 0; e < kC; ++e) acc[e] *= inv;
@@ -67,12 +93,19 @@ __global__ void __launch_bounds__(kWarps * 32) paged_merge_kernel(const PagedAtt
   store_row<D>(out, b, t, i, h, 0, lane, acc, W > 0.f ? M + log2f(W) : -INFINITY);
 }
 
-cudaError_t launch_merge(const PagedAttention& a, cudaStream_t st) {
-  const long long blocks = ((long long)a.p.T * a.Hq + kWarps - 1) / kWarps;
+template <int D, int kPerRow>
+cudaError_t launch_merge_as(const PagedAttention& a, cudaStream_t st) {
+  const long long blocks = ((long long)a.p.T * a.Hq * kPerRow + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  if (a.p.d == 64) paged_merge_kernel<64><<<(unsigned)blocks, kWarps * 32, 0, st>>>(a);
-  else paged_merge_kernel<128><<<(unsigned)blocks, kWarps * 32, 0, st>>>(a);
+  paged_merge_kernel<D, kPerRow><<<(unsigned)blocks, kWarps * 32, 0, st>>>(a);
   return cudaGetLastError();
+}
+cudaError_t launch_merge(const PagedAttention& a, cudaStream_t st) {
+  // Eight warps per row once a lone warp would take more than two turns of its four loads,
+  // as long as the rows are few (16384 rows fill the GPU twelve times with one warp each).
+  if (a.n_chunks > 8 && (long long)a.p.T * a.Hq <= 16384)
+    return a.p.d == 64 ? launch_merge_as<64, 8>(a, st) : launch_merge_as<128, 8>(a, st);
+  return a.p.d == 64 ? launch_merge_as<64, 1>(a, st) : launch_merge_as<128, 1>(a, st);
 }
 
 }  // namespace

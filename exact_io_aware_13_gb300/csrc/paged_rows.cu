@@ -106,7 +106,7 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) 
 
 // NT: 8-row groups per warp; RG: warps that share a key tile, each with NT * 8 rows.
 template <int D, int NT, int RG>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 3)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PagedAttention a) {
   using L = Layout<D>;
@@ -291,30 +291,53 @@ __global__ void __launch_bounds__(kWarps * 32)
     const bool masked = t0 < lo1 || t0 + kTile > hi0;
 
     // ---- S^T = K Q^T for the two 16-key halves
-    float x[2][NT][4];
-    float ks[2][2];
+    // The MMAs of a chain depend on one another (35 clocks each): both key halves, and for
+    // one row group both halves of the head dimension, run as chains of their own.
+    constexpr int kSplit = NT == 1 ? D / 64 : 1;
+    float xs[kSplit][2][NT][4];
+#pragma unroll
+    for (int q = 0; q < kSplit; ++q)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) xs[q][hf][nt][e] = 0.f;
+#pragma unroll
+    for (int h0 = 0; h0 < D / 64; h0 += kSplit) {
+      uint4 ku[kSplit][2], kv[kSplit][2];
+#pragma unroll
+      for (int q = 0; q < kSplit; ++q)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          ku[q][hf] = lds128(kt + koff[h0 + q] + hf * 16 * D);
+          kv[q][hf] = lds128(kt + koff[h0 + q] + (hf * 16 + 8) * D);
+        }
+#pragma unroll
+      for (int st = 0; st < 4; ++st)
+#pragma unroll
+        for (int q = 0; q < kSplit; ++q)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t uw[4] = {ku[q][hf].x, ku[q][hf].y, ku[q][hf].z, ku[q][hf].w};
+            const uint32_t vw[4] = {kv[q][hf].x, kv[q][hf].y, kv[q][hf].z, kv[q][hf].w};
+            uint32_t a0, a1, a2, a3;
+            decode4(uw[st], a0, a2);
+            decode4(vw[st], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_16816(xs[q][hf][nt], a0, a1, a2, a3, qf[nt][(h0 + q) * 4 + st][0], qf[nt][(h0 + q) * 4 + st][1]);
+          }
+    }
+    float x[2][NT][4], ks[2][2];
     int ve[2][2];
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[hf][nt][e] = 0.f;
-#pragma unroll
-      for (int half = 0; half < D / 64; ++half) {
-        const uint4 u = lds128(kt + koff[half] + hf * 16 * D);
-        const uint4 v = lds128(kt + koff[half] + (hf * 16 + 8) * D);
-        const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int st = 0; st < 4; ++st) {
-          uint32_t a0, a1, a2, a3;
-          decode4(uw[st], a0, a2);
-          decode4(vw[st], a1, a3);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_16816(x[hf][nt], a0, a1, a2, a3, qf[nt][half * 4 + st][0], qf[nt][half * 4 + st][1]);
-        }
-      }
+        for (int e = 0; e < 4; ++e)
+          x[hf][nt][e] = kSplit == 2 ? xs[0][hf][nt][e] + xs[kSplit - 1][hf][nt][e] : xs[0][hf][nt][e];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint32_t w = lds16(et + (hf * 16 + kappa(g) + 8 * e) * 2);
@@ -493,7 +516,8 @@ __global__ void __launch_bounds__(kWarps * 32)
 template <int D, int NT, int RG>
 cudaError_t launch_nt(const PagedAttention& a, const PagedMaps& maps, cudaStream_t st) {
   auto kern = paged_rows_kernel<D, NT, RG>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kAlloc);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Layout<D>::kAlloc, done);
   if (e != cudaSuccess) return e;
   const long long grid = (long long)a.p.B * a.p.Hkv * a.n_chunks;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;

@@ -13,6 +13,9 @@
 //     page-table entries fetched one tile ahead (bf16; e4m3 below);
 //   * masks are aligned at the bottom right (decode_row_keys), slots behind the sequence are
 //     masked in S and cleared in V;
+//   * a unit of at most 128 rows leaves no second query tile to overlap with, so its even
+//     key tiles go to the first softmax warpgroup and its odd ones to the second (two score
+//     buffers, two O accumulators), merged at the end;
 //   * the key axis may be cut into chunks: fp32 partial rows, merged by their log-sum-exp.
 //
 // e4m3 cache: a fourth warpgroup converts code tiles to fp16 operand tiles. The scales are
@@ -38,14 +41,15 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kRelayWarp = 10, kConvWarp = 12;
 constexpr int kInfo = 4;             // slots of the converters' per-tile scales
 constexpr uint32_t kNbP = 1, kNbPCount = 160;
 constexpr uint32_t kNbKv = 3;
+constexpr uint32_t kNbDual = 7;  // both softmax warpgroups, before a dual unit's merge
 constexpr float kPOffset = 11.0f;    // e4m3: P is scaled by 2^11 (fp16)
 constexpr int kMaxDown = 8;          // e4m3: a V tile's exponent is at least E_ref - 8
 
 template <bool kE4m3>
 struct Shape {
   static constexpr int kThreads = kE4m3 ? 512 : 384;
-  static constexpr int kStages = kE4m3 ? 3 : 4;       // operand tiles in the ring
-  static constexpr int kCodeStages = kE4m3 ? 3 : 0;   // code tiles waiting for conversion
+  static constexpr int kStages = 4;                   // operand tiles in the ring
+  static constexpr int kCodeStages = kE4m3 ? 2 : 0;   // code tiles waiting for conversion
   static constexpr uint32_t kNbKvCount = kE4m3 ? 160 : 64;
   // Registers: softmax threads hold 128 scores and the row state, the others little. The
   // launch gives kThreads x kRegsLaunch; the split must not exceed it (launch_variant checks
@@ -92,6 +96,7 @@ struct Cta {
   int row_base, rows;    // first packed row, packed rows from there on
   int c0, c1;            // keys of the chunk
   int lo, hi;            // key tiles of both query tiles together
+  bool dual;             // one query tile: its key tiles alternate between two streams
   Span span;
   TileKeys tk[kQTiles];
 };
@@ -102,8 +107,8 @@ struct Bars {
   uint64_t kv_empty[4];
   uint64_t s_full[kQTiles];
   uint64_t o_full[kQTiles];
-  uint64_t code_full[3];
-  uint64_t code_empty[3];
+  uint64_t code_full[2];
+  uint64_t code_empty[2];
   uint64_t info_full[kInfo];
   int4 info[kInfo];     // E_K, E_V, E_ref of key tile j (slot j % kInfo)
   uint32_t tmem_base;
@@ -186,6 +191,7 @@ __device__ __forceinline__ void find_work(const PagedAttention& a, Cta* w, int l
         }
         w->tk[t] = k;
       }
+      w->dual = w->rows <= BM && w->hi - w->lo >= 2;
     }
     if (__any_sync(0xffffffffu, hit)) return;
     base += __shfl_sync(0xffffffffu, incl, 31);
@@ -262,6 +268,20 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
   }
 
   WaitCtx wc{&bars->abort_flag, p.status};
+  // The softmax warps request their Q rows before the loader starts: behind its stream of
+  // keys they would take several times as long.
+  constexpr int kPer = D / 8, kRowsPerIter = 32 / kPer, kQIters = 32 / kRowsPerIter;
+  const int wt = (warp >> 2) & 1;                                // query tile of a softmax warp
+  const int wrow = (w.dual ? 0 : wt * BM) + (warp & 3) * 32;     // its first row in the unit
+  uint4 qv[kQIters];
+  if (warp < 8) {
+#pragma unroll
+    for (int it = 0; it < kQIters; ++it) {
+      const int rr = wrow + it * kRowsPerIter + lane / kPer;
+      qv[it] = make_uint4(0, 0, 0, 0);
+      if (rr < w.rows) qv[it] = __ldg(reinterpret_cast<const uint4*>(q_row(row_of(rr))) + lane % kPer);
+    }
+  }
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&bars->tmem_base), L::kTmemCols);
     tmem_relinquish();
@@ -287,10 +307,10 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     bool live = true;
     int e_ref = 0, e_k = 0, e_v = 0;
     for (int u = 0; u < 2 * n_kv; ++u) {
-      const int cs = u % 3, s = u % kStages, jj = u >> 1;
+      const int cs = u % 2, s = u % kStages, jj = u >> 1;
       const bool is_v = u & 1;
       if (live)
-        live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->code_full[cs]), (u / 3) & 1, wc));
+        live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->code_full[cs]), (u / 2) & 1, wc));
       const int valid = imin(BN, L_seq - (lo + jj) * BN);
       const uint8_t* ex = smem + L::kExp + (jj % kInfo) * BN * 2;
       if (live && !is_v) {  // the tile's exponents: lane reads rows 4 lane .. + 3 (K low byte)
@@ -384,7 +404,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
         if (r < 0) atomicOr(p.status, DEV_BAD_INPUT);
         return (int)r;
       };
-      constexpr int kDepth = kE4m3 ? 3 : kStages;
+      constexpr int kDepth = kE4m3 ? 2 : kStages;
       const uint32_t full = smem_u32(kE4m3 ? bars->code_full : bars->kv_full);
       const uint32_t empty = smem_u32(kE4m3 ? bars->code_empty : bars->kv_empty);
       int row = rows_of(lo), next = n_kv > 1 ? rows_of(lo + 1) : -1;
@@ -458,6 +478,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       const uint32_t ring = smem_u32(smem + L::kRing);
       int np[kQTiles] = {0, 0};
       const int lo = w.lo, n_kv = w.hi - lo;
+      const bool dual = w.dual;
       const int t_lo[kQTiles] = {w.tk[0].lo, w.tk[1].lo}, t_hi[kQTiles] = {w.tk[0].hi, w.tk[1].hi};
       const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->q_full), 0, wc));
       tc_fence_after_sync();
@@ -481,7 +502,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
         }
         mma_commit_if(issuer, smem_u32(&bars->s_full[t]));
       };
-      auto issue_pv = [&](int t, int u) {
+      auto issue_pv = [&](int t, int u, bool add) {  // add: O_t holds earlier products
         if (!ok) return;
         const uint32_t colS = t == 0 ? L::kColS0 : L::kColS1;
         const uint32_t colO = t == 0 ? L::kColO0 : L::kColO1;
@@ -489,33 +510,51 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
           mma_ts_if(issuer, tmem + colO, tmem + colS + kk * 8, dv + ((kk * 16 * 128) >> 4), idO,
-                    (np[t] > 0 || kk > 0) ? 1u : 0u);
+                    (add || kk > 0) ? 1u : 0u);
       };
       sync_stage(0);
-#pragma unroll
-      for (int t = 0; t < kQTiles; ++t)
-        if (lo >= t_lo[t] && lo < t_hi[t]) issue_s(t, 0);
-      commit(&bars->kv_empty[0]);
-      for (int jj = 0; jj < n_kv; ++jj) {
-        const int j = lo + jj;
-        const int uv = 2 * jj + 1, uk = 2 * jj + 2;
-        const bool next = jj + 1 < n_kv;
-        sync_stage(uv);
-#pragma unroll
-        for (int t = 0; t < kQTiles; ++t) {
-          if (j >= t_lo[t] && j < t_hi[t]) {
-            nb_sync(kNbP + t, kNbPCount);
-            tc_fence_after_sync();
-            issue_pv(t, uv);
-            ++np[t];
+      if (dual) {  // key tile jj belongs to stream jj & 1; S runs one tile ahead
+        issue_s(0, 0);
+        commit(&bars->kv_empty[0]);
+        for (int jj = 0; jj < n_kv; ++jj) {
+          const int t = jj & 1, uv = 2 * jj + 1, uk = 2 * jj + 2;
+          if (jj + 1 < n_kv) {
+            sync_stage(uk);
+            issue_s(t ^ 1, uk);
+            commit(&bars->kv_empty[uk % kStages]);
           }
-          if (next) {
-            if (t == 0) sync_stage(uk);
-            if (j + 1 >= t_lo[t] && j + 1 < t_hi[t]) issue_s(t, uk);
-          }
+          sync_stage(uv);
+          nb_sync(kNbP + t, kNbPCount);
+          tc_fence_after_sync();
+          issue_pv(t, uv, jj > 1);
+          commit(&bars->kv_empty[uv % kStages]);
         }
-        commit(&bars->kv_empty[uv % kStages]);
-        if (next) commit(&bars->kv_empty[uk % kStages]);
+      } else {
+#pragma unroll
+        for (int t = 0; t < kQTiles; ++t)
+          if (lo >= t_lo[t] && lo < t_hi[t]) issue_s(t, 0);
+        commit(&bars->kv_empty[0]);
+        for (int jj = 0; jj < n_kv; ++jj) {
+          const int j = lo + jj;
+          const int uv = 2 * jj + 1, uk = 2 * jj + 2;
+          const bool next = jj + 1 < n_kv;
+          sync_stage(uv);
+#pragma unroll
+          for (int t = 0; t < kQTiles; ++t) {
+            if (j >= t_lo[t] && j < t_hi[t]) {
+              nb_sync(kNbP + t, kNbPCount);
+              tc_fence_after_sync();
+              issue_pv(t, uv, np[t] > 0);
+              ++np[t];
+            }
+            if (next) {
+              if (t == 0) sync_stage(uk);
+              if (j + 1 >= t_lo[t] && j + 1 < t_hi[t]) issue_s(t, uk);
+            }
+          }
+          commit(&bars->kv_empty[uv % kStages]);
+          if (next) commit(&bars->kv_empty[uk % kStages]);
+        }
       }
 #pragma unroll
       for (int t = 0; t < kQTiles; ++t) commit(&bars->o_full[t]);
@@ -523,52 +562,37 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
   } else {
     setmaxnreg_inc<S::kRegsSoftmax>();
     // ------------------------------------------------------------ softmax warpgroups
-    const int t = warp >> 2;
-    const int wrow = t * BM + (warp & 3) * 32;  // this warp's first row in the unit
+    const int t = wt;
     const int row = (warp & 3) * 32 + lane;     // TMEM lane = row in the tile
-    const int r = t * BM + row;                 // row in the unit
+    const int r = wrow + lane;                  // row in the unit
     const bool has_row = r < w.rows;
     float row_scale = 1.f;  // e4m3: undoes the power of two that this thread's row was scaled by
     {
       // This warp's 32 Q rows into swizzled shared memory (rows past the end: zeros). e4m3:
       // scaled by a power of two to fp16.
-      constexpr int kPer = D / 8, kRowsPerIter = 32 / kPer;
       const int piece = lane % kPer;
 #pragma unroll
-      for (int it0 = 0; it0 < 32 / kRowsPerIter; it0 += 8) {  // eight loads in flight
-        uint4 v[8];
+      for (int it = 0; it < kQIters; ++it) {
+        if constexpr (kE4m3) {
+          uint32_t u[4] = {qv[it].x, qv[it].y, qv[it].z, qv[it].w};
+          uint32_t top = 0;
 #pragma unroll
-        for (int it = 0; it < 8; ++it) {
-          const int rr = wrow + (it0 + it) * kRowsPerIter + lane / kPer;
-          v[it] = make_uint4(0, 0, 0, 0);
-          if (rr < w.rows) v[it] = __ldg(reinterpret_cast<const uint4*>(q_row(row_of(rr))) + piece);
+          for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
+#pragma unroll
+          for (int off = kPer / 2; off > 0; off >>= 1)
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+          const int x = imax((int)(top >> 7) - 127, -112);
+          const float up = __uint_as_float((uint32_t)(14 - x + 127) << 23);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            u[e] = pack_f16x2(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xFFFF0000u) * up);
+          qv[it] = make_uint4(u[0], u[1], u[2], u[3]);
+          const int xl = __shfl_sync(0xffffffffu, x, lane % kRowsPerIter * kPer);
+          if (lane / kRowsPerIter == it) row_scale = __uint_as_float((uint32_t)(xl - 14 + 127) << 23);
         }
-#pragma unroll
-        for (int it = 0; it < 8; ++it) {
-          const int rr = wrow + (it0 + it) * kRowsPerIter + lane / kPer;
-          if constexpr (kE4m3) {
-            uint32_t u[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
-#pragma unroll
-            for (int off = kPer / 2; off > 0; off >>= 1)
-              top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const int x = imax((int)(top >> 7) - 127, -112);
-            const float up = __uint_as_float((uint32_t)(14 - x + 127) << 23);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              u[e] = pack_f16x2(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xFFFF0000u) * up);
-            v[it] = make_uint4(u[0], u[1], u[2], u[3]);
-            const int row_in_iter = lane % kRowsPerIter;
-            const int xl = __shfl_sync(0xffffffffu, x, row_in_iter * kPer);
-            if (lane / kRowsPerIter == it0 + it)
-              row_scale = __uint_as_float((uint32_t)(xl - 14 + 127) << 23);
-          }
-          const int rt = rr - t * BM;
-          *reinterpret_cast<uint4*>(smem + L::kQ + t * L::kTile + (piece >> 3) * L::kChunk + rt * 128 +
-                                    (((piece & 7) ^ (rt & 7)) << 4)) = v[it];
-        }
+        const int rt = (warp & 3) * 32 + it * kRowsPerIter + lane / kPer;
+        *reinterpret_cast<uint4*>(smem + L::kQ + t * L::kTile + (piece >> 3) * L::kChunk + rt * 128 +
+                                  (((piece & 7) ^ (rt & 7)) << 4)) = qv[it];
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -583,7 +607,8 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     decode_row_keys(a.mask_kind, a.window, w.span.L, w.span.n, me.i, row_lo, row_hi);
     row_lo = imax(row_lo, w.c0);
     row_hi = imin(row_hi, w.c1);
-    const TileKeys tk = w.tk[t];
+    const bool dual = w.dual;
+    const TileKeys tk = w.tk[dual ? 0 : t];
     const int lo = w.lo;
     const float slope = kAlibi ? alibi_slope(me.h, a.Hq) : 0.f;
     const float unit = kSoftcap ? 1.0f / a.softcap : kPagedLog2e;
@@ -594,7 +619,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     float m_run = -INFINITY, l_run = 0.f;
     int n = 0, e_ref = 0;
     bool live = true;
-    for (int j = tk.lo; j < tk.hi; ++j, ++n) {
+    for (int j = tk.lo + (dual ? t : 0); j < tk.hi; j += dual ? 2 : 1, ++n) {
       int4 info = make_int4(127, 127, 127, 0);
       if (kE4m3 && n > 0 && live) {
         // The tile's scales are there long before its scores; having seen tile j - 1's, this
@@ -730,64 +755,109 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     const bool mma_done = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->o_full[t]), 0, wc));
     const bool have_o = n > 0 && mma_done;
     tc_fence_after_sync();
-    float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-    if (kE4m3) inv *= exp_byte_scale((uint32_t)e_ref);
+    const float vs = kE4m3 ? exp_byte_scale((uint32_t)e_ref) : 1.f;
+    // A dual unit: the second warpgroup leaves its O rows (times their scale), maxima and
+    // sums in the ring, which no one uses any more; the first one merges.
+    float* other = reinterpret_cast<float*>(smem + L::kRing);   // [row][D], pieces swizzled
+    float* other_ml = other + BM * D;                           // [row][2]
+    static_assert(BM * (D + 2) * 4 <= S::kStages * L::kTile, "merge space");
+    float f0 = vs, f1 = 0.f;
+    if (dual) {
+      if (t == 1) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (have_o) {
+            tmem_ld32(tO + c * 32, o);
+            tmem_wait_ld();
+            reg_fence32(o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(other + row * D + (((c * 8 + e) ^ (row & (D / 4 - 1))) << 2)) =
+                make_float4(__uint_as_float(o[4 * e]) * vs, __uint_as_float(o[4 * e + 1]) * vs,
+                            __uint_as_float(o[4 * e + 2]) * vs, __uint_as_float(o[4 * e + 3]) * vs);
+        }
+        *reinterpret_cast<float2*>(other_ml + row * 2) = make_float2(m_run, l_run);
+      }
+      nb_sync(kNbDual, 256);
+      if (t == 0) {
+        const float2 ml = *reinterpret_cast<const float2*>(other_ml + row * 2);
+        const float M = fmaxf(m_run, ml.x);
+        const float g0 = m_run == -INFINITY ? 0.f : ex2_approx(m_run - M);
+        f1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+        f0 = g0 * vs;
+        l_run = l_run * g0 + ml.y * f1;
+        m_run = M;
+      }
+    }
+    const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+    f0 *= inv;
+    f1 *= inv;
     const float l2 = l_run > 0.f ? m_run + log2f(l_run) - (kE4m3 ? kPOffset : 0.f) : -INFINITY;
-    if (a.n_chunks > 1) {
+    const bool mine = !dual || t == 0;  // warp-uniform: this warpgroup writes the rows
+    // 32 columns of the finished row
+    auto load_o = [&](int c, float (&v)[32]) {
+      uint32_t o[32];
+      if (have_o) {
+        tmem_ld32(tO + c * 32, o);
+        tmem_wait_ld();
+        reg_fence32(o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * f0;
+      if (dual && f1 > 0.f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 x = *reinterpret_cast<const float4*>(other + row * D + (((c * 8 + e) ^ (row & (D / 4 - 1))) << 2));
+          v[4 * e] = fmaf(x.x, f1, v[4 * e]);
+          v[4 * e + 1] = fmaf(x.y, f1, v[4 * e + 1]);
+          v[4 * e + 2] = fmaf(x.z, f1, v[4 * e + 2]);
+          v[4 * e + 3] = fmaf(x.w, f1, v[4 * e + 3]);
+        }
+      }
+    };
+    if (mine && a.n_chunks > 1) {
       const long long part = ((long long)w.cc * p.T + me.t) * a.Hq + me.h;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (have_o) {
-          tmem_ld32(tO + c * 32, o);
-          tmem_wait_ld();
-          reg_fence32(o);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        }
+        float v[32];
+        load_o(c, v);
         if (!has_row) continue;
         float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + c * 32);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                               __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+        for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
       }
       if (has_row) a.part_lse[part] = l2;
-    } else {
+    } else if (mine) {
       uint8_t* otile = smem + t * L::kTile;
-      {
-        uint32_t o[D];
-        if (have_o) {  // warp-uniform
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c)
-            tmem_ld32(tO + c * 32, *reinterpret_cast<uint32_t(*)[32]>(o + c * 32));
-          tmem_wait_ld();
+      for (int c = 0; c < D / 32; ++c) {
+        float v[32];
+        load_o(c, v);
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(o + c * 32));
-        } else {
-#pragma unroll
-          for (int e = 0; e < D; ++e) o[e] = 0u;
-        }
-#pragma unroll
-        for (int gc = 0; gc < D / 8; ++gc) {
-          uint4 v;
-          v.x = pack_bf16x2(__uint_as_float(o[8 * gc + 0]) * inv, __uint_as_float(o[8 * gc + 1]) * inv);
-          v.y = pack_bf16x2(__uint_as_float(o[8 * gc + 2]) * inv, __uint_as_float(o[8 * gc + 3]) * inv);
-          v.z = pack_bf16x2(__uint_as_float(o[8 * gc + 4]) * inv, __uint_as_float(o[8 * gc + 5]) * inv);
-          v.w = pack_bf16x2(__uint_as_float(o[8 * gc + 6]) * inv, __uint_as_float(o[8 * gc + 7]) * inv);
-          *reinterpret_cast<uint4*>(otile + (gc >> 3) * L::kChunk + row * 128 + (((gc & 7) ^ (row & 7)) << 4)) = v;
+        for (int e = 0; e < 4; ++e) {
+          const int gc = c * 4 + e;  // 16-byte piece of the row
+          *reinterpret_cast<uint4*>(otile + (gc >> 3) * L::kChunk + row * 128 + (((gc & 7) ^ (row & 7)) << 4)) =
+              make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                         pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
         }
       }
       __syncwarp();
-      constexpr int kPer = D / 8, kRowsPerStore = 32 / kPer;
       const int gc = lane % kPer;
 #pragma unroll 4
-      for (int k = 0; k < 32 / kRowsPerStore; ++k) {
-        const int rt = (warp & 3) * 32 + k * kRowsPerStore + lane / kPer;
+      for (int k = 0; k < kQIters; ++k) {
+        const int rt = (warp & 3) * 32 + k * kRowsPerIter + lane / kPer;
         const uint4 v = *reinterpret_cast<const uint4*>(otile + (gc >> 3) * L::kChunk + rt * 128 +
                                                        (((gc & 7) ^ (rt & 7)) << 4));
-        if (t * BM + rt < w.rows) reinterpret_cast<uint4*>(o_row(row_of(t * BM + rt)))[gc] = v;
+        const int ru = (dual ? 0 : t * BM) + rt;
+        if (ru < w.rows) reinterpret_cast<uint4*>(o_row(row_of(ru)))[gc] = v;
       }
       if (has_row) *lse_row(me) = l2 * kPagedLn2;
     }
@@ -815,7 +885,8 @@ cudaError_t launch_variant(const PagedAttention& a, const PagedMaps& maps, unsig
     return cudaFuncGetAttributes(&attr, kern) == cudaSuccess && attr.numRegs >= S::kRegsLaunch;
   }();
   if (!regs_ok) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
   kern<<<grid, S::kThreads, smem, st>>>(maps.k, maps.v, a);
   return cudaGetLastError();

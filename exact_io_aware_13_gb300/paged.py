@@ -17,7 +17,7 @@ import torch
 
 from . import _lib
 from .attention import (MASK_NONE, SCORE_NONE, _BF16, _F32, _U8, _check_dtypes, _check_tensors,
-                        _params, _ptr, _stream)
+                        _num_sms, _params, _ptr, _stream)
 
 CACHE_BF16, CACHE_E4M3 = 0, 1
 
@@ -51,7 +51,7 @@ def _check_batch(offsets, seq_lens) -> int:
 
 def _rows(t, H: int, d: int, name: str):
     """Pointer and element strides of packed rows [T, H, d], d contiguous."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
     if t.dtype != _BF16:
         raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
@@ -104,25 +104,13 @@ def cache_read(k_cache, v_cache, page_table, offsets, seq_lens, n_tokens: int, *
     return k, v
 
 
-_SMS: dict = {}
-
-
-def _num_sms() -> int:
-    """SM count of the current device (0 without one), looked up once per device."""
-    if not torch.cuda.is_available():
-        return 0
-    dev = torch.cuda.current_device()
-    if dev not in _SMS:
-        _SMS[dev] = torch.cuda.get_device_properties(dev).multi_processor_count
-    return _SMS[dev]
-
-
-def prefill_split_keys(B: int, T: int, Hq: int, Hkv: int, max_new: int, max_seq_len: int,
-                       total_kv_tokens: int, num_sms: Optional[int] = None) -> int:
+def prefill_split_keys(cache_kind: int, B: int, T: int, Hq: int, Hkv: int, max_new: int,
+                       max_seq_len: int, total_kv_tokens: int,
+                       num_sms: Optional[int] = None) -> int:
     """The library's split size for a prefill_paged call (keys per chunk)."""
     return int(_lib.load().attn_prefill_split_keys(
-        int(B), int(T), int(Hq), int(Hkv), int(max_new), int(max_seq_len), int(total_kv_tokens),
-        _num_sms() if num_sms is None else int(num_sms)))
+        int(cache_kind), int(B), int(T), int(Hq), int(Hkv), int(max_new), int(max_seq_len),
+        int(total_kv_tokens), _num_sms() if num_sms is None else int(num_sms)))
 
 
 def prefill_workspace_size(T: int, Hq: int, d: int, max_seq_len: int, split_keys: int) -> int:
@@ -171,7 +159,8 @@ def prefill_paged(q, k_cache, v_cache, page_table, offsets, seq_lens, *, kv_exp=
     if max_new is None:
         max_new = T
     if split_keys is None:
-        split_keys = prefill_split_keys(B, T, Hq, k_cache.shape[1], max_new, max_seq_len,
+        split_keys = prefill_split_keys(CACHE_BF16 if kv_exp is None else CACHE_E4M3, B, T, Hq,
+                                        k_cache.shape[1], max_new, max_seq_len,
                                         total_kv_tokens or B * max_seq_len)
     if scale is None:
         scale = float(d) ** -0.5

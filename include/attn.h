@@ -418,12 +418,14 @@ attn_status attn_prefill_paged(const attn_paged_cache* cache, const void* q,
 size_t attn_prefill_workspace_size(int T, int Hq, int d, int max_seq_len, int split_keys);
 
 /*
- * A split_keys for attn_prefill_paged: all keys in one chunk when the row tiles alone fill
- * the SMs, else chunks of at least 512 keys, as many as fill them over total_kv_tokens (the
- * sum of seq_lens, or B * max_seq_len when unknown). Pure function of its arguments.
+ * A split_keys for attn_prefill_paged over a cache of this kind (ATTN_CACHE_*): all keys in
+ * one chunk when the row tiles alone fill the SMs, else chunks of at least 1024 keys
+ * (256 where max_new * Hq / Hkv <= 32 rows meet an e4m3 cache), several per SM over
+ * total_kv_tokens (the sum of seq_lens, or B * max_seq_len when unknown). Pure function of
+ * its arguments.
  */
-int attn_prefill_split_keys(int B, int T, int Hq, int Hkv, int max_new, int max_seq_len,
-                            long long total_kv_tokens, int num_sms);
+int attn_prefill_split_keys(int cache_kind, int B, int T, int Hq, int Hkv, int max_new,
+                            int max_seq_len, long long total_kv_tokens, int num_sms);
 
 /*
  * attn_decode_paged over an ATTN_CACHE_E4M3 cache: same queries, outputs, masks, score

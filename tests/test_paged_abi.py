@@ -150,13 +150,14 @@ def test_prefill_sizes(lib):
     assert ws(100, 8, 128, 0, 128) == 0 and ws(0, 8, 128, 4096, 128) == 0
     assert ws(101, 8, 128, 4097, 1024) == _round256(4 * 5 * 808) + _round256(4 * 5 * 808 * 128)
     split = lib.attn_prefill_split_keys
-    for args in [(1, 4096, 32, 8, 4096, 32768, 32768, 152), (16, 128, 32, 8, 8, 32768, 16 * 20000, 152),
-                 (1, 1, 8, 8, 1, 100, 100, 152), (3, 70000, 8, 1, 70000, 70000, 99999, 0),
-                 (2, 2, 8, 1, 1, (1 << 31) - 1, 1 << 32, 152)]:
-        keys = split(*args)
-        assert keys >= 128 and keys % 128 == 0, args
-    # the row tiles of one long chunk fill the SMs: no split
-    assert split(1, 4096, 32, 8, 4096, 32768, 32768, 152) == 32768
-    # a few rows over long caches: split
-    assert split(16, 128, 32, 8, 8, 32768, 16 * 20000, 152) < 32768
-    assert split(0, 0, 8, 8, 0, 0, 0, 152) == 128
+    for kind in (0, 1):
+        for args in [(1, 4096, 32, 8, 4096, 32768, 32768, 152), (16, 128, 32, 8, 8, 32768, 16 * 20000, 152),
+                     (1, 1, 8, 8, 1, 100, 100, 152), (3, 70000, 8, 1, 70000, 70000, 99999, 0),
+                     (2, 2, 8, 1, 1, (1 << 31) - 1, 1 << 32, 152), (64, 64, 32, 8, 1, 8192, 64 * 4352, 152)]:
+            keys = split(kind, *args)
+            assert keys >= 128 and keys % 128 == 0, args
+        # the row tiles of one long chunk fill the SMs: no split
+        assert split(kind, 1, 4096, 32, 8, 4096, 32768, 32768, 152) == 32768
+        # a few rows over long caches: split
+        assert split(kind, 16, 128, 32, 8, 8, 32768, 16 * 20000, 152) < 32768
+        assert split(kind, 0, 0, 8, 8, 0, 0, 0, 152) == 128
