@@ -23,6 +23,12 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _current_device() -> int:
+    """torch.cuda.current_device() without its initialisation check, for callers that hold a
+    CUDA tensor already."""
+    return torch._C._cuda_getDevice()
+
+
 def _stream(stream) -> int:
     if stream is None:  # the raw handle: a Stream object per call costs 3 us
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
@@ -97,7 +103,7 @@ def _check_tensors(*ts):
             index = t.get_device()
         elif t.get_device() != index:
             raise ValueError("tensors must all be on one device")
-    if index is not None and index != torch.cuda.current_device():
+    if index is not None and index != _current_device():
         raise ValueError(f"tensors are on cuda:{index}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
 

@@ -19,7 +19,14 @@ constexpr int kWarps = 8;          // warps per CTA, each with its own row slice
 constexpr int kPieces = 4;         // bf16 pieces of 16 bytes per lane
 constexpr int kChunksPerWarp = 32 * kPieces;
 
-// Largest finite magnitude of 8 bf16 values, as bf16 bits (their order is the numbers').
+// Largest magnitude of 8 bf16 values, as bf16 bits (their order is the numbers'; infinities
+// and NaN come out as 0x7F80 and above).
+__device__ __forceinline__ uint32_t amax8(const uint4& w) {
+  const uint32_t k = 0x7FFF7FFFu;
+  const uint32_t m = __vmaxu2(__vmaxu2(w.x & k, w.y & k), __vmaxu2(w.z & k, w.w & k));
+  return max(m & 0xFFFFu, m >> 16);
+}
+// The same over the finite values alone.
 __device__ __forceinline__ uint32_t finite_amax8(const uint4& w) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   uint32_t m = 0;
@@ -41,18 +48,20 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
 }
 
 // Eight bf16 values times inv (a power of two) to eight e4m3 codes, lowest element first.
+// (A value that is not finite has become NaN: an infinity would saturate to the largest
+// finite code.)
 __device__ __forceinline__ uint2 encode8(const uint4& w, float inv) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float lo = __uint_as_float(u[i] << 16), hi = __uint_as_float(u[i] & 0xFFFF0000u);
-    // an infinity would saturate to the largest finite code
-    lo = isinf(lo) ? __uint_as_float(0x7FC00000u) : lo * inv;
-    hi = isinf(hi) ? __uint_as_float(0x7FC00000u) : hi * inv;
-    c[i] = pack_e4m3x2(lo, hi);
-  }
+  for (int i = 0; i < 4; ++i)
+    c[i] = pack_e4m3x2(__uint_as_float(u[i] << 16) * inv, __uint_as_float(u[i] & 0xFFFF0000u) * inv);
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+__device__ __forceinline__ uint32_t nonfinite_to_nan(uint32_t u) {
+  const uint32_t lo = (u & 0x7F80u) == 0x7F80u ? 0x7FC0u : u & 0xFFFFu;
+  const uint32_t hi = (u & 0x7F800000u) == 0x7F800000u ? 0x7FC00000u : u & 0xFFFF0000u;
+  return lo | hi;
 }
 
 struct CopyArgs {
@@ -81,9 +90,25 @@ __device__ __forceinline__ bool locate(const CopyArgs& a, int lane, WarpRow& r) 
   return true;
 }
 
+// The 16-byte bf16 pieces of a warp's slice: lane l owns piece l % (D / 8) of (tensor, head)
+// rows l / (D / 8), + 32 / (D / 8), ...; rows 0 .. Hkv - 1 are K heads, then come V heads.
+template <int D>
+struct Pieces {
+  static constexpr int kPer = D / 8;
+  int piece, row0, Hkv;
+  __device__ __forceinline__ Pieces(int c0, int lane, int hkv)
+      : piece(lane % kPer), row0((c0 + lane) / kPer), Hkv(hkv) {}
+  __device__ __forceinline__ bool get(int j, int& head, bool& is_v) const {
+    const int r = row0 + j * (32 / kPer);
+    is_v = r >= Hkv;
+    head = is_v ? r - Hkv : r;
+    return r < 2 * Hkv;
+  }
+};
+
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(const CopyArgs a) {
-  constexpr int kPer = D / 8;  // 16-byte pieces per (head, K or V) row: 8 or 16 lanes
+  constexpr int kPer = D / 8;  // lanes per (tensor, head) row: 8 or 16
   const PagedProblem& p = a.p;
   const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0) report_bad_spans(p);
@@ -92,18 +117,18 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(const CopyArgs
   r.t = (int)(unit / a.slices);
   if (r.t >= p.T) return;
   r.c0 = (int)(unit % a.slices) * kChunksPerWarp;
-  const int per_tensor = p.Hkv * kPer;
+  const Pieces<D> pieces(r.c0, lane, p.Hkv);
+  const __nv_bfloat16* k = a.in[0].p + r.t * a.in[0].token_stride + pieces.piece * 8;
+  const __nv_bfloat16* v = a.in[1].p + r.t * a.in[1].token_stride + pieces.piece * 8;
   uint4 w[kPieces];
 #pragma unroll
-  for (int j = 0; j < kPieces; ++j) {  // K heads, then V heads
-    const int c = r.c0 + j * 32 + lane;
-    const bool is_v = c >= per_tensor;
-    const int cc = is_v ? c - per_tensor : c;
-    const RowView& in = a.in[is_v];
+  for (int j = 0; j < kPieces; ++j) {
+    int head;
+    bool is_v;
     w[j] = make_uint4(0, 0, 0, 0);
-    if (c < 2 * per_tensor)
-      w[j] = __ldg(reinterpret_cast<const uint4*>(in.p + (long long)r.t * in.token_stride +
-                                                  (long long)(cc / kPer) * in.head_stride) + cc % kPer);
+    if (pieces.get(j, head, is_v))
+      w[j] = __ldg(reinterpret_cast<const uint4*>((is_v ? v : k) +
+                                                  head * (is_v ? a.in[1].head_stride : a.in[0].head_stride)));
   }
   if (!locate(a, lane, r)) return;
   const long long row0 = cache_row(p, r.b, r.pos, 0);
@@ -111,25 +136,34 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(const CopyArgs
     if (lane == 0) atomicOr(p.status, DEV_BAD_INPUT);
     return;
   }
+  constexpr int kBytes = kE4m3 ? 8 : 16;  // of a piece in the cache
+  uint8_t* kc = static_cast<uint8_t*>(p.k_cache) + row0 * (kPer * kBytes) + pieces.piece * kBytes;
+  uint8_t* vc = static_cast<uint8_t*>(p.v_cache) + row0 * (kPer * kBytes) + pieces.piece * kBytes;
 #pragma unroll
   for (int j = 0; j < kPieces; ++j) {
-    const int c = r.c0 + j * 32 + lane;
-    const bool is_v = c >= per_tensor;
-    const int cc = is_v ? c - per_tensor : c;
-    const int head = cc / kPer, piece = cc % kPer;
-    const long long row = row0 + (long long)head * p.page_size;
-    void* base = is_v ? p.v_cache : p.k_cache;
+    int head;
+    bool is_v;
+    const bool ok = pieces.get(j, head, is_v);
+    const long long down = (long long)head * p.page_size;  // cache rows from head 0's
+    uint8_t* dst = (is_v ? vc : kc) + down * (kPer * kBytes);
     if constexpr (!kE4m3) {
-      if (c < 2 * per_tensor) reinterpret_cast<uint4*>(base)[row * kPer + piece] = w[j];
+      if (ok) *reinterpret_cast<uint4*>(dst) = w[j];
     } else {
-      uint32_t m = finite_amax8(w[j]);  // the kPer lanes of one head's row agree on it
+      uint32_t m = amax8(w[j]);  // the kPer lanes of one row agree on it
 #pragma unroll
       for (int off = kPer / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+      if (__any_sync(0xffffffffu, m >= 0x7F80u)) {
+        m = finite_amax8(w[j]);
+#pragma unroll
+        for (int off = kPer / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+        w[j] = make_uint4(nonfinite_to_nan(w[j].x), nonfinite_to_nan(w[j].y), nonfinite_to_nan(w[j].z),
+                          nonfinite_to_nan(w[j].w));
+      }
       const uint32_t byte = scale_byte(m);
       const float inv = __uint_as_float((254u - byte) << 23);  // 2^-(byte - 127)
-      if (c < 2 * per_tensor) {
-        reinterpret_cast<uint2*>(base)[row * kPer + piece] = encode8(w[j], inv);
-        if (piece == 0) p.kv_exp[row * 2 + is_v] = (uint8_t)byte;
+      if (ok) {
+        *reinterpret_cast<uint2*>(dst) = encode8(w[j], inv);
+        if (pieces.piece == 0) p.kv_exp[(row0 + down) * 2 + is_v] = (uint8_t)byte;
       }
     }
   }
@@ -152,34 +186,36 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(const CopyArgs 
     if (lane == 0) atomicOr(p.status, DEV_BAD_INPUT);
     return;
   }
-  const int per_tensor = p.Hkv * kPer;
+  const Pieces<D> pieces(r.c0, lane, p.Hkv);
+  constexpr int kBytes = kE4m3 ? 8 : 16;
+  const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache) + row0 * (kPer * kBytes) + pieces.piece * kBytes;
+  const uint8_t* vc = static_cast<const uint8_t*>(p.v_cache) + row0 * (kPer * kBytes) + pieces.piece * kBytes;
   uint4 w[kPieces];
   uint32_t byte[kPieces];
 #pragma unroll
   for (int j = 0; j < kPieces; ++j) {
-    const int c = r.c0 + j * 32 + lane;
-    const bool is_v = c >= per_tensor;
-    const int cc = is_v ? c - per_tensor : c;
-    const long long row = row0 + (long long)(cc / kPer) * p.page_size;
-    const void* base = is_v ? p.v_cache : p.k_cache;
+    int head;
+    bool is_v;
     w[j] = make_uint4(0, 0, 0, 0);
     byte[j] = 127;
-    if (c >= 2 * per_tensor) continue;
+    if (!pieces.get(j, head, is_v)) continue;
+    const long long down = (long long)head * p.page_size;
+    const uint8_t* src = (is_v ? vc : kc) + down * (kPer * kBytes);
     if constexpr (kE4m3) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(base) + row * kPer + cc % kPer);
-      w[j].x = v.x;
-      w[j].y = v.y;
-      byte[j] = __ldg(p.kv_exp + row * 2 + is_v);
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+      w[j].x = x.x;
+      w[j].y = x.y;
+      byte[j] = __ldg(p.kv_exp + (row0 + down) * 2 + is_v);
     } else {
-      w[j] = __ldg(reinterpret_cast<const uint4*>(base) + row * kPer + cc % kPer);
+      w[j] = __ldg(reinterpret_cast<const uint4*>(src));
     }
   }
+  const long long out_row = (long long)r.t * p.Hkv;
 #pragma unroll
   for (int j = 0; j < kPieces; ++j) {
-    const int c = r.c0 + j * 32 + lane;
-    if (c >= 2 * per_tensor) continue;
-    const bool is_v = c >= per_tensor;
-    const int cc = is_v ? c - per_tensor : c;
+    int head;
+    bool is_v;
+    if (!pieces.get(j, head, is_v)) continue;
     if constexpr (kE4m3) {
       const float s = exp_byte_scale(byte[j]);
       const uint32_t codes[4] = {w[j].x, w[j].x >> 16, w[j].y, w[j].y >> 16};
@@ -191,7 +227,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(const CopyArgs 
       }
       w[j] = make_uint4(u[0], u[1], u[2], u[3]);
     }
-    reinterpret_cast<uint4*>(a.out[is_v])[((long long)r.t * p.Hkv) * kPer + cc] = w[j];
+    reinterpret_cast<uint4*>(is_v ? a.out[1] : a.out[0])[(out_row + head) * kPer + pieces.piece] = w[j];
   }
 }
 

@@ -17,13 +17,12 @@ import torch
 
 from . import _lib
 from .attention import (MASK_NONE, SCORE_NONE, _BF16, _F32, _U8, _check_dtypes, _check_tensors,
-                        _num_sms, _params, _ptr, _stream)
+                        _current_device, _num_sms, _params, _ptr, _stream)
 
 CACHE_BF16, CACHE_E4M3 = 0, 1
 
 
 def _cache(k_cache, v_cache, page_table, kv_exp, B: int) -> _lib.PagedCache:
-    _check_tensors(k_cache, v_cache, page_table, kv_exp)
     kind = _BF16 if kv_exp is None else _U8
     _check_dtypes((k_cache, kind, "k_cache"), (v_cache, kind, "v_cache"), (kv_exp, _U8, "kv_exp"),
                   (page_table, torch.int32, "page_table"))
@@ -42,7 +41,6 @@ def _cache(k_cache, v_cache, page_table, kv_exp, B: int) -> _lib.PagedCache:
 
 
 def _check_batch(offsets, seq_lens) -> int:
-    _check_tensors(offsets, seq_lens)
     _check_dtypes((offsets, torch.int32, "offsets"), (seq_lens, torch.int32, "seq_lens"))
     if seq_lens.dim() != 1 or offsets.dim() != 1 or offsets.shape[0] != seq_lens.shape[0] + 1:
         raise ValueError("offsets must be [B + 1] and seq_lens [B]")
@@ -51,7 +49,7 @@ def _check_batch(offsets, seq_lens) -> int:
 
 def _rows(t, H: int, d: int, name: str):
     """Pointer and element strides of packed rows [T, H, d], d contiguous."""
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != _current_device():
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
     if t.dtype != _BF16:
         raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
@@ -67,6 +65,7 @@ def cache_write(k, v, k_cache, v_cache, page_table, offsets, seq_lens, *, kv_exp
     """Write the new tokens' K and V rows (bf16 [T, Hkv, d], any token and head stride that
     is a multiple of 8) into the cache: as they are, or with kv_exp as e4m3 codes under the
     smallest power-of-two scale that holds each row."""
+    _check_tensors(k_cache, v_cache, kv_exp, page_table, offsets, seq_lens)
     B = _check_batch(offsets, seq_lens)
     cache = _cache(k_cache, v_cache, page_table, kv_exp, B)
     kp, kt, kh = _rows(k, cache.Hkv, cache.d, "k")
@@ -82,9 +81,9 @@ def cache_read_into(k_cache, v_cache, page_table, offsets, seq_lens, k, v, *, kv
                     stream=None) -> None:
     """Read the newest tokens of each sequence into k and v (bf16 [T, Hkv, d], contiguous);
     rows behind offsets[B] keep what they held."""
+    _check_tensors(k_cache, v_cache, kv_exp, page_table, offsets, seq_lens, k, v)
     B = _check_batch(offsets, seq_lens)
     cache = _cache(k_cache, v_cache, page_table, kv_exp, B)
-    _check_tensors(k, v)
     _check_dtypes((k, _BF16, "k"), (v, _BF16, "v"))
     if k.dim() != 3 or tuple(k.shape[1:]) != (cache.Hkv, cache.d) or v.shape != k.shape:
         raise ValueError(f"k and v must be [T, {cache.Hkv}, {cache.d}]")
@@ -125,13 +124,13 @@ def prefill_paged_into(q, k_cache, v_cache, page_table, offsets, seq_lens, o, ls
     """attn_prefill_paged on caller-owned tensors: q bf16 [T, Hq, d] (any token and head
     stride that is a multiple of 8), o bf16 [T, Hq, d] and lse fp32 [T, Hq] contiguous. Rows
     behind offsets[B] keep what they held."""
+    _check_tensors(k_cache, v_cache, kv_exp, page_table, offsets, seq_lens, o, lse, workspace)
     B = _check_batch(offsets, seq_lens)
     cache = _cache(k_cache, v_cache, page_table, kv_exp, B)
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, d]")
     T, Hq, d = q.shape
     qp, qt, qh = _rows(q, Hq, cache.d, "q")
-    _check_tensors(o, lse, workspace)
     _check_dtypes((o, _BF16, "o"), (lse, _F32, "lse"))
     if o.shape != q.shape or lse.shape != q.shape[:2]:
         raise ValueError("o must be [T, Hq, d] and lse [T, Hq]")
