@@ -6,6 +6,7 @@ of the computation runs in the library's CUDA kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -335,14 +336,25 @@ def decode_split_keys(B: int, Hq: int, Hkv: int, Nq: int, total_kv_tokens: int,
     """The library's split size for a decode call (keys per chunk)."""
     if num_sms is None:
         num_sms = _num_sms()
-    return int(_lib.load().attn_decode_split_keys(int(B), int(Hq), int(Hkv), int(Nq),
-                                                  int(total_kv_tokens), int(num_sms)))
+    return _decode_split_keys(int(B), int(Hq), int(Hkv), int(Nq), int(total_kv_tokens),
+                              int(num_sms))
+
+
+# Pure functions of their numbers: a step that asks again with the same ones skips the calls.
+@functools.lru_cache(maxsize=1024)
+def _decode_split_keys(*args: int) -> int:
+    return int(_lib.load().attn_decode_split_keys(*args))
+
+
+@functools.lru_cache(maxsize=1024)
+def _decode_workspace_size(*args: int) -> int:
+    return int(_lib.load().attn_decode_workspace_size(*args))
 
 
 def decode_workspace_size(B: int, Hq: int, Hkv: int, Nq: int, d: int, max_seq_len: int,
                           split_keys: int) -> int:
-    return int(_lib.load().attn_decode_workspace_size(int(B), int(Hq), int(Hkv), int(Nq), int(d),
-                                                      int(max_seq_len), int(split_keys)))
+    return _decode_workspace_size(int(B), int(Hq), int(Hkv), int(Nq), int(d), int(max_seq_len),
+                                  int(split_keys))
 
 
 def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspace, *,
@@ -358,15 +370,17 @@ def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspa
     _check_tensors(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspace, kv_exp)
     _check_dtypes((q, _BF16, "q"), (k_cache, kind, "k_cache"), (v_cache, kind, "v_cache"),
                   (o, _BF16, "o"), (lse, _F32, "lse"), (kv_exp, _U8, "kv_exp"))
-    if q.dim() != 4 or tuple(o.shape) != tuple(q.shape) or tuple(lse.shape) != tuple(q.shape[:-1]):
+    shape = q.shape
+    if len(shape) != 4 or o.shape != shape or lse.shape != shape[:-1]:
         raise ValueError("q, o must be [B, Hq, Nq, d] and lse [B, Hq, Nq]")
-    B, Hq, Nq, d = q.shape
-    num_pages, Hkv, page_size, dk = k_cache.shape
-    if dk != d or tuple(v_cache.shape) != tuple(k_cache.shape):
+    B, Hq, Nq, d = shape
+    num_pages, Hkv, page_size, dk = cache_shape = k_cache.shape
+    if dk != d or v_cache.shape != cache_shape:
         raise ValueError("k_cache and v_cache must be [pages, Hkv, page_size, d]")
     if page_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise ValueError("page_table and seq_lens must be int32")
-    if page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.shape != (B,):
+    table_shape = page_table.shape
+    if len(table_shape) != 2 or table_shape[0] != B or seq_lens.shape != (B,):
         raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
     if kv_exp is not None and tuple(kv_exp.shape) != (num_pages, Hkv, page_size, 2):
         raise ValueError("kv_exp must be [pages, Hkv, page_size, 2]")
@@ -375,18 +389,17 @@ def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspa
     if kv_exp is not None:
         cache = _lib.PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), kv_exp.data_ptr(),
                                 page_table.data_ptr(), 1, num_pages, Hkv, page_size, d,
-                                page_table.shape[1])
+                                table_shape[1])
         _lib.check(_lib.load().attn_decode_paged_e4m3(
             ctypes.byref(cache), _ptr(q), _ptr(seq_lens), _ptr(o), _ptr(lse), B, Hq, Nq,
-            int(max_seq_len), int(split_keys), ctypes.c_float(scale), mask_kind, mp, score_kind,
-            sp, _ptr(workspace), ctypes.c_size_t(ws_bytes), _stream(stream)),
-            "attn_decode_paged_e4m3")
+            int(max_seq_len), int(split_keys), scale, mask_kind, mp, score_kind, sp,
+            _ptr(workspace), ws_bytes, _stream(stream)), "attn_decode_paged_e4m3")
         return
     st = _lib.load().attn_decode_paged(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(o),
-        _ptr(lse), B, Hq, Hkv, Nq, d, num_pages, page_size, page_table.shape[1],
-        int(max_seq_len), int(split_keys), ctypes.c_float(scale), mask_kind, mp, score_kind, sp,
-        _ptr(workspace), ctypes.c_size_t(ws_bytes), _stream(stream))
+        _ptr(lse), B, Hq, Hkv, Nq, d, num_pages, page_size, table_shape[1],
+        int(max_seq_len), int(split_keys), scale, mask_kind, mp, score_kind, sp,
+        _ptr(workspace), ws_bytes, _stream(stream))
     _lib.check(st, "attn_decode_paged")
 
 
@@ -398,17 +411,18 @@ def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, max_seq_len: Opti
     the page table's capacity; split_keys to the library's choice for total_kv_tokens
     (default B * max_seq_len). kv_exp selects an e4m3 cache."""
     B, Hq, Nq, d = q.shape
-    Hkv, page_size = k_cache.shape[1], k_cache.shape[2]
+    _, Hkv, page_size, _ = k_cache.shape
     if max_seq_len is None:
         max_seq_len = page_table.shape[1] * page_size
     if split_keys is None:
         split_keys = decode_split_keys(B, Hq, Hkv, Nq, total_kv_tokens or B * max_seq_len)
     if scale is None:
         scale = float(d) ** -0.5
-    o = torch.empty((B, Hq, Nq, d), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
+    device = q.device
+    o = torch.empty((B, Hq, Nq, d), dtype=_BF16, device=device)
+    lse = torch.empty((B, Hq, Nq), dtype=_F32, device=device)
     nbytes = decode_workspace_size(B, Hq, Hkv, Nq, d, max_seq_len, split_keys)
-    ws = torch.empty((nbytes,), dtype=torch.uint8, device=q.device) if nbytes else None
+    ws = torch.empty((nbytes,), dtype=_U8, device=device) if nbytes else None
     decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, ws,
                       max_seq_len=max_seq_len, split_keys=split_keys, scale=scale,
                       mask_kind=mask_kind, window=window, score_kind=score_kind, softcap=softcap,

@@ -55,9 +55,9 @@ struct Shape {
   // launch gives kThreads x kRegsLaunch; the split must not exceed it (launch_variant checks
   // what the compiler used).
   static constexpr int kRegsLaunch = kE4m3 ? 128 : 168;
-  static constexpr int kRegsSoftmax = kE4m3 ? 184 : 208;
-  static constexpr int kRegsOther = 88;
-  static constexpr int kRegsConvert = 56;
+  static constexpr int kRegsSoftmax = kE4m3 ? 168 : 200;
+  static constexpr int kRegsOther = kE4m3 ? 88 : 104;
+  static constexpr int kRegsConvert = 88;
   static_assert(256 * kRegsSoftmax + 128 * kRegsOther + (kE4m3 ? 128 * kRegsConvert : 0) <=
                     kThreads * kRegsLaunch,
                 "register pool");

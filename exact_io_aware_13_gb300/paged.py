@@ -11,6 +11,7 @@ each token's K and V scale; passing kv_exp selects it.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -26,25 +27,27 @@ def _cache(k_cache, v_cache, page_table, kv_exp, B: int) -> _lib.PagedCache:
     kind = _BF16 if kv_exp is None else _U8
     _check_dtypes((k_cache, kind, "k_cache"), (v_cache, kind, "v_cache"), (kv_exp, _U8, "kv_exp"),
                   (page_table, torch.int32, "page_table"))
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    shape, table_shape = k_cache.shape, page_table.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [pages, Hkv, page_size, d]")
-    pages, Hkv, page_size, d = k_cache.shape
-    if kv_exp is not None and tuple(kv_exp.shape) != (pages, Hkv, page_size, 2):
+    pages, Hkv, page_size, d = shape
+    if kv_exp is not None and kv_exp.shape != (pages, Hkv, page_size, 2):
         raise ValueError(f"kv_exp must have shape {(pages, Hkv, page_size, 2)}, got "
                          f"{tuple(kv_exp.shape)}")
-    if page_table.dim() != 2 or page_table.shape[0] != B:
+    if len(table_shape) != 2 or table_shape[0] != B:
         raise ValueError("page_table must be [B, max_pages]")
     return _lib.PagedCache(k_cache.data_ptr(), v_cache.data_ptr(),
                            None if kv_exp is None else kv_exp.data_ptr(), page_table.data_ptr(),
                            CACHE_BF16 if kv_exp is None else CACHE_E4M3, pages, Hkv, page_size, d,
-                           page_table.shape[1])
+                           table_shape[1])
 
 
 def _check_batch(offsets, seq_lens) -> int:
     _check_dtypes((offsets, torch.int32, "offsets"), (seq_lens, torch.int32, "seq_lens"))
-    if seq_lens.dim() != 1 or offsets.dim() != 1 or offsets.shape[0] != seq_lens.shape[0] + 1:
+    B = seq_lens.numel()
+    if seq_lens.dim() != 1 or offsets.shape != (B + 1,):
         raise ValueError("offsets must be [B + 1] and seq_lens [B]")
-    return seq_lens.shape[0]
+    return B
 
 
 def _rows(t, H: int, d: int, name: str):
@@ -53,11 +56,13 @@ def _rows(t, H: int, d: int, name: str):
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
     if t.dtype != _BF16:
         raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != d:
-        raise ValueError(f"{name} must be [T, {H}, {d}], got {tuple(t.shape)}")
-    if t.stride(2) != 1:
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != H or shape[2] != d:
+        raise ValueError(f"{name} must be [T, {H}, {d}], got {tuple(shape)}")
+    token, head, one = t.stride()
+    if one != 1:
         raise ValueError(f"{name} must be contiguous along d")
-    return (_ptr(t), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if H > 1 else 0)
+    return t.data_ptr(), token if shape[0] > 1 else 0, head if H > 1 else 0
 
 
 def cache_write(k, v, k_cache, v_cache, page_table, offsets, seq_lens, *, kv_exp=None,
@@ -107,14 +112,24 @@ def prefill_split_keys(cache_kind: int, B: int, T: int, Hq: int, Hkv: int, max_n
                        max_seq_len: int, total_kv_tokens: int,
                        num_sms: Optional[int] = None) -> int:
     """The library's split size for a prefill_paged call (keys per chunk)."""
-    return int(_lib.load().attn_prefill_split_keys(
-        int(cache_kind), int(B), int(T), int(Hq), int(Hkv), int(max_new), int(max_seq_len),
-        int(total_kv_tokens), _num_sms() if num_sms is None else int(num_sms)))
+    return _prefill_split_keys(int(cache_kind), int(B), int(T), int(Hq), int(Hkv), int(max_new),
+                               int(max_seq_len), int(total_kv_tokens),
+                               _num_sms() if num_sms is None else int(num_sms))
+
+
+# Pure functions of their numbers: a step that asks again with the same ones skips the calls.
+@functools.lru_cache(maxsize=1024)
+def _prefill_split_keys(*args: int) -> int:
+    return int(_lib.load().attn_prefill_split_keys(*args))
+
+
+@functools.lru_cache(maxsize=1024)
+def _prefill_workspace_size(*args: int) -> int:
+    return int(_lib.load().attn_prefill_workspace_size(*args))
 
 
 def prefill_workspace_size(T: int, Hq: int, d: int, max_seq_len: int, split_keys: int) -> int:
-    return int(_lib.load().attn_prefill_workspace_size(int(T), int(Hq), int(d), int(max_seq_len),
-                                                       int(split_keys)))
+    return _prefill_workspace_size(int(T), int(Hq), int(d), int(max_seq_len), int(split_keys))
 
 
 def prefill_paged_into(q, k_cache, v_cache, page_table, offsets, seq_lens, o, lse, workspace, *,
@@ -163,10 +178,11 @@ def prefill_paged(q, k_cache, v_cache, page_table, offsets, seq_lens, *, kv_exp=
                                         total_kv_tokens or B * max_seq_len)
     if scale is None:
         scale = float(d) ** -0.5
-    o = torch.empty((T, Hq, d), dtype=_BF16, device=q.device)
-    lse = torch.empty((T, Hq), dtype=_F32, device=q.device)
+    device = q.device
+    o = torch.empty((T, Hq, d), dtype=_BF16, device=device)
+    lse = torch.empty((T, Hq), dtype=_F32, device=device)
     nbytes = prefill_workspace_size(T, Hq, d, max_seq_len, split_keys)
-    ws = torch.empty((nbytes,), dtype=_U8, device=q.device) if nbytes else None
+    ws = torch.empty((nbytes,), dtype=_U8, device=device) if nbytes else None
     prefill_paged_into(q, k_cache, v_cache, page_table, offsets, seq_lens, o, lse, ws,
                        max_new=max_new, max_seq_len=max_seq_len, split_keys=split_keys,
                        scale=scale, kv_exp=kv_exp, mask_kind=mask_kind, window=window,
