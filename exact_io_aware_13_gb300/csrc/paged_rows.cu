@@ -67,11 +67,6 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -96,14 +91,6 @@ __device__ __forceinline__ uint32_t piece_offset(int row, int piece) {
   return D == 128 ? row * 128 + ((piece ^ (row & 7)) << 4)
                   : row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
 }
-// Four e4m3 codes to two half2 words.
-__device__ __forceinline__ void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"
-      " cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-
 // NT: 8-row groups per warp; RG: warps that share a key tile, each with NT * 8 rows.
 template <int D, int NT, int RG>
 __global__ void __launch_bounds__(kWarps * 32, 3)

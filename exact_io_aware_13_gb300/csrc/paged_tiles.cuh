@@ -48,8 +48,10 @@ constexpr int kMaxDown = 8;          // e4m3: a V tile's exponent is at least E_
 template <bool kE4m3>
 struct Shape {
   static constexpr int kThreads = kE4m3 ? 512 : 384;
-  static constexpr int kStages = 4;                   // operand tiles in the ring
-  static constexpr int kCodeStages = kE4m3 ? 2 : 0;   // code tiles waiting for conversion
+  static constexpr int kStages = kE4m3 ? 3 : 4;       // operand tiles in the ring
+  // Code tiles on their way or waiting for conversion. A dual unit streams its keys as fast
+  // as HBM gives them: it adds the second query tile's room (two code tiles) to its ring.
+  static constexpr int kCodeStages = kE4m3 ? 4 : 0, kCodeStagesDual = kE4m3 ? 6 : 0;
   static constexpr uint32_t kNbKvCount = kE4m3 ? 160 : 64;
   // Registers: softmax threads hold 128 scores and the row state, the others little. The
   // launch gives kThreads x kRegsLaunch; the split must not exceed it (launch_variant checks
@@ -107,8 +109,8 @@ struct Bars {
   uint64_t kv_empty[4];
   uint64_t s_full[kQTiles];
   uint64_t o_full[kQTiles];
-  uint64_t code_full[2];
-  uint64_t code_empty[2];
+  uint64_t code_full[6];
+  uint64_t code_empty[6];
   uint64_t info_full[kInfo];
   int4 info[kInfo];     // E_K, E_V, E_ref of key tile j (slot j % kInfo)
   uint32_t tmem_base;
@@ -122,11 +124,6 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
   return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -221,7 +218,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       mbar_init(smem_u32(&bars->kv_full[s]), 1);
       mbar_init(smem_u32(&bars->kv_empty[s]), 1);
     }
-    for (int s = 0; s < S::kCodeStages; ++s) {
+    for (int s = 0; s < S::kCodeStagesDual; ++s) {
       mbar_init(smem_u32(&bars->code_full[s]), 1);
       mbar_init(smem_u32(&bars->code_empty[s]), 4);  // one arrival per converter warp
     }
@@ -267,6 +264,12 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     return;
   }
 
+  // Code stage s (e4m3): the ones past kCodeStages lie in the second query tile's room.
+  auto code_tile = [&](int s) {
+    return smem + (s < S::kCodeStages ? L::kCodes + s * L::kCodeTile
+                                      : L::kQ + L::kTile + (s - S::kCodeStages) * L::kCodeTile);
+  };
+
   WaitCtx wc{&bars->abort_flag, p.status};
   // The softmax warps request their Q rows before the loader starts: behind its stream of
   // keys they would take several times as long.
@@ -294,23 +297,32 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
   if (kE4m3 && warp >= kConvWarp) {
     setmaxnreg_dec<S::kRegsConvert>();
     // ------------------------------------------------------------ converters (e4m3)
-    // A warp converts 32 of a tile's rows, 512 codes at a time. The eight lanes of a
-    // shared-memory phase read 128 contiguous bytes of codes; at d = 128 those are one row,
-    // whose pieces q and q + 4 go to the same 16-byte columns of the two operand slabs, so
-    // lanes with q >= 4 convert and write their second eight codes first.
-    constexpr int kRowsPerIter = 512 / D;            // 4 or 8
-    constexpr int kPieces = D / 16;
+    // A warp converts 32 of a tile's rows, 256 codes at a time: a lane turns eight codes (one
+    // 8-byte read) into one 16-byte column of the operand tile, so that reads and writes are
+    // free of bank conflicts as they come. The converters share the issue slots of the
+    // softmax warps, whose latency sets the pace: every instruction here counts.
+    constexpr int kGroups = D / 8, kRowsIter = 32 / kGroups, kIters = 32 / kRowsIter;
     const int cw = warp - kConvWarp;
     const int lo = w.lo, n_kv = w.hi - w.lo, L_seq = w.span.L;
-    const int sub = lane / kPieces, piece = lane % kPieces;
-    const bool swap = D == 128 ? piece >= 4 : sub & 1;
+    const int grp = lane % kGroups, sub = lane / kGroups;
+    const int row0 = cw * 32 + sub;
+    // swizzled column of this lane's write in iteration it: a function of it % kTurns
+    constexpr int kTurns = 8 / kRowsIter;
+    int column[kTurns];
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k)
+      column[k] = (grp >> 3) * L::kChunk + row0 * 128 + (((grp & 7) ^ ((sub + k * kRowsIter) & 7)) << 4);
+    const int depth = w.dual ? S::kCodeStagesDual : S::kCodeStages;
     bool live = true;
-    int e_ref = 0, e_k = 0, e_v = 0;
+    int e_ref = 0, e_k = 0, e_v = 0, cs = -1;
+    uint32_t code_parity = 1;
     for (int u = 0; u < 2 * n_kv; ++u) {
-      const int cs = u % 2, s = u % kStages, jj = u >> 1;
+      if (++cs == depth) cs = 0;
+      if (cs == 0) code_parity ^= 1;
+      const int s = u % kStages, jj = u >> 1;
       const bool is_v = u & 1;
       if (live)
-        live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->code_full[cs]), (u / 2) & 1, wc));
+        live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->code_full[cs]), code_parity, wc));
       const int valid = imin(BN, L_seq - (lo + jj) * BN);
       const uint8_t* ex = smem + L::kExp + (jj % kInfo) * BN * 2;
       if (live && !is_v) {  // the tile's exponents: lane reads rows 4 lane .. + 3 (K low byte)
@@ -340,39 +352,27 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
         bars->info[jj % kInfo] = make_int4(e_k, e_v, e_ref, 0);
         mbar_arrive(smem_u32(&bars->info_full[jj % kInfo]));
       }
-      const int row0 = cw * 32 + sub;
-      const uint8_t* src = smem + L::kCodes + cs * L::kCodeTile + row0 * D + piece * 16;
-      const uint8_t* ex_row = ex + row0 * 2 + is_v;
-      uint8_t* dst = smem + L::kRing + s * L::kTile + (piece >> 2) * L::kChunk + row0 * 128;
-      const int bias = 127 - (is_v ? e_v : e_k);
-      const int ch = (piece & 3) * 2 + swap;
-      constexpr int kIters = 32 / kRowsPerIter;
+      // 2^(e_j - E) of row cw * 32 + lane as an fp16 pair (0 below fp16's range)
+      const int e_row = ex[(cw * 32 + lane) * 2 + is_v];
+      const float ff = __uint_as_float((uint32_t)imax(127 - (is_v ? e_v : e_k) + e_row, 0) << 23);
+      const uint32_t factor = pack_f16x2(ff, ff);
+      const uint8_t* src = code_tile(cs) + row0 * D + grp * 8;
+      uint8_t* dst = smem + L::kRing + s * L::kTile;
 #pragma unroll
-      for (int it0 = 0; it0 < kIters; it0 += 4) {
-        uint4 c[4];
-        int e[4];
+      for (int it0 = 0; it0 < kIters; it0 += 8) {
+        uint2 c[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          c[q] = *reinterpret_cast<const uint4*>(src + (it0 + q) * 512);
-          e[q] = ex_row[(it0 + q) * kRowsPerIter * 2];
-        }
+        for (int q = 0; q < 8; ++q)
+          c[q] = *reinterpret_cast<const uint2*>(src + (it0 + q) * kRowsIter * D);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          // 2^(e_j - E) as an fp16 pair (0 below fp16's range)
-          const float ff = __uint_as_float((uint32_t)imax(bias + e[q], 0) << 23);
-          const uint32_t f = pack_f16x2(ff, ff);
-          const uint32_t c4[4] = {swap ? c[q].z : c[q].x, swap ? c[q].w : c[q].y,
-                                  swap ? c[q].x : c[q].z, swap ? c[q].y : c[q].w};
-          uint32_t h[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            h[2 * i] = mul_f16x2(e4m3x2_to_f16x2(c4[i]), f);
-            h[2 * i + 1] = mul_f16x2(e4m3x2_to_f16x2(c4[i] >> 16), f);
-          }
-          const int it = it0 + q, r7 = (row0 + it * kRowsPerIter) & 7;
-          uint8_t* line = dst + it * kRowsPerIter * 128;
-          *reinterpret_cast<uint4*>(line + ((ch ^ r7) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(line + ((ch ^ 1 ^ r7) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        for (int q = 0; q < 8; ++q) {
+          const int it = it0 + q;
+          const uint32_t f = __shfl_sync(0xffffffffu, factor, it * kRowsIter + sub);
+          uint32_t h[4];
+          decode4(c[q].x, h[0], h[1]);
+          decode4(c[q].y, h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + column[it % kTurns] + it * kRowsIter * 128) =
+              make_uint4(mul_f16x2(h[0], f), mul_f16x2(h[1], f), mul_f16x2(h[2], f), mul_f16x2(h[3], f));
         }
       }
       if (valid < BN) {  // rows behind the sequence hold anything, NaN codes included: clear
@@ -404,15 +404,17 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
         if (r < 0) atomicOr(p.status, DEV_BAD_INPUT);
         return (int)r;
       };
-      constexpr int kDepth = kE4m3 ? 2 : kStages;
+      const int depth = !kE4m3 ? kStages : w.dual ? S::kCodeStagesDual : S::kCodeStages;
       const uint32_t full = smem_u32(kE4m3 ? bars->code_full : bars->kv_full);
       const uint32_t empty = smem_u32(kE4m3 ? bars->code_empty : bars->kv_empty);
       int row = rows_of(lo), next = n_kv > 1 ? rows_of(lo + 1) : -1;
       bool live = true;
-      int issued = 0;
+      int issued = 0, s = -1;
+      uint32_t parity = 0;  // of the stage's last release; the first turn finds it released
       for (int u = 0; u < 2 * n_kv && live; ++u) {
-        const int s = u % kDepth;
-        live = __all_sync(0xffffffffu, mbar_wait(empty + s * 8, ((u / kDepth) & 1) ^ 1, wc));
+        if (++s == depth) s = 0;
+        if (s == 0) parity ^= 1;
+        live = __all_sync(0xffffffffu, mbar_wait(empty + s * 8, parity, wc));
         if (!live) break;
         const uint32_t bar = full + s * 8;
         const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0));
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
         if (row >= 0) {
           if constexpr (kE4m3) {
             const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache);
-            bulk_load(smem_u32(smem + L::kCodes + s * L::kCodeTile) + lane * R * D,
+            bulk_load(smem_u32(code_tile(s)) + lane * R * D,
                       src + (size_t)row * D, R * D, bar);
             if (!is_v)  // the exponents of K and V come with K
               bulk_load(smem_u32(smem + L::kExp + ((u >> 1) % kInfo) * BN * 2) + lane * R * 2,
@@ -443,8 +445,8 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
         }
       }
       // Do not leave while copies into this CTA's shared memory are in flight.
-      for (int u = imax(0, issued - kDepth); u < issued; ++u)
-        drain_wait(full + (u % kDepth) * 8, (u / kDepth) & 1);
+      for (int u = imax(0, issued - depth); u < issued; ++u)
+        drain_wait(full + (u % depth) * 8, (u / depth) & 1);
     } else if (!kE4m3 && warp == kRelayWarp) {
       // ------------------------------------------------------------ relay (bf16)
       // After a ring use's bytes have landed (and the V rows behind the sequence are
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       };
       auto issue_s = [&](int t, int u) {
         if (!ok) return;
-        const uint64_t dq = smem_desc_sw128(q_base + t * L::kTile, 16, 1024);
+        const uint64_t dq = smem_desc_sw128(q_base + (dual ? 0 : t * L::kTile), 16, 1024);
         const uint64_t dk = smem_desc_sw128(ring + (u % kStages) * L::kTile, 16, 1024);
         const uint32_t col = t == 0 ? L::kColS0 : L::kColS1;
 #pragma unroll
@@ -591,8 +593,9 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
           if (lane / kRowsPerIter == it) row_scale = __uint_as_float((uint32_t)(xl - 14 + 127) << 23);
         }
         const int rt = (warp & 3) * 32 + it * kRowsPerIter + lane / kPer;
-        *reinterpret_cast<uint4*>(smem + L::kQ + t * L::kTile + (piece >> 3) * L::kChunk + rt * 128 +
-                                  (((piece & 7) ^ (rt & 7)) << 4)) = qv[it];
+        if (t == 0 || !w.dual)  // (a dual unit's streams share the tile)
+          *reinterpret_cast<uint4*>(smem + L::kQ + t * L::kTile + (piece >> 3) * L::kChunk + rt * 128 +
+                                    (((piece & 7) ^ (rt & 7)) << 4)) = qv[it];
       }
       fence_proxy_async_smem();
       __syncwarp();
