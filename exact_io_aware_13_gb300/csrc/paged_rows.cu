@@ -93,7 +93,7 @@ __device__ __forceinline__ uint32_t piece_offset(int row, int piece) {
 }
 // NT: 8-row groups per warp; RG: warps that share a key tile, each with NT * 8 rows.
 template <int D, int NT, int RG>
-__global__ void __launch_bounds__(kWarps * 32, 3)
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)  // (168 registers would spill at NT = 2)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PagedAttention a) {
   using L = Layout<D>;
@@ -332,29 +332,59 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
         ve[hf][e] = (int)(w >> 8);
       }
     }
-    // ---- scores in log2 units, row maxima
+    // ---- scores in log2 units (rows 2 c, 2 c + 1 of a key in one packed pair), row maxima.
+    // Every decision is warp-uniform and stays outside the element loops.
     float mt[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) mt[nt][0] = mt[nt][1] = -INFINITY;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int j = t0 + hf * 16 + kappa(g) + 8 * e;
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
+          f32x2_split(mul_f32x2(f32x2(x[hf][nt][2 * e], x[hf][nt][2 * e + 1]),
+                                mul_f32x2(f32x2(k1[nt][0], k1[nt][1]), f32x2(ks[hf][e], ks[hf][e]))),
+                      x[hf][nt][2 * e], x[hf][nt][2 * e + 1]);
+    if (!plain) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float y = x[hf][nt][2 * e + r] * (ks[hf][e] * k1[nt][r]);
-            if (!plain) {
-              y -= slope[nt][r] * (float)(pos[nt][r] - j);
-              if (a.score_kind & ATTN_SCORE_SOFTCAP) y = cap * tanhf(y);
-            }
-            if (masked) y = (j >= lo[nt][r] && j < hi[nt][r]) ? y : -INFINITY;
-            x[hf][nt][2 * e + r] = y;
-            mt[nt][r] = fmaxf(mt[nt][r], y);
-          }
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = t0 + hf * 16 + kappa(g) + 8 * e;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) x[hf][nt][2 * e + r] -= slope[nt][r] * (float)(pos[nt][r] - j);
+        }
+      if (a.score_kind & ATTN_SCORE_SOFTCAP) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[hf][nt][e] = cap * tanhf(x[hf][nt][e]);
       }
+    }
+    if (masked) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = t0 + hf * 16 + kappa(g) + 8 * e;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (j < lo[nt][r] || j >= hi[nt][r]) x[hf][nt][2 * e + r] = -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mt[nt][e & 1] = fmaxf(mt[nt][e & 1], x[hf][nt][e]);
     bool grow = Et > E;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -385,23 +415,33 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
         }
     }
     // ---- P^T (fp16) and O^T += V^T P^T
+    uint64_t off2[NT], l2[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      off2[nt] = f32x2(m[nt][0] == -INFINITY ? 0.f : kPOffset - m[nt][0],
+                       m[nt][1] == -INFINITY ? 0.f : kPOffset - m[nt][1]);
+      l2[nt] = f32x2(l[nt][0], l[nt][1]);
+    }
+    const uint64_t one2 = f32x2(1.f, 1.f);
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       uint32_t pf[NT][2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int down = E - ve[hf][e];  // V scale relative to 2^E; slots behind the sequence: any
-        const float wj = down >= 0 && down <= 126 ? __uint_as_float((uint32_t)(127 - down) << 23) : 0.f;
+        // V scale relative to 2^E (0 for the smallest, and for slots behind the sequence,
+        // whose bytes are anything and whose P is 0)
+        const int down = E - ve[hf][e];
+        const float wj = __uint_as_float((uint32_t)imax(127 - imax(down, 0), 0) << 23);
+        const uint64_t wj2 = f32x2(wj, wj);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float pr[2];
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float off = m[nt][r] == -INFINITY ? 0.f : kPOffset - m[nt][r];
-            pr[r] = ex2_approx(x[hf][nt][2 * e + r] + off);
-            l[nt][r] += pr[r];
-          }
-          pf[nt][e] = transpose_8x8(pack_f16x2(pr[0] * wj, pr[1] * wj));
+          float p0, p1;
+          f32x2_split(fma_f32x2(f32x2(x[hf][nt][2 * e], x[hf][nt][2 * e + 1]), one2, off2[nt]), p0, p1);
+          p0 = ex2_approx(p0);
+          p1 = ex2_approx(p1);
+          l2[nt] = fma_f32x2(f32x2(p0, p1), one2, l2[nt]);
+          f32x2_split(mul_f32x2(f32x2(p0, p1), wj2), p0, p1);
+          pf[nt][e] = transpose_8x8(pack_f16x2(p0, p1));
         }
       }
       // keys of the transposed fragment's slots 2 c, 2 c + 1: c, c + 4 (and + 8)
@@ -431,6 +471,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
             mma_16816(o[nt][2 * i + hb], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
         }
     }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) f32x2_split(l2[nt], l[nt][0], l[nt][1]);
     // every thread has read the stage
     if (RG > 1) nb_sync(1 + kg, RG * 32);
     else __syncwarp();
