@@ -48,6 +48,16 @@ def _params(mask_kind: int, window: int, doc_offsets: Optional[torch.Tensor],
     return ctypes.byref(mp), ctypes.byref(sp), (mp, sp)
 
 
+_PLAIN = _params(0, 0, None, 0.0)  # no window, no document table, no soft-cap: never written
+
+
+def _mask_score_params(window: int, softcap: float):
+    """_params of the paged calls, which take neither documents nor dropout."""
+    if window == 0 and softcap == 0.0:
+        return _PLAIN
+    return _params(0, window, None, softcap)
+
+
 def _score_kind(score_kind: int, dropout_p: float) -> int:
     """Dropout is switched on by a positive drop probability."""
     return int(score_kind) | (SCORE_DROPOUT if dropout_p > 0 else 0)
@@ -61,7 +71,7 @@ def _dims(q: torch.Tensor, k: torch.Tensor):
     return B, Hq, Hkv, Nq, Nkv, d
 
 
-_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+_BF16, _F32, _U8, _I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
 
 
 def _check_dtypes(*named):
@@ -107,6 +117,18 @@ def _check_tensors(*ts):
     if index is not None and index != _current_device():
         raise ValueError(f"tensors are on cuda:{index}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
+
+
+def _check_call(dtyped):
+    """_check_tensors and _check_dtypes in one pass over (tensor or None, dtype, name)."""
+    device = _current_device() if torch.cuda.is_initialized() else -1
+    for t, dtype, name in dtyped:
+        if t is None:
+            continue
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != device or not t.is_contiguous():
+            _check_tensors(*(x for x, _, _ in dtyped))
 
 
 def fwd_into(q, k, v, o, lse, *, scale: float, mask_kind: int = MASK_NONE, window: int = 0,
@@ -367,9 +389,13 @@ def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspa
     caches hold e4m3 codes as uint8, as paged.cache_write fills them, and
     attn_decode_paged_e4m3 runs."""
     kind = _BF16 if kv_exp is None else _U8
-    _check_tensors(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspace, kv_exp)
-    _check_dtypes((q, _BF16, "q"), (k_cache, kind, "k_cache"), (v_cache, kind, "v_cache"),
-                  (o, _BF16, "o"), (lse, _F32, "lse"), (kv_exp, _U8, "kv_exp"))
+    _check_call(((q, _BF16, "q"), (k_cache, kind, "k_cache"), (v_cache, kind, "v_cache"),
+                 (o, _BF16, "o"), (lse, _F32, "lse"), (kv_exp, _U8, "kv_exp"),
+                 (page_table, _I32, "page_table"), (seq_lens, _I32, "seq_lens")))
+    ws_bytes = 0
+    if workspace is not None:
+        _check_tensors(workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
     shape = q.shape
     if len(shape) != 4 or o.shape != shape or lse.shape != shape[:-1]:
         raise ValueError("q, o must be [B, Hq, Nq, d] and lse [B, Hq, Nq]")
@@ -377,21 +403,18 @@ def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspa
     num_pages, Hkv, page_size, dk = cache_shape = k_cache.shape
     if dk != d or v_cache.shape != cache_shape:
         raise ValueError("k_cache and v_cache must be [pages, Hkv, page_size, d]")
-    if page_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
-        raise ValueError("page_table and seq_lens must be int32")
     table_shape = page_table.shape
     if len(table_shape) != 2 or table_shape[0] != B or seq_lens.shape != (B,):
         raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
-    if kv_exp is not None and tuple(kv_exp.shape) != (num_pages, Hkv, page_size, 2):
+    if kv_exp is not None and kv_exp.shape != (num_pages, Hkv, page_size, 2):
         raise ValueError("kv_exp must be [pages, Hkv, page_size, 2]")
-    mp, sp, _keep = _params(mask_kind, window, None, softcap)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    mp, sp, _keep = _mask_score_params(window, softcap)
     if kv_exp is not None:
         cache = _lib.PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), kv_exp.data_ptr(),
                                 page_table.data_ptr(), 1, num_pages, Hkv, page_size, d,
                                 table_shape[1])
         _lib.check(_lib.load().attn_decode_paged_e4m3(
-            ctypes.byref(cache), _ptr(q), _ptr(seq_lens), _ptr(o), _ptr(lse), B, Hq, Nq,
+            cache, q.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Nq,
             int(max_seq_len), int(split_keys), scale, mask_kind, mp, score_kind, sp,
             _ptr(workspace), ws_bytes, _stream(stream)), "attn_decode_paged_e4m3")
         return

@@ -392,6 +392,9 @@ size_t decode_lse_plane(long long n_chunks, long long rows) {
 }
 
 // ---------------------------------------------------------------- paged cache
+// Longest sequence of the paged calls: key positions past the last tile stay below 2^31.
+constexpr int kMaxSeqLen = 0x7fffffff - 4096;
+
 // Checks of a cache description and of the ragged batch over it; fills `p`. max_new and
 // max_seq_len are the caller's bounds (already clamped to what T and the table allow).
 attn_status check_cache(const attn_paged_cache* c, int B, int T, int max_new, int max_seq_len,
@@ -405,6 +408,7 @@ attn_status check_cache(const attn_paged_cache* c, int B, int T, int max_new, in
   if (!decode_page_size_ok(c->page_size)) return ATTN_ERR_SHAPE;
   if ((long long)max_seq_len > (long long)c->max_pages_per_seq * c->page_size)
     return ATTN_ERR_SHAPE;
+  if (max_seq_len > kMaxSeqLen) return ATTN_ERR_SHAPE;
   if ((long long)c->num_pages * c->Hkv > 0x7fffffffLL ||
       (long long)c->num_pages * c->Hkv * c->page_size > 0x7fffffffLL)
     return ATTN_ERR_SHAPE;
@@ -436,7 +440,7 @@ bool stride_ok(long long s) { return s >= 0 && s % 8 == 0; }
 
 int table_capacity(const attn_paged_cache* c) {
   if (!c || c->max_pages_per_seq <= 0 || c->page_size <= 0) return 0;
-  return (int)std::min<long long>((long long)c->max_pages_per_seq * c->page_size, 0x7fffffffLL);
+  return (int)std::min<long long>((long long)c->max_pages_per_seq * c->page_size, kMaxSeqLen);
 }
 
 // Score and mask arguments of the paged attention calls (as attn_decode_paged takes them).

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "kernels.h"
+#include "paged_index.cuh"
 #include "ptx.cuh"
 
 namespace attn {
@@ -11,8 +12,7 @@ namespace attn {
 constexpr float kPagedLog2e = 1.4426950408889634f;
 constexpr float kPagedLn2 = 0.69314718055994531f;
 
-// Position of the first of the n newest tokens of a sequence, and whether the sequence's
-// device inputs can be followed. n and L are clamped to 0 when they cannot.
+// The new tokens of a sequence (nothing when its device inputs cannot be followed).
 struct Span {
   int row0;  // packed row of the first new token
   int n;     // new tokens
@@ -20,7 +20,7 @@ struct Span {
 };
 
 __device__ __forceinline__ bool span_ok(const PagedProblem& p, int o0, int o1, int L) {
-  return o0 >= 0 && o1 >= o0 && o1 <= p.T && o1 - o0 <= p.max_new && L >= 0 && L <= p.max_seq_len;
+  return paged_span_ok(p.T, p.max_new, p.max_seq_len, o0, o1, L);
 }
 
 // Without offsets (decode) every sequence has p.max_new new tokens.
@@ -60,12 +60,10 @@ __device__ __forceinline__ int find_sequence(const PagedProblem& p, int t, int l
   return lo;
 }
 
-// Row index (page * Hkv + head) * page_size + slot of a token of sequence b in the cache's
-// [num_pages * Hkv * page_size, d] rows, or -1 for a page outside the pool.
+// Cache row of a token of sequence b (see paged_row). pos must lie inside the page table.
 __device__ __forceinline__ long long cache_row(const PagedProblem& p, int b, int pos, int head) {
   const int page = __ldg(p.page_table + (size_t)b * p.max_pages + pos / p.page_size);
-  if (page < 0 || page >= p.num_pages) return -1;
-  return ((long long)page * p.Hkv + head) * p.page_size + pos % p.page_size;
+  return paged_row(page, p.num_pages, p.Hkv, p.page_size, head, pos % p.page_size);
 }
 
 // 2^(byte - 127) as a float; byte 0 is the subnormal 2^-127.

@@ -135,22 +135,17 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)  // (168 registe
   const uint32_t exps = smem_u32(smem + L::kExp) + kg * kStages * kTile * 2;
   const uint32_t full = smem_u32(bars) + kg * kStages * 8;
 
-  // Requests the key group's next tile into stage s: lane q fetches its q-th page piece. The
-  // group's tiles are kKeyGroups * 32 keys apart, which is a whole number of pages or leads
-  // at most one page on, so the page and slot of the lane's piece advance without a division.
+  // Requests the key group's next tile into stage s: lane q fetches its q-th page piece.
   const int R = imin(p.page_size, kTile), pieces = kTile / R;
   constexpr int kStride = kKeyGroups * kTile;
-  const bool whole = p.page_size <= kStride;       // then it divides kStride
-  const int page_step = whole ? kStride / p.page_size : 0;
   int key = (tb + kg) * kTile + lane * R;
-  int page_idx = key / p.page_size, slot = key - page_idx * p.page_size;
+  PageWalk walk(key, p.page_size);
   const int32_t* table = p.page_table + (size_t)b * p.max_pages;
   auto request = [&](int s) {
     int row = -1;
     if (lane < pieces && key < sp.L) {
-      const int page = __ldg(table + page_idx);
-      if (page >= 0 && page < p.num_pages) row = (page * p.Hkv + hk) * p.page_size + slot;
-      else atomicOr(p.status, DEV_BAD_INPUT);
+      row = (int)paged_row(__ldg(table + walk.page), p.num_pages, p.Hkv, p.page_size, hk, walk.slot);
+      if (row < 0) atomicOr(p.status, DEV_BAD_INPUT);
     }
     const uint32_t bar = full + s * 8;
     const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0));
@@ -163,14 +158,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)  // (168 registe
       bulk_load(exps + (s * kTile + lane * R) * 2, p.kv_exp + (size_t)row * 2, R * 2, bar);
     }
     key += kStride;
-    page_idx += page_step;
-    if (!whole) {
-      slot += kStride;
-      if (slot >= p.page_size) {
-        slot -= p.page_size;
-        ++page_idx;
-      }
-    }
+    walk.advance(kStride, p.page_size);
   };
   int issued = tb + kg;  // next tile to request
   if (rg == 0)

@@ -37,7 +37,7 @@ constexpr int BM = 128;
 constexpr int BN = 128;
 constexpr int kQTiles = 2;
 constexpr int kUnitRows = kQTiles * BM;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kRelayWarp = 10, kConvWarp = 12;
+constexpr int kLoadKWarp = 8, kMmaWarp = 9, kRelayWarp = 10, kLoadVWarp = 11, kConvWarp = 12;
 constexpr int kInfo = 4;             // slots of the converters' per-tile scales
 constexpr uint32_t kNbP = 1, kNbPCount = 160;
 constexpr uint32_t kNbKv = 3;
@@ -391,15 +391,18 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     }
   } else if (warp >= 8) {
     setmaxnreg_dec<S::kRegsOther>();
-    if (warp == kLoadWarp) {
-      // ------------------------------------------------------------ loader
-      // Lane q fetches the q-th page piece of a tile: TMA boxes (bf16) or bulk copies (codes).
+    if (warp == kLoadKWarp || warp == kLoadVWarp) {
+      // ------------------------------------------------------------ loaders
+      // One warp for K, one for V (small pages: the copies of one tile take a warp hundreds
+      // of clocks to issue). Lane q fetches the q-th page piece of a tile: TMA boxes (bf16) or
+      // a bulk copy (codes). K tiles take the even stages of the ring, V tiles the odd ones.
+      const bool is_v = warp == kLoadVWarp;
       const int ps = p.page_size;
       const int R = kE4m3 && ps % 128 == 0 ? 128 : imin(ps, 64), pieces = BN / R;
       const int lo = w.lo, hi = w.hi, n_kv = hi - lo;
       auto rows_of = [&](int j) -> int {  // cache row of this lane's piece, or -1
         const int key = j * BN + lane * R;
-        if (lane >= pieces || key >= w.span.L) return -1;
+        if (j >= hi || lane >= pieces || key >= w.span.L) return -1;
         const long long r = cache_row(p, w.b, key, w.hk);
         if (r < 0) atomicOr(p.status, DEV_BAD_INPUT);
         return (int)r;
@@ -407,28 +410,27 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       const int depth = !kE4m3 ? kStages : w.dual ? S::kCodeStagesDual : S::kCodeStages;
       const uint32_t full = smem_u32(kE4m3 ? bars->code_full : bars->kv_full);
       const uint32_t empty = smem_u32(kE4m3 ? bars->code_empty : bars->kv_empty);
-      int row = rows_of(lo), next = n_kv > 1 ? rows_of(lo + 1) : -1;
+      int row = rows_of(lo), next = rows_of(lo + 1);
       bool live = true;
-      int issued = 0, s = -1;
+      int issued = 0, s = is_v - 2;
       uint32_t parity = 0;  // of the stage's last release; the first turn finds it released
-      for (int u = 0; u < 2 * n_kv && live; ++u) {
-        if (++s == depth) s = 0;
-        if (s == 0) parity ^= 1;
+      for (int jj = 0; jj < n_kv && live; ++jj) {
+        s += 2;
+        if (s >= depth) s -= depth;
+        if (s < 2) parity ^= 1;
         live = __all_sync(0xffffffffu, mbar_wait(empty + s * 8, parity, wc));
         if (!live) break;
         const uint32_t bar = full + s * 8;
         const uint32_t n = (uint32_t)__popc(__ballot_sync(0xffffffffu, row >= 0));
-        const bool is_v = u & 1;
         if (lane == 0)
           mbar_arrive_expect_tx(bar, kE4m3 ? n * R * (D + (is_v ? 0 : 2)) : n * R * D * 2);
         __syncwarp();
         if (row >= 0) {
           if constexpr (kE4m3) {
             const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache);
-            bulk_load(smem_u32(code_tile(s)) + lane * R * D,
-                      src + (size_t)row * D, R * D, bar);
+            bulk_load(smem_u32(code_tile(s)) + lane * R * D, src + (size_t)row * D, R * D, bar);
             if (!is_v)  // the exponents of K and V come with K
-              bulk_load(smem_u32(smem + L::kExp + ((u >> 1) % kInfo) * BN * 2) + lane * R * 2,
+              bulk_load(smem_u32(smem + L::kExp + (jj % kInfo) * BN * 2) + lane * R * 2,
                         p.kv_exp + (size_t)row * 2, R * 2, bar);
           } else {
 #pragma unroll
@@ -438,15 +440,14 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
           }
         }
         ++issued;
-        if (is_v) {
-          const int j = lo + (u >> 1);
-          row = next;
-          next = j + 2 < hi ? rows_of(j + 2) : -1;
-        }
+        row = next;
+        next = rows_of(lo + jj + 2);
       }
       // Do not leave while copies into this CTA's shared memory are in flight.
-      for (int u = imax(0, issued - depth); u < issued; ++u)
+      for (int jj = imax(0, issued - depth / 2); jj < issued; ++jj) {
+        const int u = 2 * jj + is_v;
         drain_wait(full + (u % depth) * 8, (u / depth) & 1);
+      }
     } else if (!kE4m3 && warp == kRelayWarp) {
       // ------------------------------------------------------------ relay (bf16)
       // After a ring use's bytes have landed (and the V rows behind the sequence are

@@ -10,44 +10,41 @@ each token's K and V scale; passing kv_exp selects it.
 """
 from __future__ import annotations
 
-import ctypes
 import functools
 from typing import Optional
 
 import torch
 
 from . import _lib
-from .attention import (MASK_NONE, SCORE_NONE, _BF16, _F32, _U8, _check_dtypes, _check_tensors,
-                        _current_device, _num_sms, _params, _ptr, _stream)
+from .attention import (MASK_NONE, SCORE_NONE, _BF16, _F32, _I32, _U8, _check_call,
+                        _check_tensors, _current_device, _mask_score_params, _num_sms, _ptr,
+                        _stream)
 
 CACHE_BF16, CACHE_E4M3 = 0, 1
 
 
-def _cache(k_cache, v_cache, page_table, kv_exp, B: int) -> _lib.PagedCache:
+def _cache(k_cache, v_cache, page_table, kv_exp, offsets, seq_lens, *more):
+    """Checks of the cache and the batch (and of `more`, (tensor, dtype, name) triples of
+    contiguous tensors); the cache description and B."""
     kind = _BF16 if kv_exp is None else _U8
-    _check_dtypes((k_cache, kind, "k_cache"), (v_cache, kind, "v_cache"), (kv_exp, _U8, "kv_exp"),
-                  (page_table, torch.int32, "page_table"))
-    shape, table_shape = k_cache.shape, page_table.shape
+    _check_call(((k_cache, kind, "k_cache"), (v_cache, kind, "v_cache"), (kv_exp, _U8, "kv_exp"),
+                 (page_table, _I32, "page_table"), (offsets, _I32, "offsets"),
+                 (seq_lens, _I32, "seq_lens"), *more))
+    shape, table_shape, B = k_cache.shape, page_table.shape, seq_lens.numel()
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [pages, Hkv, page_size, d]")
     pages, Hkv, page_size, d = shape
     if kv_exp is not None and kv_exp.shape != (pages, Hkv, page_size, 2):
         raise ValueError(f"kv_exp must have shape {(pages, Hkv, page_size, 2)}, got "
                          f"{tuple(kv_exp.shape)}")
+    if seq_lens.dim() != 1 or offsets.shape != (B + 1,):
+        raise ValueError("offsets must be [B + 1] and seq_lens [B]")
     if len(table_shape) != 2 or table_shape[0] != B:
         raise ValueError("page_table must be [B, max_pages]")
     return _lib.PagedCache(k_cache.data_ptr(), v_cache.data_ptr(),
                            None if kv_exp is None else kv_exp.data_ptr(), page_table.data_ptr(),
                            CACHE_BF16 if kv_exp is None else CACHE_E4M3, pages, Hkv, page_size, d,
-                           table_shape[1])
-
-
-def _check_batch(offsets, seq_lens) -> int:
-    _check_dtypes((offsets, torch.int32, "offsets"), (seq_lens, torch.int32, "seq_lens"))
-    B = seq_lens.numel()
-    if seq_lens.dim() != 1 or offsets.shape != (B + 1,):
-        raise ValueError("offsets must be [B + 1] and seq_lens [B]")
-    return B
+                           table_shape[1]), B
 
 
 def _rows(t, H: int, d: int, name: str):
@@ -70,39 +67,38 @@ def cache_write(k, v, k_cache, v_cache, page_table, offsets, seq_lens, *, kv_exp
     """Write the new tokens' K and V rows (bf16 [T, Hkv, d], any token and head stride that
     is a multiple of 8) into the cache: as they are, or with kv_exp as e4m3 codes under the
     smallest power-of-two scale that holds each row."""
-    _check_tensors(k_cache, v_cache, kv_exp, page_table, offsets, seq_lens)
-    B = _check_batch(offsets, seq_lens)
-    cache = _cache(k_cache, v_cache, page_table, kv_exp, B)
+    cache, B = _cache(k_cache, v_cache, page_table, kv_exp, offsets, seq_lens)
     kp, kt, kh = _rows(k, cache.Hkv, cache.d, "k")
     vp, vt, vh = _rows(v, cache.Hkv, cache.d, "v")
-    if v.shape[0] != k.shape[0]:
+    T = k.shape[0]
+    if v.shape[0] != T:
         raise ValueError("k and v disagree on the number of tokens")
-    _lib.check(_lib.load().attn_cache_write(ctypes.byref(cache), kp, kt, kh, vp, vt, vh,
-                                            _ptr(offsets), _ptr(seq_lens), B, k.shape[0],
-                                            _stream(stream)), "attn_cache_write")
+    _lib.check(_lib.load().attn_cache_write(cache, kp, kt, kh, vp, vt, vh, offsets.data_ptr(),
+                                            seq_lens.data_ptr(), B, T, _stream(stream)),
+               "attn_cache_write")
 
 
 def cache_read_into(k_cache, v_cache, page_table, offsets, seq_lens, k, v, *, kv_exp=None,
                     stream=None) -> None:
     """Read the newest tokens of each sequence into k and v (bf16 [T, Hkv, d], contiguous);
     rows behind offsets[B] keep what they held."""
-    _check_tensors(k_cache, v_cache, kv_exp, page_table, offsets, seq_lens, k, v)
-    B = _check_batch(offsets, seq_lens)
-    cache = _cache(k_cache, v_cache, page_table, kv_exp, B)
-    _check_dtypes((k, _BF16, "k"), (v, _BF16, "v"))
-    if k.dim() != 3 or tuple(k.shape[1:]) != (cache.Hkv, cache.d) or v.shape != k.shape:
+    cache, B = _cache(k_cache, v_cache, page_table, kv_exp, offsets, seq_lens, (k, _BF16, "k"),
+                      (v, _BF16, "v"))
+    shape = k.shape
+    if len(shape) != 3 or shape[1:] != (cache.Hkv, cache.d) or v.shape != shape:
         raise ValueError(f"k and v must be [T, {cache.Hkv}, {cache.d}]")
-    _lib.check(_lib.load().attn_cache_read(ctypes.byref(cache), _ptr(k), _ptr(v), _ptr(offsets),
-                                           _ptr(seq_lens), B, k.shape[0], _stream(stream)),
+    _lib.check(_lib.load().attn_cache_read(cache, k.data_ptr(), v.data_ptr(), offsets.data_ptr(),
+                                           seq_lens.data_ptr(), B, shape[0], _stream(stream)),
                "attn_cache_read")
 
 
 def cache_read(k_cache, v_cache, page_table, offsets, seq_lens, n_tokens: int, *, kv_exp=None,
                stream=None):
     """Allocating wrapper of cache_read_into for n_tokens = offsets[B] rows: (k, v)."""
-    shape = (int(n_tokens), k_cache.shape[1], k_cache.shape[3])
-    k = torch.empty(shape, dtype=_BF16, device=k_cache.device)
-    v = torch.empty(shape, dtype=_BF16, device=k_cache.device)
+    _, Hkv, _, d = k_cache.shape
+    shape, device = (int(n_tokens), Hkv, d), k_cache.device
+    k = torch.empty(shape, dtype=_BF16, device=device)
+    v = torch.empty(shape, dtype=_BF16, device=device)
     cache_read_into(k_cache, v_cache, page_table, offsets, seq_lens, k, v, kv_exp=kv_exp,
                     stream=stream)
     return k, v
@@ -139,22 +135,24 @@ def prefill_paged_into(q, k_cache, v_cache, page_table, offsets, seq_lens, o, ls
     """attn_prefill_paged on caller-owned tensors: q bf16 [T, Hq, d] (any token and head
     stride that is a multiple of 8), o bf16 [T, Hq, d] and lse fp32 [T, Hq] contiguous. Rows
     behind offsets[B] keep what they held."""
-    _check_tensors(k_cache, v_cache, kv_exp, page_table, offsets, seq_lens, o, lse, workspace)
-    B = _check_batch(offsets, seq_lens)
-    cache = _cache(k_cache, v_cache, page_table, kv_exp, B)
-    if q.dim() != 3:
+    cache, B = _cache(k_cache, v_cache, page_table, kv_exp, offsets, seq_lens, (o, _BF16, "o"),
+                      (lse, _F32, "lse"))
+    ws_bytes = 0
+    if workspace is not None:
+        _check_tensors(workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q must be [T, Hq, d]")
-    T, Hq, d = q.shape
+    T, Hq, _ = shape
     qp, qt, qh = _rows(q, Hq, cache.d, "q")
-    _check_dtypes((o, _BF16, "o"), (lse, _F32, "lse"))
-    if o.shape != q.shape or lse.shape != q.shape[:2]:
+    if o.shape != shape or lse.shape != shape[:2]:
         raise ValueError("o must be [T, Hq, d] and lse [T, Hq]")
-    mp, sp, _keep = _params(mask_kind, window, None, softcap)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    mp, sp, _keep = _mask_score_params(window, softcap)
     _lib.check(_lib.load().attn_prefill_paged(
-        ctypes.byref(cache), qp, qt, qh, _ptr(o), _ptr(lse), _ptr(offsets), _ptr(seq_lens), B, T,
-        Hq, int(max_new), int(max_seq_len), int(split_keys), scale, mask_kind, mp, score_kind, sp,
-        _ptr(workspace), ws_bytes, _stream(stream)), "attn_prefill_paged")
+        cache, qp, qt, qh, o.data_ptr(), lse.data_ptr(), offsets.data_ptr(), seq_lens.data_ptr(),
+        B, T, Hq, int(max_new), int(max_seq_len), int(split_keys), scale, mask_kind, mp,
+        score_kind, sp, _ptr(workspace), ws_bytes, _stream(stream)), "attn_prefill_paged")
 
 
 def prefill_paged(q, k_cache, v_cache, page_table, offsets, seq_lens, *, kv_exp=None,

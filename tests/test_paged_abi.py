@@ -69,6 +69,8 @@ def test_bad_caches(lib, call):
     assert call(lib, _cache(kind, pages=-1)) == SHAPE
     assert call(lib, _cache(kind, Hkv=-2)) == SHAPE
     assert call(lib, _cache(kind, maxp=-1)) == SHAPE
+    if call in (_prefill, _decode):                             # positions must fit 32 bits
+        assert call(lib, _cache(kind, ps=64, maxp=1 << 25), msl=(1 << 31) - 1) == SHAPE
     assert call(lib, _cache(kind, pages=1 << 27)) == SHAPE      # over 2^31 cache rows
     assert call(lib, _cache(kind, pages=1 << 30, Hkv=8)) == SHAPE
     assert call(lib, _cache(1, exp=None)) == ARG                # codes without scales
