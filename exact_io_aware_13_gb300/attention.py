@@ -373,10 +373,33 @@ def _decode_workspace_size(*args: int) -> int:
     return int(_lib.load().attn_decode_workspace_size(*args))
 
 
+def prefill_split_keys(cache_kind: int, B: int, T: int, Hq: int, Hkv: int, max_new: int,
+                       max_seq_len: int, total_kv_tokens: int,
+                       num_sms: Optional[int] = None) -> int:
+    """The library's split size for a prefill_paged call (keys per chunk)."""
+    return _prefill_split_keys(int(cache_kind), int(B), int(T), int(Hq), int(Hkv), int(max_new),
+                               int(max_seq_len), int(total_kv_tokens),
+                               _num_sms() if num_sms is None else int(num_sms))
+
+
+@functools.lru_cache(maxsize=1024)
+def _prefill_split_keys(*args: int) -> int:
+    return int(_lib.load().attn_prefill_split_keys(*args))
+
+
 def decode_workspace_size(B: int, Hq: int, Hkv: int, Nq: int, d: int, max_seq_len: int,
                           split_keys: int) -> int:
     return _decode_workspace_size(int(B), int(Hq), int(Hkv), int(Nq), int(d), int(max_seq_len),
                                   int(split_keys))
+
+
+@functools.lru_cache(maxsize=1024)
+def _prefill_workspace_size(*args: int) -> int:
+    return int(_lib.load().attn_prefill_workspace_size(*args))
+
+
+def prefill_workspace_size(T: int, Hq: int, d: int, max_seq_len: int, split_keys: int) -> int:
+    return _prefill_workspace_size(int(T), int(Hq), int(d), int(max_seq_len), int(split_keys))
 
 
 def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspace, *,
@@ -438,13 +461,20 @@ def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, max_seq_len: Opti
     if max_seq_len is None:
         max_seq_len = page_table.shape[1] * page_size
     if split_keys is None:
-        split_keys = decode_split_keys(B, Hq, Hkv, Nq, total_kv_tokens or B * max_seq_len)
+        total = total_kv_tokens or B * max_seq_len
+        if kv_exp is None:
+            split_keys = decode_split_keys(B, Hq, Hkv, Nq, total)
+        else:
+            split_keys = prefill_split_keys(1, B, B * Nq, Hq, Hkv, Nq, max_seq_len, total)
     if scale is None:
         scale = float(d) ** -0.5
     device = q.device
     o = torch.empty((B, Hq, Nq, d), dtype=_BF16, device=device)
     lse = torch.empty((B, Hq, Nq), dtype=_F32, device=device)
-    nbytes = decode_workspace_size(B, Hq, Hkv, Nq, d, max_seq_len, split_keys)
+    if kv_exp is None:
+        nbytes = decode_workspace_size(B, Hq, Hkv, Nq, d, max_seq_len, split_keys)
+    else:
+        nbytes = prefill_workspace_size(B * Nq, Hq, d, max_seq_len, split_keys)
     ws = torch.empty((nbytes,), dtype=_U8, device=device) if nbytes else None
     decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, ws,
                       max_seq_len=max_seq_len, split_keys=split_keys, scale=scale,

@@ -816,9 +816,12 @@ int attn_prefill_split_keys(int cache_kind, int B, int T, int Hq, int Hkv, int m
     return (int)one;
   const long long G = Hq / Hkv, rows = std::min(max_new, T) * G;
   if (cache_kind == ATTN_CACHE_E4M3 && rows <= kPagedRowsMax) {
-    // The row kernel: ten chunks per SM, as for decode. 8 new tokens of 16 sequences of 2000
-    // to 32768 (Hq = 32, Hkv = 8, d = 128): 306 us at 2048 keys, 388 at 512, 846 unsplit.
-    const long long keys = attn_decode_split_keys(B, Hq, Hkv, 1, total_kv_tokens, num_sms);
+    // The row kernel: ten chunks per SM, as for decode, of at least 1024 keys. 8 new tokens of
+    // 16 sequences of 2000 to 32768 (Hq = 32, Hkv = 8, d = 128): 259 us at 1536 keys, 343 at
+    // 512, 846 unsplit. Three sequences of up to 700 tokens: 17.5 us unsplit, 15.5 us in
+    // chunks of 256, but the merge's launch and workspace cost the host 3 us.
+    const long long keys =
+        std::max(1024, attn_decode_split_keys(B, Hq, Hkv, 1, total_kv_tokens, num_sms));
     return (int)std::min((keys + 127) / 128 * 128, one);
   }
   // The tile kernel, one CTA per SM: unsplit when the 256-row units fill the SMs (24 short
@@ -898,11 +901,12 @@ attn_status attn_decode_paged_e4m3(const attn_paged_cache* cache, const void* q,
     return s;
   if (B == 0 || Nq == 0 || Hq == 0) return ATTN_OK;
   if (!q || !o || !lse) return ATTN_ERR_ARG;
+  // (no offsets: every sequence has Nq rows)
   if ((s = check_cache_pointers(a.p, seq_lens, seq_lens)) != ATTN_OK) return s;
   if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return ATTN_ERR_ALIGN;
   a.Hq = Hq;
   a.G = Hq / Hkv;
-  const size_t need = attn_decode_workspace_size(B, Hq, Hkv, Nq, d, max_seq_len, split_keys);
+  const size_t need = attn_prefill_workspace_size(B * Nq, Hq, d, max_seq_len, split_keys);
   if ((s = set_splits(&a, split_keys, need, workspace, workspace_bytes)) != ATTN_OK) return s;
   DeviceInfo* dev = nullptr;
   if ((s = current_device(&dev)) != ATTN_OK) return s;

@@ -10,15 +10,14 @@ each token's K and V scale; passing kv_exp selects it.
 """
 from __future__ import annotations
 
-import functools
 from typing import Optional
 
 import torch
 
 from . import _lib
 from .attention import (MASK_NONE, SCORE_NONE, _BF16, _F32, _I32, _U8, _check_call,
-                        _check_tensors, _current_device, _mask_score_params, _num_sms, _ptr,
-                        _stream)
+                        _check_tensors, _current_device, _mask_score_params, _ptr, _stream,
+                        prefill_split_keys, prefill_workspace_size)
 
 CACHE_BF16, CACHE_E4M3 = 0, 1
 
@@ -102,30 +101,6 @@ def cache_read(k_cache, v_cache, page_table, offsets, seq_lens, n_tokens: int, *
     cache_read_into(k_cache, v_cache, page_table, offsets, seq_lens, k, v, kv_exp=kv_exp,
                     stream=stream)
     return k, v
-
-
-def prefill_split_keys(cache_kind: int, B: int, T: int, Hq: int, Hkv: int, max_new: int,
-                       max_seq_len: int, total_kv_tokens: int,
-                       num_sms: Optional[int] = None) -> int:
-    """The library's split size for a prefill_paged call (keys per chunk)."""
-    return _prefill_split_keys(int(cache_kind), int(B), int(T), int(Hq), int(Hkv), int(max_new),
-                               int(max_seq_len), int(total_kv_tokens),
-                               _num_sms() if num_sms is None else int(num_sms))
-
-
-# Pure functions of their numbers: a step that asks again with the same ones skips the calls.
-@functools.lru_cache(maxsize=1024)
-def _prefill_split_keys(*args: int) -> int:
-    return int(_lib.load().attn_prefill_split_keys(*args))
-
-
-@functools.lru_cache(maxsize=1024)
-def _prefill_workspace_size(*args: int) -> int:
-    return int(_lib.load().attn_prefill_workspace_size(*args))
-
-
-def prefill_workspace_size(T: int, Hq: int, d: int, max_seq_len: int, split_keys: int) -> int:
-    return _prefill_workspace_size(int(T), int(Hq), int(d), int(max_seq_len), int(split_keys))
 
 
 def prefill_paged_into(q, k_cache, v_cache, page_table, offsets, seq_lens, o, lse, workspace, *,

@@ -419,17 +419,18 @@ size_t attn_prefill_workspace_size(int T, int Hq, int d, int max_seq_len, int sp
 
 /*
  * A split_keys for attn_prefill_paged over a cache of this kind (ATTN_CACHE_*): all keys in
- * one chunk when the row tiles alone fill the SMs, else chunks of at least 1024 keys
- * (256 where max_new * Hq / Hkv <= 32 rows meet an e4m3 cache), several per SM over
- * total_kv_tokens (the sum of seq_lens, or B * max_seq_len when unknown). Pure function of
- * its arguments.
+ * one chunk when the row tiles alone fill the SMs, else chunks of at least 1024 keys,
+ * several per SM over total_kv_tokens (the sum of seq_lens, or B * max_seq_len when
+ * unknown). attn_decode_paged_e4m3 takes its result too (T = B * Nq, max_new = Nq). Pure
+ * function of its arguments.
  */
 int attn_prefill_split_keys(int cache_kind, int B, int T, int Hq, int Hkv, int max_new,
                             int max_seq_len, long long total_kv_tokens, int num_sms);
 
 /*
  * attn_decode_paged over an ATTN_CACHE_E4M3 cache: same queries, outputs, masks, score
- * modifications, split_keys and workspace (attn_decode_workspace_size).
+ * modifications and split_keys. The workspace holds one partial result per chunk and row:
+ * attn_prefill_workspace_size(B * Nq, Hq, d, max_seq_len, split_keys) bytes.
  */
 attn_status attn_decode_paged_e4m3(const attn_paged_cache* cache, const void* q,
                                    const int32_t* seq_lens, void* o, float* lse, int B, int Hq,
