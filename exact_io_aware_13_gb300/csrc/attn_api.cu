@@ -417,6 +417,9 @@ attn_status check_cache(const attn_paged_cache* c, int B, int T, int max_new, in
   p->k_cache = c->k; p->v_cache = c->v; p->kv_exp = c->kv_exp; p->page_table = c->page_table;
   p->num_pages = c->num_pages; p->Hkv = c->Hkv; p->page_size = c->page_size; p->d = c->d;
   p->max_pages = c->max_pages_per_seq;
+  p->page_shift = -1;
+  for (int k = 3; k < 31; ++k)
+    if (c->page_size == 1 << k) p->page_shift = k;
   p->B = B; p->T = T;
   p->max_new = std::min(max_new, T);
   p->max_seq_len = max_seq_len;

@@ -175,6 +175,7 @@ struct PagedProblem {
   const int32_t* seq_lens;    // [B] device
   int* status;
   int num_pages, Hkv, page_size, d, max_pages;
+  int page_shift;             // log2 page_size, or -1
   int B, T;
   int max_new;                // bound on the new tokens of a sequence
   int max_seq_len;            // bound on seq_lens (<= max_pages * page_size)

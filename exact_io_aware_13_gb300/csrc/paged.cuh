@@ -62,8 +62,9 @@ __device__ __forceinline__ int find_sequence(const PagedProblem& p, int t, int l
 
 // Cache row of a token of sequence b (see paged_row). pos must lie inside the page table.
 __device__ __forceinline__ long long cache_row(const PagedProblem& p, int b, int pos, int head) {
-  const int page = __ldg(p.page_table + (size_t)b * p.max_pages + pos / p.page_size);
-  return paged_row(page, p.num_pages, p.Hkv, p.page_size, head, pos % p.page_size);
+  const int at = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
+  const int page = __ldg(p.page_table + (size_t)b * p.max_pages + at);
+  return paged_row(page, p.num_pages, p.Hkv, p.page_size, head, pos - at * p.page_size);
 }
 
 // 2^(byte - 127) as a float; byte 0 is the subnormal 2^-127.

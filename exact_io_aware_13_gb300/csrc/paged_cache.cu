@@ -69,21 +69,18 @@ struct CopyArgs {
   RowView in[2];            // write: K and V rows
   __nv_bfloat16* out[2];    // read: contiguous [T, Hkv, d]
   int slices;               // warps per row
+  int per_warp;             // slices of kChunksPerWarp pieces that a warp takes, one by one
 };
 
-// The packed row, slice and sequence of a warp; false when there is nothing to do. A
-// position outside the sequence or the page table is reported, not followed.
-struct WarpRow {
-  int t, c0, b, pos;
-};
-__device__ __forceinline__ bool locate(const CopyArgs& a, int lane, WarpRow& r) {
-  const PagedProblem& p = a.p;
-  r.b = find_sequence(p, r.t, lane);
-  const Span s = load_span(p, r.b);
-  const int i = r.t - s.row0;
+// The sequence and position of packed row t; false when it has none. A position outside the
+// sequence is reported, not followed.
+__device__ __forceinline__ bool locate(const PagedProblem& p, int t, int lane, int& b, int& pos) {
+  b = find_sequence(p, t, lane);
+  const Span s = load_span(p, b);
+  const int i = t - s.row0;
   if (i < 0 || i >= s.n) return false;  // a row of no sequence, or bad inputs
-  r.pos = s.L - s.n + i;
-  if (r.pos < 0) {
+  pos = s.L - s.n + i;
+  if (pos < 0) {
     if (lane == 0) atomicOr(p.status, DEV_BAD_INPUT);
     return false;
   }
@@ -109,125 +106,159 @@ struct Pieces {
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(const CopyArgs a) {
   constexpr int kPer = D / 8;  // lanes per (tensor, head) row: 8 or 16
+  constexpr uint32_t kRow = kE4m3 ? D : 2 * D, kPiece = kRow / kPer;  // bytes in the cache
   const PagedProblem& p = a.p;
   const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0) report_bad_spans(p);
   const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  WarpRow r;
-  r.t = (int)(unit / a.slices);
-  if (r.t >= p.T) return;
-  r.c0 = (int)(unit % a.slices) * kChunksPerWarp;
-  const Pieces<D> pieces(r.c0, lane, p.Hkv);
-  const __nv_bfloat16* k = a.in[0].p + r.t * a.in[0].token_stride + pieces.piece * 8;
-  const __nv_bfloat16* v = a.in[1].p + r.t * a.in[1].token_stride + pieces.piece * 8;
-  uint4 w[kPieces];
+  const int t = (int)(unit / a.slices);
+  if (t >= p.T) return;
+  int c0 = (int)(unit % a.slices) * a.per_warp * kChunksPerWarp;
+  const int c_end = imin(c0 + a.per_warp * kChunksPerWarp, 2 * p.Hkv * kPer);
+  const __nv_bfloat16* k = a.in[0].p + t * a.in[0].token_stride + lane % kPer * 8;
+  const __nv_bfloat16* v = a.in[1].p + t * a.in[1].token_stride + lane % kPer * 8;
+  auto load = [&](uint4 (&w)[kPieces]) {
+    const Pieces<D> pieces(c0, lane, p.Hkv);
 #pragma unroll
-  for (int j = 0; j < kPieces; ++j) {
-    int head;
-    bool is_v;
-    w[j] = make_uint4(0, 0, 0, 0);
-    if (pieces.get(j, head, is_v))
-      w[j] = __ldg(reinterpret_cast<const uint4*>((is_v ? v : k) +
-                                                  head * (is_v ? a.in[1].head_stride : a.in[0].head_stride)));
-  }
-  if (!locate(a, lane, r)) return;
-  const long long row0 = cache_row(p, r.b, r.pos, 0);
+    for (int j = 0; j < kPieces; ++j) {
+      int head;
+      bool is_v;
+      w[j] = make_uint4(0, 0, 0, 0);
+      if (pieces.get(j, head, is_v))
+        w[j] = __ldg(reinterpret_cast<const uint4*>(
+            (is_v ? v : k) + head * (is_v ? a.in[1].head_stride : a.in[0].head_stride)));
+    }
+  };
+  uint4 w[kPieces];
+  load(w);  // on their way while the slot is looked up
+  int b, pos;
+  if (!locate(p, t, lane, b, pos)) return;
+  const long long row0 = cache_row(p, b, pos, 0);
   if (row0 < 0) {
     if (lane == 0) atomicOr(p.status, DEV_BAD_INPUT);
     return;
   }
-  constexpr int kBytes = kE4m3 ? 8 : 16;  // of a piece in the cache
-  uint8_t* kc = static_cast<uint8_t*>(p.k_cache) + row0 * (kPer * kBytes) + pieces.piece * kBytes;
-  uint8_t* vc = static_cast<uint8_t*>(p.v_cache) + row0 * (kPer * kBytes) + pieces.piece * kBytes;
+  uint8_t* kc = static_cast<uint8_t*>(p.k_cache) + row0 * kRow + lane % kPer * kPiece;
+  uint8_t* vc = static_cast<uint8_t*>(p.v_cache) + row0 * kRow + lane % kPer * kPiece;
+  uint8_t* ec = kE4m3 ? p.kv_exp + row0 * 2 : nullptr;
+  for (;;) {
+    const Pieces<D> pieces(c0, lane, p.Hkv);
 #pragma unroll
-  for (int j = 0; j < kPieces; ++j) {
-    int head;
-    bool is_v;
-    const bool ok = pieces.get(j, head, is_v);
-    const long long down = (long long)head * p.page_size;  // cache rows from head 0's
-    uint8_t* dst = (is_v ? vc : kc) + down * (kPer * kBytes);
-    if constexpr (!kE4m3) {
-      if (ok) *reinterpret_cast<uint4*>(dst) = w[j];
-    } else {
-      uint32_t m = amax8(w[j]);  // the kPer lanes of one row agree on it
-#pragma unroll
-      for (int off = kPer / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-      if (__any_sync(0xffffffffu, m >= 0x7F80u)) {
-        m = finite_amax8(w[j]);
+    for (int j = 0; j < kPieces; ++j) {
+      int head;
+      bool is_v;
+      const bool ok = pieces.get(j, head, is_v);
+      const uint32_t down = (uint32_t)(head * p.page_size);  // cache rows from head 0's
+      uint8_t* dst = (is_v ? vc : kc) + (size_t)down * kRow;
+      if constexpr (!kE4m3) {
+        if (ok) *reinterpret_cast<uint4*>(dst) = w[j];
+      } else {
+        uint32_t m = amax8(w[j]);  // the kPer lanes of one row agree on it
 #pragma unroll
         for (int off = kPer / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-        w[j] = make_uint4(nonfinite_to_nan(w[j].x), nonfinite_to_nan(w[j].y), nonfinite_to_nan(w[j].z),
-                          nonfinite_to_nan(w[j].w));
-      }
-      const uint32_t byte = scale_byte(m);
-      const float inv = __uint_as_float((254u - byte) << 23);  // 2^-(byte - 127)
-      if (ok) {
-        *reinterpret_cast<uint2*>(dst) = encode8(w[j], inv);
-        if (pieces.piece == 0) p.kv_exp[(row0 + down) * 2 + is_v] = (uint8_t)byte;
+        if (__any_sync(0xffffffffu, m >= 0x7F80u)) {
+          m = finite_amax8(w[j]);
+#pragma unroll
+          for (int off = kPer / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+          w[j] = make_uint4(nonfinite_to_nan(w[j].x), nonfinite_to_nan(w[j].y), nonfinite_to_nan(w[j].z),
+                            nonfinite_to_nan(w[j].w));
+        }
+        const uint32_t byte = scale_byte(m);
+        const float inv = __uint_as_float((254u - byte) << 23);  // 2^-(byte - 127)
+        if (ok) {
+          *reinterpret_cast<uint2*>(dst) = encode8(w[j], inv);
+          if (lane % kPer == 0) ec[down * 2ull + is_v] = (uint8_t)byte;
+        }
       }
     }
+    c0 += kChunksPerWarp;
+    if (c0 >= c_end) return;
+    load(w);
   }
+}
+
+// Two e4m3 codes as fp16 (h) times 2^e to a bf16 pair: fp16's fields moved to bf16's stand for
+// the value times 2^-112 (every code but 0 is a normal fp16 number), and one bf16 product with
+// `up` = 2^(112 + e) is exact. For e <= 15.
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h, uint32_t up) {
+  const uint32_t b = ((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(up));
+  return r;
 }
 
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(const CopyArgs a) {
   constexpr int kPer = D / 8;
+  constexpr uint32_t kRow = kE4m3 ? D : 2 * D, kPiece = kRow / kPer;
   const PagedProblem& p = a.p;
   const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0) report_bad_spans(p);
   const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  WarpRow r;
-  r.t = (int)(unit / a.slices);
-  if (r.t >= p.T) return;
-  r.c0 = (int)(unit % a.slices) * kChunksPerWarp;
-  if (!locate(a, lane, r)) return;
-  const long long row0 = cache_row(p, r.b, r.pos, 0);
+  const int t = (int)(unit / a.slices);
+  if (t >= p.T) return;
+  int c0 = (int)(unit % a.slices) * a.per_warp * kChunksPerWarp;
+  const int c_end = imin(c0 + a.per_warp * kChunksPerWarp, 2 * p.Hkv * kPer);
+  int b, pos;
+  if (!locate(p, t, lane, b, pos)) return;
+  const long long row0 = cache_row(p, b, pos, 0);
   if (row0 < 0) {
     if (lane == 0) atomicOr(p.status, DEV_BAD_INPUT);
     return;
   }
-  const Pieces<D> pieces(r.c0, lane, p.Hkv);
-  constexpr int kBytes = kE4m3 ? 8 : 16;
-  const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache) + row0 * (kPer * kBytes) + pieces.piece * kBytes;
-  const uint8_t* vc = static_cast<const uint8_t*>(p.v_cache) + row0 * (kPer * kBytes) + pieces.piece * kBytes;
-  uint4 w[kPieces];
-  uint32_t byte[kPieces];
+  const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache) + row0 * kRow + lane % kPer * kPiece;
+  const uint8_t* vc = static_cast<const uint8_t*>(p.v_cache) + row0 * kRow + lane % kPer * kPiece;
+  const uint8_t* ec = kE4m3 ? p.kv_exp + row0 * 2 : nullptr;
+  const size_t out_row = (size_t)t * p.Hkv * kPer + lane % kPer;
+  uint4* ko = reinterpret_cast<uint4*>(a.out[0]) + out_row;
+  uint4* vo = reinterpret_cast<uint4*>(a.out[1]) + out_row;
+  for (; c0 < c_end; c0 += kChunksPerWarp) {
+    const Pieces<D> pieces(c0, lane, p.Hkv);
+    uint4 w[kPieces];
+    uint32_t byte[kPieces];
 #pragma unroll
-  for (int j = 0; j < kPieces; ++j) {
-    int head;
-    bool is_v;
-    w[j] = make_uint4(0, 0, 0, 0);
-    byte[j] = 127;
-    if (!pieces.get(j, head, is_v)) continue;
-    const long long down = (long long)head * p.page_size;
-    const uint8_t* src = (is_v ? vc : kc) + down * (kPer * kBytes);
-    if constexpr (kE4m3) {
-      const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
-      w[j].x = x.x;
-      w[j].y = x.y;
-      byte[j] = __ldg(p.kv_exp + (row0 + down) * 2 + is_v);
-    } else {
-      w[j] = __ldg(reinterpret_cast<const uint4*>(src));
-    }
-  }
-  const long long out_row = (long long)r.t * p.Hkv;
-#pragma unroll
-  for (int j = 0; j < kPieces; ++j) {
-    int head;
-    bool is_v;
-    if (!pieces.get(j, head, is_v)) continue;
-    if constexpr (kE4m3) {
-      const float s = exp_byte_scale(byte[j]);
-      const uint32_t codes[4] = {w[j].x, w[j].x >> 16, w[j].y, w[j].y >> 16};
-      uint32_t u[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(codes[i]));
-        u[i] = pack_bf16x2(f.x * s, f.y * s);
+    for (int j = 0; j < kPieces; ++j) {
+      int head;
+      bool is_v;
+      w[j] = make_uint4(0, 0, 0, 0);
+      byte[j] = 0;
+      if (!pieces.get(j, head, is_v)) continue;
+      const uint32_t down = (uint32_t)(head * p.page_size);
+      const uint8_t* src = (is_v ? vc : kc) + (size_t)down * kRow;
+      if constexpr (kE4m3) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+        w[j].x = x.x;
+        w[j].y = x.y;
+        byte[j] = __ldg(ec + down * 2ull + is_v);
+      } else {
+        w[j] = __ldg(reinterpret_cast<const uint4*>(src));
       }
-      w[j] = make_uint4(u[0], u[1], u[2], u[3]);
     }
-    reinterpret_cast<uint4*>(is_v ? a.out[1] : a.out[0])[(out_row + head) * kPer + pieces.piece] = w[j];
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      int head;
+      bool is_v;
+      const bool ok = pieces.get(j, head, is_v);
+      if constexpr (kE4m3) {
+        uint32_t h[4];
+        decode4(w[j].x, h[0], h[1]);
+        decode4(w[j].y, h[2], h[3]);
+        if (__any_sync(0xffffffffu, byte[j] > 142u)) {  // e > 15: through fp32
+          const float s = exp_byte_scale(byte[j]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = f16x2_to_float2(h[i]);
+            h[i] = pack_bf16x2(f.x * s, f.y * s);
+          }
+        } else {
+          const uint32_t up = (byte[j] + 112u) * 0x00800080u;  // 2^(112 + e), twice
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = f16x2_to_bf16x2(h[i], up);
+        }
+        w[j] = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+      if (ok) (is_v ? vo : ko)[head * kPer] = w[j];
+    }
   }
 }
 
@@ -236,7 +267,12 @@ cudaError_t launch_copy(const CopyArgs& args, bool write, cudaStream_t st) {
   CopyArgs a = args;
   const int chunks = 2 * p.Hkv * (p.d / 8);
   if (p.T == 0 || chunks == 0) return cudaSuccess;
-  a.slices = ceil_div(chunks, kChunksPerWarp);
+  // A few rows (a decode step) are spread over as many warps as there are slices; long
+  // batches give a warp a whole row, whose sequence and slot it looks up once: both kernels
+  // are bound by their instructions then (prompts of 25000 tokens: 46 us a slice per warp).
+  const int all = ceil_div(chunks, kChunksPerWarp);
+  a.per_warp = (long long)p.T * all > 16384 ? all : 1;
+  a.slices = ceil_div(all, a.per_warp);
   const long long blocks = ((long long)p.T * a.slices + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const unsigned g = (unsigned)blocks, t = kWarps * 32;
