@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(const CopyArgs
 }
 
 // Two e4m3 codes as fp16 (h) times 2^e to a bf16 pair: fp16's fields moved to bf16's stand for
-// the value times 2^-112 (every code but 0 is a normal fp16 number), and one bf16 product with
-// `up` = 2^(112 + e) is exact. For e <= 15.
+// the value times 2^-112 (every code but 0 and NaN is a normal fp16 number), and one bf16
+// product with `up` = 2^(112 + e) is exact. For e <= 15 and codes that are not NaN.
 __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h, uint32_t up) {
   const uint32_t b = ((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u);
   uint32_t r;
@@ -243,7 +243,10 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(const CopyArgs 
         uint32_t h[4];
         decode4(w[j].x, h[0], h[1]);
         decode4(w[j].y, h[2], h[3]);
-        if (__any_sync(0xffffffffu, byte[j] > 142u)) {  // e > 15: through fp32
+        // a byte 0x7F or 0xFF of the codes carries into its top bit
+        const uint32_t k = 0x7F7F7F7Fu, one = 0x01010101u;
+        const bool nan = (((w[j].x & k) + one) | ((w[j].y & k) + one)) & 0x80808080u;
+        if (__any_sync(0xffffffffu, nan || byte[j] > 142u)) {  // NaN, or e > 15: through fp32
           const float s = exp_byte_scale(byte[j]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {

@@ -400,7 +400,10 @@ attn_status attn_cache_read(const attn_paged_cache* cache, void* k, void* v,
  * max_seq_len <= split_keys no merge runs and no workspace is needed. workspace: DEVICE
  * memory of attn_prefill_workspace_size bytes, 256-byte aligned, not shared with a
  * concurrent call (two captured graphs that may run at the same time need one each).
- * An e4m3 cache is attended to as the values its codes stand for.
+ * An e4m3 cache is attended to as the values its codes stand for: exactly while the scales
+ * of the keys of one 128-key tile lie within 2^15 of each other, and within bf16's rounding
+ * up to 2^24. A NaN or infinity in the V row of a cached token reaches every query row of
+ * the tiles that hold the token, those that mask it too (0 * NaN); K rows do not.
  */
 attn_status attn_prefill_paged(const attn_paged_cache* cache, const void* q,
                                long long q_token_stride, long long q_head_stride, void* o,

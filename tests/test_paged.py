@@ -435,6 +435,104 @@ def test_prefill_bad_device_inputs(kind):
     assert ea.device_status() == 0
 
 
+def test_read_every_scale():
+    """Every code under every scale byte: the rounded bf16 of code * 2^(byte - 127)."""
+    ea = _ea()
+    codes = torch.arange(256, dtype=torch.int32).to(torch.uint8).reshape(1, 2, 128)
+    n = 255
+    kc = codes.repeat(n, 1, 1)                       # token t, heads 0 and 1, half the codes each
+    pages, page = 16, 16
+    cache = torch.zeros(pages, 2, page, 128, dtype=torch.uint8)
+    ex = torch.zeros(pages, 2, page, 2, dtype=torch.uint8)
+    t = torch.arange(n)
+    cache[t // page, :, t % page] = kc
+    ex[t // page, :, t % page] = t.to(torch.uint8)[:, None, None].expand(-1, 2, 2)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    k, v = ea.cache_read(cache.cuda(), cache.cuda(), table, i32(0, n), i32(n), n, kv_exp=ex.cuda())
+    assert ea.device_status() == 0
+    want = torch.from_numpy(P.decode(kc.numpy(), t.to(torch.uint8)[:, None].expand(-1, 2).numpy()))
+    want = want.float().to(torch.bfloat16)           # exact in fp32, or beyond its largest number
+    for got in (k.cpu(), v.cpu()):
+        nan = torch.isnan(want)
+        assert torch.equal(torch.isnan(got), nan)
+        assert torch.equal(got[~nan].view(torch.int16), want[~nan].view(torch.int16))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_caches_past_32_bits(kind):
+    """Pages whose byte offsets pass 2^32 (and, for bf16, element offsets too): written, read
+    back, attended to and decoded like the same pages at the front of a small pool."""
+    ea = _ea()
+    w = Batch([200, 1, 3], [300, 700, 3], Hq=8, Hkv=4, d=128, page=64, kind=kind, seed=50)
+    c = w.cuda()
+    row_bytes = 128 * (2 if kind == "bf16" else 1)
+    far = (1 << 32) * 9 // 8 // (row_bytes * 4 * 64)         # first page past 2^32 bytes, and on
+    big = dict(c)
+    for n in ("k_cache", "v_cache", "kv_exp"):
+        if c[n] is not None:
+            t = torch.empty((far + w.pages,) + tuple(c[n].shape[1:]), dtype=c[n].dtype, device="cuda")
+            t[far:] = c[n]
+            big[n] = t
+    big["table"] = torch.where(c["table"] >= 0, c["table"] + far, c["table"])
+    for x in (c, big):
+        _write(w, x)
+    for n in ("k_cache", "v_cache", "kv_exp"):
+        if c[n] is not None:
+            view = torch.int16 if kind == "bf16" else torch.uint8
+            assert torch.equal(big[n][far:].view(view), c[n].view(view))
+    outs = []
+    for x in (c, big):
+        kv = ea.cache_read(x["k_cache"], x["v_cache"], x["table"], x["offsets"], x["seq_lens"], w.rows,
+                           kv_exp=x["kv_exp"])
+        o = run_prefill(w, x, split=128)
+        d = ea.decode_paged(x["q"][:3].reshape(3, 8, 1, 128), x["k_cache"], x["v_cache"], x["table"],
+                            x["seq_lens"], kv_exp=x["kv_exp"])
+        outs.append(kv + o + d)
+    torch.cuda.synchronize()
+    assert ea.device_status() == 0
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_bf16_cache_from_prompt_to_decode():
+    """The bf16 path a serving step takes: prompts written, attended to in chunks, then decode
+    steps by attn_decode_paged on the cache that cache_write filled."""
+    ea = _ea()
+    w = Batch([37, 5, 80], [37, 5, 80], Hq=8, Hkv=2, d=128, page=16, seed=51)
+    c = w.cuda()
+    _write(w, c)
+    w.k_cache, w.v_cache, _ = w.written()
+    o, lse = run_prefill(w, c)
+    check_attention(o, lse, oracle(w), "prompts")
+    last = torch.tensor([36, 41, 121], device="cuda")         # the newest token of each sequence
+    od, ld = ea.decode_paged(c["q"][last][:, :, None].contiguous(), c["k_cache"], c["v_cache"],
+                             c["table"], c["seq_lens"])
+    ref = [x[last.cpu().numpy()] for x in oracle(w)]
+    check_attention(od[:, :, 0], ld[:, :, 0], ref, "decode on the written cache")
+    assert ea.device_status() == 0
+
+
+def test_two_streams_at_once():
+    """Calls with workspaces of their own on two streams: each gets the result it gets alone."""
+    ea = _ea()
+    ws = [Batch([20, 3, 150], [900, 700, 400], d=128, kind=k, seed=52) for k in KINDS]
+    cs = [w.cuda() for w in ws]
+    alone = [run_prefill(w, c, split=256) for w, c in zip(ws, cs)]
+    streams = [torch.cuda.Stream() for _ in ws]
+    for _ in range(5):
+        outs = []
+        for w, c, st in zip(ws, cs, streams):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                outs.append(ea.prefill_paged(c["q"], c["k_cache"], c["v_cache"], c["table"], c["offsets"],
+                                             c["seq_lens"], kv_exp=c["kv_exp"], split_keys=256,
+                                             mask_kind=MASK_CAUSAL))
+        torch.cuda.synchronize()
+        for (o, z), (o1, z1) in zip(outs, alone):
+            assert torch.equal(o, o1) and torch.equal(z, z1)
+
+
 # ------------------------------------------------------------------ decode over e4m3
 def run_decode(w, nq, *, mask=MASK_NONE, window=0, score=0, softcap=7.0, split=128, max_seq_len=None):
     ea = _ea()
