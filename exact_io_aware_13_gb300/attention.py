@@ -121,7 +121,7 @@ def _check_tensors(*ts):
 
 def _check_call(dtyped):
     """_check_tensors and _check_dtypes in one pass over (tensor or None, dtype, name)."""
-    device = _current_device() if torch.cuda.is_initialized() else -1
+    device = _current_device() if torch.cuda.is_initialized() else None
     for t, dtype, name in dtyped:
         if t is None:
             continue
@@ -402,6 +402,52 @@ def prefill_workspace_size(T: int, Hq: int, d: int, max_seq_len: int, split_keys
     return _prefill_workspace_size(int(T), int(Hq), int(d), int(max_seq_len), int(split_keys))
 
 
+def _workspace_bytes(workspace) -> int:
+    if workspace is None:
+        return 0
+    _check_tensors(workspace)
+    return workspace.numel() * workspace.element_size()
+
+
+def _decode_inputs(q, k_cache, v_cache, page_table, seq_lens, kv_exp, *outputs):
+    """Checks of a decode call's tensors (`outputs`: further (tensor, dtype, name) triples);
+    (B, Hq, Nq, d, num_pages, Hkv, page_size, max_pages)."""
+    kind = _BF16 if kv_exp is None else _U8
+    _check_call(((q, _BF16, "q"), (k_cache, kind, "k_cache"), (v_cache, kind, "v_cache"),
+                 (kv_exp, _U8, "kv_exp"), (page_table, _I32, "page_table"),
+                 (seq_lens, _I32, "seq_lens"), *outputs))
+    shape, cache_shape, table_shape = q.shape, k_cache.shape, page_table.shape
+    if len(shape) != 4:
+        raise ValueError("q must be [B, Hq, Nq, d]")
+    if len(cache_shape) != 4 or cache_shape[3] != shape[3] or v_cache.shape != cache_shape:
+        raise ValueError("k_cache and v_cache must be [pages, Hkv, page_size, d]")
+    if len(table_shape) != 2 or table_shape[0] != shape[0] or seq_lens.shape != shape[:1]:
+        raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
+    if kv_exp is not None and kv_exp.shape != (*cache_shape[:3], 2):
+        raise ValueError("kv_exp must be [pages, Hkv, page_size, 2]")
+    return (*shape, *cache_shape[:3], table_shape[1])
+
+
+def _decode_launch(dims, q, k_cache, v_cache, page_table, seq_lens, kv_exp, o, lse, workspace,
+                   ws_bytes, max_seq_len, split_keys, scale, mask_kind, window, score_kind,
+                   softcap, stream) -> None:
+    B, Hq, Nq, d, num_pages, Hkv, page_size, max_pages = dims
+    mp, sp, _keep = _mask_score_params(window, softcap)
+    if kv_exp is not None:
+        cache = _lib.PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), kv_exp.data_ptr(),
+                                page_table.data_ptr(), 1, num_pages, Hkv, page_size, d, max_pages)
+        _lib.check(_lib.load().attn_decode_paged_e4m3(
+            cache, q.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Nq,
+            int(max_seq_len), int(split_keys), scale, mask_kind, mp, score_kind, sp,
+            _ptr(workspace), ws_bytes, _stream(stream)), "attn_decode_paged_e4m3")
+        return
+    _lib.check(_lib.load().attn_decode_paged(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+        seq_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Nq, d, num_pages, page_size,
+        max_pages, int(max_seq_len), int(split_keys), scale, mask_kind, mp, score_kind, sp,
+        _ptr(workspace), ws_bytes, _stream(stream)), "attn_decode_paged")
+
+
 def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspace, *,
                       max_seq_len: int, split_keys: int, scale: float,
                       mask_kind: int = MASK_NONE, window: int = 0, score_kind: int = SCORE_NONE,
@@ -411,55 +457,26 @@ def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspa
     seq_lens int32 [B]; writes o and lse. With kv_exp (uint8 [pages, Hkv, page_size, 2]) the
     caches hold e4m3 codes as uint8, as paged.cache_write fills them, and
     attn_decode_paged_e4m3 runs."""
-    kind = _BF16 if kv_exp is None else _U8
-    _check_call(((q, _BF16, "q"), (k_cache, kind, "k_cache"), (v_cache, kind, "v_cache"),
-                 (o, _BF16, "o"), (lse, _F32, "lse"), (kv_exp, _U8, "kv_exp"),
-                 (page_table, _I32, "page_table"), (seq_lens, _I32, "seq_lens")))
-    ws_bytes = 0
-    if workspace is not None:
-        _check_tensors(workspace)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    shape = q.shape
-    if len(shape) != 4 or o.shape != shape or lse.shape != shape[:-1]:
+    dims = _decode_inputs(q, k_cache, v_cache, page_table, seq_lens, kv_exp, (o, _BF16, "o"),
+                          (lse, _F32, "lse"))
+    if o.shape != q.shape or lse.shape != q.shape[:-1]:
         raise ValueError("q, o must be [B, Hq, Nq, d] and lse [B, Hq, Nq]")
-    B, Hq, Nq, d = shape
-    num_pages, Hkv, page_size, dk = cache_shape = k_cache.shape
-    if dk != d or v_cache.shape != cache_shape:
-        raise ValueError("k_cache and v_cache must be [pages, Hkv, page_size, d]")
-    table_shape = page_table.shape
-    if len(table_shape) != 2 or table_shape[0] != B or seq_lens.shape != (B,):
-        raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
-    if kv_exp is not None and kv_exp.shape != (num_pages, Hkv, page_size, 2):
-        raise ValueError("kv_exp must be [pages, Hkv, page_size, 2]")
-    mp, sp, _keep = _mask_score_params(window, softcap)
-    if kv_exp is not None:
-        cache = _lib.PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), kv_exp.data_ptr(),
-                                page_table.data_ptr(), 1, num_pages, Hkv, page_size, d,
-                                table_shape[1])
-        _lib.check(_lib.load().attn_decode_paged_e4m3(
-            cache, q.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Nq,
-            int(max_seq_len), int(split_keys), scale, mask_kind, mp, score_kind, sp,
-            _ptr(workspace), ws_bytes, _stream(stream)), "attn_decode_paged_e4m3")
-        return
-    st = _lib.load().attn_decode_paged(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(o),
-        _ptr(lse), B, Hq, Hkv, Nq, d, num_pages, page_size, table_shape[1],
-        int(max_seq_len), int(split_keys), scale, mask_kind, mp, score_kind, sp,
-        _ptr(workspace), ws_bytes, _stream(stream))
-    _lib.check(st, "attn_decode_paged")
+    _decode_launch(dims, q, k_cache, v_cache, page_table, seq_lens, kv_exp, o, lse, workspace,
+                   _workspace_bytes(workspace), max_seq_len, split_keys, scale, mask_kind, window,
+                   score_kind, softcap, stream)
 
 
 def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, max_seq_len: Optional[int] = None,
                  split_keys: Optional[int] = None, total_kv_tokens: Optional[int] = None,
                  scale: Optional[float] = None, mask_kind: int = MASK_NONE, window: int = 0,
                  score_kind: int = SCORE_NONE, softcap: float = 0.0, kv_exp=None, stream=None):
-    """Allocating wrapper of decode_paged_into: returns (o, lse). max_seq_len defaults to
+    """Allocating form of decode_paged_into: returns (o, lse). max_seq_len defaults to
     the page table's capacity; split_keys to the library's choice for total_kv_tokens
     (default B * max_seq_len). kv_exp selects an e4m3 cache."""
-    B, Hq, Nq, d = q.shape
-    _, Hkv, page_size, _ = k_cache.shape
+    dims = _decode_inputs(q, k_cache, v_cache, page_table, seq_lens, kv_exp)
+    B, Hq, Nq, d, _, Hkv, page_size, max_pages = dims
     if max_seq_len is None:
-        max_seq_len = page_table.shape[1] * page_size
+        max_seq_len = max_pages * page_size
     if split_keys is None:
         total = total_kv_tokens or B * max_seq_len
         if kv_exp is None:
@@ -468,16 +485,14 @@ def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, max_seq_len: Opti
             split_keys = prefill_split_keys(1, B, B * Nq, Hq, Hkv, Nq, max_seq_len, total)
     if scale is None:
         scale = float(d) ** -0.5
+    o = torch.empty_like(q)
     device = q.device
-    o = torch.empty((B, Hq, Nq, d), dtype=_BF16, device=device)
     lse = torch.empty((B, Hq, Nq), dtype=_F32, device=device)
     if kv_exp is None:
         nbytes = decode_workspace_size(B, Hq, Hkv, Nq, d, max_seq_len, split_keys)
     else:
         nbytes = prefill_workspace_size(B * Nq, Hq, d, max_seq_len, split_keys)
     ws = torch.empty((nbytes,), dtype=_U8, device=device) if nbytes else None
-    decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, ws,
-                      max_seq_len=max_seq_len, split_keys=split_keys, scale=scale,
-                      mask_kind=mask_kind, window=window, score_kind=score_kind, softcap=softcap,
-                      kv_exp=kv_exp, stream=stream)
+    _decode_launch(dims, q, k_cache, v_cache, page_table, seq_lens, kv_exp, o, lse, ws, nbytes,
+                   max_seq_len, split_keys, scale, mask_kind, window, score_kind, softcap, stream)
     return o, lse

@@ -16,7 +16,7 @@ import torch
 
 from . import _lib
 from .attention import (MASK_NONE, SCORE_NONE, _BF16, _F32, _I32, _U8, _check_call,
-                        _check_tensors, _current_device, _mask_score_params, _ptr, _stream,
+                        _current_device, _mask_score_params, _ptr, _stream, _workspace_bytes,
                         prefill_split_keys, prefill_workspace_size)
 
 CACHE_BF16, CACHE_E4M3 = 0, 1
@@ -103,6 +103,16 @@ def cache_read(k_cache, v_cache, page_table, offsets, seq_lens, n_tokens: int, *
     return k, v
 
 
+def _prefill_launch(cache, B, q_rows, T, Hq, offsets, seq_lens, o, lse, workspace, ws_bytes,
+                    max_new, max_seq_len, split_keys, scale, mask_kind, window, score_kind,
+                    softcap, stream) -> None:
+    mp, sp, _keep = _mask_score_params(window, softcap)
+    _lib.check(_lib.load().attn_prefill_paged(
+        cache, *q_rows, o.data_ptr(), lse.data_ptr(), offsets.data_ptr(), seq_lens.data_ptr(), B, T,
+        Hq, int(max_new), int(max_seq_len), int(split_keys), scale, mask_kind, mp, score_kind, sp,
+        _ptr(workspace), ws_bytes, _stream(stream)), "attn_prefill_paged")
+
+
 def prefill_paged_into(q, k_cache, v_cache, page_table, offsets, seq_lens, o, lse, workspace, *,
                        max_new: int, max_seq_len: int, split_keys: int, scale: float,
                        kv_exp=None, mask_kind: int = MASK_NONE, window: int = 0,
@@ -112,22 +122,15 @@ def prefill_paged_into(q, k_cache, v_cache, page_table, offsets, seq_lens, o, ls
     behind offsets[B] keep what they held."""
     cache, B = _cache(k_cache, v_cache, page_table, kv_exp, offsets, seq_lens, (o, _BF16, "o"),
                       (lse, _F32, "lse"))
-    ws_bytes = 0
-    if workspace is not None:
-        _check_tensors(workspace)
-        ws_bytes = workspace.numel() * workspace.element_size()
     shape = q.shape
     if len(shape) != 3:
         raise ValueError("q must be [T, Hq, d]")
-    T, Hq, _ = shape
-    qp, qt, qh = _rows(q, Hq, cache.d, "q")
+    q_rows = _rows(q, shape[1], cache.d, "q")
     if o.shape != shape or lse.shape != shape[:2]:
         raise ValueError("o must be [T, Hq, d] and lse [T, Hq]")
-    mp, sp, _keep = _mask_score_params(window, softcap)
-    _lib.check(_lib.load().attn_prefill_paged(
-        cache, qp, qt, qh, o.data_ptr(), lse.data_ptr(), offsets.data_ptr(), seq_lens.data_ptr(),
-        B, T, Hq, int(max_new), int(max_seq_len), int(split_keys), scale, mask_kind, mp,
-        score_kind, sp, _ptr(workspace), ws_bytes, _stream(stream)), "attn_prefill_paged")
+    _prefill_launch(cache, B, q_rows, shape[0], shape[1], offsets, seq_lens, o, lse, workspace,
+                    _workspace_bytes(workspace), max_new, max_seq_len, split_keys, scale,
+                    mask_kind, window, score_kind, softcap, stream)
 
 
 def prefill_paged(q, k_cache, v_cache, page_table, offsets, seq_lens, *, kv_exp=None,
@@ -135,29 +138,30 @@ def prefill_paged(q, k_cache, v_cache, page_table, offsets, seq_lens, *, kv_exp=
                   split_keys: Optional[int] = None, total_kv_tokens: Optional[int] = None,
                   scale: Optional[float] = None, mask_kind: int = MASK_NONE, window: int = 0,
                   score_kind: int = SCORE_NONE, softcap: float = 0.0, stream=None):
-    """Allocating wrapper of prefill_paged_into: (o, lse) of the chunks' rows. max_new (the
+    """Allocating form of prefill_paged_into: (o, lse) of the chunks' rows. max_new (the
     longest chunk) defaults to T, max_seq_len to the page table's capacity, split_keys to
     the library's choice (total_kv_tokens, the sum of seq_lens when the caller knows it,
     lets it weigh long sequences against short ones)."""
-    T, Hq, d = q.shape
-    B = seq_lens.shape[0]
+    cache, B = _cache(k_cache, v_cache, page_table, kv_exp, offsets, seq_lens)
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError("q must be [T, Hq, d]")
+    T, Hq, d = shape
+    q_rows = _rows(q, Hq, cache.d, "q")
     if max_seq_len is None:
-        max_seq_len = page_table.shape[1] * k_cache.shape[2]
+        max_seq_len = cache.max_pages_per_seq * cache.page_size
     if max_new is None:
         max_new = T
     if split_keys is None:
-        split_keys = prefill_split_keys(CACHE_BF16 if kv_exp is None else CACHE_E4M3, B, T, Hq,
-                                        k_cache.shape[1], max_new, max_seq_len,
+        split_keys = prefill_split_keys(cache.kind, B, T, Hq, cache.Hkv, max_new, max_seq_len,
                                         total_kv_tokens or B * max_seq_len)
     if scale is None:
         scale = float(d) ** -0.5
     device = q.device
-    o = torch.empty((T, Hq, d), dtype=_BF16, device=device)
+    o = torch.empty(shape, dtype=_BF16, device=device)
     lse = torch.empty((T, Hq), dtype=_F32, device=device)
     nbytes = prefill_workspace_size(T, Hq, d, max_seq_len, split_keys)
     ws = torch.empty((nbytes,), dtype=_U8, device=device) if nbytes else None
-    prefill_paged_into(q, k_cache, v_cache, page_table, offsets, seq_lens, o, lse, ws,
-                       max_new=max_new, max_seq_len=max_seq_len, split_keys=split_keys,
-                       scale=scale, kv_exp=kv_exp, mask_kind=mask_kind, window=window,
-                       score_kind=score_kind, softcap=softcap, stream=stream)
+    _prefill_launch(cache, B, q_rows, T, Hq, offsets, seq_lens, o, lse, ws, nbytes, max_new,
+                    max_seq_len, split_keys, scale, mask_kind, window, score_kind, softcap, stream)
     return o, lse

@@ -163,3 +163,21 @@ def test_prefill_sizes(lib):
         # a few rows over long caches: split
         assert split(kind, 16, 128, 32, 8, 8, 32768, 16 * 20000, 152) < 32768
         assert split(kind, 0, 0, 8, 8, 0, 0, 0, 152) == 128
+
+
+def test_binding_refuses_cpu_tensors():
+    """CPU tensors never reach the library, also where CUDA was never initialised."""
+    import torch
+
+    import exact_io_aware_13_gb300 as ea
+    bf = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    rows = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        ea.cache_write(rows, rows, bf, bf, i32(1, 4), i32(2), i32(1))
+    with pytest.raises(ValueError):
+        ea.cache_read(bf, bf, i32(1, 4), i32(2), i32(1), 3)
+    with pytest.raises(ValueError):
+        ea.prefill_paged(rows, bf, bf, i32(1, 4), i32(2), i32(1))
+    with pytest.raises(ValueError):
+        ea.decode_paged(rows[None], bf, bf, i32(1, 4), i32(1))
