@@ -6,10 +6,12 @@
 // is a power of two because a floating-point code loses nothing by it, and because
 // code * 2^e is then exact in bf16 and in the attention kernels' fp16 operands.
 //
-// Both directions move each byte once and compute next to nothing: they are bound by HBM
-// for long batches and by the chain of dependent loads (offsets, lengths, page table) for
-// a decode step. A warp owns one packed row's slice of kChunksPerWarp 16-byte pieces, all
-// of them in flight at once; the row's values are fetched before its slot is known.
+// Both directions move each byte once: bound by HBM for long batches if the instructions per
+// byte stay few, and by the chain of dependent loads (offsets, lengths, page table) for a
+// decode step. A warp takes a packed row, or a slice of it, kChunksPerWarp 16-byte pieces at
+// a time, all in flight at once; a row's first values are fetched before its slot is known.
+// Measured (Hkv = 8, d = 128): 78000 tokens from e4m3 back to bf16 in 91 us = 6.6 TB/s;
+// 25000 prompt tokens into e4m3 in 34 us = 5.2 TB/s (the quantiser's instructions).
 #include "paged.cuh"
 
 namespace attn {

@@ -20,6 +20,12 @@
 //     With the 128-byte swizzle every such shared-memory read is free of bank conflicts;
 //   * P^T's fragment is S^T's, transposed by movmatrix: no shared memory in between.
 //
+// Measured: decode of 64 sequences of 512 to 8192 tokens (Hq = 32, Hkv = 8, d = 128) 88 us in
+// the kernel, 5.8 TB/s of HBM (85 % of the copy rate); the whole call with the merge 96 us.
+// Two sequences of 131072: 101 us. 8 new tokens of 16 sequences (32 rows): 254 us, bound by
+// its instructions (39 per key and kv head), half of them the conversions that both warps of
+// a tile repeat.
+//
 // Number ranges (fp16 operands, fp32 sums). Q: each row times a power of two that brings its
 // largest magnitude to [2^14, 2^15) - exact but for elements below 2^-29 of it, which lose
 // bits below 2^-39 of it. P: 2^(s - m + 11) <= 2^15 (the running maximum m may lag by 2^4),

@@ -400,9 +400,9 @@ attn_status attn_cache_read(const attn_paged_cache* cache, void* k, void* v,
  * max_seq_len <= split_keys no merge runs and no workspace is needed. workspace: DEVICE
  * memory of attn_prefill_workspace_size bytes, 256-byte aligned, not shared with a
  * concurrent call (two captured graphs that may run at the same time need one each).
- * An e4m3 cache is attended to as the values its codes stand for: exactly while the scales
- * of the keys of one 128-key tile lie within 2^15 of each other, and within bf16's rounding
- * up to 2^24. A NaN or infinity in the V row of a cached token reaches every query row of
+ * An e4m3 cache is attended to as the values its codes stand for: exactly while the K scales,
+ * and the V scales, of the keys that a query's tile walks over lie within 2^15 of each
+ * other, and within bf16's rounding up to 2^24 (attn_decode_paged_e4m3 too). A NaN or infinity in the V row of a cached token reaches every query row of
  * the tiles that hold the token, those that mask it too (0 * NaN); K rows do not.
  */
 attn_status attn_prefill_paged(const attn_paged_cache* cache, const void* q,
