@@ -107,6 +107,24 @@ def load() -> ctypes.CDLL:
     return lib
 
 
+_binding = None
+
+
+def binding():
+    """The compiled binding of the paged-cache calls (csrc/binding.cpp)."""
+    global _binding
+    if _binding is None:
+        load()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise RuntimeError(
+                f"{os.path.join(PKG, '_binding.so')} cannot be loaded ({e}): build it first "
+                "(python -c 'import __graft_entry__ as g; g.build()').") from e
+        _binding = module
+    return _binding
+
+
 class AttnError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status

@@ -6,7 +6,6 @@ of the computation runs in the library's CUDA kernels.
 from __future__ import annotations
 
 import ctypes
-import functools
 from typing import Optional
 
 import torch
@@ -48,16 +47,6 @@ def _params(mask_kind: int, window: int, doc_offsets: Optional[torch.Tensor],
     return ctypes.byref(mp), ctypes.byref(sp), (mp, sp)
 
 
-_PLAIN = _params(0, 0, None, 0.0)  # no window, no document table, no soft-cap: never written
-
-
-def _mask_score_params(window: int, softcap: float):
-    """_params of the paged calls, which take neither documents nor dropout."""
-    if window == 0 and softcap == 0.0:
-        return _PLAIN
-    return _params(0, window, None, softcap)
-
-
 def _score_kind(score_kind: int, dropout_p: float) -> int:
     """Dropout is switched on by a positive drop probability."""
     return int(score_kind) | (SCORE_DROPOUT if dropout_p > 0 else 0)
@@ -71,7 +60,7 @@ def _dims(q: torch.Tensor, k: torch.Tensor):
     return B, Hq, Hkv, Nq, Nkv, d
 
 
-_BF16, _F32, _U8, _I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
 
 
 def _check_dtypes(*named):
@@ -117,18 +106,6 @@ def _check_tensors(*ts):
     if index is not None and index != _current_device():
         raise ValueError(f"tensors are on cuda:{index}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-
-
-def _check_call(dtyped):
-    """_check_tensors and _check_dtypes in one pass over (tensor or None, dtype, name)."""
-    device = _current_device() if torch.cuda.is_initialized() else None
-    for t, dtype, name in dtyped:
-        if t is None:
-            continue
-        if t.dtype is not dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.get_device() != device or not t.is_contiguous():
-            _check_tensors(*(x for x, _, _ in dtyped))
 
 
 def fwd_into(q, k, v, o, lse, *, scale: float, mask_kind: int = MASK_NONE, window: int = 0,
@@ -356,96 +333,15 @@ def _num_sms() -> int:
 def decode_split_keys(B: int, Hq: int, Hkv: int, Nq: int, total_kv_tokens: int,
                       num_sms: Optional[int] = None) -> int:
     """The library's split size for a decode call (keys per chunk)."""
-    if num_sms is None:
-        num_sms = _num_sms()
-    return _decode_split_keys(int(B), int(Hq), int(Hkv), int(Nq), int(total_kv_tokens),
-                              int(num_sms))
-
-
-# Pure functions of their numbers: a step that asks again with the same ones skips the calls.
-@functools.lru_cache(maxsize=1024)
-def _decode_split_keys(*args: int) -> int:
-    return int(_lib.load().attn_decode_split_keys(*args))
-
-
-@functools.lru_cache(maxsize=1024)
-def _decode_workspace_size(*args: int) -> int:
-    return int(_lib.load().attn_decode_workspace_size(*args))
-
-
-def prefill_split_keys(cache_kind: int, B: int, T: int, Hq: int, Hkv: int, max_new: int,
-                       max_seq_len: int, total_kv_tokens: int,
-                       num_sms: Optional[int] = None) -> int:
-    """The library's split size for a prefill_paged call (keys per chunk)."""
-    return _prefill_split_keys(int(cache_kind), int(B), int(T), int(Hq), int(Hkv), int(max_new),
-                               int(max_seq_len), int(total_kv_tokens),
-                               _num_sms() if num_sms is None else int(num_sms))
-
-
-@functools.lru_cache(maxsize=1024)
-def _prefill_split_keys(*args: int) -> int:
-    return int(_lib.load().attn_prefill_split_keys(*args))
+    return int(_lib.load().attn_decode_split_keys(
+        int(B), int(Hq), int(Hkv), int(Nq), int(total_kv_tokens),
+        _num_sms() if num_sms is None else int(num_sms)))
 
 
 def decode_workspace_size(B: int, Hq: int, Hkv: int, Nq: int, d: int, max_seq_len: int,
                           split_keys: int) -> int:
-    return _decode_workspace_size(int(B), int(Hq), int(Hkv), int(Nq), int(d), int(max_seq_len),
-                                  int(split_keys))
-
-
-@functools.lru_cache(maxsize=1024)
-def _prefill_workspace_size(*args: int) -> int:
-    return int(_lib.load().attn_prefill_workspace_size(*args))
-
-
-def prefill_workspace_size(T: int, Hq: int, d: int, max_seq_len: int, split_keys: int) -> int:
-    return _prefill_workspace_size(int(T), int(Hq), int(d), int(max_seq_len), int(split_keys))
-
-
-def _workspace_bytes(workspace) -> int:
-    if workspace is None:
-        return 0
-    _check_tensors(workspace)
-    return workspace.numel() * workspace.element_size()
-
-
-def _decode_inputs(q, k_cache, v_cache, page_table, seq_lens, kv_exp, *outputs):
-    """Checks of a decode call's tensors (`outputs`: further (tensor, dtype, name) triples);
-    (B, Hq, Nq, d, num_pages, Hkv, page_size, max_pages)."""
-    kind = _BF16 if kv_exp is None else _U8
-    _check_call(((q, _BF16, "q"), (k_cache, kind, "k_cache"), (v_cache, kind, "v_cache"),
-                 (kv_exp, _U8, "kv_exp"), (page_table, _I32, "page_table"),
-                 (seq_lens, _I32, "seq_lens"), *outputs))
-    shape, cache_shape, table_shape = q.shape, k_cache.shape, page_table.shape
-    if len(shape) != 4:
-        raise ValueError("q must be [B, Hq, Nq, d]")
-    if len(cache_shape) != 4 or cache_shape[3] != shape[3] or v_cache.shape != cache_shape:
-        raise ValueError("k_cache and v_cache must be [pages, Hkv, page_size, d]")
-    if len(table_shape) != 2 or table_shape[0] != shape[0] or seq_lens.shape != shape[:1]:
-        raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
-    if kv_exp is not None and kv_exp.shape != (*cache_shape[:3], 2):
-        raise ValueError("kv_exp must be [pages, Hkv, page_size, 2]")
-    return (*shape, *cache_shape[:3], table_shape[1])
-
-
-def _decode_launch(dims, q, k_cache, v_cache, page_table, seq_lens, kv_exp, o, lse, workspace,
-                   ws_bytes, max_seq_len, split_keys, scale, mask_kind, window, score_kind,
-                   softcap, stream) -> None:
-    B, Hq, Nq, d, num_pages, Hkv, page_size, max_pages = dims
-    mp, sp, _keep = _mask_score_params(window, softcap)
-    if kv_exp is not None:
-        cache = _lib.PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), kv_exp.data_ptr(),
-                                page_table.data_ptr(), 1, num_pages, Hkv, page_size, d, max_pages)
-        _lib.check(_lib.load().attn_decode_paged_e4m3(
-            cache, q.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Nq,
-            int(max_seq_len), int(split_keys), scale, mask_kind, mp, score_kind, sp,
-            _ptr(workspace), ws_bytes, _stream(stream)), "attn_decode_paged_e4m3")
-        return
-    _lib.check(_lib.load().attn_decode_paged(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-        seq_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Nq, d, num_pages, page_size,
-        max_pages, int(max_seq_len), int(split_keys), scale, mask_kind, mp, score_kind, sp,
-        _ptr(workspace), ws_bytes, _stream(stream)), "attn_decode_paged")
+    return int(_lib.load().attn_decode_workspace_size(int(B), int(Hq), int(Hkv), int(Nq), int(d),
+                                                      int(max_seq_len), int(split_keys)))
 
 
 def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspace, *,
@@ -457,13 +353,11 @@ def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspa
     seq_lens int32 [B]; writes o and lse. With kv_exp (uint8 [pages, Hkv, page_size, 2]) the
     caches hold e4m3 codes as uint8, as paged.cache_write fills them, and
     attn_decode_paged_e4m3 runs."""
-    dims = _decode_inputs(q, k_cache, v_cache, page_table, seq_lens, kv_exp, (o, _BF16, "o"),
-                          (lse, _F32, "lse"))
-    if o.shape != q.shape or lse.shape != q.shape[:-1]:
-        raise ValueError("q, o must be [B, Hq, Nq, d] and lse [B, Hq, Nq]")
-    _decode_launch(dims, q, k_cache, v_cache, page_table, seq_lens, kv_exp, o, lse, workspace,
-                   _workspace_bytes(workspace), max_seq_len, split_keys, scale, mask_kind, window,
-                   score_kind, softcap, stream)
+    if o is None or lse is None:
+        raise ValueError("o and lse must be tensors")
+    _lib.check(_lib.binding().decode(q, k_cache, v_cache, page_table, seq_lens, kv_exp, stream, o,
+                                     lse, workspace, max_seq_len, split_keys, None, scale,
+                                     mask_kind, window, score_kind, softcap) or 0, "decode_paged")
 
 
 def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, max_seq_len: Optional[int] = None,
@@ -473,26 +367,9 @@ def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, max_seq_len: Opti
     """Allocating form of decode_paged_into: returns (o, lse). max_seq_len defaults to
     the page table's capacity; split_keys to the library's choice for total_kv_tokens
     (default B * max_seq_len). kv_exp selects an e4m3 cache."""
-    dims = _decode_inputs(q, k_cache, v_cache, page_table, seq_lens, kv_exp)
-    B, Hq, Nq, d, _, Hkv, page_size, max_pages = dims
-    if max_seq_len is None:
-        max_seq_len = max_pages * page_size
-    if split_keys is None:
-        total = total_kv_tokens or B * max_seq_len
-        if kv_exp is None:
-            split_keys = decode_split_keys(B, Hq, Hkv, Nq, total)
-        else:
-            split_keys = prefill_split_keys(1, B, B * Nq, Hq, Hkv, Nq, max_seq_len, total)
-    if scale is None:
-        scale = float(d) ** -0.5
-    o = torch.empty_like(q)
-    device = q.device
-    lse = torch.empty((B, Hq, Nq), dtype=_F32, device=device)
-    if kv_exp is None:
-        nbytes = decode_workspace_size(B, Hq, Hkv, Nq, d, max_seq_len, split_keys)
-    else:
-        nbytes = prefill_workspace_size(B * Nq, Hq, d, max_seq_len, split_keys)
-    ws = torch.empty((nbytes,), dtype=_U8, device=device) if nbytes else None
-    _decode_launch(dims, q, k_cache, v_cache, page_table, seq_lens, kv_exp, o, lse, ws, nbytes,
-                   max_seq_len, split_keys, scale, mask_kind, window, score_kind, softcap, stream)
-    return o, lse
+    out = _lib.binding().decode(q, k_cache, v_cache, page_table, seq_lens, kv_exp, stream, None,
+                                None, None, max_seq_len, split_keys, total_kv_tokens, scale,
+                                mask_kind, window, score_kind, softcap)
+    if out.__class__ is int:
+        _lib.check(out, "decode_paged")
+    return out

@@ -1,8 +1,10 @@
-"""Compile libattn.so (the CUDA kernels and the C ABI) in-tree for sm_103a.
+"""Compile libattn.so (the CUDA kernels and the C ABI) in-tree for sm_103a, and _binding.so.
 
 Each .cu file is compiled to an object in parallel with nvcc, then linked into
 exact_io_aware_13_gb300/libattn.so. No CMake, no torch extension machinery: the
-library exports plain C symbols (include/attn.h).
+library exports plain C symbols (include/attn.h). _binding.so is the Python module of the
+paged-cache calls (csrc/binding.cpp, compiled against torch's headers by g++); it links to
+the library next to it.
 """
 from __future__ import annotations
 
@@ -18,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libattn.so")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
 
 SOURCES = ["attn_api.cu", "simt.cu", "fwd_tc.cu", "fwd256_tc.cu", "bwd_tc.cu", "bwd256_tc.cu", "fp8.cu", "decode_tc.cu",
            "decode_copies2.cu", "paged_cache.cu", "paged_attn.cu", "paged_rows.cu",
@@ -54,21 +57,60 @@ def _compile(src: str, extra: list[str], verbose: bool) -> str:
     return obj
 
 
+def _compile_binding(verbose: bool) -> str:
+    """binding.cpp to an object; torch tells where its headers are."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    obj = os.path.join(BUILD_DIR, "binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wno-attributes",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-c", os.path.join(CSRC, "binding.cpp"),
+           "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "lib64")
+    tmp = BINDING_PATH + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libattn.so", "-L", lib, "-ltorch_python",
+           "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-L", cuda, "-lcudart",
+           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _binding.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Build libattn.so if a source is newer than it; return its path."""
-    if (not force and os.path.exists(LIB_PATH)
-            and os.path.getmtime(LIB_PATH) >= _deps_mtime()):
+    """Build libattn.so and _binding.so if a source is newer; return the library's path."""
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _deps_mtime()
+                         for p in (LIB_PATH, BINDING_PATH)):
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     extra = list(extra or [])
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, extra, verbose), SOURCES))
+        binding_obj = binding.result()
     tmp = LIB_PATH + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding_obj)
     return LIB_PATH
 
 
