@@ -91,15 +91,28 @@ int size_of(int64_t n, const char* name) {
   return (int)n;
 }
 
-void* stream_of(PyObject* o) {
-  if (none(o)) return c10::cuda::getCurrentCUDAStream().stream();
-  PyObject* handle = PyObject_GetAttrString(o, "cuda_stream");
-  if (!handle) throw BadArgument{};
-  void* p = PyLong_AsVoidPtr(handle);
-  Py_DECREF(handle);
-  if (!p && PyErr_Occurred()) throw BadArgument{};
-  return p;
-}
+// The stream of a call: the current one, or a torch.cuda.Stream. Tensors made for a call on
+// another stream belong to the current one's allocations: the allocator has to know that they
+// are in use there, or the workspace would be handed out again as soon as the call returns.
+struct Stream {
+  cudaStream_t handle;
+  bool foreign = false;
+  explicit Stream(PyObject* o) {
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream();
+    handle = current.stream();
+    if (none(o)) return;
+    PyObject* value = PyObject_GetAttrString(o, "cuda_stream");
+    if (!value) throw BadArgument{};
+    handle = static_cast<cudaStream_t>(PyLong_AsVoidPtr(value));
+    Py_DECREF(value);
+    if (!handle && PyErr_Occurred()) throw BadArgument{};
+    foreign = handle != current.stream();
+  }
+  void uses(const at::Tensor& t) const {
+    if (foreign && t.defined() && t.numel() > 0)
+      t.record_stream(c10::cuda::getStreamFromExternal(handle, c10::cuda::current_device()).unwrap());
+  }
+};
 
 int num_sms() {
   static int count[64];
@@ -249,21 +262,21 @@ BINDING(cache_write, 9) {
   const Rows k = rows_of(a[0], c.Hkv, c.d, "k"), v = rows_of(a[1], c.Hkv, c.d, "v");
   if (k.T != v.T) fail("k and v disagree on the number of tokens");
   return status(attn_cache_write(&c, k.p, k.token, k.head, v.p, v.token, v.head, b.offsets,
-                                 b.seq_lens, b.B, k.T, stream_of(a[8])));
+                                 b.seq_lens, b.B, k.T, Stream(a[8]).handle));
 }
 
 // k_cache, v_cache, page_table, offsets, seq_lens, kv_exp, stream, k or None, v or None, n_tokens
 BINDING(cache_read, 10) {
   const attn_paged_cache c = cache_of(a[0], a[1], a[2], a[5]);
   const Batch b = batch_of(a[2], a[3], a[4]);
-  void* stream = stream_of(a[6]);
+  const Stream stream(a[6]);
   if (!none(a[7])) {
     const at::Tensor& k = buffer(a[7], at::kBFloat16, "k");
     const at::Tensor& v = buffer(a[8], at::kBFloat16, "v");
     if (k.dim() != 3 || k.size(1) != c.Hkv || k.size(2) != c.d || v.sizes() != k.sizes())
       fail("k and v must be [T, %d, %d]", c.Hkv, c.d);
     return status(attn_cache_read(&c, k.data_ptr(), v.data_ptr(), b.offsets, b.seq_lens, b.B,
-                                  size_of(k.size(0), "k"), stream));
+                                  size_of(k.size(0), "k"), stream.handle));
   }
   const int T = number(a[9], "n_tokens");
   if (T < 0) fail("n_tokens must not be negative");
@@ -271,7 +284,9 @@ BINDING(cache_read, 10) {
   const at::Tensor k = make(like, {T, c.Hkv, c.d}, at::kBFloat16);
   const at::Tensor v = make(like, {T, c.Hkv, c.d}, at::kBFloat16);
   const attn_status s =
-      attn_cache_read(&c, k.data_ptr(), v.data_ptr(), b.offsets, b.seq_lens, b.B, T, stream);
+      attn_cache_read(&c, k.data_ptr(), v.data_ptr(), b.offsets, b.seq_lens, b.B, T, stream.handle);
+  stream.uses(k);
+  stream.uses(v);
   return s == ATTN_OK ? pair(k, v) : status(s);
 }
 
@@ -304,12 +319,16 @@ BINDING(prefill, 20) {
   }
   const Workspace ws(a[10], allocate, like,
                      attn_prefill_workspace_size(q.T, q.H, c.d, max_seq_len, split));
+  const Stream stream(a[7]);
   const attn_status s = attn_prefill_paged(
       &c, q.p, q.token, q.head, o.data_ptr(), static_cast<float*>(lse.data_ptr()), b.offsets, b.seq_lens,
       b.B, q.T, q.H, max_new, max_seq_len, split, sc.scale, sc.mask_kind, &sc.mask, sc.score_kind,
-      &sc.score, ws.p, ws.bytes, stream_of(a[7]));
+      &sc.score, ws.p, ws.bytes, stream.handle);
+  stream.uses(ws.own);
   if (s != ATTN_OK) return status(s);
   if (!allocate) Py_RETURN_NONE;
+  stream.uses(o);
+  stream.uses(lse);
   return pair(o, lse);
 }
 
@@ -350,17 +369,20 @@ BINDING(decode, 18) {
                           : attn_decode_workspace_size(B, Hq, c.Hkv, Nq, c.d, max_seq_len, split));
   const int32_t* seq_lens = static_cast<const int32_t*>(lens.data_ptr());
   float* l = static_cast<float*>(lse.data_ptr());
-  void* stream = stream_of(a[6]);
+  const Stream stream(a[6]);
   const attn_status s =
       e4m3 ? attn_decode_paged_e4m3(&c, q.data_ptr(), seq_lens, o.data_ptr(), l, B, Hq, Nq, max_seq_len,
                                     split, sc.scale, sc.mask_kind, &sc.mask, sc.score_kind, &sc.score,
-                                    ws.p, ws.bytes, stream)
+                                    ws.p, ws.bytes, stream.handle)
            : attn_decode_paged(q.data_ptr(), c.k, c.v, c.page_table, seq_lens, o.data_ptr(), l, B, Hq,
                                c.Hkv, Nq, c.d, c.num_pages, c.page_size, c.max_pages_per_seq,
                                max_seq_len, split, sc.scale, sc.mask_kind, &sc.mask, sc.score_kind,
-                               &sc.score, ws.p, ws.bytes, stream);
+                               &sc.score, ws.p, ws.bytes, stream.handle);
+  stream.uses(ws.own);
   if (s != ATTN_OK) return status(s);
   if (!allocate) Py_RETURN_NONE;
+  stream.uses(o);
+  stream.uses(lse);
   return pair(o, lse);
 }
 

@@ -912,8 +912,8 @@ cudaError_t launch_tiles(const PagedAttention& a, const PagedMaps& maps, cudaStr
   // Row units: at most T G / 256 full ones and one more per sequence.
   const long long per_seq = ((long long)p.max_new * a.G + kUnitRows - 1) / kUnitRows;
   const long long units = imin64((long long)p.T * a.G / kUnitRows + p.B, per_seq * p.B);
-  const long long grid = units * p.Hkv * a.n_chunks;
-  if (grid == 0) return cudaSuccess;
+  // (one CTA at least: it reports chunks that are longer than a max_new of 0)
+  const long long grid = units * p.Hkv * a.n_chunks > 0 ? units * p.Hkv * a.n_chunks : 1;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   const unsigned g = (unsigned)grid;
   const bool al = a.score_kind & ATTN_SCORE_ALIBI, sc = a.score_kind & ATTN_SCORE_SOFTCAP;

@@ -533,6 +533,46 @@ def test_two_streams_at_once():
             assert torch.equal(o, o1) and torch.equal(z, z1)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_given_stream_keeps_the_call_s_tensors(kind):
+    """A call on a stream that is not the current one, queued behind other work there: the
+    workspace and outputs made for it are not handed out again before it has run."""
+    ea = _ea()
+    w = Batch([20, 3, 2], [900, 700, 400], d=128, Hq=8, kind=kind, seed=53)
+    c = w.cuda()
+    q1 = c["q"][:3].reshape(3, 8, 1, 128)
+    want = run_prefill(w, c, split=256)
+    want_d = ea.decode_paged(q1, c["k_cache"], c["v_cache"], c["table"], c["seq_lens"],
+                             kv_exp=c["kv_exp"], split_keys=256)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)                  # some 10 ms
+    got = ea.prefill_paged(c["q"], c["k_cache"], c["v_cache"], c["table"], c["offsets"],
+                           c["seq_lens"], kv_exp=c["kv_exp"], split_keys=256,
+                           mask_kind=MASK_CAUSAL, stream=s)
+    got_d = ea.decode_paged(q1, c["k_cache"], c["v_cache"], c["table"], c["seq_lens"],
+                            kv_exp=c["kv_exp"], split_keys=256, stream=s)
+    msl = c["table"].shape[1] * w.page
+    for T in (w.T, 3):                                 # what the allocator would hand out next
+        n = ea.prefill_workspace_size(T, 8, 128, msl, 256)
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    for a, b in zip(got + got_d, want + want_d):
+        assert torch.equal(a, b)
+    del junk
+    assert ea.device_status() == 0
+
+
+def test_max_new_of_zero_is_reported():
+    ea = _ea()
+    for kind in KINDS:
+        w = Batch([5], [40], Hq=40, Hkv=1, kind=kind, seed=54)
+        run_prefill(w, max_new=0)
+        assert ea.device_status() == 8
+
+
 # ------------------------------------------------------------------ decode over e4m3
 def run_decode(w, nq, *, mask=MASK_NONE, window=0, score=0, softcap=7.0, split=128, max_seq_len=None):
     ea = _ea()
