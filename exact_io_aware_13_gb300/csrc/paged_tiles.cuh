@@ -30,8 +30,8 @@
 // [2^14, 2^15).
 //
 // What bounds it, measured (one chunk of 4096 tokens after 28672 cached ones, Hq = 32, Hkv =
-// 8, d = 128, 2.06 TFLOP): bf16 1355 us = 1520 TFLOP/s, a step of two query tiles against a
-// key tile in 2790 clocks where the MMAs alone need 2048: the chain S -> softmax -> P V of a
+// 8, d = 128, 2.06 TFLOP): bf16 1314 us = 1569 TFLOP/s, a step of two query tiles against a
+// key tile in 2700 clocks where the MMAs alone need 2048: the chain S -> softmax -> P V of a
 // tile, as in the forward kernel. e4m3 1790 us = 1150 TFLOP/s: the softmax of a tile takes
 // 2160 clocks instead of 1310 beside the converters, whose fp16 tiles also cost 512 clocks of
 // shared-memory writes per step (without the conversion: 1440 TFLOP/s). Few rows over long
@@ -49,9 +49,12 @@ constexpr int kQTiles = 2;
 constexpr int kUnitRows = kQTiles * BM;
 constexpr int kLoadKWarp = 8, kMmaWarp = 9, kRelayWarp = 10, kLoadVWarp = 11, kConvWarp = 12;
 constexpr int kInfo = 4;             // slots of the converters' per-tile scales
+// Named barriers: kNbP + 2 t + part: P_t, or half of it, in tensor memory, softmax warpgroup t
+// and the MMA warp; kNbKv + s: operand stage s filled; kNbDual: both softmax warpgroups, before
+// a dual unit's merge.
 constexpr uint32_t kNbP = 1, kNbPCount = 160;
-constexpr uint32_t kNbKv = 3;
-constexpr uint32_t kNbDual = 7;  // both softmax warpgroups, before a dual unit's merge
+constexpr uint32_t kNbKv = 5;
+constexpr uint32_t kNbDual = 9;
 constexpr float kPOffset = 11.0f;    // e4m3: P is scaled by 2^11 (fp16)
 constexpr int kMaxDown = 8;          // e4m3: a V tile's exponent is at least E_ref - 8
 
@@ -67,12 +70,16 @@ struct Shape {
   // launch gives kThreads x kRegsLaunch; the split must not exceed it (launch_variant checks
   // what the compiler used).
   static constexpr int kRegsLaunch = kE4m3 ? 128 : 168;
-  static constexpr int kRegsSoftmax = kE4m3 ? 168 : 200;
-  static constexpr int kRegsOther = kE4m3 ? 88 : 104;
+  static constexpr int kRegsSoftmax = kE4m3 ? 168 : 208;
+  static constexpr int kRegsOther = 88;
   static constexpr int kRegsConvert = 88;
   static_assert(256 * kRegsSoftmax + 128 * kRegsOther + (kE4m3 ? 128 * kRegsConvert : 0) <=
                     kThreads * kRegsLaunch,
                 "register pool");
+  // P is handed to the MMA warp in two halves, so that the first products overlap the second
+  // half's exponentials: long chunk 1361 -> 1314 us over bf16. Over e4m3, whose softmax warps
+  // have fewer registers, six chunks went 689 -> 710 us: one part there.
+  static constexpr int kPParts = kE4m3 ? 1 : 2;
   static constexpr float kLag = kE4m3 ? 4.0f : 8.0f;  // O is rescaled beyond this growth (log2)
 };
 
@@ -515,15 +522,22 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
         }
         mma_commit_if(issuer, smem_u32(&bars->s_full[t]));
       };
-      auto issue_pv = [&](int t, int u, bool add) {  // add: O_t holds earlier products
-        if (!ok) return;
+      // O_t += P_t V, each part as soon as its P is there (add: O_t holds earlier products).
+      auto issue_pv = [&](int t, int u, bool add) {
         const uint32_t colS = t == 0 ? L::kColS0 : L::kColS1;
         const uint32_t colO = t == 0 ? L::kColO0 : L::kColO1;
         const uint64_t dv = smem_desc_sw128(ring + (u % kStages) * L::kTile, L::kChunk, 1024);
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts_if(issuer, tmem + colO, tmem + colS + kk * 8, dv + ((kk * 16 * 128) >> 4), idO,
-                    (add || kk > 0) ? 1u : 0u);
+        for (int part = 0; part < S::kPParts; ++part) {
+          nb_sync(kNbP + 2 * t + part, kNbPCount);
+          tc_fence_after_sync();
+          if (!ok) continue;
+          constexpr int kSteps = BN / 16 / S::kPParts;
+#pragma unroll
+          for (int kk = part * kSteps; kk < (part + 1) * kSteps; ++kk)
+            mma_ts_if(issuer, tmem + colO, tmem + colS + kk * 8, dv + ((kk * 16 * 128) >> 4), idO,
+                      (add || kk > 0) ? 1u : 0u);
+        }
       };
       sync_stage(0);
       if (dual) {  // key tile jj belongs to stream jj & 1; S runs one tile ahead
@@ -537,8 +551,6 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
             commit(&bars->kv_empty[uk % kStages]);
           }
           sync_stage(uv);
-          nb_sync(kNbP + t, kNbPCount);
-          tc_fence_after_sync();
           issue_pv(t, uv, jj > 1);
           commit(&bars->kv_empty[uv % kStages]);
         }
@@ -555,8 +567,6 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
 #pragma unroll
           for (int t = 0; t < kQTiles; ++t) {
             if (j >= t_lo[t] && j < t_hi[t]) {
-              nb_sync(kNbP + t, kNbPCount);
-              tc_fence_after_sync();
               issue_pv(t, uv, np[t] > 0);
               ++np[t];
             }
@@ -649,7 +659,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
         info = bars->info[jj % kInfo];
       }
       if (!live) {  // aborted: keep the barrier schedule with the MMA warp, do nothing else
-        nb_sync(kNbP + t, kNbPCount);
+        for (int part = 0; part < S::kPParts; ++part) nb_sync(kNbP + 2 * t + part, kNbPCount);
         continue;
       }
       tc_fence_after_sync();
@@ -741,6 +751,36 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
           }
           tmem_st8(tS + c * 16 + hf * 8, ph);
         }
+        if ((c + 1) % (4 / S::kPParts) == 0) {  // a part is in: its products may start
+          if (c + 1 == 4 / S::kPParts && warp_grow && n > 0) {
+            if constexpr (S::kPParts == 1) {
+#pragma unroll
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[32];
+                tmem_ld32(tO + q * 32, o);
+                tmem_wait_ld();
+                reg_fence32(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                tmem_st32(tO + q * 32, o);
+              }
+            } else {  // 16 columns at a time: 64 scores are still in registers
+#pragma unroll 1
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t o[16];
+                tmem_ld16(tO + q * 16, o);
+                tmem_wait_ld();
+                reg_fence16(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                tmem_st16(tO + q * 16, o);
+              }
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before_sync();
+          nb_arrive(kNbP + 2 * t + c * S::kPParts / 4, kNbPCount);
+        }
       }
       float acc[8];
 #pragma unroll
@@ -748,21 +788,6 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       const float sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
       // the row sum keeps the plain weights (0 <= E_ref - E_V <= kMaxDown)
       l_run = kE4m3 ? fmaf(sum, __uint_as_float((uint32_t)(127 + info.z - info.y) << 23), l_run) : l_run + sum;
-      if (warp_grow && n > 0) {
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + c * 32, o);
-          tmem_wait_ld();
-          reg_fence32(o);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-          tmem_st32(tO + c * 32, o);
-        }
-      }
-      tmem_wait_st();
-      tc_fence_before_sync();
-      nb_arrive(kNbP + t, kNbPCount);
     }
     // ---------------------------------------------------------- epilogue
     // Every tile waits for the CTA's last MMA: the staging below writes over Q.
