@@ -21,9 +21,12 @@ __global__ void __launch_bounds__(kWarps * 32) paged_merge_kernel(const PagedAtt
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kPerRow;
   const long long unit = ((long long)blockIdx.x * kWarps + warp) / kPerRow;
   const int t = (int)(unit / a.Hq), h = (int)(unit % a.Hq);
-  if (t >= p.T) return;  // (with eight warps per row a CTA has one row)
-  const int b = find_sequence(p, t, lane);
+  const int b = find_sequence(p, imin(t, p.T - 1), lane);
   const Span s = load_span(p, b);
+  // Launched while the attention kernel's last CTAs write their results: everything above
+  // reads inputs only; no thread passes (or leaves) before that kernel has completed.
+  grid_dependency_wait();
+  if (t >= p.T) return;  // (with eight warps per row a CTA has one row)
   const int i = t - s.row0;
   if (i < 0 || i >= s.n) return;
   int lo, hi;
@@ -97,8 +100,16 @@ template <int D, int kPerRow>
 cudaError_t launch_merge_as(const PagedAttention& a, cudaStream_t st) {
   const long long blocks = ((long long)a.p.T * a.Hq * kPerRow + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  paged_merge_kernel<D, kPerRow><<<(unsigned)blocks, kWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, kPerRow>, a);
 }
 cudaError_t launch_merge(const PagedAttention& a, cudaStream_t st) {
   // Eight warps per row once a lone warp would take more than two turns of its four loads,

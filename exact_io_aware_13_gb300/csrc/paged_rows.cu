@@ -483,6 +483,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)  // (168 registe
     for (int i = 0; i < kStages; ++i) drain_wait(full + i * 8, i < s ? parity ^ 1 : parity);
 
   // ---- merge of the key groups: factors 2^(m_k - M) 2^E_k, fixed order
+  grid_dependents_launch();
   __syncthreads();
   constexpr int kRows = NT * 8 * RG;
   float* sm_m = reinterpret_cast<float*>(smem);            // [key group][row]

@@ -790,6 +790,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       l_run = kE4m3 ? fmaf(sum, __uint_as_float((uint32_t)(127 + info.z - info.y) << 23), l_run) : l_run + sum;
     }
     // ---------------------------------------------------------- epilogue
+    grid_dependents_launch();
     // Every tile waits for the CTA's last MMA: the staging below writes over Q.
     const bool mma_done = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->o_full[t]), 0, wc));
     const bool have_o = n > 0 && mma_done;
