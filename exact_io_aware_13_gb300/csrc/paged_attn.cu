@@ -36,13 +36,13 @@ __global__ void __launch_bounds__(kWarps * 32) paged_merge_kernel(const PagedAtt
   const int c_begin = imin(ca + part * each, cb), c_end = imin(c_begin + each, cb);
   const long long rows = (long long)p.T * a.Hq, row = (long long)t * a.Hq + h;
   float M = -INFINITY;
-  for (int c = c_begin + lane; c < c_end; c += 32) M = fmaxf(M, a.part_lse[c * rows + row]);
+  for (int c = c_begin + lane; c < c_end; c += 32) M = max_nan(M, a.part_lse[c * rows + row]);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  for (int off = 16; off > 0; off >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, off));
   float W = 0.f, acc[kC];
 #pragma unroll
   for (int e = 0; e < kC; ++e) acc[e] = 0.f;
-  if (M > -INFINITY)
+  if (M != -INFINITY)  // (a NaN chunk makes the row NaN)
     for (int c0 = c_begin; c0 < c_end; c0 += 4) {  // four chunks' loads in flight
       float l2[4], v[4][kC];
 #pragma unroll
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_merge_kernel(const PagedAtt
     __syncthreads();
     if (part != 0) return;
 #pragma unroll
-    for (int k = 0; k < kPerRow; ++k) M = fmaxf(M, sm[k][D]);
+    for (int k = 0; k < kPerRow; ++k) M = max_nan(M, sm[k][D]);
     W = 0.f;
 #pragma unroll
     for (int e = 0; e < kC; ++e) acc[e] = 0.f;
@@ -88,12 +88,12 @@ __global__ void __launch_bounds__(kWarps * 32) paged_merge_kernel(const PagedAtt
       for (int e = 0; e < kC; ++e) acc[e] = fmaf(f, sm[k][lane * kC + e], acc[e]);
     }
   }
-  const float inv = W > 0.f ? 1.f / W : 0.f;
+  const float inv = W == 0.f ? 0.f : 1.f / W;
 #pragma unroll
   for (int e = 0; e < kC; ++e) acc[e] *= inv;
   PagedAttention out = a;
   out.n_chunks = 1;
-  store_row<D>(out, b, t, i, h, 0, lane, acc, W > 0.f ? M + log2f(W) : -INFINITY);
+  store_row<D>(out, b, t, i, h, 0, lane, acc, W == 0.f ? -INFINITY : M + log2f(W));
 }
 
 template <int D, int kPerRow>

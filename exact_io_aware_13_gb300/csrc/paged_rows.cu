@@ -528,10 +528,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)  // (168 registe
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) acc[e] = f > 0.f ? fmaf(f, src[e], acc[e]) : acc[e];
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (a NaN sum makes the row NaN)
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] *= inv;
-    const float l2 = sum > 0.f ? M - kPOffset + log2f(sum) : -INFINITY;
+    const float l2 = sum == 0.f ? -INFINITY : M - kPOffset + log2f(sum);
     const int i = rr / a.G;
     store_row<D>(a, b, sp.row0 + i, i, hk * a.G + rr - i * a.G, cc, lane, acc, l2);
   }

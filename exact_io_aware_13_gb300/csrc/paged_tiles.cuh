@@ -834,10 +834,10 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
         m_run = M;
       }
     }
-    const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+    const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // (a NaN sum makes the row NaN)
     f0 *= inv;
     f1 *= inv;
-    const float l2 = l_run > 0.f ? m_run + log2f(l_run) - (kE4m3 ? kPOffset : 0.f) : -INFINITY;
+    const float l2 = l_run == 0.f ? -INFINITY : m_run + log2f(l_run) - (kE4m3 ? kPOffset : 0.f);
     const bool mine = !dual || t == 0;  // warp-uniform: this warpgroup writes the rows
     // 32 columns of the finished row
     auto load_o = [&](int c, float (&v)[32]) {

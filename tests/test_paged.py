@@ -324,6 +324,44 @@ def test_prefill_query_magnitudes(kind):
     parity(w, "query magnitudes", mask=MASK_NONE, delta=score_delta(w))
 
 
+def _nan_key(w, b, t):
+    """Makes the K row of token t of sequence b NaN, in every kv head."""
+    page, slot = w.table[b, t // w.page], t % w.page
+    if w.kind == "bf16":
+        w.k_cache[page, :, slot] = float("nan")
+    else:
+        w.k_cache[page, :, slot] = 127
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("split", [128, 1 << 20])
+@pytest.mark.parametrize("n,Hq", [(1, 2), (4, 4), (16, 4), (20, 4), (140, 4), (300, 2)])
+def test_nan_rows_stay_rows(n, Hq, split, kind):
+    """NaN in a query row, and in the K row of a new token under a causal mask: the rows that
+    see it become NaN in O and lse, the others are what they are without it. The lengths put
+    the NaN key into the first, a middle and the last chunk and tile, alone there too."""
+    for mask, at in ((MASK_CAUSAL, 0.5), (MASK_CAUSAL, 0.0), (MASK_NONE, 1.0), (MASK_SLIDING_WINDOW, 0.5)):
+        w = Batch([n, n], [1500, n + 130], Hq=Hq, Hkv=2, d=64, page=16, kind=kind, seed=19)
+        o_ref, l_ref, mag = oracle(w, mask, 5)
+        bad = np.zeros((w.T, Hq), dtype=bool)
+        w.q[n // 2, 1] = float("nan")
+        bad[n // 2, 1] = True
+        for b, L in enumerate(w.lens):
+            key = L - n + min(int(at * n), n - 1)
+            _nan_key(w, b, key)
+            for i in range(n):
+                pos = L - n + i
+                seen = (mask == MASK_NONE or key <= pos) and (mask != MASK_SLIDING_WINDOW or pos - key < 5)
+                bad[b * n + i] |= seen
+        o, lse = run_prefill(w, split=split, mask=mask, window=5)
+        assert _ea().device_status() == 0
+        got = np.isnan(lse.cpu().numpy())
+        assert np.array_equal(got, bad), (mask, at, np.argwhere(got != bad)[:8])
+        assert np.array_equal(np.isnan(o.float().cpu().numpy()).all(-1), bad), (mask, at)
+        l_ref[bad] = np.nan
+        check_attention(o, lse, (o_ref, l_ref, mag), f"NaN beside {mask} {at}")
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_prefill_strided_queries_and_spare_rows(kind):
     """q as a slice of fused rows and head-major; rows behind the last sequence stay."""
@@ -615,6 +653,13 @@ def test_decode_e4m3_row_counts(Hq, Hkv, nq):
     w = Batch([nq] * 4, [nq, 70, 300, 513], Hq=Hq, Hkv=Hkv, d=128, page=32, kind="e4m3", seed=Hq + nq)
     run_decode(w, nq, mask=MASK_CAUSAL, split=192)
     run_decode(w, nq, mask=MASK_CAUSAL, split=1 << 20)
+
+
+@pytest.mark.parametrize("Hq,split", [(33, 64), (40, 192), (150, 64), (260, 320)])
+def test_decode_e4m3_chunks_that_cut_a_tile(Hq, split):
+    """More rows than the row kernel takes, in chunks that are no multiple of a key tile."""
+    run_decode(Batch([1] * 7, LENS, Hq=Hq, Hkv=1, d=64, page=64, kind="e4m3", seed=34), 1,
+               mask=MASK_CAUSAL, split=split)
 
 
 def test_decode_e4m3_long_and_empty():
