@@ -97,9 +97,11 @@ __device__ __forceinline__ uint32_t piece_offset(int row, int piece) {
   return D == 128 ? row * 128 + ((piece ^ (row & 7)) << 4)
                   : row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
 }
-// NT: 8-row groups per warp; RG: warps that share a key tile, each with NT * 8 rows.
+// NT: 8-row groups per warp; RG: warps that share a key tile, each with NT * 8 rows. Three CTAs
+// per SM where 168 registers hold a warp's state: d = 64 at NT = 2 216 -> 190 us (32 rows) and
+// 118 -> 97 us (16 rows) against two; d = 128 at NT = 2 would spill.
 template <int D, int NT, int RG>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)  // (168 registers would spill at NT = 2)
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PagedAttention a) {
   using L = Layout<D>;
