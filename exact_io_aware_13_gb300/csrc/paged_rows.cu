@@ -113,6 +113,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   constexpr int kKeyGroups = kWarps / RG, kStages = kRingTiles / kKeyGroups;
+  constexpr int kTurns = 6;  // release barriers of a pair
+  static_assert(RG == 1 || (RG == 2 && kStages % 2 == 0 && kKeyGroups * kTurns < 16), "named barriers");
   const int kg = warp / RG, rg = warp % RG, row0 = rg * NT * 8;  // key group, first row
   if (blockIdx.x == 0) report_bad_spans(p);
   const int cc = (int)(blockIdx.x % a.n_chunks);
@@ -143,16 +145,37 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
   const uint32_t exps = smem_u32(smem + L::kExp) + kg * kStages * kTile * 2;
   const uint32_t full = smem_u32(bars) + kg * kStages * 8;
 
-  // Requests the key group's next tile into stage s: lane q fetches its q-th page piece.
+  // The query rows' loads are on their way while the first tiles are requested.
+  uint32_t qw[NT][kSteps][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = row0 + nt * 8 + g;
+    const bool ok = r < rows;
+    const int i = ok ? r / a.G : 0, h = hk * a.G + (ok ? r - i * a.G : 0);
+    const long long t = p.offsets ? sp.row0 + i : i;
+    const __nv_bfloat16* q = a.q + (p.offsets ? 0 : b) * a.q_batch + t * a.q_token + h * a.q_head;
+#pragma unroll
+    for (int v = 0; v < kSteps / 2; ++v) {  // 16-byte loads: two steps each
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (ok) x = __ldg(reinterpret_cast<const uint4*>(q + (v >> 1) * 64 + c * 16 + (v & 1) * 8));
+      qw[nt][2 * v][0] = x.x; qw[nt][2 * v][1] = x.y;
+      qw[nt][2 * v + 1][0] = x.z; qw[nt][2 * v + 1][1] = x.w;
+    }
+  }
+
+  // Requests this warp's next tile into stage s: lane q fetches its q-th page piece, whose
+  // page-table entry it loaded at the request before. The warps of a pair take turns (kStages
+  // is even, so a stage stays with its warp): a request costs 600 clocks, a tile 1600.
   const int R = imin(p.page_size, kTile), pieces = kTile / R;
-  constexpr int kStride = kKeyGroups * kTile;
-  int key = (tb + kg) * kTile + lane * R;
+  constexpr int kStride = kKeyGroups * RG * kTile;
+  int key = (tb + kg + kKeyGroups * rg) * kTile + lane * R;
   PageWalk walk(key, p.page_size);
   const int32_t* table = p.page_table + (size_t)b * p.max_pages;
+  int page = lane < pieces && key < sp.L ? __ldg(table + walk.page) : -1;
   auto request = [&](int s) {
     int row = -1;
     if (lane < pieces && key < sp.L) {
-      row = (int)paged_row(__ldg(table + walk.page), p.num_pages, p.Hkv, p.page_size, hk, walk.slot);
+      row = (int)paged_row(page, p.num_pages, p.Hkv, p.page_size, hk, walk.slot);
       if (row < 0) atomicOr(p.status, DEV_BAD_INPUT);
     }
     const uint32_t bar = full + s * 8;
@@ -167,10 +190,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
     }
     key += kStride;
     walk.advance(kStride, p.page_size);
+    page = lane < pieces && key < sp.L ? __ldg(table + walk.page) : -1;
   };
-  int issued = tb + kg;  // next tile to request
-  if (rg == 0)
-    for (int s = 0; s < kStages && issued < te; ++s, issued += kKeyGroups) request(s);
+  int issued = tb + kg + kKeyGroups * rg;  // next tile to request
+  for (int s = rg; s < kStages && issued < te; s += RG, issued += kKeyGroups * RG) request(s);
 
   // Q fragments: thread (g, c) holds, of row nt * 8 + g, the head dimensions 16 c + 4 s .. + 3
   // (and 64 + ... for steps 4-7) of step s, the pieces it reads of K.
@@ -180,20 +203,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
   const float unit = (a.score_kind & ATTN_SCORE_SOFTCAP) ? 1.0f / a.softcap : kPagedLog2e;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = row0 + nt * 8 + g;
-    uint32_t w[kSteps][2];
+    const uint32_t (&w)[kSteps][2] = qw[nt];
     uint32_t top = 0;
-    const bool ok = r < rows;
-    const int i = ok ? r / a.G : 0, h = hk * a.G + (ok ? r - i * a.G : 0);
-    const long long t = p.offsets ? sp.row0 + i : i;
-    const __nv_bfloat16* q = a.q + (p.offsets ? 0 : b) * a.q_batch + t * a.q_token + h * a.q_head;
-#pragma unroll
-    for (int v = 0; v < kSteps / 2; ++v) {  // 16-byte loads: two steps each
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (ok) x = __ldg(reinterpret_cast<const uint4*>(q + (v >> 1) * 64 + c * 16 + (v & 1) * 8));
-      w[2 * v][0] = x.x; w[2 * v][1] = x.y;
-      w[2 * v + 1][0] = x.z; w[2 * v + 1][1] = x.w;
-    }
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
@@ -251,10 +262,27 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
   bool live = true;
   int s = 0;
   uint32_t parity = 0;
+  // A pair releases its i-th tile through named barrier i % kTurns: the warp that will not
+  // refill the stage arrives when it has read the tile, the one that will waits there after
+  // its next tile, so that neither waits for the other's request. Neither gets more than two
+  // tiles ahead (an arrival is followed by a wait for the other's), so at most five
+  // consecutive barriers are in use. Returns whether this warp refills the stage before.
+  int i_tile = 0, turn = 0;
+  auto release = [&]() -> bool {
+    const int before = turn == 0 ? kTurns - 1 : turn - 1, at = turn;
+    turn = turn == kTurns - 1 ? 0 : turn + 1;
+    const bool mine = i_tile % RG == rg, first = i_tile == 0;
+    ++i_tile;
+    if (mine) return false;
+    nb_arrive(1 + kg * kTurns + at, RG * 32);
+    if (first) return false;
+    nb_sync(1 + kg * kTurns + before, RG * 32);
+    return true;
+  };
   for (int tile = tb + kg; tile < te; tile += kKeyGroups) {
     if (live) live = __all_sync(0xffffffffu, mbar_wait(full + s * 8, parity, wc));
     if (!live) {  // keep the barriers of the warps that share the tile paired
-      if (RG > 1) nb_sync(1 + kg, RG * 32);
+      if (RG > 1) release();
       continue;
     }
     const int t0 = tile * kTile;
@@ -469,18 +497,18 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) f32x2_split(l2[nt], l[nt][0], l[nt][1]);
-    // every thread has read the stage
-    if (RG > 1) nb_sync(1 + kg, RG * 32);
-    else __syncwarp();
-    if (rg == 0 && issued < te) {
-      request(s);
-      issued += kKeyGroups;
+    __syncwarp();  // every thread has read the stage
+    if ((RG == 1 || release()) && issued < te) {
+      request(RG == 1 ? s : s == 0 ? kStages - 1 : s - 1);
+      issued += kKeyGroups * RG;
     }
     if (++s == kStages) {
       s = 0;
       parity ^= 1;
     }
   }
+  if (RG > 1 && i_tile > 0 && (i_tile - 1) % RG == rg)  // the other's last arrival
+    nb_sync(1 + kg * kTurns + (turn == 0 ? kTurns - 1 : turn - 1), RG * 32);
   if (!live)  // leave no copy in flight into this CTA's shared memory
     for (int i = 0; i < kStages; ++i) drain_wait(full + i * 8, i < s ? parity ^ 1 : parity);
 
