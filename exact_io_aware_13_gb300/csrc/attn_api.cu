@@ -820,8 +820,8 @@ int attn_prefill_split_keys(int cache_kind, int B, int T, int Hq, int Hkv, int m
   const long long G = Hq / Hkv, rows = std::min(max_new, T) * G;
   if (cache_kind == ATTN_CACHE_E4M3 && rows <= kPagedRowsMax) {
     // The row kernel: ten chunks per SM, as for decode, of at least 1024 keys. 8 new tokens of
-    // 16 sequences of 2000 to 32768 (Hq = 32, Hkv = 8, d = 128): 259 us at 1536 keys, 343 at
-    // 512, 846 unsplit. Three sequences of up to 700 tokens: 17.5 us unsplit, 15.5 us in
+    // 16 sequences of 2000 to 32768 (Hq = 32, Hkv = 8, d = 128): 233 us at 1792 keys, 300 at
+    // 512, 245 at 4096. Three sequences of up to 700 tokens: 17.5 us unsplit, 15.5 us in
     // chunks of 256, but the merge's launch and workspace cost the host 3 us.
     const long long keys =
         std::max(1024, attn_decode_split_keys(B, Hq, Hkv, 1, total_kv_tokens, num_sms));

@@ -21,10 +21,13 @@
 //   * P^T's fragment is S^T's, transposed by movmatrix: no shared memory in between.
 //
 // Measured: decode of 64 sequences of 512 to 8192 tokens (Hq = 32, Hkv = 8, d = 128) 88 us in
-// the kernel, 5.8 TB/s of HBM (85 % of the copy rate); the whole call with the merge 96 us.
-// Two sequences of 131072: 101 us. 8 new tokens of 16 sequences (32 rows): 254 us, bound by
-// its instructions (39 per key and kv head), half of them the conversions that both warps of
-// a tile repeat.
+// the kernel, 5.8 TB/s of HBM (85 % of the copy rate); the whole call with the merge 94 us.
+// Two sequences of 131072: 100 us. 8 new tokens of 16 sequences (32 rows): 230 us. That is
+// the latency of a warp's steps: 2450 clocks per key tile (reading, converting and
+// multiplying 1600, its share of the requests 400, the rest waits), with the eight warps per
+// SM that 240 registers allow; leaving out every conversion or every exponential changes
+// nothing, a quarter of the MMAs with their conversions takes it to 205 us. A CTA's start and
+// end add 8000 clocks to 69000.
 //
 // Number ranges (fp16 operands, fp32 sums). Q: each row times a power of two that brings its
 // largest magnitude to [2^14, 2^15) - exact but for elements below 2^-29 of it, which lose
