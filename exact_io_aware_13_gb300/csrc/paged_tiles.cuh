@@ -11,7 +11,7 @@
 //     memory themselves (any strides, any G);
 //   * key tiles come from pages: two loader warps (K, V) issue one TMA box (bf16) or bulk
 //     copy (codes) per page piece, their page-table entries fetched one tile ahead. With one
-//     warp for both, pages of 16 ran at 1900 us where pages of 64 took 1355 (now 1351);
+//     warp for both, pages of 16 took 1900 us where pages of 64 took 1355; with two, 1351;
 //   * masks are aligned at the bottom right (decode_row_keys), slots behind the sequence are
 //     masked in S and cleared in V;
 //   * a unit of at most 128 rows leaves no second query tile to overlap with, so its even
