@@ -33,8 +33,14 @@
 // largest magnitude to [2^14, 2^15) - exact but for elements below 2^-29 of it, which lose
 // bits below 2^-39 of it. P: 2^(s - m + 11) <= 2^15 (the running maximum m may lag by 2^4),
 // so weights keep fp16's 11 bits down to 2^-25 of the largest. The V scales are powers of
-// two: P is multiplied by 2^(e_j - E) <= 1, E the largest V exponent so far, and O carries
-// 2^E; the row sum keeps the plain weights.
+// two: key j counts 2^(e_j - E) <= 1, E the largest V exponent so far, and O carries 2^E; the
+// row sum keeps the plain weights. While all of a tile's scales lie within 2^8 of 2^E, P takes
+// that factor and keeps its bits down to 2^-17 of the largest weight at least. In the other
+// tiles (one V row of a large norm is enough) V's codes take up to 2^-15 of it, exactly, and P
+// what is beyond: with all of it on P, the tail of a long sequence beside one large V row lost
+// its weights.
+#include <type_traits>
+
 #include "paged.cuh"
 #include "paged_out.cuh"
 
@@ -45,6 +51,8 @@ constexpr int kWarps = 4;
 constexpr int kTile = 32;        // keys per ring stage
 constexpr float kPOffset = 11.0f;  // P is scaled by 2^11
 constexpr float kLag = 4.0f;       // O is rescaled when the maximum grows by more than 2^4
+constexpr int kNear = 8;           // V scales down to 2^-8 of the largest go to P alone
+constexpr int kVDown = 15;         // beyond, V's codes take up to 2^-15 (exact in fp16)
 
 // Key tiles of a CTA in its rings, 8.1 KB each at d = 128: three CTAs fit an SM.
 constexpr int kRingTiles = 8;
@@ -70,6 +78,11 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t r;
@@ -301,6 +314,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
     }
     const uint32_t e_lane = lds16(et + lane * 2) >> 8;  // V exponent of key t0 + lane
     const int Et = (int)__reduce_max_sync(0xffffffffu, lane < valid ? e_lane : 0u);
+    const int E_min = (int)__reduce_min_sync(0xffffffffu, lane < valid && e_lane ? e_lane : 255u);
     // Whether every row sees every key of the tile (warp-uniform)
     const bool masked = t0 < lo1 || t0 + kTile > hi0;
 
@@ -441,6 +455,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
           }
         }
     }
+    // Whether P alone cannot take the tile's V scales. (Byte 0, a row of zeros for the most
+    // part, is not among E_min; such a row adds nothing beside E > kVDown + kNear.)
+    const bool far = E - E_min > kNear || (E > kNear && E <= kVDown + kNear);
     // ---- P^T (fp16) and O^T += V^T P^T
     uint64_t off2[NT], l2[NT];
 #pragma unroll
@@ -450,54 +467,74 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
       l2[nt] = f32x2(l[nt][0], l[nt][1]);
     }
     const uint64_t one2 = f32x2(1.f, 1.f);
+    // kFar: V's codes take a part of the scales. (One branch around both key halves: inside, it
+    // keeps the second half's exponentials from running beside the first half's MMAs, and 8 new
+    // tokens of 16 sequences take 236 us instead of 233.)
+    auto add_pv = [&](auto is_far) {
+      constexpr bool kFar = decltype(is_far)::value;
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      uint32_t pf[NT][2];
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t pf[NT][2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // V scale relative to 2^E (0 for the smallest, and for slots behind the sequence,
-        // whose bytes are anything and whose P is 0)
-        const int down = E - ve[hf][e];
-        const float wj = __uint_as_float((uint32_t)imax(127 - imax(down, 0), 0) << 23);
-        const uint64_t wj2 = f32x2(wj, wj);
+        for (int e = 0; e < 2; ++e) {
+          // V scale relative to 2^E (0 for the smallest, and for slots behind the sequence,
+          // whose bytes are anything and whose P is 0)
+          const int down = E - ve[hf][e] - (kFar ? kVDown : 0);
+          const float wj = __uint_as_float((uint32_t)imax(127 - imax(down, 0), 0) << 23);
+          const uint64_t wj2 = f32x2(wj, wj);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float p0, p1;
-          f32x2_split(fma_f32x2(f32x2(x[hf][nt][2 * e], x[hf][nt][2 * e + 1]), one2, off2[nt]), p0, p1);
-          p0 = ex2_approx(p0);
-          p1 = ex2_approx(p1);
-          l2[nt] = fma_f32x2(f32x2(p0, p1), one2, l2[nt]);
-          f32x2_split(mul_f32x2(f32x2(p0, p1), wj2), p0, p1);
-          pf[nt][e] = transpose_8x8(pack_f16x2(p0, p1));
+          for (int nt = 0; nt < NT; ++nt) {
+            float p0, p1;
+            f32x2_split(fma_f32x2(f32x2(x[hf][nt][2 * e], x[hf][nt][2 * e + 1]), one2, off2[nt]), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            l2[nt] = fma_f32x2(f32x2(p0, p1), one2, l2[nt]);
+            f32x2_split(mul_f32x2(f32x2(p0, p1), wj2), p0, p1);
+            pf[nt][e] = transpose_8x8(pack_f16x2(p0, p1));
+          }
         }
+        // keys of the transposed fragment's slots 2 c, 2 c + 1: c, c + 4 (and + 8)
+        uint32_t w[4][D / 32], f01 = 0, f23 = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t at = kt + voff[k & 1] + (hf * 16 + 8 * (k >> 1)) * D;
+          if constexpr (D == 128) {
+            const uint4 v = lds128(at);
+            w[k][0] = v.x; w[k][1] = v.y; w[k][2] = v.z; w[k][3] = v.w;
+          } else {
+            const uint2 v = lds64(at);
+            w[k][0] = v.x; w[k][1] = v.y;
+          }
+        }
+        if constexpr (kFar) {
+          auto factor = [&](int k) {  // V's part of the scale of key hf * 16 + k
+            const int down = E - (int)(lds16(et + (hf * 16 + k) * 2) >> 8);
+            return __uint_as_float((uint32_t)(127 - imin(imax(down, 0), kVDown)) << 23);
+          };
+          f01 = pack_f16x2(factor(c), factor(c + 4));
+          f23 = pack_f16x2(factor(c + 8), factor(c + 12));
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int hb = 0; hb < 2; ++hb) {  // two head dimensions of the word: one O tile
+            const uint32_t sel = hb ? 0x7362u : 0x5140u;
+            const uint32_t u = prmt(w[0][i], w[1][i], sel), v = prmt(w[2][i], w[3][i], sel);
+            uint32_t a0, a1, a2, a3;
+            decode4(u, a0, a1);
+            decode4(v, a2, a3);
+            if constexpr (kFar) {
+              a0 = mul_f16x2(a0, f01); a1 = mul_f16x2(a1, f01);
+              a2 = mul_f16x2(a2, f23); a3 = mul_f16x2(a3, f23);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_16816(o[nt][2 * i + hb], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+          }
       }
-      // keys of the transposed fragment's slots 2 c, 2 c + 1: c, c + 4 (and + 8)
-      uint32_t w[4][D / 32];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t at = kt + voff[k & 1] + (hf * 16 + 8 * (k >> 1)) * D;
-        if constexpr (D == 128) {
-          const uint4 v = lds128(at);
-          w[k][0] = v.x; w[k][1] = v.y; w[k][2] = v.z; w[k][3] = v.w;
-        } else {
-          const uint2 v = lds64(at);
-          w[k][0] = v.x; w[k][1] = v.y;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {  // two head dimensions of the word: one O tile
-          const uint32_t sel = hb ? 0x7362u : 0x5140u;
-          const uint32_t u = prmt(w[0][i], w[1][i], sel), v = prmt(w[2][i], w[3][i], sel);
-          uint32_t a0, a1, a2, a3;
-          decode4(u, a0, a1);
-          decode4(v, a2, a3);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_16816(o[nt][2 * i + hb], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-        }
-    }
+    };
+    if (far) add_pv(std::true_type{});
+    else add_pv(std::false_type{});
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) f32x2_split(l2[nt], l[nt][0], l[nt][1]);
     __syncwarp();  // every thread has read the stage

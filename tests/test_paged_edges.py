@@ -1,0 +1,112 @@
+"""GPU parity of the paged attention calls at the edges of their range. Bounds as in
+test_paged.py, with what a test adds to them stated there."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_oracle as P
+from tests.paged_inputs import Batch
+from tests.test_paged import check_attention, oracle, run_prefill
+from workloads import MASK_CAUSAL, MASK_NONE, MASK_SLIDING_WINDOW
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def _ea():
+    import exact_io_aware_13_gb300 as ea
+    return ea
+
+
+def _put(w, b, t, k=None, v=None):
+    """Replaces tokens t of sequence b in the e4m3 cache by rows k, v [len(t), d], the same in
+    every kv head."""
+    t = np.atleast_1d(t)
+    pages, slots = w.table[b, t // w.page], t % w.page
+    for i, (cache, x) in enumerate(((w.k_cache, k), (w.v_cache, v))):
+        codes, e = P.encode(np.broadcast_to(np.asarray(x, dtype=np.float64), (len(t), w.d)))
+        cache[pages, :, slots] = torch.from_numpy(codes)[:, None].expand(-1, w.Hkv, -1)
+        w.kv_exp[pages, :, slots, i] = torch.from_numpy(e)[:, None].expand(-1, w.Hkv)
+
+
+# ------------------------------------------------------------------ V scales far apart
+def _light_tail(n, Hq, where, sink):
+    """A sink key with V of magnitude `sink`, thousands of tail keys of 2^-20 of its weight that
+    carry the output, and one token whose V is 2^15 times theirs: nearly no weight (light), or
+    just below the window of every row (masked). The tail keeps its share.
+
+    P holds weights down to 2^-17 of the largest in fp16's 11 bits, and those below in steps of
+    2^-27 of it: half a step for each of the L tail keys of at most 1.25 comes beside the
+    module's bound (the token that stands out weighs less than 2^-90)."""
+    d, L, s0 = 64, 3000, 20.5 * np.log(2.0)
+    w = Batch([n], [L], Hq=Hq, Hkv=1, d=d, page=16, kind="e4m3", seed=70)
+    q = np.sign(np.random.default_rng(70).standard_normal(d))
+    w.q[:] = torch.from_numpy(q).to(torch.bfloat16)
+    lo = 100 if where == "masked" else 0          # lowest key that the first row sees
+    rng = np.random.default_rng(71)
+    _put(w, 0, np.arange(L), k=0.0, v=1.0 + 0.25 * rng.random((L, d)))
+    _put(w, 0, lo + n + 1, k=q * (s0 / 8.0), v=sink * rng.standard_normal(d))  # score s0
+    big = 2.0 ** 15 * (1.0 + rng.random(d))
+    if where == "light":
+        _put(w, 0, 0, k=q * -8.0, v=big)                          # score -64
+        kw = dict(mask=MASK_NONE)
+    else:
+        _put(w, 0, lo - 1, k=0.0, v=big)
+        kw = dict(mask=MASK_SLIDING_WINDOW, window=L - n - lo + 1)
+    o_ref, l_ref, mag = oracle(w, **kw)
+    more = 2.0 ** -28 * L * 1.25 / 2.0 ** -8       # as a part of A, which the bound takes 2^-8 of
+    for split in (1 << 20, 1024):
+        o, lse = run_prefill(w, split=split, **kw)
+        assert _ea().device_status() == 0
+        check_attention(o, lse, (o_ref, l_ref, mag + more), f"{where} {split}")
+
+
+@pytest.mark.parametrize("where", ["light", "masked"])
+@pytest.mark.parametrize("n,Hq", [(1, 1), (1, 8), (4, 4), (3, 8), (4, 8)])
+def test_light_tail_beside_a_large_value(n, Hq, where):
+    """Row kernel; the sink's scale lies 2^25 below the largest."""
+    _light_tail(n, Hq, where, 2.0 ** -10)
+
+
+@pytest.mark.parametrize("where", ["light", "masked"])
+@pytest.mark.parametrize("n,Hq", [(33, 1), (80, 4)])
+def test_light_tail_beside_a_large_value_in_tiles(n, Hq, where):
+    """Tile kernel, inside the 2^24 between scales that it is stated for: 2^21 here, codes from 1
+    on are exact there. (At 2^25 the factor of the sink's row, 2^-25, is half of fp16's smallest
+    number and rounds to 0: that row is lost.)"""
+    _light_tail(n, Hq, where, 2.0 ** -6)
+
+
+@pytest.mark.parametrize("G", [2, 4, 6, 8])
+def test_scales_far_apart_in_few_rows(G):
+    """K and V scales that differ by many powers of two, zero rows among them, in ragged chunks
+    of up to four tokens and in decode with three (8 to 32 rows per kv head)."""
+    new, lens = [4, 0, 1, 3, 4], [300, 9, 500, 37, 1300]
+    for chunks in (True, False):
+        w = Batch(new if chunks else [3] * 5, lens, Hq=2 * G, Hkv=2, d=128, kind="e4m3", page=16,
+                  seed=76 + G, k_scale=0.02)
+        rng = np.random.default_rng(76)
+        owned = w.kv_exp.numpy() != 255
+        shift = rng.integers(-12, 3, size=w.kv_exp.shape)
+        w.kv_exp = torch.from_numpy(np.where(owned, np.clip(w.kv_exp.numpy().astype(int) + shift, 0, 254),
+                                             255).astype(np.uint8))
+        for b, t in ((0, 3), (0, 298), (2, 0), (2, 130), (4, 1299)):
+            _put(w, b, t, k=0.0, v=0.0)
+        for split, mask in ((1 << 20, MASK_CAUSAL), (256, MASK_NONE), (128, MASK_SLIDING_WINDOW)):
+            kw = dict(mask=mask, window=90)
+            if chunks:
+                o, lse = run_prefill(w, split=split, max_new=4, **kw)
+            else:
+                c = w.cuda()
+                q = c["q"].reshape(w.B, 3, w.Hq, w.d).transpose(1, 2).contiguous()
+                o, lse = _ea().decode_paged(q, c["k_cache"], c["v_cache"], c["table"], c["seq_lens"],
+                                            split_keys=split, mask_kind=mask, window=90,
+                                            kv_exp=c["kv_exp"])
+                o, lse = o.transpose(1, 2).reshape(-1, w.Hq, w.d), lse.transpose(1, 2).reshape(-1, w.Hq)
+            assert _ea().device_status() == 0
+            check_attention(o, lse, oracle(w, **kw), f"chunks {chunks} split {split} mask {mask}")
