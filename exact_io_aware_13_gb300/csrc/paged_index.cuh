@@ -22,6 +22,13 @@ ATTN_HD long long paged_row(int page, int num_pages, int Hkv, int page_size, int
   return ((long long)page * Hkv + head) * page_size + slot;
 }
 
+// Keys at the start of the tile at t0 that are not loaded: the page pieces of R keys (a power of
+// two) that end at or below k_lo, the lowest key that any row of the CTA sees. Their pages may be gone (a sliding
+// window has passed them) or be another sequence's by now; their V rows count as zeros.
+ATTN_HD int paged_skipped_keys(int t0, int k_lo, int R) {
+  return k_lo > t0 ? (k_lo - t0) & -R : 0;
+}
+
 // The page-table index and slot of a key that moves on by a fixed stride (a power of two,
 // 64 or 128), without a division: a page size of at most the stride divides it (8, 16, 32,
 // 64, 128), so the slot stays; a larger one is passed at most once.

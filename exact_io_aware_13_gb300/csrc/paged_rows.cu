@@ -187,10 +187,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
   int key = (tb + kg + kKeyGroups * rg) * kTile + lane * R;
   PageWalk walk(key, p.page_size);
   const int32_t* table = p.page_table + (size_t)b * p.max_pages;
-  int page = lane < pieces && key < sp.L ? __ldg(table + walk.page) : -1;
+  auto wanted = [&] { return lane < pieces && key < sp.L && key + R > k_lo; };
+  int page = wanted() ? __ldg(table + walk.page) : -1;
   auto request = [&](int s) {
     int row = -1;
-    if (lane < pieces && key < sp.L) {
+    if (wanted()) {
       row = (int)paged_row(page, p.num_pages, p.Hkv, p.page_size, hk, walk.slot);
       if (row < 0) atomicOr(p.status, DEV_BAD_INPUT);
     }
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
     }
     key += kStride;
     walk.advance(kStride, p.page_size);
-    page = lane < pieces && key < sp.L ? __ldg(table + walk.page) : -1;
+    page = wanted() ? __ldg(table + walk.page) : -1;
   };
   int issued = tb + kg + kKeyGroups * rg;  // next tile to request
   for (int s = rg; s < kStages && issued < te; s += RG, issued += kKeyGroups * RG) request(s);
@@ -304,17 +305,22 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
     const int t0 = tile * kTile;
     const uint32_t kt = ring + s * L::kStage, vt = kt + L::kCodes, et = exps + s * kTile * 2;
     const int valid = imin(kTile, sp.L - t0);
-    if (valid < kTile) {  // slots behind the sequence: their V must not reach the sums
-      for (int e = lane; e < (kTile - valid) * (D / 16); e += 32) {
-        const int row = valid + e / (D / 16), piece = e % (D / 16);
+    // Slots behind the sequence and keys that were not loaded: their V must not reach the sums.
+    const int skip = paged_skipped_keys(t0, k_lo, R);
+    if (valid < kTile || skip > 0) {
+      for (int e = lane; e < kTile * (D / 16); e += 32) {
+        const int row = e / (D / 16), piece = e % (D / 16);
         const uint32_t at = vt + piece_offset<D>(row, piece);
-        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+        if (row < skip || row >= valid)
+          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
       }
+      fence_proxy_async_smem();  // the first tile's stage is refilled by TMA
       __syncwarp();  // (warps that share the tile write the same zeros before they read it)
     }
     const uint32_t e_lane = lds16(et + lane * 2) >> 8;  // V exponent of key t0 + lane
-    const int Et = (int)__reduce_max_sync(0xffffffffu, lane < valid ? e_lane : 0u);
-    const int E_min = (int)__reduce_min_sync(0xffffffffu, lane < valid && e_lane ? e_lane : 255u);
+    const bool seen = t0 + lane >= k_lo && t0 + lane < k_hi;  // by some row
+    const int Et = (int)__reduce_max_sync(0xffffffffu, seen ? e_lane : 0u);
+    const int E_min = (int)__reduce_min_sync(0xffffffffu, seen && e_lane ? e_lane : 255u);
     // Whether every row sees every key of the tile (warp-uniform)
     const bool masked = t0 < lo1 || t0 + kTile > hi0;
 
@@ -477,8 +483,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
         uint32_t pf[NT][2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          // V scale relative to 2^E (0 for the smallest, and for slots behind the sequence,
-          // whose bytes are anything and whose P is 0)
+          // V scale relative to 2^E (0 for the smallest; at most 1, also for keys that no row
+          // sees, whose bytes are anything and whose P is 0)
           const int down = E - ve[hf][e] - (kFar ? kVDown : 0);
           const float wj = __uint_as_float((uint32_t)imax(127 - imax(down, 0), 0) << 23);
           const uint64_t wj2 = f32x2(wj, wj);

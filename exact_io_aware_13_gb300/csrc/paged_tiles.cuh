@@ -13,7 +13,8 @@
 //     copy (codes) per page piece, their page-table entries fetched one tile ahead. With one
 //     warp for both, pages of 16 took 1900 us where pages of 64 took 1355; with two, 1351;
 //   * masks are aligned at the bottom right (decode_row_keys), slots behind the sequence are
-//     masked in S and cleared in V;
+//     masked in S and cleared in V, and so are the pages of the first key tile that no row of
+//     the unit sees: they are not loaded (a sliding window may have given them back);
 //   * a unit of at most 128 rows leaves no second query tile to overlap with, so its even
 //     key tiles go to the first softmax warpgroup and its odd ones to the second (two score
 //     buffers, two O accumulators), merged at the end;
@@ -114,6 +115,7 @@ struct Cta {
   int b, hk, cc;         // sequence (< 0: nothing to do), kv head, key chunk
   int row_base, rows;    // first packed row, packed rows from there on
   int c0, c1;            // keys of the chunk
+  int k_lo;              // lowest key that any row sees
   int lo, hi;            // key tiles of both query tiles together
   bool dual;             // one query tile: its key tiles alternate between two streams
   Span span;
@@ -184,6 +186,7 @@ __device__ __forceinline__ void find_work(const PagedAttention& a, Cta* w, int l
       w->c1 = a.n_chunks == 1 ? s.L : (int)imin64((long long)w->c0 + a.chunk, s.L);
       w->span = s;
       w->lo = 1 << 30;
+      w->k_lo = w->c1;
       w->hi = 0;
       for (int t = 0; t < kQTiles; ++t) {
         TileKeys k{0, 0, 0, 0};
@@ -200,6 +203,7 @@ __device__ __forceinline__ void find_work(const PagedAttention& a, Cta* w, int l
             k.lo = k_lo / BN;
             k.hi = (k_hi + BN - 1) / BN;
             w->lo = imin(w->lo, k.lo);
+            w->k_lo = imin(w->k_lo, k_lo);
             w->hi = imax(w->hi, k.hi);
           }
         }
@@ -287,6 +291,11 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
                                       : L::kQ + L::kTile + (s - S::kCodeStages) * L::kCodeTile);
   };
 
+  // Page pieces: keys of one copy. Those of the first key tile that lie wholly below every
+  // row's keys are not loaded.
+  auto piece_keys = [&] { return kE4m3 && p.page_size % 128 == 0 ? 128 : imin(p.page_size, 64); };
+  auto skipped = [&] { return paged_skipped_keys(w.lo * BN, w.k_lo, piece_keys()); };
+
   WaitCtx wc{&bars->abort_flag, p.status};
   // The softmax warps request their Q rows before the loader starts: behind its stream of
   // keys they would take several times as long.
@@ -331,7 +340,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       column[k] = (grp >> 3) * L::kChunk + row0 * 128 + (((grp & 7) ^ ((sub + k * kRowsIter) & 7)) << 4);
     const int depth = w.dual ? S::kCodeStagesDual : S::kCodeStages;
     bool live = true;
-    int e_ref = 0, e_k = 0, e_v = 0, cs = -1;
+    int e_ref = 0, e_k = 0, e_v = 0, cs = -1, skip = skipped();
     uint32_t code_parity = 1;
     for (int u = 0; u < 2 * n_kv; ++u) {
       if (++cs == depth) cs = 0;
@@ -340,21 +349,22 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       const bool is_v = u & 1;
       if (live)
         live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->code_full[cs]), code_parity, wc));
+      if (u == 2) skip = 0;
       const int valid = imin(BN, L_seq - (lo + jj) * BN);
+      const bool partial = valid < BN || skip > 0;
       const uint8_t* ex = smem + L::kExp + (jj % kInfo) * BN * 2;
       if (live && !is_v) {  // the tile's exponents: lane reads rows 4 lane .. + 3 (K low byte)
-        const uint2 x = *reinterpret_cast<const uint2*>(ex + lane * 8);
-        uint32_t mk = 0, mv = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t pair = ((e & 2) ? x.y : x.x) >> ((e & 1) * 16);
-          if (4 * lane + e < valid) {
-            mk = max(mk, pair & 255u);
-            mv = max(mv, (pair >> 8) & 255u);
-          }
+        uint2 x = *reinterpret_cast<const uint2*>(ex + lane * 8);
+        if (partial) {  // (skip is a multiple of 8: a lane's rows are in or out together)
+          const int in = 4 * lane < skip ? 0 : valid - 4 * lane;
+          x.x &= in >= 2 ? 0xFFFFFFFFu : in == 1 ? 0xFFFFu : 0u;
+          x.y &= in >= 4 ? 0xFFFFFFFFu : in == 3 ? 0xFFFFu : 0u;
         }
-        e_k = (int)__reduce_max_sync(0xffffffffu, mk);
-        e_v = (int)__reduce_max_sync(0xffffffffu, mv);
+        constexpr uint32_t kLow = 0x00FF00FFu;
+        const uint32_t mk = __vmaxu2(x.x & kLow, x.y & kLow);
+        const uint32_t mv = __vmaxu2((x.x >> 8) & kLow, (x.y >> 8) & kLow);
+        e_k = (int)__reduce_max_sync(0xffffffffu, max(mk & 255u, mk >> 16));
+        e_v = (int)__reduce_max_sync(0xffffffffu, max(mv & 255u, mv >> 16));
         e_ref = imax(e_ref, e_v);
         e_v = imax(e_v, e_ref - kMaxDown);
       }
@@ -392,11 +402,11 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
               make_uint4(mul_f16x2(h[0], f), mul_f16x2(h[1], f), mul_f16x2(h[2], f), mul_f16x2(h[3], f));
         }
       }
-      if (valid < BN) {  // rows behind the sequence hold anything, NaN codes included: clear
+      if (partial) {  // the other rows hold anything, NaN codes included: clear
         __syncwarp();
         for (int e = lane; e < 32 * 8 * L::kSlabs; e += 32) {
           const int slab = e / 256, row = cw * 32 + (e % 256) / 8;
-          if (row >= valid)
+          if (row < skip || row >= valid)
             *reinterpret_cast<uint4*>(smem + L::kRing + s * L::kTile + slab * L::kChunk + row * 128 +
                                       (e % 8) * 16) = make_uint4(0, 0, 0, 0);
         }
@@ -414,12 +424,11 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       // of clocks to issue). Lane q fetches the q-th page piece of a tile: TMA boxes (bf16) or
       // a bulk copy (codes). K tiles take the even stages of the ring, V tiles the odd ones.
       const bool is_v = warp == kLoadVWarp;
-      const int ps = p.page_size;
-      const int R = kE4m3 && ps % 128 == 0 ? 128 : imin(ps, 64), pieces = BN / R;
-      const int lo = w.lo, hi = w.hi, n_kv = hi - lo;
+      const int R = piece_keys(), pieces = BN / R;
+      const int lo = w.lo, hi = w.hi, n_kv = hi - lo, k_lo = w.k_lo;
       auto rows_of = [&](int j) -> int {  // cache row of this lane's piece, or -1
         const int key = j * BN + lane * R;
-        if (j >= hi || lane >= pieces || key >= w.span.L) return -1;
+        if (j >= hi || lane >= pieces || key >= w.span.L || key + R <= k_lo) return -1;
         const long long r = cache_row(p, w.b, key, w.hk);
         if (r < 0) atomicOr(p.status, DEV_BAD_INPUT);
         return (int)r;
@@ -467,20 +476,23 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
       }
     } else if (!kE4m3 && warp == kRelayWarp) {
       // ------------------------------------------------------------ relay (bf16)
-      // After a ring use's bytes have landed (and the V rows behind the sequence are
-      // cleared), arrive on its named barrier for the MMA warp. After an abort, rendezvous.
+      // After a ring use's bytes have landed (and the V rows behind the sequence or not loaded
+      // are cleared), arrive on its named barrier for the MMA warp. After an abort, rendezvous.
       bool live = true;
       const int lo = w.lo, n_kv = w.hi - lo;
+      int skip = skipped();
       for (int u = 0; u < 2 * n_kv; ++u) {
         const int s = u % kStages;
         if (live)
           live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->kv_full[s]), (u / kStages) & 1, wc));
+        if (u == 2) skip = 0;
         const int valid = w.span.L - (lo + (u >> 1)) * BN;
-        if (live && (u & 1) && valid < BN) {
-          for (int e = lane; e < (BN - valid) * 8 * L::kSlabs; e += 32) {
-            const int slab = e / ((BN - valid) * 8), rem = e - slab * (BN - valid) * 8;
-            *reinterpret_cast<uint4*>(smem + L::kRing + s * L::kTile + slab * L::kChunk +
-                                      (valid + rem / 8) * 128 + (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
+        if (live && (u & 1) && (valid < BN || skip > 0)) {
+          for (int e = lane; e < BN * 8 * L::kSlabs; e += 32) {
+            const int slab = e / (BN * 8), row = e / 8 % BN;
+            if (row < skip || row >= valid)
+              *reinterpret_cast<uint4*>(smem + L::kRing + s * L::kTile + slab * L::kChunk +
+                                        row * 128 + (e % 8) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();

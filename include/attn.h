@@ -344,8 +344,9 @@ int attn_decode_split_keys(int B, int Hq, int Hkv, int Nq, long long total_kv_to
  * t * token_stride + h * head_stride + c (strides in elements, non-negative multiples of
  * 8; base 16-byte aligned), so the q, k and v slices of a fused projection need no copy.
  * Bad DEVICE inputs (offsets that break the rule above, a length above the page table's
- * capacity or max_seq_len, a page index outside [0, num_pages), for cache_write and
- * cache_read a position below 0) are skipped, never followed, and reported by
+ * capacity or max_seq_len, a page index outside [0, num_pages) of a page that the call reads
+ * or writes, for cache_write and cache_read a position below 0) are skipped, never followed,
+ * and reported by
  * attn_device_status as ATTN_ERR_DEVICE_INPUT; the results of that call are then
  * unspecified. The calls allocate nothing, take any B and T (0 included) and are
  * deterministic.
@@ -392,7 +393,9 @@ attn_status attn_cache_read(const attn_paged_cache* cache, void* k, void* v,
  * Attention of a ragged batch of chunks of new tokens over the cache (chunked prefill; the
  * new tokens' own K and V are in the cache already, see attn_cache_write).
  *   q    bf16 [T, Hq, d], strided;  o bf16 [T, Hq, d];  lse fp32 [T, Hq] (natural log)
- * Masks, ALiBi, soft-cap and their positions are those of attn_decode_paged. A row without
+ * Masks, ALiBi, soft-cap and their positions are those of attn_decode_paged. Of a sliding
+ * window's sequence only the pages that hold a key of some query row are read
+ * (attn_decode_paged_e4m3 too): the entries of the pages below may be anything. A row without
  * an allowed key gets O = 0 and lse = -inf. max_new bounds every n_b and max_seq_len
  * (<= max_pages_per_seq * page_size) every seq_lens[b]; tighter bounds launch fewer CTAs.
  * split_keys (a positive multiple of 128, see attn_prefill_split_keys) cuts the keys into

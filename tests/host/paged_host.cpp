@@ -12,6 +12,8 @@ long long host_row(int page, int num_pages, int Hkv, int page_size, int head, in
   return attn::paged_row(page, num_pages, Hkv, page_size, head, slot);
 }
 
+int host_skipped_keys(int t0, int k_lo, int R) { return attn::paged_skipped_keys(t0, k_lo, R); }
+
 // (page, slot) of key0, key0 + stride, ... (n of them), by the walk.
 void host_walk(int key0, int stride, int page_size, int n, int* pages, int* slots) {
   attn::PageWalk w(key0, page_size);

@@ -110,3 +110,61 @@ def test_scales_far_apart_in_few_rows(G):
                 o, lse = o.transpose(1, 2).reshape(-1, w.Hq, w.d), lse.transpose(1, 2).reshape(-1, w.Hq)
             assert _ea().device_status() == 0
             check_attention(o, lse, oracle(w, **kw), f"chunks {chunks} split {split} mask {mask}")
+
+
+# ------------------------------------------------------------------ pages that are gone
+def _free_behind(w, window, how):
+    """The page table after the pages that lie wholly below every row's window were freed:
+    their entries are -1, or belong to someone whose page is NaN all over."""
+    table = w.table.copy()
+    owned = set(w.table[w.table >= 0].tolist())
+    nan_page = next(p for p in range(w.pages) if p not in owned)   # Batch fills it with NaN
+    freed = 0
+    for b, (n, L) in enumerate(zip(w.new, w.lens)):
+        if n == 0:
+            continue
+        gone = max(0, L - n - window + 1) // w.page
+        table[b, :gone] = -1 if how == "gone" else nan_page
+        freed += gone
+    assert freed > 0
+    return torch.from_numpy(table).cuda()
+
+
+@pytest.mark.parametrize("how", ["gone", "another's"])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [8, 16, 32, 64, 192])
+@pytest.mark.parametrize("n,Hq", [(1, 2), (4, 8), (6, 8), (40, 4), (200, 2), (300, 2)])
+def test_window_over_freed_pages(n, Hq, page, kind, how):
+    """Pages wholly below the windows of all of a call's rows are never followed."""
+    for window in (5, 70, 333):
+        w = Batch([n, 0, n], [n + 1000, 40, n + 417], Hq=Hq, Hkv=2, d=64, page=page, kind=kind, seed=72)
+        ref = oracle(w, MASK_SLIDING_WINDOW, window)
+        c = w.cuda()
+        c["table"] = _free_behind(w, window, how)
+        for split in (128, 1 << 20):
+            o, lse = run_prefill(w, c, split=split, mask=MASK_SLIDING_WINDOW, window=window, max_new=n)
+            assert _ea().device_status() == 0, (window, split)
+            check_attention(o, lse, ref, f"window {window} split {split}")
+
+
+def _decode_over_freed_pages(nq, Hq, page, kind, how):
+    for window in (5, 70, 333):
+        w = Batch([nq] * 3, [1000, 400, 777], Hq=Hq, Hkv=2, d=128, page=page, kind=kind, seed=73)
+        ref = oracle(w, MASK_SLIDING_WINDOW, window)
+        c = w.cuda()
+        q = c["q"].reshape(w.B, nq, Hq, w.d).transpose(1, 2).contiguous()
+        table = _free_behind(w, window, how)
+        for split in (64, 256, 1 << 20):
+            o, lse = _ea().decode_paged(q, c["k_cache"], c["v_cache"], table, c["seq_lens"],
+                                        split_keys=split, mask_kind=MASK_SLIDING_WINDOW,
+                                        window=window, kv_exp=c["kv_exp"])
+            assert _ea().device_status() == 0, (window, split)
+            check_attention(o.transpose(1, 2).reshape(-1, Hq, w.d),
+                            lse.transpose(1, 2).reshape(-1, Hq), ref, f"window {window} split {split}")
+
+
+@pytest.mark.parametrize("how", ["gone", "another's"])
+@pytest.mark.parametrize("page", [8, 16, 32, 64, 192])
+@pytest.mark.parametrize("nq,Hq", [(1, 8), (3, 16), (9, 16)])
+def test_decode_e4m3_window_over_freed_pages(nq, Hq, page, how):
+    _decode_over_freed_pages(nq, Hq, page, "e4m3", how)

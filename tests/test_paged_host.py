@@ -57,3 +57,16 @@ def test_walk_is_division(host, stride, ps):
         host.host_walk(key0, stride, ps, n, p(pages), p(slots))
         keys = key0 + stride * np.arange(n)
         assert np.array_equal(pages, keys // ps) and np.array_equal(slots, keys % ps)
+
+
+@pytest.mark.parametrize("tile", [32, 64, 128])
+@pytest.mark.parametrize("R", [8, 16, 32, 64, 128])
+def test_skipped_keys_are_the_pieces_below(host, tile, R):
+    """In the tile that holds k_lo: every key of a piece that ends at or below k_lo, no other."""
+    if R > tile:
+        return
+    for t0 in (0, tile, 7 * tile, (2**31 - 4096) // tile * tile - tile):
+        for k_lo in range(max(0, t0 - 3), t0 + tile):
+            want = sum((t0 + k) // R * R + R <= k_lo for k in range(tile))
+            assert host.host_skipped_keys(t0, k_lo, R) == want
+    assert host.host_skipped_keys(0, 0, R) == 0
