@@ -46,8 +46,9 @@
 //
 // The last tile of a sequence can end inside a page whose later slots hold no token
 // (possibly NaN). S columns past the sequence are masked before the max; the V rows
-// there are zeroed in shared memory by the loader before the P V product (0 * NaN
-// would be NaN).
+// there are zeroed in shared memory by the relay before the P V product (0 * NaN
+// would be NaN). Pages of an item's first tile that lie wholly below every row's keys are
+// not loaded (a sliding window may have given them back): the same holds for their rows.
 //
 // Split mode (more than one chunk per sequence, or two row copies): each item writes,
 // per row and copy, O_c / l_c in fp32 and L2_c = m_c + log2 l_c; the combine kernel forms
@@ -60,6 +61,7 @@
 #include <climits>
 
 #include "kernels.h"
+#include "paged_index.cuh"
 #include "ptx.cuh"
 
 namespace attn {
@@ -159,6 +161,7 @@ struct Item {
   int b, hk, rt, c, Lb;
   int rows_here;
   int max_lo, min_hi;   // over the tile's valid rows: largest first key, smallest end
+  int skip;             // keys of the first tile that are not loaded
   int tb, n_t;          // first 64-key tile and tile count (0: no key for any row)
   bool live;            // processed: has tiles, or (single-chunk launch) owns its rows
 };
@@ -288,6 +291,7 @@ __device__ inline Item make_item(const Args& a, const Cursor& cu, int lane) {
   it.max_lo = warp_max(mx_lo); it.min_hi = warp_min(mn_hi);
   const int k_lo = imax(c0, mn_lo), k_hi = imin(c1, mx_hi);
   it.tb = k_hi > k_lo ? k_lo / BN : 0;
+  it.skip = k_hi > k_lo ? paged_skipped_keys(it.tb * BN, k_lo, imin(p.page_size, BN)) : 0;
   it.n_t = k_hi > k_lo ? ceil_div(k_hi, BN) - it.tb : 0;
   it.live = it.n_t > 0 || a.direct;
   return it;
@@ -427,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!live) return;
         const int t0 = (it.tb + t) * BN;
         const int valid = imin(BN, it.Lb - t0);  // keys of the tile inside the sequence
+        const int skip = t == 0 ? it.skip : 0;
         const int first_page = t0 / ps;
         while (first_page - wbase >= 32) {  // warp-uniform
           wbase += 32;
@@ -442,14 +447,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int pa = __shfl_sync(0xffffffffu, cur, off & 31);
           const int pb = __shfl_sync(0xffffffffu, nxt, off & 31);
           const int page = off < 32 ? pa : pb;
-          const bool in_seq = lane < pieces && key < it.Lb;
+          const bool in_seq = lane < pieces && key < it.Lb && q * R >= skip;
           good = in_seq && page >= 0 && page < p.num_pages;
           if (in_seq && !good) atomicOr(p.status, DEV_BAD_INPUT);
           coord = (int)(((long long)page * p.Hkv + it.hk) * ps + key % ps);
         }
         const uint32_t mask = __ballot_sync(0xffffffffu, good);
         const uint32_t bytes = (uint32_t)__popc(mask) * R * 128 * L::kHalves;
-        const bool tail = valid < BN;
+        const bool tail = valid < BN || skip > 0;
         const uint32_t kst = smem_u32(smem + L::kRing + s * L::kStage);
         const uint32_t vst = kst + L::kTileBytes;
         const uint32_t kbar = smem_u32(&bars->k_full[s]);
@@ -478,8 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kRelayWarp) {
     // ------------------------------------------------------------ relay
-    // Once K and V of a stage have landed (and the unused V rows of a sequence's last
-    // tile are cleared), arrive on the stage's named barrier for the MMA warp. After an
+    // Once K and V of a stage have landed (and the unused V rows of a sequence's last and an
+    // item's first tile are cleared), arrive on the stage's named barrier for the MMA warp. After an
     // abort, rendezvous (bar.sync) instead, so every barrier phase still pairs.
     bool live = true;
     auto pass = [&](uint32_t bar, uint32_t parity, uint32_t id) {
@@ -495,19 +500,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->k_full[s]), (u / kStages) & 1, wc));
         const int t0 = (it.tb + t) * BN;
         const int valid = imin(BN, it.Lb - t0);
-        if (valid < BN) {
-          // The last tile of a sequence ends inside a page: its V copy completed on
-          // tail[s]. Clear V rows [valid, BN) of each 128-byte column block in place (a
-          // swizzled row stays inside its own 128 bytes), then complete v_full[s]. Stage
-          // s is reused only after v_full[s], so tail[s] is never two phases ahead.
+        const int skip = t == 0 ? it.skip : 0;
+        if (valid < BN || skip > 0) {
+          // The last tile of a sequence ends inside a page, or the first keys were not
+          // loaded: the V copy completed on tail[s]. Clear V rows [0, skip) and [valid, BN)
+          // of each 128-byte column block in place (a swizzled row stays inside its own 128
+          // bytes), then complete v_full[s]. Stage s is reused only after v_full[s], so
+          // tail[s] is never two phases ahead.
           if (live)
             live = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->tail[s]), (tail_parity >> s) & 1u, wc));
           tail_parity ^= 1u << s;
           if (live) {
-            const int zrows = BN - valid;
+            const int zrows = skip + BN - valid;
             for (int e = lane; e < zrows * 8 * L::kHalves; e += 32) {
               const int hf = e / (zrows * 8), rem = e - hf * zrows * 8;
-              const int row = valid + rem / 8, chunk16 = rem % 8;
+              const int zr = rem / 8, row = zr < skip ? zr : valid + zr - skip, chunk16 = rem % 8;
               *reinterpret_cast<uint4*>(smem + L::kRing + s * L::kStage + L::kTileBytes +
                                         hf * L::kKvHalf + row * 128 + chunk16 * 16) =
                   make_uint4(0, 0, 0, 0);

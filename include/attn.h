@@ -274,9 +274,10 @@ attn_status attn_quantize_fp8(const void* x, void* out, float* scales, int BH, i
  *   o          bf16 [B, Hq, Nq, d];  lse fp32 [B, Hq, Nq] (natural log)
  * All pointers are DEVICE memory; tensors 16-byte aligned, page_table and seq_lens
  * 4-byte aligned. page_table and seq_lens are read on the device only; a length
- * outside [0, max_seq_len] or a page index outside [0, num_pages) for a token the call
- * reads makes attn_device_status report ATTN_ERR_DEVICE_INPUT (the results of that
- * call are then unspecified; nothing outside the given buffers is touched).
+ * outside [0, max_seq_len] or a page index outside [0, num_pages) of a page that holds a
+ * key of some query row makes attn_device_status report ATTN_ERR_DEVICE_INPUT (the results
+ * of that call are then unspecified; nothing outside the given buffers is touched). Entries
+ * of pages that a sliding window has passed for every query row may be anything.
  *
  * Masks use the positions above (aligned at the bottom right): ATTN_MASK_NONE (every
  * cached token), ATTN_MASK_CAUSAL (j <= position of the query), ATTN_MASK_SLIDING_WINDOW
@@ -346,9 +347,8 @@ int attn_decode_split_keys(int B, int Hq, int Hkv, int Nq, long long total_kv_to
  * Bad DEVICE inputs (offsets that break the rule above, a length above the page table's
  * capacity or max_seq_len, a page index outside [0, num_pages) of a page that the call reads
  * or writes, for cache_write and cache_read a position below 0) are skipped, never followed,
- * and reported by
- * attn_device_status as ATTN_ERR_DEVICE_INPUT; the results of that call are then
- * unspecified. The calls allocate nothing, take any B and T (0 included) and are
+ * and reported by attn_device_status as ATTN_ERR_DEVICE_INPUT; the results of that call are
+ * then unspecified. The calls allocate nothing, take any B and T (0 included) and are
  * deterministic.
  */
 enum { ATTN_CACHE_BF16 = 0, ATTN_CACHE_E4M3 = 1 };

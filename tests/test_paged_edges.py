@@ -168,3 +168,10 @@ def _decode_over_freed_pages(nq, Hq, page, kind, how):
 @pytest.mark.parametrize("nq,Hq", [(1, 8), (3, 16), (9, 16)])
 def test_decode_e4m3_window_over_freed_pages(nq, Hq, page, how):
     _decode_over_freed_pages(nq, Hq, page, "e4m3", how)
+
+
+@pytest.mark.parametrize("how", ["gone", "another's"])
+@pytest.mark.parametrize("page", [8, 16, 32, 64, 192])
+@pytest.mark.parametrize("nq,Hq", [(1, 8), (3, 16), (9, 16), (9, 8)])
+def test_decode_bf16_window_over_freed_pages(nq, Hq, page, how):
+    _decode_over_freed_pages(nq, Hq, page, "bf16", how)
