@@ -9,8 +9,9 @@ namespace {
 constexpr int kWarps = 8;
 
 // Merge of the key chunks' partial results, in a fixed order:
-//   M = max_c L2_c, w_c = 2^(L2_c - M), O = sum_c w_c O_c / sum_c w_c, L = M + log2 sum_c w_c.
-// Only chunks that hold keys of the row were written. A row takes one warp, or with many
+//   M = max_c L2_c, W = sum_c 2^(L2_c - M), O = sum_c (2^(L2_c - M) / W) O_c, L = M + log2 W.
+// The weights are divided before they meet the values, which may lie near the top of fp32's
+// range. Only chunks that hold keys of the row were written. A row takes one warp, or with many
 // chunks and few rows eight (each a contiguous part of them, joined through shared memory):
 // a lone warp's loads for 98 chunks of a 131072-token sequence took 25 us one after the other.
 template <int D, int kPerRow>
@@ -35,14 +36,21 @@ __global__ void __launch_bounds__(kWarps * 32) paged_merge_kernel(const PagedAtt
   const int each = (cb - ca + kPerRow - 1) / kPerRow;
   const int c_begin = imin(ca + part * each, cb), c_end = imin(c_begin + each, cb);
   const long long rows = (long long)p.T * a.Hq, row = (long long)t * a.Hq + h;
-  float M = -INFINITY;
-  for (int c = c_begin + lane; c < c_end; c += 32) M = max_nan(M, a.part_lse[c * rows + row]);
+  const int c_lane = c_begin + lane;
+  const float first = c_lane < c_end ? a.part_lse[c_lane * rows + row] : -INFINITY;
+  float M = first;
+  for (int c = c_lane + 32; c < c_end; c += 32) M = max_nan(M, a.part_lse[c * rows + row]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, off));
   float W = 0.f, acc[kC];
 #pragma unroll
   for (int e = 0; e < kC; ++e) acc[e] = 0.f;
-  if (M != -INFINITY)  // (a NaN chunk makes the row NaN)
+  if (M != -INFINITY) {  // (a NaN chunk makes the row NaN)
+    W = ex2_approx(first - M);
+    for (int c = c_lane + 32; c < c_end; c += 32) W += ex2_approx(a.part_lse[c * rows + row] - M);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) W += __shfl_xor_sync(0xffffffffu, W, off);
+    const float inv = 1.f / W;  // W >= 1
     for (int c0 = c_begin; c0 < c_end; c0 += 4) {  // four chunks' loads in flight
       float l2[4], v[4][kC];
 #pragma unroll
@@ -60,12 +68,12 @@ __global__ void __launch_bounds__(kWarps * 32) paged_merge_kernel(const PagedAtt
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float w = ex2_approx(l2[k] - M);
-        W += w;
+        const float w = ex2_approx(l2[k] - M) * inv;
 #pragma unroll
         for (int e = 0; e < kC; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
       }
     }
+  }
   if constexpr (kPerRow > 1) {
 #pragma unroll
     for (int e = 0; e < kC; ++e) sm[warp][lane * kC + e] = acc[e];
@@ -77,20 +85,21 @@ __global__ void __launch_bounds__(kWarps * 32) paged_merge_kernel(const PagedAtt
     if (part != 0) return;
 #pragma unroll
     for (int k = 0; k < kPerRow; ++k) M = max_nan(M, sm[k][D]);
+    float share[kPerRow];
     W = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPerRow; ++k) {
+      share[k] = sm[k][D] == -INFINITY ? 0.f : ex2_approx(sm[k][D] - M) * sm[k][D + 1];
+      W += share[k];
+    }
+    const float inv = W == 0.f ? 0.f : 1.f / W;
 #pragma unroll
     for (int e = 0; e < kC; ++e) acc[e] = 0.f;
 #pragma unroll
-    for (int k = 0; k < kPerRow; ++k) {
-      const float mk = sm[k][D], f = mk == -INFINITY ? 0.f : ex2_approx(mk - M);
-      W = fmaf(f, sm[k][D + 1], W);
+    for (int k = 0; k < kPerRow; ++k)
 #pragma unroll
-      for (int e = 0; e < kC; ++e) acc[e] = fmaf(f, sm[k][lane * kC + e], acc[e]);
-    }
+      for (int e = 0; e < kC; ++e) acc[e] = fmaf(share[k] * inv, sm[k][lane * kC + e], acc[e]);
   }
-  const float inv = W == 0.f ? 0.f : 1.f / W;
-#pragma unroll
-  for (int e = 0; e < kC; ++e) acc[e] *= inv;
   PagedAttention out = a;
   out.n_chunks = 1;
   store_row<D>(out, b, t, i, h, 0, lane, acc, W == 0.f ? -INFINITY : M + log2f(W));

@@ -558,15 +558,18 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
   if (!live)  // leave no copy in flight into this CTA's shared memory
     for (int i = 0; i < kStages; ++i) drain_wait(full + i * 8, i < s ? parity ^ 1 : parity);
 
-  // ---- merge of the key groups: factors 2^(m_k - M) 2^E_k, fixed order
+  // ---- merge of the key groups: factors 2^(m_k - M) 2^E_k, fixed order. 2^E_k comes after the
+  // division by the row sum: V may lie near the top of fp32's range, and O carries 2^11 and the
+  // sum until then.
   grid_dependents_launch();
   __syncthreads();
   constexpr int kRows = NT * 8 * RG;
   float* sm_m = reinterpret_cast<float*>(smem);            // [key group][row]
   float* sm_l = sm_m + kKeyGroups * kRows;
   float* sm_o = sm_l + kKeyGroups * kRows;                 // [key group][row][D + 4]
-  static_assert((2 + D + 4) * kKeyGroups * kRows * 4 <= L::kRing, "merge space");
-  const float vs = exp_byte_scale((uint32_t)E);
+  float* sm_v = sm_o + kKeyGroups * kRows * (D + 4);       // [warp]: 2^E_k
+  static_assert(((2 + D + 4) * kKeyGroups * kRows + kWarps) * 4 <= L::kRing, "merge space");
+  if (lane == 0) sm_v[warp] = exp_byte_scale((uint32_t)E);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
       for (int st = 0; st < kSteps; ++st) {
         const int dim = D == 128 ? 16 * kappa(g) + 2 * st : 8 * g + 2 * st;
         *reinterpret_cast<float2*>(sm_o + rr * (D + 4) + dim) =
-            make_float2(o[nt][st][r] * vs, o[nt][st][2 + r] * vs);
+            make_float2(o[nt][st][r], o[nt][st][2 + r]);
       }
     }
   __syncthreads();
@@ -621,9 +624,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 || D == 64 ? 3 : 2)
 #pragma unroll
     for (int k = 0; k < kKeyGroups; ++k) {
       const float f = __shfl_sync(0xffffffffu, fk[k], n);
+      const float vs = sm_v[k * RG];  // (the warps of a pair have seen the same scales)
       const float* src = sm_o + (k * kRows + rr) * (D + 4) + lane * (D / 32);
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] = f != 0.f ? fmaf(f, src[e], acc[e]) : acc[e];
+      for (int e = 0; e < D / 32; ++e) acc[e] = f != 0.f ? fmaf(f * src[e], vs, acc[e]) : acc[e];
     }
     const int i = __shfl_sync(0xffffffffu, i_row, n), h = __shfl_sync(0xffffffffu, h_row, n);
     store_row<D>(a, b, sp.row0 + i, i, h, cc, lane, acc, __shfl_sync(0xffffffffu, l2, n));

@@ -808,12 +808,13 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
     const bool have_o = n > 0 && mma_done;
     tc_fence_after_sync();
     const float vs = kE4m3 ? exp_byte_scale((uint32_t)e_ref) : 1.f;
-    // A dual unit: the second warpgroup leaves its O rows (times their scale), maxima and
-    // sums in the ring, which no one uses any more; the first one merges.
+    // A dual unit: the second warpgroup leaves its O rows, their maxima, sums and scale in the
+    // ring, which no one uses any more; the first one merges. The scales come last: V may lie
+    // near the top of fp32's range, and O carries 2^11 and the row sum until it is divided.
     float* other = reinterpret_cast<float*>(smem + L::kRing);   // [row][D], pieces swizzled
-    float* other_ml = other + BM * D;                           // [row][2]
-    static_assert(BM * (D + 2) * 4 <= S::kStages * L::kTile, "merge space");
-    float f0 = vs, f1 = 0.f;
+    float* other_ml = other + BM * D;                           // [row][4]
+    static_assert(BM * (D + 4) * 4 <= S::kStages * L::kTile, "merge space");
+    float f0 = 1.f, f1 = 0.f, vs1 = 1.f;
     if (dual) {
       if (t == 1) {
 #pragma unroll
@@ -830,19 +831,19 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             *reinterpret_cast<float4*>(other + row * D + (((c * 8 + e) ^ (row & (D / 4 - 1))) << 2)) =
-                make_float4(__uint_as_float(o[4 * e]) * vs, __uint_as_float(o[4 * e + 1]) * vs,
-                            __uint_as_float(o[4 * e + 2]) * vs, __uint_as_float(o[4 * e + 3]) * vs);
+                make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                            __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
         }
-        *reinterpret_cast<float2*>(other_ml + row * 2) = make_float2(m_run, l_run);
+        *reinterpret_cast<float4*>(other_ml + row * 4) = make_float4(m_run, l_run, vs, 0.f);
       }
       nb_sync(kNbDual, 256);
       if (t == 0) {
-        const float2 ml = *reinterpret_cast<const float2*>(other_ml + row * 2);
+        const float4 ml = *reinterpret_cast<const float4*>(other_ml + row * 4);
+        vs1 = ml.z;
         const float M = fmaxf(m_run, ml.x);
-        const float g0 = m_run == -INFINITY ? 0.f : ex2_approx(m_run - M);
+        f0 = m_run == -INFINITY ? 0.f : ex2_approx(m_run - M);
         f1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-        f0 = g0 * vs;
-        l_run = l_run * g0 + ml.y * f1;
+        l_run = l_run * f0 + ml.y * f1;
         m_run = M;
       }
     }
@@ -863,15 +864,15 @@ __global__ void __launch_bounds__(Shape<kE4m3>::kThreads, 1)
         for (int e = 0; e < 32; ++e) o[e] = 0u;
       }
 #pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * f0;
+      for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * f0 * vs;
       if (dual && f1 > 0.f) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float4 x = *reinterpret_cast<const float4*>(other + row * D + (((c * 8 + e) ^ (row & (D / 4 - 1))) << 2));
-          v[4 * e] = fmaf(x.x, f1, v[4 * e]);
-          v[4 * e + 1] = fmaf(x.y, f1, v[4 * e + 1]);
-          v[4 * e + 2] = fmaf(x.z, f1, v[4 * e + 2]);
-          v[4 * e + 3] = fmaf(x.w, f1, v[4 * e + 3]);
+          v[4 * e] = fmaf(x.x * f1, vs1, v[4 * e]);
+          v[4 * e + 1] = fmaf(x.y * f1, vs1, v[4 * e + 1]);
+          v[4 * e + 2] = fmaf(x.z * f1, vs1, v[4 * e + 2]);
+          v[4 * e + 3] = fmaf(x.w * f1, vs1, v[4 * e + 3]);
         }
       }
     };

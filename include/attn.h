@@ -407,7 +407,9 @@ attn_status attn_cache_read(const attn_paged_cache* cache, void* k, void* v,
  * and the V scales, of the keys that a query's tile walks over lie within 2^15 of each
  * other, and within bf16's rounding up to 2^24 (attn_decode_paged_e4m3 too). Over such a cache
  * the softmax weights that multiply V are rounded to 11 bits, those below 2^-17 of the row's
- * largest to multiples of 2^-27 of it; the row sum is not. A NaN in a query
+ * largest to multiples of 2^-27 of it; the row sum is not. Over a bf16 cache O is summed
+ * before it is divided by the row sum (attn_decode_paged too): it needs max |V| times the keys
+ * that share the weight below 2^119. A NaN in a query
  * row, or in the K row of a token that it sees, makes that row's O and lse NaN and no
  * other's. A NaN or infinity in the V row of a cached token reaches O in every query row of
  * the tiles that hold the token, those that mask it too (0 * NaN).

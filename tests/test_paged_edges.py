@@ -175,3 +175,48 @@ def test_decode_e4m3_window_over_freed_pages(nq, Hq, page, how):
 @pytest.mark.parametrize("nq,Hq", [(1, 8), (3, 16), (9, 16), (9, 8)])
 def test_decode_bf16_window_over_freed_pages(nq, Hq, page, how):
     _decode_over_freed_pages(nq, Hq, page, "bf16", how)
+
+
+# ------------------------------------------------------------------ V near the top of the range
+@pytest.mark.parametrize("split", [128, 1024, 1 << 20])
+@pytest.mark.parametrize("n,Hq", [(1, 2), (4, 4), (4, 8), (33, 2), (70, 1), (300, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_near_the_top_of_the_range(n, Hq, d, split):
+    """V of one sign up to 1.75 * 2^126 whose weight is spread over every key: the unnormalised
+    sums pass fp32's range, the results do not."""
+    w = Batch([n], [1500], Hq=Hq, Hkv=1, d=d, page=16, kind="e4m3", seed=74)
+    owned = w.kv_exp[..., 1] != 255
+    w.v_cache = (w.v_cache & 0x0F) | 0x70                        # 128 .. 448 (no NaN code), positive
+    w.v_cache = torch.where(w.v_cache == 0x7F, torch.full_like(w.v_cache, 0x7E), w.v_cache)
+    w.kv_exp[..., 1] = torch.where(owned, torch.full_like(w.kv_exp[..., 1], 127 + 118), w.kv_exp[..., 1])
+    for mask in (MASK_NONE, MASK_CAUSAL):
+        o, lse = run_prefill(w, split=split, mask=mask, max_new=n)
+        assert _ea().device_status() == 0
+        check_attention(o, lse, oracle(w, mask), f"mask {mask}")
+
+
+@pytest.mark.parametrize("split", [64, 256, 1 << 20])
+def test_decode_values_near_the_top_of_the_range(split):
+    w = Batch([1, 1], [20000, 700], Hq=4, Hkv=1, d=128, page=64, kind="e4m3", seed=77)
+    w.v_cache, w.kv_exp[..., 1] = torch.full_like(w.v_cache, 0x7E), 127 + 118     # 448 * 2^118
+    c = w.cuda()
+    o, lse = _ea().decode_paged(c["q"][:, :, None].contiguous(), c["k_cache"], c["v_cache"], c["table"],
+                                c["seq_lens"], split_keys=split, kv_exp=c["kv_exp"])
+    assert _ea().device_status() == 0
+    check_attention(o[:, :, 0], lse[:, :, 0], oracle(w, MASK_NONE), f"split {split}")
+
+
+@pytest.mark.parametrize("split", [128, 1 << 20])
+@pytest.mark.parametrize("n,Hq", [(1, 2), (4, 8), (70, 1), (300, 2)])
+def test_values_near_the_bottom_of_the_range(n, Hq, split):
+    """V of one sign about 2^-118 whose weight is spread over every key: O is a normal number
+    of bf16, and keeps its bits (the module's 1e-6 put aside by scaling both sides)."""
+    w = Batch([n], [1500], Hq=Hq, Hkv=1, d=64, page=16, kind="e4m3", seed=78)
+    owned = w.kv_exp[..., 1] != 255
+    w.v_cache = (w.v_cache & 0x0F) | 0x60                        # 32 .. 120, positive
+    w.kv_exp[..., 1] = torch.where(owned, torch.full_like(w.kv_exp[..., 1], 4), w.kv_exp[..., 1])
+    o, lse = run_prefill(w, split=split, mask=MASK_NONE, max_new=n)
+    o_ref, l_ref, mag = oracle(w, MASK_NONE)
+    s = 2.0 ** 118
+    check_attention(o.double() * s, lse, (o_ref * s, l_ref, mag * s), f"split {split}")
+
