@@ -412,9 +412,10 @@ attn_status check_cache(const attn_paged_cache* c, int B, int T, int max_new, in
   if ((long long)c->num_pages * c->Hkv > 0x7fffffffLL ||
       (long long)c->num_pages * c->Hkv * c->page_size > 0x7fffffffLL)
     return ATTN_ERR_SHAPE;
-  if ((c->kind == ATTN_CACHE_E4M3) != (c->kv_exp != nullptr)) return ATTN_ERR_ARG;
+  if (c->kind == ATTN_CACHE_BF16 && c->kv_exp) return ATTN_ERR_ARG;
   *p = PagedProblem{};
   p->k_cache = c->k; p->v_cache = c->v; p->kv_exp = c->kv_exp; p->page_table = c->page_table;
+  p->e4m3 = c->kind == ATTN_CACHE_E4M3;
   p->num_pages = c->num_pages; p->Hkv = c->Hkv; p->page_size = c->page_size; p->d = c->d;
   p->max_pages = c->max_pages_per_seq;
   p->page_shift = -1;
@@ -426,12 +427,14 @@ attn_status check_cache(const attn_paged_cache* c, int B, int T, int max_new, in
   return ATTN_OK;
 }
 
-// Pointers of the cache and of the batch, once the sizes show that there is work.
+// Pointers of the cache and of the batch, once the sizes show that there is work. (A pool
+// without pages has empty tensors, whose pointers are null.)
 attn_status check_cache_pointers(const PagedProblem& p, const int32_t* offsets,
                                  const int32_t* seq_lens) {
   if (!offsets || !seq_lens) return ATTN_ERR_ARG;
   if (p.max_seq_len > 0 &&
-      (!p.k_cache || !p.v_cache || !p.page_table || p.num_pages == 0 || p.Hkv == 0))
+      (!p.k_cache || !p.v_cache || (p.e4m3 && !p.kv_exp) || !p.page_table || p.num_pages == 0 ||
+       p.Hkv == 0))
     return ATTN_ERR_ARG;
   if (!aligned16(p.k_cache) || !aligned16(p.v_cache) || !aligned16(p.kv_exp) ||
       !aligned4(p.page_table) || !aligned4(offsets) || !aligned4(seq_lens))
@@ -493,7 +496,7 @@ attn_status run_paged_attention(const PagedAttention& a, cudaStream_t st) {
     attn_status s = make_map_codes(&maps.k, p.k_cache, rows, p.d, box);
     if (s == ATTN_OK) s = make_map_codes(&maps.v, p.v_cache, rows, p.d, box);
     if (s != ATTN_OK) return s;
-  } else if (!p.kv_exp && p.max_seq_len > 0) {
+  } else if (!p.e4m3 && p.max_seq_len > 0) {
     const unsigned box = (unsigned)std::min(p.page_size, 64);
     attn_status s = make_map(&maps.k, p.k_cache, 1, rows, p.d, box);
     if (s == ATTN_OK) s = make_map(&maps.v, p.v_cache, 1, rows, p.d, box);

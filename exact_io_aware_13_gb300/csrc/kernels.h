@@ -169,11 +169,12 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_
 // no offsets: sequence b's rows are b * max_new .. b * max_new + max_new - 1.
 struct PagedProblem {
   void *k_cache, *v_cache;    // [num_pages, Hkv, page_size, d], bf16 or e4m3
-  uint8_t* kv_exp;            // [num_pages, Hkv, page_size, 2] (e4m3), else null
+  uint8_t* kv_exp;            // [num_pages, Hkv, page_size, 2] (e4m3)
   const int32_t* page_table;  // [B, max_pages] device
   const int32_t* offsets;     // [B + 1] device, or null
   const int32_t* seq_lens;    // [B] device
   int* status;
+  bool e4m3;                  // codes and kv_exp, else bf16
   int num_pages, Hkv, page_size, d, max_pages;
   int page_shift;             // log2 page_size, or -1
   int B, T;
@@ -220,7 +221,7 @@ struct PagedMaps {
 // caches run in 233 us there, in 339 us as tiles; with 64 rows it would read every key twice.
 constexpr int kPagedRowsMax = 32;
 inline bool paged_few_rows(const PagedAttention& a) {
-  return a.p.kv_exp != nullptr && (long long)a.p.max_new * a.G <= kPagedRowsMax;
+  return a.p.e4m3 && (long long)a.p.max_new * a.G <= kPagedRowsMax;
 }
 cudaError_t launch_paged_rows(const PagedAttention& a, const PagedMaps& maps, cudaStream_t st);
 cudaError_t launch_paged_tiles_bf16(const PagedAttention& a, const PagedMaps& maps, cudaStream_t st);

@@ -138,7 +138,7 @@ cudaError_t launch_paged_attention(const PagedAttention& a, const PagedMaps& map
     const cudaError_t e = launch_paged_rows(a, maps, st);
     return e != cudaSuccess || a.n_chunks == 1 ? e : launch_merge(a, st);
   }
-  const cudaError_t e = a.p.kv_exp ? launch_paged_tiles_e4m3(a, st) : launch_paged_tiles_bf16(a, maps, st);
+  const cudaError_t e = a.p.e4m3 ? launch_paged_tiles_e4m3(a, st) : launch_paged_tiles_bf16(a, maps, st);
   return e != cudaSuccess || a.n_chunks == 1 ? e : launch_merge(a, st);
 }
 

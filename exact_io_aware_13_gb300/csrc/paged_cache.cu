@@ -281,7 +281,7 @@ cudaError_t launch_copy(const CopyArgs& args, bool write, cudaStream_t st) {
   const long long blocks = ((long long)p.T * a.slices + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const unsigned g = (unsigned)blocks, t = kWarps * 32;
-  const bool e = p.kv_exp != nullptr;
+  const bool e = p.e4m3;
   if (write) {
     if (p.d == 64) e ? cache_write_kernel<64, true><<<g, t, 0, st>>>(a) : cache_write_kernel<64, false><<<g, t, 0, st>>>(a);
     else e ? cache_write_kernel<128, true><<<g, t, 0, st>>>(a) : cache_write_kernel<128, false><<<g, t, 0, st>>>(a);

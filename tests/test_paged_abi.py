@@ -181,3 +181,16 @@ def test_binding_refuses_cpu_tensors():
         ea.prefill_paged(rows, bf, bf, i32(1, 4), i32(2), i32(1))
     with pytest.raises(ValueError):
         ea.decode_paged(rows[None], bf, bf, i32(1, 4), i32(1))
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+def test_pools_without_pages(lib, kind):
+    """A pool of no pages has empty tensors, whose pointers are null: calls without rows are
+    no-ops over it, calls with rows are refused, for both kinds alike."""
+    c = _cache(kind, pages=0, kc=None, vc=None, exp=None)
+    for call in CALLS:
+        assert call(lib, c, T=0) == OK and call(lib, c, B=0) == OK, call
+        assert call(lib, c) == ARG, call
+    if kind == 1:
+        assert _decode(lib, c, B=0) == OK and _decode(lib, c, Nq=0) == OK
+        assert _decode(lib, c) == ARG

@@ -220,3 +220,24 @@ def test_values_near_the_bottom_of_the_range(n, Hq, split):
     s = 2.0 ** 118
     check_attention(o.double() * s, lse, (o_ref * s, l_ref, mag * s), f"split {split}")
 
+
+# ------------------------------------------------------------------ pools without pages
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_rows_over_a_pool_without_pages(kind):
+    """Nothing is cached and no page exists: rows without keys, on both kernels' sizes."""
+    ea = _ea()
+    t, e = (torch.bfloat16, None) if kind == "bf16" else (torch.uint8, torch.empty(0, 2, 16, 2, dtype=torch.uint8))
+    e = None if e is None else e.cuda()
+    cache = torch.empty(0, 2, 16, 64, dtype=t, device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.empty(2, 0, dtype=torch.int32, device="cuda")
+    for n in (1, 50):
+        q = torch.ones(2 * n, 4, 64, dtype=torch.bfloat16, device="cuda")
+        o, lse = ea.prefill_paged(q, cache, cache, table, i32(0, n, 2 * n), i32(0, 0), kv_exp=e)
+        assert bool((o == 0).all()) and bool(torch.isneginf(lse).all())
+    o, lse = ea.decode_paged(q[:2, :, None].contiguous(), cache, cache, table, i32(0, 0), kv_exp=e)
+    assert bool((o == 0).all()) and bool(torch.isneginf(lse).all())
+    k = q[:0, :2]
+    ea.cache_write(k, k, cache, cache, table, i32(0, 0, 0), i32(0, 0), kv_exp=e)
+    assert ea.cache_read(cache, cache, table, i32(0, 0, 0), i32(0, 0), 0, kv_exp=e)[0].shape == (0, 2, 64)
+    assert ea.device_status() == 0
