@@ -344,6 +344,10 @@ def decode_workspace_size(B: int, Hq: int, Hkv: int, Nq: int, d: int, max_seq_le
                                                       int(max_seq_len), int(split_keys)))
 
 
+def _decode_entry(kv_exp) -> str:
+    return "attn_decode_paged" if kv_exp is None else "attn_decode_paged_e4m3"
+
+
 def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspace, *,
                       max_seq_len: int, split_keys: int, scale: float,
                       mask_kind: int = MASK_NONE, window: int = 0, score_kind: int = SCORE_NONE,
@@ -356,8 +360,9 @@ def decode_paged_into(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspa
     if o is None or lse is None:
         raise ValueError("o and lse must be tensors")
     _lib.check(_lib.binding().decode(q, k_cache, v_cache, page_table, seq_lens, kv_exp, stream, o,
-                                     lse, workspace, max_seq_len, split_keys, None, scale,
-                                     mask_kind, window, score_kind, softcap) or 0, "decode_paged")
+                                     lse, workspace, int(max_seq_len), int(split_keys), None,
+                                     float(scale), mask_kind, window, score_kind, softcap) or 0,
+               _decode_entry(kv_exp))
 
 
 def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, max_seq_len: Optional[int] = None,
@@ -371,5 +376,5 @@ def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, max_seq_len: Opti
                                 None, None, max_seq_len, split_keys, total_kv_tokens, scale,
                                 mask_kind, window, score_kind, softcap)
     if out.__class__ is int:
-        _lib.check(out, "decode_paged")
+        _lib.check(out, _decode_entry(kv_exp))
     return out

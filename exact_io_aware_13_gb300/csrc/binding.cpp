@@ -76,10 +76,29 @@ int number(PyObject* o, const char* name) {
   if (v < INT_MIN || v > INT_MAX) fail("%s does not fit 32 bits", name);
   return (int)v;
 }
-long long wide(PyObject* o) {
-  const long long v = PyLong_AsLongLong(o);
+// What int() makes of o: lengths and sizes may come as floats and as numpy or tensor scalars.
+long long size_arg(PyObject* o) {
+  if (PyLong_CheckExact(o)) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) throw BadArgument{};
+    return v;
+  }
+  PyObject* i = PyNumber_Long(o);
+  if (!i) throw BadArgument{};
+  const long long v = PyLong_AsLongLong(i);
+  Py_DECREF(i);
   if (v == -1 && PyErr_Occurred()) throw BadArgument{};
   return v;
+}
+int size_arg(PyObject* o, const char* name) {
+  const long long v = size_arg(o);
+  if (v < INT_MIN || v > INT_MAX) fail("%s does not fit 32 bits", name);
+  return (int)v;
+}
+// total_kv_tokens, or without one (None or 0) every sequence at its bound.
+long long total_tokens(PyObject* o, int B, int max_seq_len) {
+  const long long v = none(o) ? 0 : size_arg(o);
+  return v > 0 ? v : (long long)B * max_seq_len;
 }
 float real(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
@@ -278,7 +297,7 @@ BINDING(cache_read, 10) {
     return status(attn_cache_read(&c, k.data_ptr(), v.data_ptr(), b.offsets, b.seq_lens, b.B,
                                   size_of(k.size(0), "k"), stream.handle));
   }
-  const int T = number(a[9], "n_tokens");
+  const int T = size_arg(a[9], "n_tokens");
   if (T < 0) fail("n_tokens must not be negative");
   const at::Tensor& like = THPVariable_Unpack(a[0]);
   const at::Tensor k = make(like, {T, c.Hkv, c.d}, at::kBFloat16);
@@ -299,12 +318,12 @@ BINDING(prefill, 20) {
   const Rows q = rows_of(a[0], -1, c.d, "q");
   const Scores sc(a + 16, a[15], c.d);
   const long long capacity = (long long)c.max_pages_per_seq * c.page_size;
-  const int max_seq_len = none(a[12]) ? size_of(capacity, "the page table") : number(a[12], "max_seq_len");
-  const int max_new = none(a[11]) ? q.T : number(a[11], "max_new");
-  const long long total = none(a[14]) || wide(a[14]) <= 0 ? (long long)b.B * max_seq_len : wide(a[14]);
+  const int max_seq_len = none(a[12]) ? size_of(capacity, "the page table") : size_arg(a[12], "max_seq_len");
+  const int max_new = none(a[11]) ? q.T : size_arg(a[11], "max_new");
+  const long long total = total_tokens(a[14], b.B, max_seq_len);
   const int split = none(a[13]) ? attn_prefill_split_keys(c.kind, b.B, q.T, q.H, c.Hkv, max_new,
                                                           max_seq_len, total, num_sms())
-                                : number(a[13], "split_keys");
+                                : size_arg(a[13], "split_keys");
   const at::Tensor& like = THPVariable_Unpack(a[0]);
   const bool allocate = none(a[8]);
   at::Tensor o, lse;
@@ -346,10 +365,10 @@ BINDING(decode, 18) {
   if (THPVariable_Unpack(a[3]).size(0) != q.size(0)) fail("page_table must be [B, max_pages]");
   const Scores sc(a + 14, a[13], c.d);
   const long long capacity = (long long)c.max_pages_per_seq * c.page_size;
-  const int max_seq_len = none(a[10]) ? size_of(capacity, "the page table") : number(a[10], "max_seq_len");
-  const long long total = none(a[12]) || wide(a[12]) <= 0 ? (long long)B * max_seq_len : wide(a[12]);
+  const int max_seq_len = none(a[10]) ? size_of(capacity, "the page table") : size_arg(a[10], "max_seq_len");
+  const long long total = total_tokens(a[12], B, max_seq_len);
   const int rows = size_of((int64_t)B * Nq, "B * Nq");
-  const int split = !none(a[11]) ? number(a[11], "split_keys")
+  const int split = !none(a[11]) ? size_arg(a[11], "split_keys")
                     : e4m3 ? attn_prefill_split_keys(c.kind, B, rows, Hq, c.Hkv, Nq, max_seq_len,
                                                      total, num_sms())
                            : attn_decode_split_keys(B, Hq, c.Hkv, Nq, total, num_sms());

@@ -241,3 +241,35 @@ def test_rows_over_a_pool_without_pages(kind):
     ea.cache_write(k, k, cache, cache, table, i32(0, 0, 0), i32(0, 0), kv_exp=e)
     assert ea.cache_read(cache, cache, table, i32(0, 0, 0), i32(0, 0), 0, kv_exp=e)[0].shape == (0, 2, 64)
     assert ea.device_status() == 0
+
+
+# ------------------------------------------------------------------ numbers of decode_paged
+def test_decode_takes_the_numbers_that_int_takes():
+    """max_seq_len, split_keys and total_kv_tokens as floats and numpy and tensor scalars; the
+    form on caller-owned tensors takes no None for them; errors name the entry point."""
+    ea = _ea()
+    for kind in ("bf16", "e4m3"):
+        w = Batch([1, 1], [90, 300], Hq=4, Hkv=2, d=64, kind=kind, seed=75)
+        c = w.cuda()
+        args = (c["q"].reshape(2, 4, 1, 64), c["k_cache"], c["v_cache"], c["table"], c["seq_lens"])
+        want = ea.decode_paged(*args, max_seq_len=304, split_keys=128, total_kv_tokens=390,
+                               kv_exp=c["kv_exp"])
+        for cast in (float, np.float64, np.int64, torch.tensor, np.float32):
+            got = ea.decode_paged(*args, max_seq_len=cast(304), split_keys=cast(128),
+                                  total_kv_tokens=cast(390), kv_exp=c["kv_exp"])
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), cast
+        ea.decode_paged(*args, total_kv_tokens=390.0, kv_exp=c["kv_exp"])
+        o, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+        ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+        good = dict(max_seq_len=304.0, split_keys=128, scale=0.125)
+        ea.decode_paged_into(*args, o, lse, ws, kv_exp=c["kv_exp"], **good)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        for name in good:
+            with pytest.raises(TypeError):
+                ea.decode_paged_into(*args, o, lse, ws, kv_exp=c["kv_exp"], **{**good, name: None})
+        with pytest.raises(TypeError):
+            ea.decode_paged(*args, max_seq_len=[304], kv_exp=c["kv_exp"])
+        with pytest.raises(ValueError):
+            ea.decode_paged(*args, max_seq_len=float("nan"), kv_exp=c["kv_exp"])
+        with pytest.raises(ea.AttnError, match="^attn_decode_paged" + ("_e4m3" if kind == "e4m3" else "") + ":"):
+            ea.decode_paged(*args, split_keys=100, kv_exp=c["kv_exp"])
