@@ -4,11 +4,13 @@ Each .cu file is compiled to an object in parallel with nvcc, then linked into
 exact_io_aware_13_gb300/libattn.so. No CMake, no torch extension machinery: the
 library exports plain C symbols (include/attn.h). _binding.so is the Python module of the
 paged-cache calls (csrc/binding.cpp, compiled against torch's headers by g++); it links to
-the library next to it.
+the library next to it. It holds torch's C++ interface of one version: the version it was
+built against is kept beside it, and another one rebuilds it.
 """
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -21,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libattn.so")
 BINDING_PATH = os.path.join(PKG, "_binding.so")
+BINDING_STAMP = os.path.join(BUILD_DIR, "binding.stamp")
 
 SOURCES = ["attn_api.cu", "simt.cu", "fwd_tc.cu", "fwd256_tc.cu", "bwd_tc.cu", "bwd256_tc.cu", "fp8.cu", "decode_tc.cu",
            "decode_copies2.cu", "paged_cache.cu", "paged_attn.cu", "paged_rows.cu",
@@ -42,6 +45,19 @@ def _deps_mtime() -> float:
     paths.append(os.path.join(INCLUDE, "attn.h"))
     paths.append(os.path.abspath(__file__))
     return max(os.path.getmtime(p) for p in paths)
+
+
+def _binding_target() -> str:
+    """What _binding.so is built for: torch's and Python's versions."""
+    return f"torch {importlib.metadata.version('torch')} {sys.implementation.cache_tag}"
+
+
+def _binding_is_for_this_torch() -> bool:
+    try:
+        with open(BINDING_STAMP) as f:
+            return f.read() == _binding_target()
+    except OSError:
+        return False
 
 
 def _compile(src: str, extra: list[str], verbose: bool) -> str:
@@ -91,14 +107,19 @@ def _link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link of _binding.so failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING_PATH)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_binding_target())
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Build libattn.so and _binding.so if a source is newer; return the library's path."""
+    """Build libattn.so and _binding.so if a source is newer, _binding.so also if torch is
+    another one; return the library's path."""
+    os.makedirs(BUILD_DIR, exist_ok=True)
     if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _deps_mtime()
                          for p in (LIB_PATH, BINDING_PATH)):
+        if not _binding_is_for_this_torch():
+            _link_binding(_compile_binding(verbose))
         return LIB_PATH
-    os.makedirs(BUILD_DIR, exist_ok=True)
     extra = list(extra or [])
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(_compile_binding, verbose)
