@@ -143,7 +143,8 @@ class ClockSampler:
 # headers) at capture time. A kernel whose sources have changed since reports null.
 KERNEL_SOURCES = {"fwd_tc_kernel": ("fwd_tc.cu",), "dkdv_kernel": ("bwd_tc.cu", "bwd_common.cuh"),
                   "dq_kernel": ("bwd_tc.cu", "bwd_common.cuh"), "rowdot_kernel": ("simt.cu",),
-                  "decode_tc_kernel": ("decode_tc.cuh", "decode_tc.cu", "decode_copies2.cu")}
+                  "decode_tc_kernel": ("decode_tc.cuh", "decode_tc.cu", "decode_copies2.cu",
+                                       "paged_index.cuh")}
 SHARED_HEADERS = ("ptx.cuh", "mask.cuh", "kernels.h")
 # decode_tc_kernel: the paged-decode workload (B=64, lengths 512-8192).
 NCU_TRAFFIC = {
@@ -155,8 +156,8 @@ NCU_TRAFFIC = {
                   "sha256": "526940b6bb4d74aa8715e5e80f5891713689e090d95e518855f0cf99c8c2d535"},
     "dq_kernel": {"bytes": 270654208 + 49328640,
                 "sha256": "526940b6bb4d74aa8715e5e80f5891713689e090d95e518855f0cf99c8c2d535"},
-    "decode_tc_kernel": {"bytes": 1119356160 + 9067520,
-                       "sha256": "e5baa6b786d411da95b06bbe6b9f34436a88ad59aaa68a53ecd64ab8a0bbfa26"},
+    "decode_tc_kernel": {"bytes": 1119380224 + 9139456,
+                       "sha256": "8175d159a6e5a0ac88ba4df84c06e4410c118ed1d474eaa0cdcdc10802585ace"},
 }
 
 def kernel_source_sha(kernel: str) -> str:

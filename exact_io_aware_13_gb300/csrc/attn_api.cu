@@ -13,6 +13,7 @@
 
 #include "attn.h"
 #include "kernels.h"
+#include "paged.h"
 #include "ptx.cuh"
 
 namespace attn {

@@ -32,7 +32,6 @@ struct MaskSpec {
 ATTN_HD int ceil_div(int a, int b) { return (a + b - 1) / b; }
 ATTN_HD int imin(int a, int b) { return a < b ? a : b; }
 ATTN_HD int imax(int a, int b) { return a > b ? a : b; }
-ATTN_HD long long imin64(long long a, long long b) { return a < b ? a : b; }
 
 // Index of the document holding position t: the last doc with doc[idx] <= t.
 ATTN_HD int doc_index(const MaskSpec& m, int t) {

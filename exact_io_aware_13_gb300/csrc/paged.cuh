@@ -3,7 +3,7 @@
 // that find a packed row's sequence, position and cache slot.
 #pragma once
 
-#include "kernels.h"
+#include "paged.h"
 #include "paged_index.cuh"
 #include "ptx.cuh"
 
@@ -22,6 +22,16 @@ __device__ __forceinline__ void grid_dependents_launch() {
 }
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// 2-D tiled load of one box.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
 }
 
 // Maximum that keeps a NaN (fmaxf drops it).

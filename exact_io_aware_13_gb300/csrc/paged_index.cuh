@@ -9,6 +9,8 @@
 
 namespace attn {
 
+ATTN_HD long long imin64(long long a, long long b) { return a < b ? a : b; }
+
 // Whether a sequence's packed rows [o0, o1) and length can be used: inside the call's T rows
 // and bounds.
 ATTN_HD bool paged_span_ok(int T, int max_new, int max_seq_len, int o0, int o1, int L) {

@@ -58,6 +58,13 @@ def test_traffic_is_reported_only_for_the_captured_sources(monkeypatch):
         assert len(bench.kernel_source_sha(k)) == 64
 
 
+def test_traffic_figures_belong_to_the_present_sources():
+    """A kernel whose sources change is captured anew, or its figure leaves the table: else the
+    line's traffic is null without anyone having taken it out."""
+    for k in bench.NCU_TRAFFIC:
+        assert bench.ncu_traffic(k) is not None, k
+
+
 def test_workload_configs():
     c = bench.workload_config(CAUSAL_FWD_BWD, {"parallelism": "replicas x1"})
     assert c["N"] == 8192 and c["d"] == 128 and c["mask"] == "causal"
