@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <cuda_runtime_api.h>
 #include <torch/csrc/Exceptions.h>
@@ -110,14 +111,15 @@ int size_of(int64_t n, const char* name) {
   return (int)n;
 }
 
-// The stream of a call: the current one, or a torch.cuda.Stream. Tensors made for a call on
-// another stream belong to the current one's allocations: the allocator has to know that they
-// are in use there, or the workspace would be handed out again as soon as the call returns.
+// The stream of a call: the current one, or a torch.cuda.Stream. Tensors for a call on another
+// stream are made on that stream: memory freed on the current one may still be in use by work
+// queued there, which the call does not wait for. Its outputs are recorded on the current
+// stream too, where the caller goes on with them; the workspace goes back to its own.
 struct Stream {
+  c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream();
   cudaStream_t handle;
   bool foreign = false;
   explicit Stream(PyObject* o) {
-    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream();
     handle = current.stream();
     if (none(o)) return;
     PyObject* value = PyObject_GetAttrString(o, "cuda_stream");
@@ -127,9 +129,17 @@ struct Stream {
     if (!handle && PyErr_Occurred()) throw BadArgument{};
     foreign = handle != current.stream();
   }
-  void uses(const at::Tensor& t) const {
-    if (foreign && t.defined() && t.numel() > 0)
-      t.record_stream(c10::cuda::getStreamFromExternal(handle, c10::cuda::current_device()).unwrap());
+  at::Tensor workspace(const at::Tensor& like, c10::IntArrayRef sizes, at::ScalarType type) const {
+    const auto options = like.options().dtype(type).requires_grad(false);
+    if (!foreign) return at::empty(sizes, options);
+    const c10::cuda::CUDAStreamGuard on(
+        c10::cuda::getStreamFromExternal(handle, c10::cuda::current_device()));
+    return at::empty(sizes, options);
+  }
+  at::Tensor output(const at::Tensor& like, c10::IntArrayRef sizes, at::ScalarType type) const {
+    at::Tensor t = workspace(like, sizes, type);
+    if (foreign && t.numel() > 0) t.record_stream(current.unwrap());
+    return t;
   }
 };
 
@@ -204,10 +214,6 @@ Rows rows_of(PyObject* o, int H, int d, const char* name) {
               t.size(0) > 1 ? t.stride(0) : 0, t.size(1) > 1 ? t.stride(1) : 0};
 }
 
-at::Tensor make(const at::Tensor& like, c10::IntArrayRef sizes, at::ScalarType type) {
-  return at::empty(sizes, like.options().dtype(type).requires_grad(false));
-}
-
 PyObject* pair(const at::Tensor& a, const at::Tensor& b) {
   PyObject* x = THPVariable_Wrap(a);
   PyObject* y = THPVariable_Wrap(b);
@@ -237,7 +243,7 @@ struct Workspace {
   at::Tensor own;
   void* p = nullptr;
   size_t bytes = 0;
-  Workspace(PyObject* o, bool allocate, const at::Tensor& like, size_t need) {
+  Workspace(PyObject* o, bool allocate, const Stream& stream, const at::Tensor& like, size_t need) {
     if (!none(o)) {
       const at::Tensor& t = tensor(o, "workspace");
       check_device(t, "workspace");
@@ -245,7 +251,7 @@ struct Workspace {
       p = t.data_ptr();
       bytes = t.nbytes();
     } else if (allocate && need > 0) {
-      own = make(like, {(int64_t)need}, at::kByte);
+      own = stream.workspace(like, {(int64_t)need}, at::kByte);
       p = own.data_ptr();
       bytes = need;
     }
@@ -300,12 +306,10 @@ BINDING(cache_read, 10) {
   const int T = size_arg(a[9], "n_tokens");
   if (T < 0) fail("n_tokens must not be negative");
   const at::Tensor& like = THPVariable_Unpack(a[0]);
-  const at::Tensor k = make(like, {T, c.Hkv, c.d}, at::kBFloat16);
-  const at::Tensor v = make(like, {T, c.Hkv, c.d}, at::kBFloat16);
+  const at::Tensor k = stream.output(like, {T, c.Hkv, c.d}, at::kBFloat16);
+  const at::Tensor v = stream.output(like, {T, c.Hkv, c.d}, at::kBFloat16);
   const attn_status s =
       attn_cache_read(&c, k.data_ptr(), v.data_ptr(), b.offsets, b.seq_lens, b.B, T, stream.handle);
-  stream.uses(k);
-  stream.uses(v);
   return s == ATTN_OK ? pair(k, v) : status(s);
 }
 
@@ -325,29 +329,26 @@ BINDING(prefill, 20) {
                                                           max_seq_len, total, num_sms())
                                 : size_arg(a[13], "split_keys");
   const at::Tensor& like = THPVariable_Unpack(a[0]);
+  const Stream stream(a[7]);
   const bool allocate = none(a[8]);
   at::Tensor o, lse;
   if (allocate) {
-    o = make(like, {q.T, q.H, c.d}, at::kBFloat16);
-    lse = make(like, {q.T, q.H}, at::kFloat);
+    o = stream.output(like, {q.T, q.H, c.d}, at::kBFloat16);
+    lse = stream.output(like, {q.T, q.H}, at::kFloat);
   } else {
     o = buffer(a[8], at::kBFloat16, "o");
     lse = buffer(a[9], at::kFloat, "lse");
     check_shape(o, {q.T, q.H, c.d}, "o");
     check_shape(lse, {q.T, q.H}, "lse");
   }
-  const Workspace ws(a[10], allocate, like,
+  const Workspace ws(a[10], allocate, stream, like,
                      attn_prefill_workspace_size(q.T, q.H, c.d, max_seq_len, split));
-  const Stream stream(a[7]);
   const attn_status s = attn_prefill_paged(
       &c, q.p, q.token, q.head, o.data_ptr(), static_cast<float*>(lse.data_ptr()), b.offsets, b.seq_lens,
       b.B, q.T, q.H, max_new, max_seq_len, split, sc.scale, sc.mask_kind, &sc.mask, sc.score_kind,
       &sc.score, ws.p, ws.bytes, stream.handle);
-  stream.uses(ws.own);
   if (s != ATTN_OK) return status(s);
   if (!allocate) Py_RETURN_NONE;
-  stream.uses(o);
-  stream.uses(lse);
   return pair(o, lse);
 }
 
@@ -372,23 +373,23 @@ BINDING(decode, 18) {
                     : e4m3 ? attn_prefill_split_keys(c.kind, B, rows, Hq, c.Hkv, Nq, max_seq_len,
                                                      total, num_sms())
                            : attn_decode_split_keys(B, Hq, c.Hkv, Nq, total, num_sms());
+  const Stream stream(a[6]);
   const bool allocate = none(a[7]);
   at::Tensor o, lse;
   if (allocate) {
-    o = make(q, q.sizes(), at::kBFloat16);
-    lse = make(q, {B, Hq, Nq}, at::kFloat);
+    o = stream.output(q, q.sizes(), at::kBFloat16);
+    lse = stream.output(q, {B, Hq, Nq}, at::kFloat);
   } else {
     o = buffer(a[7], at::kBFloat16, "o");
     lse = buffer(a[8], at::kFloat, "lse");
     check_shape(o, {B, Hq, Nq, c.d}, "o");
     check_shape(lse, {B, Hq, Nq}, "lse");
   }
-  const Workspace ws(a[9], allocate, q,
+  const Workspace ws(a[9], allocate, stream, q,
                      e4m3 ? attn_prefill_workspace_size(rows, Hq, c.d, max_seq_len, split)
                           : attn_decode_workspace_size(B, Hq, c.Hkv, Nq, c.d, max_seq_len, split));
   const int32_t* seq_lens = static_cast<const int32_t*>(lens.data_ptr());
   float* l = static_cast<float*>(lse.data_ptr());
-  const Stream stream(a[6]);
   const attn_status s =
       e4m3 ? attn_decode_paged_e4m3(&c, q.data_ptr(), seq_lens, o.data_ptr(), l, B, Hq, Nq, max_seq_len,
                                     split, sc.scale, sc.mask_kind, &sc.mask, sc.score_kind, &sc.score,
@@ -397,11 +398,8 @@ BINDING(decode, 18) {
                                c.Hkv, Nq, c.d, c.num_pages, c.page_size, c.max_pages_per_seq,
                                max_seq_len, split, sc.scale, sc.mask_kind, &sc.mask, sc.score_kind,
                                &sc.score, ws.p, ws.bytes, stream.handle);
-  stream.uses(ws.own);
   if (s != ATTN_OK) return status(s);
   if (!allocate) Py_RETURN_NONE;
-  stream.uses(o);
-  stream.uses(lse);
   return pair(o, lse);
 }
 

@@ -273,3 +273,37 @@ def test_decode_takes_the_numbers_that_int_takes():
             ea.decode_paged(*args, max_seq_len=float("nan"), kv_exp=c["kv_exp"])
         with pytest.raises(ea.AttnError, match="^attn_decode_paged" + ("_e4m3" if kind == "e4m3" else "") + ":"):
             ea.decode_paged(*args, split_keys=100, kv_exp=c["kv_exp"])
+
+
+# ------------------------------------------------------------------ streams
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_a_given_stream_does_not_wait_for_the_current_one(kind):
+    """Memory that was freed on the current stream while work on it is still queued there is not
+    given to a call on another stream, which would finish before that work writes."""
+    ea = _ea()
+    w = Batch([20, 3, 2], [900, 700, 400], d=128, Hq=8, kind=kind, seed=79)
+    c = w.cuda()
+    q1 = c["q"][:3].reshape(3, 8, 1, 128)
+    cache = (c["k_cache"], c["v_cache"], c["table"])
+
+    def calls(stream):
+        out = ea.prefill_paged(c["q"], *cache, c["offsets"], c["seq_lens"], kv_exp=c["kv_exp"],
+                               split_keys=256, mask_kind=MASK_CAUSAL, stream=stream)
+        out += ea.decode_paged(q1, *cache, c["seq_lens"], kv_exp=c["kv_exp"], split_keys=256, stream=stream)
+        return out + ea.cache_read(*cache, c["offsets"], c["seq_lens"], w.T, kv_exp=c["kv_exp"], stream=stream)
+
+    want = calls(None)
+    msl = c["table"].shape[1] * w.page
+    sizes = [t.nbytes for t in want] + [ea.prefill_workspace_size(T, 8, 128, msl, 256) for T in (w.T, 3)]
+    sizes.append(ea.decode_workspace_size(3, 8, w.Hkv, 1, 128, msl, 256))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                  # some 10 ms on the current stream
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    del junk                                       # its fills are still queued
+    got = calls(s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert ea.device_status() == 0
