@@ -113,8 +113,9 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(const CopyArgs
   const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0) report_bad_spans(p);
   const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int t = (int)(unit / a.slices);
-  if (t >= p.T) return;
+  const long long at = unit / a.slices;
+  if (at >= p.T || at >= __ldg(p.offsets + p.B)) return;  // (the rows behind are not read)
+  const int t = (int)at;
   int c0 = (int)(unit % a.slices) * a.per_warp * kChunksPerWarp;
   const int c_end = imin(c0 + a.per_warp * kChunksPerWarp, 2 * p.Hkv * kPer);
   const __nv_bfloat16* k = a.in[0].p + t * a.in[0].token_stride + lane % kPer * 8;
@@ -197,8 +198,9 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(const CopyArgs 
   const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0) report_bad_spans(p);
   const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int t = (int)(unit / a.slices);
-  if (t >= p.T) return;
+  const long long at = unit / a.slices;
+  if (at >= p.T) return;
+  const int t = (int)at;
   int c0 = (int)(unit % a.slices) * a.per_warp * kChunksPerWarp;
   const int c_end = imin(c0 + a.per_warp * kChunksPerWarp, 2 * p.Hkv * kPer);
   int b, pos;

@@ -307,3 +307,52 @@ def test_a_given_stream_does_not_wait_for_the_current_one(kind):
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     assert ea.device_status() == 0
+
+
+# ------------------------------------------------------------------ rows of no sequence
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_rows_behind_the_last_sequence_need_no_memory(kind):
+    """The C calls with a T beyond offsets[B]: inputs hold the sequences' rows alone, and what
+    lies behind the outputs' rows stays."""
+    import ctypes
+
+    from exact_io_aware_13_gb300 import _lib
+    ea, lib = _ea(), _lib.load()
+    w = Batch([4, 0, 9], [30, 7, 9], Hq=4, Hkv=2, d=64, page=16, kind=kind, seed=80)
+    c = w.cuda()
+    more = w.T + 5000                                     # rows of the calls
+    cache = _lib.PagedCache(c["k_cache"].data_ptr(), c["v_cache"].data_ptr(),
+                            None if kind == "bf16" else c["kv_exp"].data_ptr(), c["table"].data_ptr(),
+                            kind == "e4m3", w.pages, w.Hkv, w.page, w.d, w.table.shape[1])
+    ref = ctypes.byref(cache)
+    where = (c["offsets"].data_ptr(), c["seq_lens"].data_ptr(), w.B, more)
+    stream = torch.cuda.current_stream().cuda_stream
+    row = w.Hkv * w.d
+    assert lib.attn_cache_write(ref, c["k"].data_ptr(), row, w.d, c["v"].data_ptr(), row, w.d, *where,
+                                stream) == 0
+    torch.cuda.synchronize()
+    want = w.written()
+    for got, x in zip((c["k_cache"], c["v_cache"], c["kv_exp"]), want):
+        if x is not None:
+            view = torch.int16 if x.dtype == torch.bfloat16 else x.dtype
+            assert torch.equal(got.cpu().view(view), x.view(view))
+    k, v, o = (torch.full((w.T + 3, h, w.d), 7.0, dtype=torch.bfloat16, device="cuda") for h in (2, 2, 4))
+    lse = torch.full((w.T + 3, 4), 7.0, device="cuda")
+    assert lib.attn_cache_read(ref, k.data_ptr(), v.data_ptr(), *where, stream) == 0
+    ws = torch.empty(ea.prefill_workspace_size(more, 4, w.d, 32, 128) + 256, dtype=torch.uint8, device="cuda")
+    assert lib.attn_prefill_paged(ref, c["q"].data_ptr(), 4 * w.d, w.d, o.data_ptr(), lse.data_ptr(),
+                                  *where, 4, 9, 32, 128, ctypes.c_float(w.d ** -0.5), MASK_CAUSAL, None,
+                                  0, None, ws.data_ptr(), ws.numel(), stream) == 0
+    torch.cuda.synchronize()
+    assert ea.device_status() == 0
+    w.k_cache, w.v_cache, w.kv_exp = want
+    check_attention(o[:w.T], lse[:w.T], oracle(w), "rows")
+    for x in (k, v, o, lse):
+        assert bool((x[w.T:] == 7.0).all())
+    ex = None if want[2] is None else want[2].numpy()
+    kc, vc = (want[0], want[1]) if ex is None else (want[0].numpy(), want[1].numpy())
+    for b, n in enumerate(w.new):
+        K, V = P.sequence(kc, vc, ex, w.table[b], w.lens[b] - n, w.lens[b])
+        for got, x in ((k, K), (v, V)):
+            rows = got[w.offsets[b]:w.offsets[b] + n].double().cpu().numpy()
+            assert np.array_equal(rows, np.asarray(x, dtype=np.float64))
