@@ -35,6 +35,31 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
+class _Memory:
+    """Tensors that a call makes. For a call on another stream they are made on that stream:
+    memory freed on the current one may still be in use by work queued there, which the call
+    does not wait for. Outputs are recorded on the current stream too, where the caller goes on
+    with them; a workspace goes back to the call's stream alone."""
+
+    def __init__(self, stream):
+        self.stream = None
+        if stream is not None and stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
+            self.stream = (stream if isinstance(stream, torch.cuda.Stream)
+                           else torch.cuda.ExternalStream(stream.cuda_stream))
+
+    def workspace(self, shape, dtype, device) -> torch.Tensor:
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+    def output(self, shape, dtype, device) -> torch.Tensor:
+        t = self.workspace(shape, dtype, device)
+        if self.stream is not None:
+            t.record_stream(torch.cuda.current_stream())
+        return t
+
+
 def _params(mask_kind: int, window: int, doc_offsets: Optional[torch.Tensor],
             softcap: float, dropout_p: float = 0.0, dropout_seed: int = 0):
     mp = _lib.MaskParams(int(window), None, 0)
@@ -139,8 +164,9 @@ def forward(q, k, v, *, scale: Optional[float] = None, mask_kind: int = MASK_NON
     d = q.shape[-1]
     if scale is None:
         scale = float(torch.tensor(d, dtype=torch.float32).rsqrt())
-    o = torch.empty_like(q)
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    memory = _Memory(stream)
+    o = memory.output(q.shape, q.dtype, q.device)
+    lse = memory.output(q.shape[:-1], _F32, q.device)
     fwd_into(q, k, v, o, lse, scale=scale, mask_kind=mask_kind, window=window,
              doc_offsets=doc_offsets, score_kind=score_kind, softcap=softcap,
              dropout_p=dropout_p, dropout_seed=dropout_seed, stream=stream, impl=impl)
@@ -205,10 +231,9 @@ def backward(q, k, v, o, lse, dout, *, scale: Optional[float] = None,
     d = q.shape[-1]
     if scale is None:
         scale = float(torch.tensor(d, dtype=torch.float32).rsqrt())
-    dq = torch.empty_like(q)
-    dk = torch.empty_like(k)
-    dv = torch.empty_like(v)
-    ws = torch.empty(max(bwd_workspace_size(q, k), 256), dtype=torch.uint8, device=q.device)
+    memory = _Memory(stream)
+    dq, dk, dv = (memory.output(t.shape, t.dtype, t.device) for t in (q, k, v))
+    ws = memory.workspace((max(bwd_workspace_size(q, k), 256),), _U8, q.device)
     bwd_into(q, k, v, o, lse, dout, dq, dk, dv, ws, scale=scale, mask_kind=mask_kind,
              window=window, doc_offsets=doc_offsets, score_kind=score_kind, softcap=softcap,
              dropout_p=dropout_p, dropout_seed=dropout_seed, stream=stream, impl=impl)
@@ -220,7 +245,7 @@ def classify_tiles(mask_kind: int, Nq: int, Nkv: int, *, window: int = 0, doc_of
     """Tile classes [ceil(Nq/128), ceil(Nkv/128)] int32: 0 empty, 1 partial, 2 full."""
     lib = _lib.load()
     nqt, nkt = -(-Nq // TILE), -(-Nkv // TILE)
-    out = torch.empty((nqt, nkt), dtype=torch.int32, device=device)
+    out = _Memory(stream).output((nqt, nkt), torch.int32, device)
     mp, _, keep = _params(mask_kind, window, doc_offsets, 0.0)
     st = lib.attn_classify_tiles(mask_kind, mp, Nq, Nkv, _ptr(out), _stream(stream))
     del keep
@@ -262,13 +287,13 @@ def quantize_fp8(x: torch.Tensor, layout: int = FP8_TILES, stream=None):
     _check_dtypes((x, _BF16, "x"))
     lib = _lib.load()
     B, H, N, d = x.shape
+    memory = _Memory(stream)
     if layout == FP8_TILES:
-        codes = torch.empty((B, H, N, d), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((B * H, (N + 127) // 128), dtype=torch.float32, device=x.device)
+        codes = memory.output((B, H, N, d), _U8, x.device)
+        scales = memory.output((B * H, (N + 127) // 128), _F32, x.device)
     else:
-        codes = torch.empty((B, H, d, int(lib.attn_fp8_v_row_bytes(N))), dtype=torch.uint8,
-                            device=x.device)
-        scales = torch.empty((B * H,), dtype=torch.float32, device=x.device)
+        codes = memory.output((B, H, d, int(lib.attn_fp8_v_row_bytes(N))), _U8, x.device)
+        scales = memory.output((B * H,), _F32, x.device)
     st = lib.attn_quantize_fp8(_ptr(x), _ptr(codes), _ptr(scales), B * H, N, d, layout,
                                _stream(stream))
     _lib.check(st, "attn_quantize_fp8")
@@ -308,8 +333,9 @@ def forward_fp8(q, k, v, *, scale: Optional[float] = None, mask_kind: int = MASK
     if scale is None:
         scale = float(torch.tensor(d, dtype=torch.float32).rsqrt())
     (q8, sq), (k8, sk), (v8t, sv) = quant = fp8_inputs(q, k, v, stream)
-    o = torch.empty_like(q)
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    memory = _Memory(stream)
+    o = memory.output(q.shape, q.dtype, q.device)
+    lse = memory.output(q.shape[:-1], _F32, q.device)
     fwd_fp8_into(q8, sq, k8, sk, v8t, sv, o, lse, Nkv=k.shape[2], scale=scale,
                  mask_kind=mask_kind, window=window, doc_offsets=doc_offsets,
                  score_kind=score_kind, softcap=softcap, stream=stream)
