@@ -356,3 +356,20 @@ def test_rows_behind_the_last_sequence_need_no_memory(kind):
         for got, x in ((k, K), (v, V)):
             rows = got[w.offsets[b]:w.offsets[b] + n].double().cpu().numpy()
             assert np.array_equal(rows, np.asarray(x, dtype=np.float64))
+
+
+# ------------------------------------------------------------------ many units
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_more_units_than_sms_over_unequal_caches(kind):
+    """Few rows of many sequences in the tile kernel, unsplit by the library's choice, some caches
+    a hundred times as long as others; and the same rows in chunks of the library's smallest
+    choice."""
+    ea = _ea()
+    lens = [40 + 37 * i if i % 7 else 4000 + i for i in range(80)]
+    w = Batch([5 + i % 4 for i in range(80)], lens, Hq=20, Hkv=2, d=64, page=64, kind=kind, seed=81)
+    assert ea.prefill_split_keys(kind == "e4m3", 80, w.T, 20, 2, 8, 4096, sum(lens)) >= 4096
+    rows = np.unique(np.concatenate([w.offsets[:-1], w.offsets[1:] - 1]))   # the oracle's share
+    for split, mask in ((None, MASK_CAUSAL), (1024, MASK_NONE)):
+        o, lse = run_prefill(w, split=split, mask=mask, max_new=8, total_kv_tokens=sum(lens))
+        assert ea.device_status() == 0
+        check_attention(o, lse, oracle(w, mask, rows=rows), f"split {split}")
