@@ -121,9 +121,12 @@ cudaError_t launch_merge_as(const PagedAttention& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, kPerRow>, a);
 }
 cudaError_t launch_merge(const PagedAttention& a, cudaStream_t st) {
-  // Eight warps per row once a lone warp would take more than two turns of its four loads,
-  // as long as the rows are few (16384 rows fill the GPU twelve times with one warp each).
-  if (a.n_chunks > 8 && (long long)a.p.T * a.Hq <= 16384)
+  // Eight warps per row once a lone warp would take more than two turns of its four loads, as
+  // long as the rows are few: from some 2000 rows on, one warp each keeps enough loads in flight
+  // and needs no join. The kernel alone, one warp | eight (d = 128): 13 chunks, 64 rows 8.0 | 4.5
+  // us, 1024 8.6 | 8.3, 4096 10.8 | 19.6, 16384 26 | 64; 102 chunks, 64 rows 37 | 8.5, 1024
+  // 37 | 17, 4096 44 | 48, 16384 143 | 166.
+  if (a.n_chunks > 8 && (long long)a.p.T * a.Hq <= 2048)
     return a.p.d == 64 ? launch_merge_as<64, 8>(a, st) : launch_merge_as<128, 8>(a, st);
   return a.p.d == 64 ? launch_merge_as<64, 1>(a, st) : launch_merge_as<128, 1>(a, st);
 }

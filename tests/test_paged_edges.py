@@ -373,3 +373,14 @@ def test_more_units_than_sms_over_unequal_caches(kind):
         o, lse = run_prefill(w, split=split, mask=mask, max_new=8, total_kv_tokens=sum(lens))
         assert ea.device_status() == 0
         check_attention(o, lse, oracle(w, mask, rows=rows), f"split {split}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [255, 257])
+def test_merge_on_both_sides_of_its_rule(n, kind):
+    """More than eight chunks with just under and just over 2048 rows."""
+    w = Batch([n], [1500], Hq=8, Hkv=2, d=128, page=64, kind=kind, seed=82)
+    rows = np.arange(0, n, 16)
+    o, lse = run_prefill(w, split=128)
+    assert _ea().device_status() == 0
+    check_attention(o, lse, oracle(w, MASK_CAUSAL, rows=rows), f"rows {8 * n}")
