@@ -826,14 +826,19 @@ int attn_prefill_split_keys(int cache_kind, int B, int T, int Hq, int Hkv, int m
     // The row kernel: ten chunks per SM, as for decode, of at least 1024 keys. 8 new tokens of
     // 16 sequences of 2000 to 32768 (Hq = 32, Hkv = 8, d = 128): 233 us at 1792 keys, 300 at
     // 512, 245 at 4096. Three sequences of up to 700 tokens: 17.5 us unsplit, 15.5 us in
-    // chunks of 256, but the merge's launch and workspace cost the host 3 us.
+    // chunks of 256, but the merge's launch and workspace cost the host 3 us. The floor was
+    // measured on batches that fill the SMs; one sequence leaves some idle (8192 tokens, Hkv = 8:
+    // 64 CTAs, 18.4 us).
     const long long keys =
         std::max(1024, attn_decode_split_keys(B, Hq, Hkv, 1, total_kv_tokens, num_sms));
     return (int)std::min((keys + 127) / 128 * 128, one);
   }
   // The tile kernel, one CTA per SM: unsplit when the 256-row units fill the SMs (24 short
   // turns, 180 units: 36 us, 62 us in chunks of 1024), else four chunks per SM (the batch
-  // above over bf16, 128 units: 288 us at 4096 keys, 345 at 2048, 337 unsplit).
+  // above over bf16, 128 units: 288 us at 4096 keys, 345 at 2048, 337 unsplit). The number of
+  // units does not tell short caches from long ones: over unequal long caches (2000 to 32768)
+  // 8 new tokens of 16, 18, 19, 24 and 32 sequences, unsplit from 19 on, reach 5.1, 5.0, 5.1,
+  // 4.5 and 5.5 TB/s.
   const long long units = std::min((long long)T * G / 256 + B, B * ((rows + 255) / 256));
   const long long sms = num_sms > 0 ? num_sms : 148;
   if (units * Hkv >= sms) return (int)one;

@@ -72,7 +72,8 @@ struct PagedMaps {
   CUtensorMap k, v;
 };
 // Few query rows per kv head over an e4m3 cache take the row kernel: 32 rows over 16 long
-// caches run in 233 us there, in 339 us as tiles; with 64 rows it would read every key twice.
+// caches ran in 233 us there, in 339 us as tiles (both with a merge 9 us slower than now); with
+// 64 rows it would read every key twice.
 constexpr int kPagedRowsMax = 32;
 inline bool paged_few_rows(const PagedAttention& a) {
   return a.p.e4m3 && (long long)a.p.max_new * a.G <= kPagedRowsMax;

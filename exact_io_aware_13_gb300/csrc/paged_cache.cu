@@ -11,7 +11,7 @@
 // decode step. A warp takes a packed row, or a slice of it, kChunksPerWarp 16-byte pieces at
 // a time, all in flight at once; a row's first values are fetched before its slot is known.
 // Measured (Hkv = 8, d = 128): 97000 tokens from e4m3 back to bf16 in 95 us = 6.3 TB/s;
-// 29000 prompt tokens into e4m3 in 37.5 us = 4.7 TB/s (the quantiser's instructions).
+// 29000 prompt tokens into e4m3 in 38 us = 4.6 TB/s (the quantiser's instructions).
 #include "paged.cuh"
 
 namespace attn {
@@ -276,7 +276,7 @@ cudaError_t launch_copy(const CopyArgs& args, bool write, cudaStream_t st) {
   if (p.T == 0 || chunks == 0) return cudaSuccess;
   // A few rows (a decode step) are spread over as many warps as there are slices; long
   // batches give a warp a whole row, whose sequence and slot it looks up once: both kernels
-  // are bound by their instructions then (prompts of 29000 tokens: 41 us a slice per warp, 37.5 us now).
+  // are bound by their instructions then (prompts of 29000 tokens: 41 us a slice per warp, 38 us now).
   const int all = ceil_div(chunks, kChunksPerWarp);
   a.per_warp = (long long)p.T * all > 16384 ? all : 1;
   a.slices = ceil_div(all, a.per_warp);

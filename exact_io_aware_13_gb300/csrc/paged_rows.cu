@@ -20,14 +20,14 @@
 //     With the 128-byte swizzle every such shared-memory read is free of bank conflicts;
 //   * P^T's fragment is S^T's, transposed by movmatrix: no shared memory in between.
 //
-// Measured: decode of 64 sequences of 512 to 8192 tokens (Hq = 32, Hkv = 8, d = 128) 88 us in
-// the kernel, 5.8 TB/s of HBM (85 % of the copy rate); the whole call with the merge 94 us.
-// Two sequences of 131072: 100 us. 8 new tokens of 16 sequences (32 rows): 230 us. That is
-// the latency of a warp's steps: 2450 clocks per key tile (reading, converting and
-// multiplying 1600, its share of the requests 400, the rest waits), with the eight warps per
-// SM that 240 registers allow; leaving out every conversion or every exponential changes
-// nothing, a quarter of the MMAs with their conversions takes it to 205 us. A CTA's start and
-// end add 8000 clocks to 69000.
+// Measured: decode of 64 sequences of 512 to 8192 tokens (Hq = 32, Hkv = 8, d = 128) 94 us with
+// the merge, 5.5 TB/s of HBM (81 % of the copy rate); the kernel alone under ncu 92 us. Two
+// sequences of 131072: 100 us. 8 new tokens of 16 sequences (32 rows): 225 us, of which 216 in
+// the kernel. That is the latency of a warp's steps, with the eight warps per SM that 240
+// registers allow: some 2500 clocks per key tile, of which reading, converting and multiplying
+// take 1600 and its share of the requests 400, the rest waits. Leaving out every conversion or
+// every exponential changed nothing; a quarter of the MMAs with their conversions took 12 %
+// off. A CTA's start and end add 8000 clocks to 69000.
 //
 // Number ranges (fp16 operands, fp32 sums). Q: each row times a power of two that brings its
 // largest magnitude to [2^14, 2^15) - exact but for elements below 2^-29 of it, which lose

@@ -10,8 +10,9 @@
 //     head) against one key chunk; the softmax warps bring their Q rows into swizzled shared
 //     memory themselves (any strides, any G);
 //   * key tiles come from pages: two loader warps (K, V) issue one TMA box (bf16) or bulk
-//     copy (codes) per page piece, their page-table entries fetched one tile ahead. With one
-//     warp for both, pages of 16 took 1900 us where pages of 64 took 1355; with two, 1351;
+//     copy (codes) per page piece, their page-table entries fetched one tile ahead. Pages of
+//     64, 16 and 8 take the long chunk below 1392, 1396 and 1661 us; one warp for both took
+//     pages of 16 1.4 times as long as pages of 64;
 //   * masks are aligned at the bottom right (decode_row_keys), slots behind the sequence are
 //     masked in S and cleared in V, and so are the pages of the first key tile that no row of
 //     the unit sees: they are not loaded (a sliding window may have given them back);
@@ -31,12 +32,13 @@
 // [2^14, 2^15).
 //
 // What bounds it, measured (one chunk of 4096 tokens after 28672 cached ones, Hq = 32, Hkv =
-// 8, d = 128, 2.06 TFLOP): bf16 1314 us = 1569 TFLOP/s, a step of two query tiles against a
+// 8, d = 128, 2.06 TFLOP): bf16 1370 to 1416 us in runs that heat the GPU up to its power cap
+// (1500 to 1455 TFLOP/s; 1314 us once, with cool clocks), a step of two query tiles against a
 // key tile in 2700 clocks where the MMAs alone need 2048: the chain S -> softmax -> P V of a
-// tile, as in the forward kernel. e4m3 1790 us = 1150 TFLOP/s: the softmax of a tile takes
+// tile, as in the forward kernel. e4m3 1827 us = 1128 TFLOP/s: the softmax of a tile takes
 // 2160 clocks instead of 1310 beside the converters, whose fp16 tiles also cost 512 clocks of
 // shared-memory writes per step (without the conversion: 1440 TFLOP/s). Few rows over long
-// caches are bound by HBM (bf16, 32 rows: 4.8 TB/s) or by the conversion (e4m3).
+// caches are bound by HBM (bf16, 32 rows: 5.1 TB/s) or by the conversion (e4m3).
 #pragma once
 
 #include "paged.cuh"
@@ -78,7 +80,7 @@ struct Shape {
                     kThreads * kRegsLaunch,
                 "register pool");
   // P is handed to the MMA warp in two halves, so that the first products overlap the second
-  // half's exponentials: long chunk 1361 -> 1314 us over bf16. Over e4m3, whose softmax warps
+  // half's exponentials: long chunk 1361 -> 1314 us over bf16 (cool clocks both). Over e4m3, whose softmax warps
   // have fewer registers, six chunks went 689 -> 710 us: one part there.
   static constexpr int kPParts = kE4m3 ? 1 : 2;
   static constexpr float kLag = kE4m3 ? 4.0f : 8.0f;  // O is rescaled beyond this growth (log2)

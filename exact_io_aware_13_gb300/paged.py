@@ -7,7 +7,9 @@ A call's rows are packed: offsets int32 [B + 1] cuts them into sequences, and se
 rows are its newest tokens, row i of n at position seq_lens[b] - n + i. An e4m3 cache is two
 uint8 tensors of codes plus kv_exp uint8 [pages, Hkv, page_size, 2], the biased exponents of
 each token's K and V scale; passing kv_exp selects it. Wrong tensors raise ValueError, a
-refusal of the library AttnError.
+refusal of the library AttnError. stream (default: the current one) may be another stream of
+the device: the call waits for nothing on the current one, and the tensors that it makes are
+memory of that stream.
 """
 from __future__ import annotations
 
