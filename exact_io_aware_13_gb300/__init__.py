@@ -12,4 +12,7 @@ from .attention import (MASK_CAUSAL, MASK_DOCUMENT_CAUSAL, MASK_NONE,  # noqa: F
 from .paged import (CACHE_BF16, CACHE_E4M3, cache_read, cache_read_into, cache_write,  # noqa: F401
                     prefill_paged, prefill_paged_into, prefill_split_keys,
                     prefill_workspace_size)
+from .pool import (cache_compact, cache_compact_into, cache_copy, cache_fork,  # noqa: F401
+                   cache_resize, cache_resize_into, compact_workspace_size, copy_workspace_size,
+                   fork_workspace_size, resize_workspace_size, verify_drafts, verify_drafts_into)
 from ._lib import AttnError  # noqa: F401

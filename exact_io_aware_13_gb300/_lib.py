@@ -73,6 +73,15 @@ SIGNATURES = {
     "attn_prefill_split_keys": (_I, [_I] * 7 + [_L, _I]),
     "attn_decode_paged_e4m3": (_I, [_CP, _P, _P, _P, _P] + [_I] * 5 +
                                [_F, _I, _MP, _I, _SP, _P, ctypes.c_size_t, _P]),
+    "attn_cache_fork": (_I, [_P] * 4 + [_I] * 4 + [_P, ctypes.c_size_t, _P]),
+    "attn_fork_workspace_size": (ctypes.c_size_t, [_I] * 2),
+    "attn_cache_resize": (_I, [_CP, _P, _P, _P, _P, _I, _I, _P, _P, ctypes.c_size_t, _P]),
+    "attn_resize_workspace_size": (ctypes.c_size_t, [_I] * 3),
+    "attn_cache_compact": (_I, [_CP, _P, _P, _P, _I, _P, _P, _P, ctypes.c_size_t, _P]),
+    "attn_compact_workspace_size": (ctypes.c_size_t, [_I]),
+    "attn_cache_copy": (_I, [_CP, _CP, _P, _P, _I, _P, ctypes.c_size_t, _P]),
+    "attn_copy_workspace_size": (ctypes.c_size_t, [_I] * 2),
+    "attn_verify_drafts": (_I, [_I, _P, _L, _P, _L] + [_P] * 5 + [_I] * 3 + [_P] * 4),
     "attn_check_doc_offsets": (_I, [_P, _I, _I, _P]),
     "attn_device_status": (_I, [_P]),
     "attn_selftest_wait_timeout": (_I, [_P]),

@@ -27,7 +27,7 @@ BINDING_STAMP = os.path.join(BUILD_DIR, "binding.stamp")
 
 SOURCES = ["attn_api.cu", "simt.cu", "fwd_tc.cu", "fwd256_tc.cu", "bwd_tc.cu", "bwd256_tc.cu", "fp8.cu", "decode_tc.cu",
            "decode_copies2.cu", "paged_cache.cu", "paged_attn.cu", "paged_rows.cu",
-           "paged_tiles_bf16.cu", "paged_tiles_e4m3.cu"]
+           "paged_tiles_bf16.cu", "paged_tiles_e4m3.cu", "pool.cu", "pool_copy.cu", "verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]

@@ -14,6 +14,7 @@
 #include "attn.h"
 #include "kernels.h"
 #include "paged.h"
+#include "pool.h"
 #include "ptx.cuh"
 
 namespace attn {
@@ -448,6 +449,58 @@ bool stride_ok(long long s) { return s >= 0 && s % 8 == 0; }
 int table_capacity(const attn_paged_cache* c) {
   if (!c || c->max_pages_per_seq <= 0 || c->page_size <= 0) return 0;
   return (int)std::min<long long>((long long)c->max_pages_per_seq * c->page_size, kMaxSeqLen);
+}
+
+// ---------------------------------------------------------------- pages held by sequences
+// Pieces of a caller's workspace, each 256-byte aligned.
+struct Carve {
+  uint8_t* at;
+  int32_t* ints(long long n) {
+    int32_t* p = reinterpret_cast<int32_t*>(at);
+    at += round256((size_t)n * 4);
+    return p;
+  }
+};
+
+attn_status check_pool_state(int32_t* page_table, int32_t* seq_lens, int32_t* page_refs, int B,
+                             int max_pages, int num_pages, int page_size, PoolState* s) {
+  if (B > 0 && (!seq_lens || (max_pages > 0 && !page_table))) return ATTN_ERR_ARG;
+  if (num_pages > 0 && !page_refs) return ATTN_ERR_ARG;
+  if (!aligned4(page_table) || !aligned4(seq_lens) || !aligned4(page_refs)) return ATTN_ERR_ALIGN;
+  *s = PoolState{};
+  s->table = page_table; s->lens = seq_lens; s->refs = page_refs;
+  s->B = B; s->max_pages = max_pages; s->num_pages = num_pages; s->page_size = page_size;
+  s->page_shift = -1;
+  for (int k = 3; k < 31; ++k)
+    if (page_size == 1 << k) s->page_shift = k;
+  return ATTN_OK;
+}
+
+attn_status check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (need > 0 && (!workspace || bytes < need)) return ATTN_ERR_WORKSPACE;
+  return (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ? ATTN_ERR_ALIGN : ATTN_OK;
+}
+
+// The pool's tensors (a pool without pages, or without heads, has null ones).
+attn_status check_pool_tensors(const PagedProblem& p) {
+  if (p.num_pages > 0 && p.Hkv > 0 && (!p.k_cache || !p.v_cache || (p.e4m3 && !p.kv_exp)))
+    return ATTN_ERR_ARG;
+  if (!aligned16(p.k_cache) || !aligned16(p.v_cache) || !aligned16(p.kv_exp)) return ATTN_ERR_ALIGN;
+  return ATTN_OK;
+}
+
+PageCopy page_copy(const PagedProblem& from, const PagedProblem& to) {
+  PageCopy c{};
+  c.from[0] = from.k_cache; c.from[1] = from.v_cache; c.from[2] = from.kv_exp;
+  c.to[0] = to.k_cache; c.to[1] = to.v_cache; c.to[2] = to.kv_exp;
+  c.Hkv = from.Hkv; c.page_size = from.page_size; c.d = from.d; c.e4m3 = from.e4m3;
+  return c;
+}
+
+// Bytes of a pool's tensor 0 (K), 1 (V) or 2 (scales).
+size_t pool_bytes(const PagedProblem& p, int which) {
+  const size_t rows = (size_t)p.num_pages * p.Hkv * p.page_size;
+  return which == 2 ? (p.e4m3 ? rows * 2 : 0) : rows * p.d * (p.e4m3 ? 1 : 2);
 }
 
 // Score and mask arguments of the paged attention calls (as attn_decode_paged takes them).
@@ -932,6 +985,202 @@ attn_status attn_decode_paged_e4m3(const attn_paged_cache* cache, const void* q,
   a.q_token = a.o_token = d;
   a.l_batch = (long long)Hq * Nq; a.l_head = Nq; a.l_token = 1;
   return run_paged_attention(a, static_cast<cudaStream_t>(stream));
+}
+
+size_t attn_fork_workspace_size(int B, int max_pages_per_seq) {
+  if (B <= 0 || max_pages_per_seq < 0) return 0;
+  return round256((size_t)B * max_pages_per_seq * 4) + round256((size_t)B * 4);
+}
+
+attn_status attn_cache_fork(int32_t* page_table, int32_t* seq_lens, int32_t* page_refs,
+                            const int32_t* parents, int B, int max_pages_per_seq, int num_pages,
+                            int page_size, void* workspace, size_t workspace_bytes, void* stream) {
+  if (B < 0 || B > kForkMaxRows || max_pages_per_seq < 0 || num_pages < 0) return ATTN_ERR_SHAPE;
+  if (!decode_page_size_ok(page_size)) return ATTN_ERR_SHAPE;
+  if (B == 0) return ATTN_OK;
+  ForkArgs a{};
+  attn_status s = check_pool_state(page_table, seq_lens, page_refs, B, max_pages_per_seq, num_pages,
+                                   page_size, &a.s);
+  if (s != ATTN_OK) return s;
+  if (!parents) return ATTN_ERR_ARG;
+  if (!aligned4(parents)) return ATTN_ERR_ALIGN;
+  if ((s = check_workspace(workspace, workspace_bytes,
+                           attn_fork_workspace_size(B, max_pages_per_seq))) != ATTN_OK)
+    return s;
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != ATTN_OK) return s;
+  a.s.status = dev->status;
+  a.parents = parents;
+  Carve ws{static_cast<uint8_t*>(workspace)};
+  a.rows = ws.ints((long long)B * max_pages_per_seq);
+  a.lens = ws.ints(B);
+  return from_cuda(launch_fork(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_resize_workspace_size(int B, int max_pages_per_seq, int num_pages) {
+  if (B < 0 || max_pages_per_seq < 0 || num_pages < 0) return 0;
+  const long long list = std::min<long long>(num_pages, (long long)B * max_pages_per_seq);
+  return 6 * round256((size_t)B * 4) + round256((size_t)list * 4) + 256;
+}
+
+attn_status attn_cache_resize(const attn_paged_cache* cache, int32_t* page_table,
+                              int32_t* seq_lens, int32_t* page_refs, const int32_t* new_lens,
+                              int B, int window, int32_t* missing, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  PagedProblem p;
+  attn_status s = check_cache(cache, B, 0, 0, 0, &p);
+  if (s != ATTN_OK) return s;
+  if (window < 0 || !missing || (B > 0 && !new_lens)) return ATTN_ERR_ARG;
+  ResizeArgs a{};
+  if ((s = check_pool_state(page_table, seq_lens, page_refs, B, p.max_pages, p.num_pages, p.page_size,
+                            &a.s)) != ATTN_OK)
+    return s;
+  if ((s = check_pool_tensors(p)) != ATTN_OK) return s;
+  if (!aligned4(new_lens) || !aligned4(missing)) return ATTN_ERR_ALIGN;
+  if ((s = check_workspace(workspace, workspace_bytes,
+                           attn_resize_workspace_size(B, p.max_pages, p.num_pages))) != ATTN_OK)
+    return s;
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != ATTN_OK) return s;
+  a.s.status = dev->status;
+  a.new_lens = new_lens;
+  a.window = window;
+  a.missing = missing;
+  Carve ws{static_cast<uint8_t*>(workspace)};
+  a.write_page = ws.ints(B);
+  a.row_rank = ws.ints(B);
+  a.row_move = ws.ints(B);
+  a.free_list = ws.ints(std::min<long long>(p.num_pages, (long long)B * p.max_pages));
+  a.moves.src = ws.ints(B);
+  a.moves.dst = ws.ints(B);
+  a.moves.tokens = ws.ints(B);
+  a.moves.count = ws.ints(1);
+  a.moves.most = B;
+  PageCopy c = page_copy(p, p);
+  c.moves = a.moves;
+  return from_cuda(launch_resize(a, c, dev->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_compact_workspace_size(int num_pages) {
+  return num_pages < 0 ? 0 : 2 * round256((size_t)num_pages * 4) + 256;
+}
+
+attn_status attn_cache_compact(const attn_paged_cache* cache, int32_t* page_table,
+                               const int32_t* seq_lens, int32_t* page_refs, int B, int32_t* used,
+                               int32_t* page_map, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  PagedProblem p;
+  attn_status s = check_cache(cache, B, 0, 0, 0, &p);
+  if (s != ATTN_OK) return s;
+  if (!used || (p.num_pages > 0 && !page_map)) return ATTN_ERR_ARG;
+  CompactArgs a{};
+  if ((s = check_pool_state(page_table, const_cast<int32_t*>(seq_lens), page_refs, B, p.max_pages,
+                            p.num_pages, p.page_size, &a.s)) != ATTN_OK)
+    return s;
+  if ((s = check_pool_tensors(p)) != ATTN_OK) return s;
+  if (!aligned4(used) || !aligned4(page_map)) return ATTN_ERR_ALIGN;
+  if ((s = check_workspace(workspace, workspace_bytes, attn_compact_workspace_size(p.num_pages))) !=
+      ATTN_OK)
+    return s;
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != ATTN_OK) return s;
+  a.s.status = dev->status;
+  a.used = used;
+  a.page_map = page_map;
+  Carve ws{static_cast<uint8_t*>(workspace)};
+  a.moves.src = ws.ints(p.num_pages);
+  a.moves.dst = ws.ints(p.num_pages);
+  a.moves.count = ws.ints(1);
+  a.moves.most = p.num_pages / 2;
+  PageCopy c = page_copy(p, p);
+  c.moves = a.moves;
+  return from_cuda(launch_compact(a, c, dev->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_copy_workspace_size(int num_pages_to, int n) {
+  if (num_pages_to < 0 || n < 0) return 0;
+  return round256((size_t)num_pages_to * 4) + 2 * round256((size_t)n * 4) + 256;
+}
+
+attn_status attn_cache_copy(const attn_paged_cache* from, const attn_paged_cache* to,
+                            const int32_t* src_pages, const int32_t* dst_pages, int n,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  PagedProblem pf, pt;
+  attn_status s = check_cache(from, 0, 0, 0, 0, &pf);
+  if (s == ATTN_OK) s = check_cache(to, 0, 0, 0, 0, &pt);
+  if (s != ATTN_OK) return s;
+  if (pf.e4m3 != pt.e4m3) return ATTN_ERR_ARG;
+  if (n < 0 || pf.Hkv != pt.Hkv || pf.page_size != pt.page_size || pf.d != pt.d) return ATTN_ERR_SHAPE;
+  if (n == 0) return ATTN_OK;
+  if (!src_pages || !dst_pages) return ATTN_ERR_ARG;
+  if ((s = check_pool_tensors(pf)) != ATTN_OK || (s = check_pool_tensors(pt)) != ATTN_OK) return s;
+  PageCopy c = page_copy(pf, pt);
+  const bool same = pf.k_cache == pt.k_cache && pf.v_cache == pt.v_cache && pf.kv_exp == pt.kv_exp;
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < 3; ++j) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(c.from[i]), y = reinterpret_cast<uintptr_t>(c.to[j]);
+      if (x < y + pool_bytes(pt, j) && y < x + pool_bytes(pf, i) && !(same && i == j)) return ATTN_ERR_ARG;
+    }
+  if (!aligned4(src_pages) || !aligned4(dst_pages)) return ATTN_ERR_ALIGN;
+  if ((s = check_workspace(workspace, workspace_bytes, attn_copy_workspace_size(pt.num_pages, n))) !=
+      ATTN_OK)
+    return s;
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != ATTN_OK) return s;
+  CopyPlanArgs a{};
+  a.src = src_pages;
+  a.dst = dst_pages;
+  a.n = n;
+  a.num_pages_from = pf.num_pages;
+  a.num_pages_to = pt.num_pages;
+  // (one pool described with two sizes: the smaller one holds both pages)
+  a.same_pool = same;
+  if (same) a.num_pages_from = a.num_pages_to = std::min(pf.num_pages, pt.num_pages);
+  a.status = dev->status;
+  Carve ws{static_cast<uint8_t*>(workspace)};
+  a.owner = ws.ints(pt.num_pages);
+  a.moves.src = ws.ints(n);
+  a.moves.dst = ws.ints(n);
+  a.moves.count = ws.ints(1);
+  a.moves.most = n;
+  c.moves = a.moves;
+  return from_cuda(launch_copy_pages(a, c, dev->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+attn_status attn_verify_drafts(int prob_type, const void* target, long long target_stride,
+                               const void* draft, long long draft_stride, const int32_t* tokens,
+                               const int32_t* offsets, const float* accept_u,
+                               const float* sample_u, const int32_t* seq_lens, int B, int T, int V,
+                               int32_t* accepted, int32_t* next_tokens, int32_t* kept_lens,
+                               void* stream) {
+  if (prob_type != ATTN_PROB_FP32 && prob_type != ATTN_PROB_BF16 && prob_type != ATTN_PROB_FP16)
+    return ATTN_ERR_ARG;
+  if (B < 0 || T < 0 || V < 0 || B > kVerifyMaxRows) return ATTN_ERR_SHAPE;
+  if (target_stride < 0 || draft_stride < 0) return ATTN_ERR_SHAPE;
+  if (B == 0) return ATTN_OK;
+  if (!offsets || !sample_u || !accepted || !next_tokens || !seq_lens != !kept_lens) return ATTN_ERR_ARG;
+  if (T > 0 && (!tokens || !accept_u || (V > 0 && !target))) return ATTN_ERR_ARG;
+  const uintptr_t size = prob_type == ATTN_PROB_FP32 ? 4 : 2;
+  for (const void* x : {target, draft})
+    if (reinterpret_cast<uintptr_t>(x) % size != 0) return ATTN_ERR_ALIGN;
+  for (const void* x : {(const void*)tokens, (const void*)offsets, (const void*)accept_u,
+                        (const void*)sample_u, (const void*)seq_lens, (const void*)accepted,
+                        (const void*)next_tokens, (const void*)kept_lens})
+    if (!aligned4(x)) return ATTN_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  attn_status s = current_device(&dev);
+  if (s != ATTN_OK) return s;
+  VerifyArgs a{};
+  a.target = target; a.draft = draft;
+  a.target_stride = target_stride; a.draft_stride = draft_stride;
+  a.tokens = tokens; a.offsets = offsets;
+  a.accept_u = accept_u; a.sample_u = sample_u;
+  a.seq_lens = seq_lens;
+  a.accepted = accepted; a.next_tokens = next_tokens; a.kept_lens = kept_lens;
+  a.status = dev->status;
+  a.B = B; a.T = T; a.V = V;
+  a.type = prob_type;
+  return from_cuda(launch_verify(a, static_cast<cudaStream_t>(stream)));
 }
 
 attn_status attn_classify_tiles(int mask_kind, const attn_mask_params* mask_params, int Nq,

@@ -40,6 +40,7 @@ const char* name_of(at::ScalarType t) {
     case at::kFloat: return "torch.float32";
     case at::kInt: return "torch.int32";
     case at::kByte: return "torch.uint8";
+    case at::kHalf: return "torch.float16";
     default: return c10::toString(t);
   }
 }
@@ -154,31 +155,37 @@ int num_sms() {
   return count[dev];
 }
 
-// The cache's tensors. kv_exp selects e4m3.
-attn_paged_cache cache_of(PyObject* k, PyObject* v, PyObject* table, PyObject* kv_exp) {
+// A pool's tensors. kv_exp selects e4m3.
+attn_paged_cache pool_of(PyObject* k, PyObject* v, PyObject* kv_exp, const char* k_name,
+                         const char* v_name, const char* exp_name) {
   const bool e4m3 = !none(kv_exp);
   const at::ScalarType type = e4m3 ? at::kByte : at::kBFloat16;
-  const at::Tensor& kt = buffer(k, type, "k_cache");
-  const at::Tensor& vt = buffer(v, type, "v_cache");
-  const at::Tensor& tt = buffer(table, at::kInt, "page_table");
+  const at::Tensor& kt = buffer(k, type, k_name);
+  const at::Tensor& vt = buffer(v, type, v_name);
   if (kt.dim() != 4 || vt.sizes() != kt.sizes())
-    fail("k_cache and v_cache must be [pages, Hkv, page_size, d]");
-  if (tt.dim() != 2) fail("page_table must be [B, max_pages]");
+    fail("%s and %s must be [pages, Hkv, page_size, d]", k_name, v_name);
   attn_paged_cache c{};
   c.kind = e4m3 ? ATTN_CACHE_E4M3 : ATTN_CACHE_BF16;
   c.k = kt.data_ptr();
   c.v = vt.data_ptr();
-  c.page_table = static_cast<const int32_t*>(tt.data_ptr());
   c.num_pages = size_of(kt.size(0), "the pool");
   c.Hkv = size_of(kt.size(1), "Hkv");
   c.page_size = size_of(kt.size(2), "page_size");
   c.d = size_of(kt.size(3), "d");
-  c.max_pages_per_seq = size_of(tt.size(1), "page_table");
   if (e4m3) {
-    const at::Tensor& et = buffer(kv_exp, at::kByte, "kv_exp");
-    check_shape(et, {kt.size(0), kt.size(1), kt.size(2), 2}, "kv_exp");
+    const at::Tensor& et = buffer(kv_exp, at::kByte, exp_name);
+    check_shape(et, {kt.size(0), kt.size(1), kt.size(2), 2}, exp_name);
     c.kv_exp = static_cast<uint8_t*>(et.data_ptr());
   }
+  return c;
+}
+// The cache's tensors.
+attn_paged_cache cache_of(PyObject* k, PyObject* v, PyObject* table, PyObject* kv_exp) {
+  attn_paged_cache c = pool_of(k, v, kv_exp, "k_cache", "v_cache", "kv_exp");
+  const at::Tensor& tt = buffer(table, at::kInt, "page_table");
+  if (tt.dim() != 2) fail("page_table must be [B, max_pages]");
+  c.page_table = static_cast<const int32_t*>(tt.data_ptr());
+  c.max_pages_per_seq = size_of(tt.size(1), "page_table");
   return c;
 }
 
@@ -403,11 +410,169 @@ BINDING(decode, 18) {
   return pair(o, lse);
 }
 
+// The integers that say who holds which page.
+struct Pool {
+  int32_t *table, *lens, *refs;
+  int B, max_pages, num_pages;
+  const at::Tensor* like;
+  // num_pages < 0: as many as there are counts
+  Pool(PyObject* table_, PyObject* lens_, PyObject* refs_, int64_t pages) {
+    const at::Tensor& t = buffer(table_, at::kInt, "page_table");
+    const at::Tensor& l = buffer(lens_, at::kInt, "seq_lens");
+    const at::Tensor& r = buffer(refs_, at::kInt, "page_refs");
+    if (t.dim() != 2 || l.dim() != 1 || t.size(0) != l.size(0))
+      fail("page_table must be [B, max_pages] and seq_lens [B]");
+    if (r.dim() != 1 || (pages >= 0 && r.size(0) != pages)) fail("page_refs must be [pages]");
+    table = static_cast<int32_t*>(t.data_ptr());
+    lens = static_cast<int32_t*>(l.data_ptr());
+    refs = static_cast<int32_t*>(r.data_ptr());
+    B = size_of(t.size(0), "B");
+    max_pages = size_of(t.size(1), "page_table");
+    num_pages = size_of(r.size(0), "page_refs");
+    like = &t;
+  }
+};
+
+const int32_t* ints(PyObject* o, int64_t n, const char* name) {
+  const at::Tensor& t = buffer(o, at::kInt, name);
+  check_shape(t, {n}, name);
+  return static_cast<const int32_t*>(t.data_ptr());
+}
+
+// An output of the caller's, or one made for this call.
+at::Tensor ints_out(PyObject* o, int64_t n, const char* name, const Stream& stream, const at::Tensor& like) {
+  if (none(o)) return stream.output(like, {n}, at::kInt);
+  ints(o, n, name);
+  return THPVariable_Unpack(o);
+}
+int32_t* data(const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); }
+
+// page_table, seq_lens, page_refs, parents, page_size, workspace or None, stream
+BINDING(cache_fork, 7) {
+  const Pool s(a[0], a[1], a[2], -1);
+  const int32_t* parents = ints(a[3], s.B, "parents");
+  const Stream stream(a[6]);
+  const Workspace ws(a[5], true, stream, *s.like, attn_fork_workspace_size(s.B, s.max_pages));
+  return status(attn_cache_fork(s.table, s.lens, s.refs, parents, s.B, s.max_pages, s.num_pages,
+                                size_arg(a[4], "page_size"), ws.p, ws.bytes, stream.handle));
+}
+
+// k_cache, v_cache, page_table, seq_lens, page_refs, new_lens, kv_exp, window, stream, missing or
+// None, workspace or None
+BINDING(cache_resize, 11) {
+  const attn_paged_cache c = cache_of(a[0], a[1], a[2], a[6]);
+  const Pool s(a[2], a[3], a[4], c.num_pages);
+  const int32_t* new_lens = ints(a[5], s.B, "new_lens");
+  const Stream stream(a[8]);
+  const at::Tensor missing = ints_out(a[9], 1, "missing", stream, *s.like);
+  const Workspace ws(a[10], none(a[9]), stream, *s.like,
+                     attn_resize_workspace_size(s.B, s.max_pages, s.num_pages));
+  const attn_status r =
+      attn_cache_resize(&c, s.table, s.lens, s.refs, new_lens, s.B, size_arg(a[7], "window"),
+                        data(missing), ws.p, ws.bytes, stream.handle);
+  return r == ATTN_OK ? THPVariable_Wrap(missing) : status(r);
+}
+
+// k_cache, v_cache, page_table, seq_lens, page_refs, kv_exp, stream, used or None, page_map or
+// None, workspace or None
+BINDING(cache_compact, 10) {
+  const attn_paged_cache c = cache_of(a[0], a[1], a[2], a[5]);
+  const Pool s(a[2], a[3], a[4], c.num_pages);
+  const Stream stream(a[6]);
+  const at::Tensor used = ints_out(a[7], 1, "used", stream, *s.like);
+  const at::Tensor map = ints_out(a[8], s.num_pages, "page_map", stream, *s.like);
+  const Workspace ws(a[9], none(a[7]), stream, *s.like, attn_compact_workspace_size(s.num_pages));
+  const attn_status r = attn_cache_compact(&c, s.table, s.lens, s.refs, s.B, data(used), data(map),
+                                           ws.p, ws.bytes, stream.handle);
+  return r == ATTN_OK ? pair(used, map) : status(r);
+}
+
+// k_cache, v_cache, k_to, v_to, src_pages, dst_pages, kv_exp, kv_exp_to, workspace or None, stream
+BINDING(cache_copy, 10) {
+  const attn_paged_cache from = pool_of(a[0], a[1], a[6], "k_cache", "v_cache", "kv_exp");
+  const attn_paged_cache to = pool_of(a[2], a[3], a[7], "k_to", "v_to", "kv_exp_to");
+  if (from.kind != to.kind) fail("kv_exp and kv_exp_to must both be given or both be None");
+  if (from.Hkv != to.Hkv || from.page_size != to.page_size || from.d != to.d)
+    fail("the pools must agree in Hkv, page_size and d");
+  const at::Tensor& src = buffer(a[4], at::kInt, "src_pages");
+  if (src.dim() != 1) fail("src_pages must be [n]");
+  const int n = size_of(src.size(0), "src_pages");
+  const int32_t* dst = ints(a[5], n, "dst_pages");
+  const Stream stream(a[9]);
+  const Workspace ws(a[8], true, stream, src, attn_copy_workspace_size(to.num_pages, n));
+  return status(attn_cache_copy(&from, &to, static_cast<const int32_t*>(src.data_ptr()), dst, n, ws.p,
+                                ws.bytes, stream.handle));
+}
+
+// Rows of probabilities [T, V], contiguous along V.
+long long prob_rows(const at::Tensor& t, at::ScalarType type, int64_t V, const char* name) {
+  if (t.scalar_type() != type) fail("%s must be %s, got %s", name, name_of(type), name_of(t.scalar_type()));
+  check_device(t, name);
+  if (t.dim() != 2 || t.size(1) != V) fail("%s must be [T, V]", name);
+  if (t.size(1) > 1 && t.stride(1) != 1) fail("%s must be contiguous along V", name);
+  return t.size(0) > 1 ? t.stride(0) : 0;
+}
+const float* floats(PyObject* o, int64_t n, const char* name) {
+  const at::Tensor& t = buffer(o, at::kFloat, name);
+  check_shape(t, {n}, name);
+  return static_cast<const float*>(t.data_ptr());
+}
+
+// target, tokens, offsets, accept_u, sample_u, draft or None, seq_lens or None, stream, accepted
+// or None, next_tokens or None, kept_lens or None
+BINDING(verify_drafts, 11) {
+  const at::Tensor& target = tensor(a[0], "target");
+  const at::ScalarType type = target.scalar_type();
+  if (type != at::kFloat && type != at::kBFloat16 && type != at::kHalf)
+    fail("target must be torch.float32, torch.bfloat16 or torch.float16, got %s", name_of(type));
+  if (target.dim() != 2) fail("target must be [T, V]");
+  const int T = size_of(target.size(0), "target"), V = size_of(target.size(1), "target");
+  const long long target_stride = prob_rows(target, type, V, "target");
+  const void* draft = nullptr;
+  long long draft_stride = 0;
+  if (!none(a[5])) {
+    const at::Tensor& d = tensor(a[5], "draft");
+    draft_stride = prob_rows(d, type, V, "draft");
+    if (d.size(0) != T) fail("draft must be [T, V]");
+    draft = d.data_ptr();
+  }
+  const int32_t* tokens = ints(a[1], T, "tokens");
+  const at::Tensor& offsets = buffer(a[2], at::kInt, "offsets");
+  if (offsets.dim() != 1 || offsets.size(0) < 1) fail("offsets must be [B + 1]");
+  const int B = size_of(offsets.size(0) - 1, "B");
+  const float *accept_u = floats(a[3], T, "accept_u"), *sample_u = floats(a[4], B, "sample_u");
+  const int32_t* lens = none(a[6]) ? nullptr : ints(a[6], B, "seq_lens");
+  const Stream stream(a[7]);
+  const at::Tensor accepted = ints_out(a[8], B, "accepted", stream, target);
+  const at::Tensor next = ints_out(a[9], B, "next_tokens", stream, target);
+  at::Tensor kept;
+  if (lens) kept = ints_out(a[10], B, "kept_lens", stream, target);
+  else if (!none(a[10])) fail("kept_lens needs seq_lens");
+  const attn_status r = attn_verify_drafts(
+      type == at::kFloat ? ATTN_PROB_FP32 : type == at::kHalf ? ATTN_PROB_FP16 : ATTN_PROB_BF16,
+      target.data_ptr(), target_stride, draft, draft_stride, tokens,
+      static_cast<const int32_t*>(offsets.data_ptr()), accept_u, sample_u, lens, B, T, V, data(accepted),
+      data(next), lens ? data(kept) : nullptr, stream.handle);
+  if (r != ATTN_OK) return status(r);
+  if (!lens) return pair(accepted, next);
+  PyObject* two = pair(accepted, next);
+  PyObject* third = THPVariable_Wrap(kept);
+  PyObject* out = PyTuple_Pack(3, PyTuple_GET_ITEM(two, 0), PyTuple_GET_ITEM(two, 1), third);
+  Py_XDECREF(two);
+  Py_XDECREF(third);
+  return out;
+}
+
 PyMethodDef kMethods[] = {
     {"cache_write", (PyCFunction)(void (*)())cache_write, METH_FASTCALL, nullptr},
     {"cache_read", (PyCFunction)(void (*)())cache_read, METH_FASTCALL, nullptr},
     {"prefill", (PyCFunction)(void (*)())prefill, METH_FASTCALL, nullptr},
     {"decode", (PyCFunction)(void (*)())decode, METH_FASTCALL, nullptr},
+    {"cache_fork", (PyCFunction)(void (*)())cache_fork, METH_FASTCALL, nullptr},
+    {"cache_resize", (PyCFunction)(void (*)())cache_resize, METH_FASTCALL, nullptr},
+    {"cache_compact", (PyCFunction)(void (*)())cache_compact, METH_FASTCALL, nullptr},
+    {"cache_copy", (PyCFunction)(void (*)())cache_copy, METH_FASTCALL, nullptr},
+    {"verify_drafts", (PyCFunction)(void (*)())verify_drafts, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", "Binding of the paged-cache calls.", -1,
                        kMethods, nullptr, nullptr, nullptr, nullptr};

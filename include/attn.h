@@ -452,6 +452,141 @@ attn_status attn_decode_paged_e4m3(const attn_paged_cache* cache, const void* q,
                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * ---- Who holds which page: the cache's pages forked, grown, rolled back, given back,
+ * compacted and copied on the device, so that a serving loop needs no host round trip
+ * ("FlashAttention/es", "Variantes y sucesores": PagedAttention's pages are shared by many
+ * sequences). Three int32 DEVICE tensors hold the state, changed in place by these calls:
+ *   page_table  [B, max_pages_per_seq]: as in attn_decode_paged. Row b holds the pages of
+ *               entries 0 .. ceil(seq_lens[b] / page_size) - 1; a negative entry among them
+ *               holds none (a sliding window has passed it). Entries behind are not read.
+ *   seq_lens    [B]
+ *   page_refs   [num_pages]: how many table entries hold the page, plus whatever else the
+ *               caller counts as a holder (a prefix kept for later); a page with 0 is free
+ * The tensors of one call must not overlap. Bad DEVICE inputs (a length outside [0,
+ * max_pages_per_seq * page_size], an entry at or above num_pages that the call reads, a parent at
+ * or above B) are skipped, never followed, and reported by attn_device_status as ATTN_ERR_DEVICE_INPUT;
+ * the results of that call are then unspecified. The calls allocate nothing, take any B (0
+ * included, attn_cache_fork up to 49152) and are deterministic. workspace: DEVICE memory of
+ * the size that the call's size function gives, 256-byte aligned, not shared with a concurrent
+ * call (two captured graphs that may run at the same time need one each).
+ */
+
+/*
+ * Row i takes over what row parents[i] (int32 [B]) held before the call: its entries and its
+ * length; a negative parent leaves row i empty, parents[i] = i leaves it as it is. Several rows
+ * may have one parent (beams, samples of one prompt) and share its pages then, the last,
+ * partly filled one too: attn_cache_resize copies that page before one of them writes into
+ * it. Pages lose the holders that let go of them; those of no holder are free. Entries that
+ * no longer hold a page of their row become -1.
+ */
+attn_status attn_cache_fork(int32_t* page_table, int32_t* seq_lens, int32_t* page_refs,
+                            const int32_t* parents, int B, int max_pages_per_seq, int num_pages,
+                            int page_size, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of attn_cache_fork: round256(4 B max_pages_per_seq) + round256(4 B). */
+size_t attn_fork_workspace_size(int B, int max_pages_per_seq);
+
+/*
+ * Takes every row from seq_lens[b] to new_lens[b] tokens (int32 [B]): room for new tokens
+ * before attn_cache_write, a roll-back of drafted tokens that were not accepted, or 0 for a
+ * sequence that has ended. In this order:
+ *   1. Rows give back the entries behind their new length and, with window > 0, the pages
+ *      wholly below position min(seq_lens[b], new_lens[b]) - window + 1, the lowest one that a
+ *      sliding window leaves visible to the tokens to come: from there down to the next entry
+ *      that holds no page. Their entries become -1.
+ *   2. A row that grows from inside a page writes into that page. Where others hold it too the
+ *      row takes a new page and the tokens that it has there are copied (K, V and scales): of
+ *      the g rows that write into a page with r holders all do if r > g, else all but the
+ *      lowest row.
+ *   3. Rows take the pages for their new tokens. Free pages (those given back in step 1 are
+ *      among them) are handed out in ascending order, rows in order, a row's copied page first.
+ * If the pages do not suffice nothing is changed, and *missing (DEVICE int32) says how many
+ * lack; else it is 0. Only the cache's sizes, kind, k, v and kv_exp are used (cache->page_table
+ * is not read). What new pages hold behind the copied tokens stays.
+ */
+attn_status attn_cache_resize(const attn_paged_cache* cache, int32_t* page_table,
+                              int32_t* seq_lens, int32_t* page_refs, const int32_t* new_lens,
+                              int B, int window, int32_t* missing, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * Workspace bytes of attn_cache_resize: 6 round256(4 B) + round256(4 min(num_pages, B
+ * max_pages_per_seq)) + 256.
+ */
+size_t attn_resize_workspace_size(int B, int max_pages_per_seq, int num_pages);
+
+/*
+ * Moves the used pages (page_refs != 0) to the front of the pool: with U of them, the k-th
+ * highest used page at or above U moves to the k-th lowest free page below it, with its count,
+ * and the table's entries follow (held ones alone). Afterwards pages U .. num_pages - 1 are free:
+ * the pool can be cut there. *used (DEVICE int32) receives U and page_map (DEVICE int32
+ * [num_pages]) each page's new index, -1 for a free page, for holders outside of the table.
+ * Only the cache's sizes, kind, k, v and kv_exp are used (cache->page_table is not read).
+ */
+attn_status attn_cache_compact(const attn_paged_cache* cache, int32_t* page_table,
+                               const int32_t* seq_lens, int32_t* page_refs, int B, int32_t* used,
+                               int32_t* page_map, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* Workspace bytes of attn_cache_compact: 2 round256(4 num_pages) + 256. */
+size_t attn_compact_workspace_size(int num_pages);
+
+/*
+ * Copies page src_pages[i] of one pool to page dst_pages[i] of another (int32 [n]), K, V and
+ * scales, for i = 0 .. n - 1: to another engine's pool, or out of the way and back. Both caches
+ * agree in kind, Hkv, page_size and d; their page tables are not read. An entry with a negative
+ * page is skipped. `to` may be the same pool as `from`; pools that overlap in any other way are
+ * refused (ATTN_ERR_ARG). Every source is read as it was before the call: of the entries with one
+ * destination only the first is copied, and within one pool none whose source is another entry's
+ * destination; the entries left out, and pages outside the pools, are reported
+ * (ATTN_ERR_DEVICE_INPUT) while the others are copied. Counts and tables are the caller's.
+ */
+attn_status attn_cache_copy(const attn_paged_cache* from, const attn_paged_cache* to,
+                            const int32_t* src_pages, const int32_t* dst_pages, int n,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of attn_cache_copy: round256(4 num_pages of `to`) + 2 round256(4 n) + 256. */
+size_t attn_copy_workspace_size(int num_pages_to, int n);
+
+/* Types of probabilities. */
+enum { ATTN_PROB_FP32 = 0, ATTN_PROB_BF16 = 1, ATTN_PROB_FP16 = 2 };
+
+/*
+ * Verification of drafted tokens (speculative decoding), after attn_prefill_paged has scored
+ * them: decides from given random numbers which of a sequence's drafts stay, and draws the
+ * token that follows, so that the tokens are distributed as the target's own.
+ *
+ * The call takes the packed rows of the scored chunks: offsets int32 [B + 1] as in
+ * attn_prefill_paged. Row 0 of a sequence's n rows is the token it ended in, rows 1 .. n - 1 are
+ * its drafts (tokens int32 [T]; row 0's is not read).
+ *   target  [T, V] probabilities of the token after each row
+ *   draft   [T, V], row t: the probabilities that tokens[t + 1] was drawn from (the last row of
+ *           a sequence is not read); NULL for drafts that were not drawn (looked up): they count
+ *           as drawn from a distribution that has all its weight on them
+ *           both of prob_type, element (t, x) at t * stride + x (any stride in elements)
+ *   accept_u fp32 [T], sample_u fp32 [B]: random numbers, uniform in [0, 1)
+ * Draft x of row t stays iff accept_u[t] * draft[t, x] < target[t, x] (exactly, without
+ * rounding) and the drafts before it stay. accepted[b] (int32 [B]) of them stay. If that is all
+ * n - 1, the next token is drawn from the last row of target, else from
+ * max(target[t] - draft[t], 0) of the first row t whose draft does not stay (from target[t] if
+ * that is zero everywhere): next_tokens[b] (int32 [B]) is the lowest x whose cumulative weight
+ * exceeds sample_u[b] times the total weight (the last with any weight if rounding leaves
+ * none). Rows need not sum to one; what is not a positive finite number has no weight. Sums
+ * are held to about 48 bits. A sequence without rows gets 0 and -1; one whose row has no weight
+ * gets -1 and is reported (ATTN_ERR_DEVICE_INPUT), as are offsets that break the rule and a draft
+ * outside [0, V), which does not stay.
+ * With seq_lens (int32 [B], the cached tokens with all rows of the chunk; else NULL)
+ * kept_lens[b] = seq_lens[b] - (drafts that do not stay): attn_cache_resize takes it.
+ * The outputs are DEVICE tensors. Allocates nothing; deterministic.
+ */
+attn_status attn_verify_drafts(int prob_type, const void* target, long long target_stride,
+                               const void* draft, long long draft_stride, const int32_t* tokens,
+                               const int32_t* offsets, const float* accept_u,
+                               const float* sample_u, const int32_t* seq_lens, int B, int T, int V,
+                               int32_t* accepted, int32_t* next_tokens, int32_t* kept_lens,
+                               void* stream);
+
+/*
  * Block-sparsity classifier ("El FlexAttention de PyTorch con FlashAttention-4 es
  * un cambio radical", "Limitaciones actuales", names block sparsity): writes
  * classes[r * ceil(Nkv/128) + c] = EMPTY / PARTIAL / FULL for query tile r and key
