@@ -1155,7 +1155,8 @@ attn_status attn_verify_drafts(int prob_type, const void* target, long long targ
                                void* stream) {
   if (prob_type != ATTN_PROB_FP32 && prob_type != ATTN_PROB_BF16 && prob_type != ATTN_PROB_FP16)
     return ATTN_ERR_ARG;
-  if (B < 0 || T < 0 || V < 0 || B > kVerifyMaxRows) return ATTN_ERR_SHAPE;
+  if (B < 0 || T < 0 || V < 0 || B > kVerifyMaxRows || V > kVerifyMaxTokens)
+    return ATTN_ERR_SHAPE;
   if (target_stride < 0 || draft_stride < 0) return ATTN_ERR_SHAPE;
   if (B == 0) return ATTN_OK;
   if (!offsets || !sample_u || !accepted || !next_tokens || !seq_lens != !kept_lens) return ATTN_ERR_ARG;
@@ -1180,7 +1181,7 @@ attn_status attn_verify_drafts(int prob_type, const void* target, long long targ
   a.status = dev->status;
   a.B = B; a.T = T; a.V = V;
   a.type = prob_type;
-  return from_cuda(launch_verify(a, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_verify(a, dev->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 attn_status attn_classify_tiles(int mask_kind, const attn_mask_params* mask_params, int Nq,

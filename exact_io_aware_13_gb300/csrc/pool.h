@@ -85,6 +85,7 @@ struct VerifyArgs {
   int type;                               // ATTN_PROB_*
 };
 constexpr int kVerifyMaxRows = 1 << 26;  // sequences of a call: clusters of a grid
-cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t st);
+constexpr int kVerifyMaxTokens = 1 << 30;  // of a vocabulary
+cudaError_t launch_verify(const VerifyArgs& a, int num_sms, cudaStream_t st);
 
 }  // namespace attn

@@ -6,8 +6,12 @@
 // One thread-block cluster per sequence, each warp a contiguous piece of the vocabulary. Sums
 // have to be so exact that the drawn token does not depend on their order: weights are p - q
 // and its rounding error, accumulated as pairs of fp32 (about 48 bits), since fp64 runs at a
-// sixty-fourth of the fp32 rate. HBM-bound: V values of p, and of q, per sequence.
+// sixty-fourth of the fp32 rate: with fp64 sums over the warps and CTAs alone 128 sequences of
+// 128000 bf16 tokens took 90 us. HBM-bound for a batch: V values of p, and of q, per sequence;
+// for few sequences the chain offsets -> tokens -> p, q of the drafts -> rows -> token.
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "paged.cuh"
 #include "pool.cuh"
@@ -15,158 +19,203 @@
 namespace attn {
 namespace {
 
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyCtasPerSm = 4;
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // An unevaluated sum of two fp32 numbers.
-struct Pair {
-  float hi = 0.f, lo = 0.f;
+struct alignas(8) Pair {  // (one word of distributed shared memory)
+  float hi, lo;
   __device__ __forceinline__ void add(float x, float err) {
     const float s = hi + x, t = s - hi;  // Knuth's two-sum
     lo += ((hi - (s - t)) + (x - t)) + err;
     hi = s;
   }
-  __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
-};
-
-// A weight max(p - q, 0) and its rounding error (exact: p >= q >= 0). What is not a positive
-// finite number counts as no weight.
-struct Weight {
-  float w, err;
-  __device__ __forceinline__ Weight(float p, float q) {
-    w = p - q;
-    err = (p - w) - q;
-    if (!(w > 0.f && w < INFINITY)) w = err = 0.f;
+  __device__ __forceinline__ Pair normal() const {  // hi is the sum rounded
+    Pair p;
+    p.hi = hi + lo;
+    p.lo = lo - (p.hi - hi);
+    return p;
   }
 };
-
-// The p and q of one row, in groups of kVec elements that start at 16-byte boundaries of p.
-// Elements outside [0, V) and skipped ones have no weight.
-template <class T>
-struct RowReader {
-  static constexpr int kVec = 16 / sizeof(T);
-  const T *p, *q;
-  int V, shift, skip;  // element of group g, lane j: g * kVec + j - shift; skip: weightless token
-  bool q_vec;          // q's groups start at 16-byte boundaries too
-  __device__ __forceinline__ RowReader(const T* p_, const T* q_, int V_, int skip_)
-      : p(p_), q(q_), V(V_), skip(skip_) {
-    shift = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
-    q_vec = q && ((reinterpret_cast<uintptr_t>(q) & 15) / sizeof(T)) == (uintptr_t)shift;
+__device__ __forceinline__ Pair operator+(Pair a, const Pair& b) {
+  a.add(b.hi, b.lo);
+  return a.normal();
+}
+__device__ __forceinline__ bool operator>(const Pair& a, const Pair& b) {  // both normal
+  return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
+}
+__device__ __forceinline__ Pair operator*(float u, const Pair& a) {
+  Pair p;
+  p.hi = u * a.hi;
+  p.lo = fmaf(u, a.hi, -p.hi) + u * a.lo;
+  return p.normal();
+}
+__device__ __forceinline__ bool some_weight(const Pair& p) { return p.hi > 0.f && p.hi < INFINITY; }
+// Two of them, for the elements of even and of odd index.
+struct Pair2 {
+  uint64_t hi = 0, lo = 0;
+  __device__ __forceinline__ void add(uint64_t x, uint64_t err) {
+    const uint64_t s = add_f32x2(hi, x), t = sub_f32x2(s, hi);
+    lo = add_f32x2(lo, add_f32x2(add_f32x2(sub_f32x2(hi, sub_f32x2(s, t)), sub_f32x2(x, t)), err));
+    hi = s;
   }
-  __device__ __forceinline__ int groups() const { return (int)(((long long)V + shift + kVec - 1) / kVec); }
-  __device__ __forceinline__ int first(int g) const { return g * kVec - shift; }
-  __device__ __forceinline__ void load(int g, float (&pv)[kVec], float (&qv)[kVec]) const {
-    const int v0 = first(g);
-    if (v0 >= 0 && v0 + kVec <= V) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p + v0));
-      const T* e = reinterpret_cast<const T*>(&x);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) pv[j] = to_float(e[j]);
-      if (q_vec) {
-        const uint4 y = __ldg(reinterpret_cast<const uint4*>(q + v0));
-        const T* f = reinterpret_cast<const T*>(&y);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) qv[j] = to_float(f[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) qv[j] = q ? to_float(q[v0 + j]) : 0.f;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const bool in = v0 + j >= 0 && v0 + j < V;
-        pv[j] = in ? to_float(p[v0 + j]) : 0.f;
-        qv[j] = in && q ? to_float(q[v0 + j]) : 0.f;
-      }
-    }
-    if (skip >= v0 && skip < v0 + kVec) {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (v0 + j == skip) pv[j] = 0.f;
-    }
+  __device__ __forceinline__ Pair sum() const {
+    Pair p, r;
+    f32x2_split(hi, p.hi, r.hi);
+    f32x2_split(lo, p.lo, r.lo);
+    return p + r;
   }
 };
+__device__ __forceinline__ Pair shfl(const Pair& x, int lane) {
+  return Pair{__shfl_sync(0xffffffffu, x.hi, lane), __shfl_sync(0xffffffffu, x.lo, lane)};
+}
 
-__device__ __forceinline__ double warp_sum(double x) {
+// The inclusive prefix of x over the warp's lanes.
+__device__ __forceinline__ Pair warp_scan(Pair x, int lane) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  for (int off = 1; off < 32; off <<= 1) {
+    const Pair y{__shfl_up_sync(0xffffffffu, x.hi, off), __shfl_up_sync(0xffffffffu, x.lo, off)};
+    if (lane >= off) x = y + x;
+  }
   return x;
 }
 
-// First part of `n` whose running sum passes `threshold` (or the last with a sum at all, -1
-// without one); `before` is the sum in front of it. Every caller sees the same numbers.
-__device__ __forceinline__ int pick_part(const double* sums, int n, double base, double threshold,
-                                         double& before) {
-  int last = -1;
-  before = base;
-  double run = base;
-  for (int i = 0; i < n; ++i) {
-    if (!(sums[i] > 0.0)) continue;
-    last = i;
-    before = run;
-    run += sums[i];
-    if (run > threshold) break;
-  }
-  return last;
+// First lane whose running sum passes the threshold, the last with a sum at all if none does.
+// run: the inclusive prefix of mine. `before`: the running sum in front of that lane.
+__device__ __forceinline__ int pick_lane(const Pair& mine, const Pair& run, const Pair& threshold, int lane,
+                                         Pair& before) {
+  const uint32_t some = __ballot_sync(0xffffffffu, mine.hi > 0.f);
+  const uint32_t over = some & __ballot_sync(0xffffffffu, run > threshold);
+  const int who = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0;
+  const Pair x = shfl(run, who > 0 ? who - 1 : 0);
+  before = who > 0 ? x : Pair{0.f, 0.f};
+  return who;
 }
 
-// The token of a warp's groups [g0, g1) at which the running sum from `base` passes `threshold`;
-// the last with any weight if none does.
+// One row of p and, for a residual, of q; the weight of x is max(p - q, 0), none for `skip`. What
+// is not a positive finite number counts as no weight. Vector loads take groups of kVec
+// elements that start at 16-byte boundaries of p: group g holds g * kVec - shift onwards.
 template <class T>
-__device__ int find_token(const RowReader<T>& row, int g0, int g1, double base, double threshold, int lane) {
-  constexpr int kVec = RowReader<T>::kVec;
-  int last = -1;
-  for (int g = g0; g < g1; g += 32) {
-    float pv[kVec], qv[kVec];
-    const bool in = g + lane < g1;
-    if (in) row.load(g + lane, pv, qv);
-    double mine = 0.0;
-    int mine_last = -1;
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      if (!in) continue;
-      const Weight w(pv[j], qv[j]);
-      mine += (double)w.w + (double)w.err;
-      if (w.w > 0.f) mine_last = row.first(g + lane) + j;
+struct Row {
+  static constexpr int kVec = 16 / sizeof(T);
+  const T *p, *q;  // q may be null
+  int V, skip, shift;
+  bool vec;        // q's groups start at 16-byte boundaries too
+  __device__ __forceinline__ Row(const T* p_, const T* q_, int V_, int skip_) : p(p_), q(q_), V(V_), skip(skip_) {
+    shift = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+    vec = !q || ((reinterpret_cast<uintptr_t>(q) & 15) / sizeof(T)) == (uintptr_t)shift;
+  }
+  // The weight and its rounding error (exact, since p >= q >= 0).
+  __device__ __forceinline__ Pair weight(int x) const {
+    const float a = to_float(p[x]), b = q ? to_float(q[x]) : 0.f;
+    const float w = a - b, err = (a - w) - b;
+    const bool ok = w > 0.f && w < INFINITY && x != skip;
+    return Pair{ok ? w : 0.f, ok ? err : 0.f};
+  }
+  // Pieces of the row: whole steps of a warp's vector loads, from element at(i, per) on.
+  __device__ __forceinline__ int per_piece(int pieces) const {
+    const int groups = (int)(((unsigned)V + shift + kVec - 1) / kVec);
+    return ((groups + pieces - 1) / pieces + 31) / 32 * 32 * kVec;
+  }
+  __device__ __forceinline__ int at(int i, int per) const {
+    return (int)min(max((long long)per * i - shift, 0LL), (long long)V);
+  }
+  // Values 2j and 2j + 1 of a group.
+  static __device__ __forceinline__ uint64_t two(const uint4& x, int j) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if constexpr (sizeof(T) == 4) {
+      return f32x2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      return f32x2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+    } else {
+      const float2 f = f16x2_to_float2(w[j]);
+      return f32x2(f.x, f.y);
     }
-    double run = mine;
+  }
+};
+
+// Sum over whole groups [g0, g1), a lane's share of them, two elements per instruction and the
+// loads of kAhead groups in flight. fmaxf drops NaN; an infinity spoils the sum for good, which
+// the caller sees.
+template <class T, bool kQ>
+__device__ __forceinline__ Pair sum_groups(const Row<T>& row, int g0, int g1, int lane) {
+  constexpr int kVec = Row<T>::kVec, kAhead = kQ ? 2 : 4;
+  const uint4* p = reinterpret_cast<const uint4*>(row.p - row.shift);
+  const uint4* q = reinterpret_cast<const uint4*>(row.q - row.shift);
+  const int skip_group = !kQ && row.skip >= 0 ? (row.skip + row.shift) / kVec : -1;
+  const int skip_at = !kQ ? (row.skip + row.shift) % kVec : 0;
+  Pair2 sum;
+#pragma unroll 1
+  for (int g = g0 + lane; g - lane < g1; g += 32 * kAhead) {
+    uint4 x[kAhead], y[kAhead];
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, run, off);
-      if (lane >= off) run += y;
-    }
-    const uint32_t over = __ballot_sync(0xffffffffu, base + run > threshold && mine > 0.0);
-    if (over) {
-      const int who = __ffs(over) - 1;
-      int token = -1;
-      if (lane == who) {
-        double c = base + (run - mine);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const Weight w(pv[j], qv[j]);
-          c += (double)w.w + (double)w.err;
-          if (w.w > 0.f && c > threshold && token < 0) token = row.first(g + lane) + j;
-        }
-        if (token < 0) token = mine_last;
+    for (int i = 0; i < kAhead; ++i) {
+      x[i] = y[i] = make_uint4(0, 0, 0, 0);  // (no weight)
+      if (g + 32 * i < g1) {
+        x[i] = __ldg(p + g + 32 * i);
+        if constexpr (kQ) y[i] = __ldg(q + g + 32 * i);
       }
-      return __shfl_sync(0xffffffffu, token, who);
     }
-    base += __shfl_sync(0xffffffffu, run, 31);
-    const uint32_t some = __ballot_sync(0xffffffffu, mine_last >= 0);
-    if (some) last = __shfl_sync(0xffffffffu, mine_last, 31 - __clz(some));
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int j = 0; j < kVec / 2; ++j) {
+        uint64_t err = 0;
+        float u, v;
+        if constexpr (kQ) {
+          const uint64_t pv = Row<T>::two(x[i], j), qv = Row<T>::two(y[i], j), d = sub_f32x2(pv, qv);
+          float eu, ev;
+          f32x2_split(d, u, v);
+          f32x2_split(sub_f32x2(sub_f32x2(pv, d), qv), eu, ev);
+          err = f32x2(u > 0.f ? eu : 0.f, v > 0.f ? ev : 0.f);
+        } else {
+          f32x2_split(Row<T>::two(x[i], j), u, v);
+          if (g + 32 * i == skip_group && skip_at == 2 * j) u = 0.f;
+          if (g + 32 * i == skip_group && skip_at == 2 * j + 1) v = 0.f;
+        }
+        sum.add(f32x2(fmaxf(u, 0.f), fmaxf(v, 0.f)), err);
+      }
   }
-  return last;
+  return sum.sum();
+}
+
+// Sum of the weights of [x0, x1), a piece of the row, by one warp; every lane has it.
+template <class T, bool kQ>
+__device__ __forceinline__ Pair sum_piece(const Row<T>& row, int x0, int x1, int lane) {
+  constexpr int kVec = Row<T>::kVec;
+  // whole groups [g0, g1), loaded as such; the elements beside them one by one
+  const int shift = row.shift;
+  int g0 = (x0 + shift + kVec - 1) / kVec, g1 = (int)(((long long)x1 + shift) / kVec);
+  if (!row.vec || g1 < g0) g0 = g1 = (x1 + shift) / kVec;
+  Pair sum = sum_groups<T, kQ>(row, g0, g1, lane);
+  if (!__all_sync(0xffffffffu, sum.hi < INFINITY)) {
+    g0 = g1 = (x1 + shift) / kVec;
+    sum = Pair{0.f, 0.f};
+  }
+  const int lo = imin(imax(g0 * kVec - shift, x0), x1), hi = g1 > g0 ? g1 * kVec - shift : lo;
+  const int left = lo - x0, single = left + (x1 - hi);
+#pragma unroll 1
+  for (int i = lane; i < single; i += 32) sum = sum + row.weight(i < left ? x0 + i : hi + (i - left));
+  return shfl(warp_scan(sum, lane), 31);
 }
 
 template <class T>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVerifyThreads, kVerifyCtasPerSm) verify_kernel(const VerifyArgs a) {
   __shared__ int s_kept;
-  __shared__ double warp_sums[kVerifyWarps];
-  __shared__ Totals sums;
+  __shared__ Pair sums[kPlanMaxCtas * kVerifyWarps];  // of every warp of the cluster
+  __shared__ Pair span_sums[kVerifyWarps];
+  __shared__ int first_over, last_some;  // threads
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t cta = cluster_rank(), ctas = cluster_size();
   const int b = blockIdx.x / ctas;
@@ -187,18 +236,19 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
   cluster_started_arrive();
   if (warp == 0) {  // drafts that stay, 32 at a time
     int kept = n - 1;
+#pragma unroll 1
     for (int i0 = 0; i0 < n - 1; i0 += 32) {
       const int t = r0 + i0 + lane;
       bool stays = true;
       if (i0 + lane < n - 1) {
         const int x = __ldg(a.tokens + t + 1);
-        const double u = __ldg(a.accept_u + t);
-        if (x >= 0 && x < a.V) {
-          const double p = to_float(target[(size_t)t * a.target_stride + x]);
-          const double q = draft ? to_float(draft[(size_t)t * a.draft_stride + x]) : 1.f;
-          stays = u * q < p;
+        const float u = __ldg(a.accept_u + t);
+        stays = x >= 0 && x < a.V;
+        if (stays) {
+          const float p = to_float(target[(size_t)t * a.target_stride + x]);
+          const float q = draft ? to_float(draft[(size_t)t * a.draft_stride + x]) : 1.f;
+          stays = (double)u * (double)q < (double)p;  // exact
         } else {
-          stays = false;
           atomicOr(a.status, DEV_BAD_INPUT);
         }
       }
@@ -208,72 +258,108 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
         break;
       }
     }
-    if (lane == 0) s_kept = kept;
+    if (lane == 0) {
+      s_kept = kept;
+      first_over = kVerifyThreads;
+      last_some = 0;
+    }
   }
   __syncthreads();
   cluster_started_wait();
   const int kept = s_kept, t = r0 + kept;
   const bool rejected = kept < n - 1;
-  const T* p = target + (size_t)t * a.target_stride;
-  const T* q = rejected && draft ? draft + (size_t)t * a.draft_stride : nullptr;
-  const int skip = rejected && !draft ? __ldg(a.tokens + t + 1) : -1;
-  // the warp's groups of a row shared by `warps` warps, and the sums of the CTA's warps over theirs
-  int g0, g1;
-  auto sum_row = [&](const RowReader<T>& row, int me, int warps) {
-    constexpr int kVec = RowReader<T>::kVec;
-    const int groups = row.groups(), per = ((groups + warps - 1) / warps + 31) / 32 * 32;
-    g0 = (int)imin64((long long)me * per, groups);
-    g1 = (int)imin64((long long)(me + 1) * per, groups);
-    Pair sum;
-    for (int g = g0 + lane; g < g1; g += 32) {
-      float pv[kVec], qv[kVec];
-      row.load(g, pv, qv);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const Weight w(pv[j], qv[j]);
-        sum.add(w.w, w.err);
-      }
-    }
-    const double mine = warp_sum(sum.value());
-    if (lane == 0) warp_sums[warp] = mine;
-    __syncthreads();
-    double x = 0.0;
-    for (int w = 0; w < kVerifyWarps; ++w) x += warp_sums[w];
-    return x;
-  };
-  const double u = __ldg(a.sample_u + b);
-  auto draw = [&](const RowReader<T>& row, double before, double threshold) {
-    double mine_before;
-    if (pick_part(warp_sums, kVerifyWarps, before, threshold, mine_before) != warp) return;
-    const int token = find_token(row, g0, g1, mine_before, threshold, lane);
-    if (lane == 0) a.next_tokens[b] = token;
-  };
-  const RowReader<T> row(p, q, a.V, skip);
-  const double mine = sum_row(row, cta * kVerifyWarps + warp, ctas * kVerifyWarps);
-  if (warp == 0) sums.publish(__double_as_longlong(mine), lane);
-  cluster_sync();
-  double of[kPlanMaxCtas], total = 0.0;
-  for (int c = 0; c < kPlanMaxCtas; ++c) {
-    of[c] = c < (int)ctas ? __longlong_as_double(sums.of[c]) : 0.0;
-    total += of[c];
-  }
-  if (total > 0.0) {
-    double before;
-    if (pick_part(of, ctas, 0.0, u * total, before) == (int)cta) draw(row, before, u * total);
-  } else if (cta == 0) {
-    // p <= q everywhere: from p itself, by one CTA (p = q, or rows without a weight: rare)
-    const RowReader<T> all(p, nullptr, a.V, -1);
-    total = rejected ? sum_row(all, warp, kVerifyWarps) : 0.0;
-    if (total > 0.0) {
-      draw(all, 0.0, u * total);
-    } else if (threadIdx.x == 0) {
-      a.next_tokens[b] = -1;
-      atomicOr(a.status, DEV_BAD_INPUT);
-    }
-  }
+  const float u = __ldg(a.sample_u + b);
   if (cta == 0 && threadIdx.x == 0) {
     a.accepted[b] = kept;
     if (a.kept_lens) a.kept_lens[b] = __ldg(a.seq_lens + b) - (n - 1 - kept);
+  }
+  const int warps = ctas * kVerifyWarps, me = cta * kVerifyWarps + warp;
+  // Round 0: the residual, or the last row, by the whole cluster. Round 1, where p <= q
+  // everywhere (p = q): p itself, by one CTA.
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {
+    const bool residual = rejected && round == 0;
+    const Row<T> row(target + (size_t)t * a.target_stride,
+                     residual && draft ? draft + (size_t)t * a.draft_stride : nullptr, a.V,
+                     residual && !draft ? __ldg(a.tokens + t + 1) : -1);
+    const int pieces = round == 0 ? warps : kVerifyWarps;
+    const int per = row.per_piece(pieces);
+    const Pair s = row.q ? sum_piece<T, true>(row, row.at(me, per), row.at(me + 1, per), lane)
+                         : sum_piece<T, false>(row, row.at(me, per), row.at(me + 1, per), lane);
+    if (round == 0) {
+      if (lane < (int)ctas)
+        store_peer(&sums[me], lane, (unsigned long long)__float_as_uint(s.lo) << 32 | __float_as_uint(s.hi));
+      cluster_sync();
+    } else {  // (its peers may be gone)
+      if (lane == 0) sums[me] = s;
+      __syncthreads();
+    }
+    // every warp: the piece in which the running sum passes u times the total
+    constexpr int kEach = kPlanMaxCtas * kVerifyWarps / 32;
+    Pair of{0.f, 0.f};
+#pragma unroll 1
+    for (int i = 0; i < kEach; ++i)
+      if (lane * kEach + i < pieces) of = of + sums[lane * kEach + i];
+    Pair run = warp_scan(of, lane), before;
+    const Pair total = shfl(run, 31);
+    if (!some_weight(total)) {
+      if (cta != 0) return;
+      if (total.hi == 0.f && residual) {
+        __syncthreads();  // (sums has been read)
+        continue;
+      }
+      if (threadIdx.x == 0) {  // no weight, or sums above fp32's range
+        a.next_tokens[b] = -1;
+        atomicOr(a.status, DEV_BAD_INPUT);
+      }
+      return;
+    }
+    const Pair threshold = u * total;
+    int piece = pick_lane(of, run, threshold, lane, before) * kEach, last = piece;
+    Pair base = before;
+#pragma unroll 1
+    for (int i = piece; i < imin(piece + kEach, pieces); ++i) {  // among the lane's
+      if (!(sums[i].hi > 0.f)) continue;
+      last = i;
+      base = before;
+      before = before + sums[i];
+      if (before > threshold) break;
+    }
+    if (round == 0 && last / kVerifyWarps != (int)cta) return;
+    // by the whole CTA: a contiguous span of the piece per thread, the running sums at its ends,
+    // and the element where they enclose the threshold
+    const int x0 = row.at(last, per), x1 = row.at(last + 1, per);
+    const int span = (x1 - x0 + kVerifyThreads - 1) / kVerifyThreads;
+    const int at = imin(x0 + (int)threadIdx.x * span, x1), end = imin(at + span, x1);
+    Pair sum{0.f, 0.f};
+#pragma unroll 4
+    for (int x = at; x < end; ++x) sum = sum + row.weight(x);
+    run = warp_scan(sum, lane);
+    if (lane == 31) span_sums[warp] = run;
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < warp; ++w) base = base + span_sums[w];
+    run = base + run;
+    before = Pair{__shfl_up_sync(0xffffffffu, run.hi, 1), __shfl_up_sync(0xffffffffu, run.lo, 1)};
+    if (lane == 0) before = base;
+    if (sum.hi > 0.f) {
+      if (run > threshold) atomicMin(&first_over, (int)threadIdx.x);
+      else atomicMax(&last_some, (int)threadIdx.x);
+    }
+    __syncthreads();
+    if ((int)threadIdx.x != (first_over < kVerifyThreads ? first_over : last_some)) return;
+    int token = -1;
+#pragma unroll 4
+    for (int x = at; x < end; ++x) {
+      const Pair w = row.weight(x);
+      before = before + w;
+      if (w.hi > 0.f) {
+        token = x;
+        if (before > threshold) break;
+      }
+    }
+    a.next_tokens[b] = token;
+    return;
   }
 }
 
@@ -294,8 +380,11 @@ cudaError_t launch(const VerifyArgs& a, int ctas, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t st) {
-  const int ctas = a.V > 8192 ? 8 : 1;
+cudaError_t launch_verify(const VerifyArgs& a, int num_sms, cudaStream_t st) {
+  // CTAs per sequence: what the SMs hold at once, shared by the sequences, and a step of the
+  // warps' vector loads each at least
+  const long long held = (long long)num_sms * kVerifyCtasPerSm / a.B;
+  const int ctas = (int)imin64(imin64(held > 1 ? held : 1, kPlanMaxCtas), a.V / 4096 + 1);
   switch (a.type) {
     case ATTN_PROB_FP32: return launch<float>(a, ctas, st);
     case ATTN_PROB_BF16: return launch<__nv_bfloat16>(a, ctas, st);
