@@ -989,7 +989,7 @@ attn_status attn_decode_paged_e4m3(const attn_paged_cache* cache, const void* q,
 
 size_t attn_fork_workspace_size(int B, int max_pages_per_seq) {
   if (B <= 0 || max_pages_per_seq < 0) return 0;
-  return round256((size_t)B * max_pages_per_seq * 4) + round256((size_t)B * 4);
+  return round256((size_t)B * max_pages_per_seq * 4) + 2 * round256((size_t)B * 4);
 }
 
 attn_status attn_cache_fork(int32_t* page_table, int32_t* seq_lens, int32_t* page_refs,
@@ -1013,14 +1013,15 @@ attn_status attn_cache_fork(int32_t* page_table, int32_t* seq_lens, int32_t* pag
   a.parents = parents;
   Carve ws{static_cast<uint8_t*>(workspace)};
   a.rows = ws.ints((long long)B * max_pages_per_seq);
-  a.lens = ws.ints(B);
-  return from_cuda(launch_fork(a, static_cast<cudaStream_t>(stream)));
+  a.old_lens = ws.ints(B);
+  a.new_lens = ws.ints(B);
+  return from_cuda(launch_fork(a, dev->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t attn_resize_workspace_size(int B, int max_pages_per_seq, int num_pages) {
   if (B < 0 || max_pages_per_seq < 0 || num_pages < 0) return 0;
   const long long list = std::min<long long>(num_pages, (long long)B * max_pages_per_seq);
-  return 6 * round256((size_t)B * 4) + round256((size_t)list * 4) + 256;
+  return 6 * round256((size_t)B * 4) + 2 * round256((size_t)num_pages * 4) + round256((size_t)list * 4) + 256;
 }
 
 attn_status attn_cache_resize(const attn_paged_cache* cache, int32_t* page_table,
@@ -1050,6 +1051,8 @@ attn_status attn_cache_resize(const attn_paged_cache* cache, int32_t* page_table
   a.write_page = ws.ints(B);
   a.row_rank = ws.ints(B);
   a.row_move = ws.ints(B);
+  a.writers = ws.ints(p.num_pages);
+  a.lowest = ws.ints(p.num_pages);
   a.free_list = ws.ints(std::min<long long>(p.num_pages, (long long)B * p.max_pages));
   a.moves.src = ws.ints(B);
   a.moves.dst = ws.ints(B);
@@ -1058,6 +1061,7 @@ attn_status attn_cache_resize(const attn_paged_cache* cache, int32_t* page_table
   a.moves.most = B;
   PageCopy c = page_copy(p, p);
   c.moves = a.moves;
+  c.status = dev->status;
   return from_cuda(launch_resize(a, c, dev->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -1094,6 +1098,7 @@ attn_status attn_cache_compact(const attn_paged_cache* cache, int32_t* page_tabl
   a.moves.most = p.num_pages / 2;
   PageCopy c = page_copy(p, p);
   c.moves = a.moves;
+  c.status = dev->status;
   return from_cuda(launch_compact(a, c, dev->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -1144,6 +1149,7 @@ attn_status attn_cache_copy(const attn_paged_cache* from, const attn_paged_cache
   a.moves.count = ws.ints(1);
   a.moves.most = n;
   c.moves = a.moves;
+  c.status = dev->status;
   return from_cuda(launch_copy_pages(a, c, dev->num_sms, static_cast<cudaStream_t>(stream)));
 }
 

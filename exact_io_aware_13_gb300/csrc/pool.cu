@@ -22,166 +22,246 @@ __device__ __forceinline__ void add_refs(const PoolState& s, int page, int n) {
 
 // ---------------------------------------------------------------- fork
 // Row i takes what row parents[i] held. A row r that c rows take adds c - 1 holders to each of
-// its pages. The new rows are gathered into the workspace before any row is overwritten.
-__global__ void __launch_bounds__(kPlanThreads) fork_kernel(const ForkArgs a) {
+// its pages. The new rows are gathered into the workspace before any row is overwritten: in one
+// cluster (kBoth) for few entries, else in two launches over all SMs. A warp takes kForkChunk
+// entries of a row at a time, a lane's loads all in flight.
+enum ForkPhase { kGather = 1, kScatter = 2, kBoth = 3 };
+constexpr int kForkChunk = 256, kForkEach = kForkChunk / 32;
+__host__ __device__ constexpr int fork_chunks(int max_pages) {
+  return max_pages > 0 ? (max_pages + kForkChunk - 1) / kForkChunk : 1;
+}
+
+template <int kPhase>
+__global__ void __launch_bounds__(kPlanThreads, 1) fork_kernel(const ForkArgs a) {
   extern __shared__ int taken[];  // [B]: rows that take row r
   const PoolState& s = a.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int step = cluster_size() * kPlanWarps, first = cluster_rank() * kPlanWarps + warp;
-  for (int b = threadIdx.x; b < s.B; b += kPlanThreads) taken[b] = 0;
-  __syncthreads();
+  const int chunks = fork_chunks(s.max_pages);
+  const long long items = (long long)s.B * chunks;
+  const long long step = (long long)gridDim.x * kPlanWarps, first = (long long)blockIdx.x * kPlanWarps + warp;
   auto parent_of = [&](int b) {
     const int p = __ldg(a.parents + b);
     if (p < s.B) return p < 0 ? -1 : p;
     report(s);
     return b;
   };
-  for (int b = threadIdx.x; b < s.B; b += kPlanThreads) {
-    const int p = parent_of(b);
-    if (p >= 0) atomicAdd(&taken[p], 1);
-  }
-  __syncthreads();
-  auto held = [&](int b) {  // pages of row b before the fork
+  auto length = [&](int b) {  // before the fork
     const int L = s.lens[b];
-    if (length_ok(s, L)) return pages_of(s, L);
+    if (length_ok(s, L)) return L;
     report(s);
     return 0;
   };
-  for (int b = first; b < s.B; b += step) {
-    const int32_t* row = s.table + (size_t)b * s.max_pages;
-    const int c = taken[b];
-    if (c != 1)
-      for (int i = lane, n = held(b); i < n; i += 32) add_refs(s, row[i], c - 1);
-    const int p = parent_of(b);
-    if (p == b) continue;
-    const int n = p < 0 ? 0 : held(p);
-    const int32_t* from = s.table + (size_t)(p < 0 ? 0 : p) * s.max_pages;
-    int32_t* to = a.rows + (size_t)b * s.max_pages;
-    for (int i = lane; i < n; i += 32) {
-      const int page = from[i];
-      if (page >= s.num_pages) report(s);
-      to[i] = page;
+  if constexpr (kPhase & kGather) {
+    grid_dependents_launch();
+    for (int b = threadIdx.x; b < s.B; b += kPlanThreads) taken[b] = 0;
+    __syncthreads();
+    for (int b = threadIdx.x; b < s.B; b += kPlanThreads) {
+      const int p = parent_of(b);
+      if (p >= 0) atomicAdd(&taken[p], 1);
     }
-    if (lane == 0) a.lens[b] = n > 0 ? s.lens[p] : 0;
+    __syncthreads();
+    for (long long item = first; item < items; item += step) {
+      const int b = (int)(item / chunks), i0 = (int)(item - (long long)b * chunks) * kForkChunk + lane;
+      const int c = taken[b], p = parent_of(b);
+      const int L = length(b), n = c != 1 ? pages_of(s, L) : 0;
+      const int32_t* row = s.table + (size_t)b * s.max_pages;
+      int page[kForkEach];
+#pragma unroll
+      for (int j = 0; j < kForkEach; ++j) page[j] = i0 + 32 * j < n ? row[i0 + 32 * j] : -1;
+#pragma unroll
+      for (int j = 0; j < kForkEach; ++j) add_refs(s, page[j], c - 1);
+      if (p == b) continue;
+      const int new_length = p < 0 ? 0 : length(p), m = pages_of(s, new_length);
+      const int32_t* from = s.table + (size_t)(p < 0 ? 0 : p) * s.max_pages;
+      int32_t* to = a.rows + (size_t)b * s.max_pages;
+#pragma unroll
+      for (int j = 0; j < kForkEach; ++j) page[j] = i0 + 32 * j < m ? from[i0 + 32 * j] : -1;
+#pragma unroll
+      for (int j = 0; j < kForkEach; ++j) {
+        if (page[j] >= s.num_pages) report(s);
+        if (i0 + 32 * j < m) to[i0 + 32 * j] = page[j];
+      }
+      if (i0 == 0) {
+        a.old_lens[b] = L;
+        a.new_lens[b] = new_length;
+      }
+    }
   }
-  cluster_sync();
-  for (int b = first; b < s.B; b += step) {
-    if (parent_of(b) == b) continue;
-    const int old = held(b), L = __ldcg(a.lens + b), n = pages_of(s, L);
-    __syncwarp();
-    int32_t* row = s.table + (size_t)b * s.max_pages;
-    const int32_t* from = a.rows + (size_t)b * s.max_pages;
-    for (int i = lane; i < n; i += 32) row[i] = __ldcg(from + i);
-    for (int i = n + lane; i < old; i += 32) row[i] = -1;
-    if (lane == 0) s.lens[b] = L;
+  if constexpr (kPhase == kBoth) cluster_sync();
+  if constexpr (kPhase == kScatter) grid_dependency_wait();
+  if constexpr (kPhase & kScatter) {
+    for (long long item = first; item < items; item += step) {
+      const int b = (int)(item / chunks), i0 = (int)(item - (long long)b * chunks) * kForkChunk + lane;
+      if (parent_of(b) == b) continue;
+      const int L = __ldcg(a.new_lens + b), n = pages_of(s, L), old = pages_of(s, __ldcg(a.old_lens + b));
+      int32_t* row = s.table + (size_t)b * s.max_pages;
+      const int32_t* from = a.rows + (size_t)b * s.max_pages;
+      int page[kForkEach];
+#pragma unroll
+      for (int j = 0; j < kForkEach; ++j) page[j] = i0 + 32 * j < n ? __ldcg(from + i0 + 32 * j) : -1;
+#pragma unroll
+      for (int j = 0; j < kForkEach; ++j)
+        if (i0 + 32 * j < (n > old ? n : old)) row[i0 + 32 * j] = page[j];
+      if (i0 == 0) s.lens[b] = L;
+    }
   }
 }
 
 // ---------------------------------------------------------------- resize
-// Lengths of row b before and after; a bad length leaves the row as it is.
+// Lengths of row b before and after; a bad length leaves the row as it is, no row at all has none.
 struct RowLens {
-  int L, N;
-  __device__ __forceinline__ RowLens(const ResizeArgs& a, int b) {
+  int L = 0, N = 0;
+  bool ok = true;
+  __device__ __forceinline__ RowLens(const ResizeArgs& a, int b, int end) {
+    if (b >= end) return;
     L = a.s.lens[b];
     N = __ldg(a.new_lens + b);
-    if (!length_ok(a.s, L)) L = N = 0;
-    if (!length_ok(a.s, N)) N = L;
+    ok = length_ok(a.s, L) && length_ok(a.s, N);
+    if (!ok) {
+      if (!length_ok(a.s, L)) L = 0;
+      N = L;
+    }
   }
 };
 
-// Calls f(i, page) for the table entries that row b gives back, all lanes of a warp together:
-// those behind its new length (empty ones too), and with a window those wholly below it, from
-// the window's edge down to the next entry that holds no page.
+// Calls f(b, i, page) for the table entries that the warp's rows give back (lane l has row b0 + l):
+// those behind a row's new length (empty ones too), and with a window those wholly below it, from
+// the window's edge down to the next entry that holds no page. The warp takes its rows one by one.
+constexpr int kWalk = 4;  // words of a row in flight
 template <class F>
-__device__ __forceinline__ void released(const ResizeArgs& a, int b, const RowLens& r, int lane, F f) {
+__device__ __forceinline__ void released(const ResizeArgs& a, int b0, const RowLens& r, int lane, F f) {
   const PoolState& s = a.s;
-  const int32_t* row = s.table + (size_t)b * s.max_pages;
-  for (int i = pages_of(s, r.N) + lane, n = pages_of(s, r.L); i < n; i += 32) f(i, row[i]);
-  if (a.window <= 0) return;
-  const int low = imin(r.L, r.N) - a.window + 1;  // the lowest position that stays visible
-  for (int top = low > 0 ? page_index(s, low) - 1 : -1; top >= 0; top -= 32) {
-    const int i = top - lane;
-    const int page = i >= 0 ? row[i] : -1;
-    const uint32_t holes = __ballot_sync(0xffffffffu, page < 0);
-    if (lane < (holes ? __ffs(holes) - 1 : 32)) f(i, page);
-    if (holes) break;
+  const int n0 = pages_of(s, r.N), n1 = pages_of(s, r.L);
+  int top = -1;  // the last entry wholly below the lowest position that stays visible
+  if (a.window > 0) {
+    const int low = imin(r.L, r.N) - a.window + 1;
+    if (low > 0) top = page_index(s, low) - 1;
+    if (top >= 0 && s.table[(size_t)(b0 + lane) * s.max_pages + top] < 0) top = -1;  // the usual case
+  }
+#pragma unroll 1
+  for (uint32_t todo = __ballot_sync(0xffffffffu, n1 > n0 || top >= 0); todo; todo &= todo - 1) {
+    const int who = __ffs(todo) - 1, b = b0 + who;
+    const int32_t* row = s.table + (size_t)b * s.max_pages;
+    const int end = __shfl_sync(0xffffffffu, n1, who);
+#pragma unroll 8
+    for (int i = __shfl_sync(0xffffffffu, n0, who) + lane; i < end; i += 32) f(b, i, row[i]);
+    bool more = true;
+#pragma unroll 1
+    for (int t = __shfl_sync(0xffffffffu, top, who) - lane; more; t -= 32 * kWalk) {
+      int page[kWalk];
+#pragma unroll
+      for (int j = 0; j < kWalk; ++j) page[j] = t - 32 * j >= 0 ? row[t - 32 * j] : -1;
+#pragma unroll
+      for (int j = 0; j < kWalk; ++j) {
+        const uint32_t holes = __ballot_sync(0xffffffffu, page[j] < 0);
+        if (more && lane < (holes ? __ffs(holes) - 1 : 32)) f(b, t - 32 * j, page[j]);
+        more = more && !holes;
+      }
+    }
+  }
+}
+
+// Calls f(first page, mask of the free ones among 32 pages from there) for [lo, hi), kMasks words of
+// counts in flight; f says whether to go on.
+constexpr int kMasks = 8;
+template <class F>
+__device__ __forceinline__ void free_masks(const int32_t* refs, int lo, int hi, int lane, F f) {
+#pragma unroll 1
+  for (int p = lo; p < hi; p += 32 * kMasks) {
+    uint32_t is_free = 0;
+#pragma unroll
+    for (int j = 0; j < kMasks; ++j) {
+      const int at = p + 32 * j + lane;
+      if (at < hi && __ldcg(refs + at) == 0) is_free |= 1u << j;
+    }
+#pragma unroll 1
+    for (int j = 0; j < kMasks && p + 32 * j < hi; ++j)
+      if (!f(p + 32 * j, __ballot_sync(0xffffffffu, is_free >> j & 1))) return;
   }
 }
 
 constexpr int kNoMove = -1, kFreshPage = -2;
 
-__global__ void __launch_bounds__(kPlanThreads) resize_kernel(const ResizeArgs a) {
+__global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const ResizeArgs a) {
   __shared__ unsigned long long scan[kPlanWarps];
   __shared__ Totals needs, move_counts, frees;
   __shared__ int warp_free[kPlanWarps];
   const PoolState& s = a.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t cta = cluster_rank(), ctas = cluster_size();
-  const Share rows(s.B, cta, ctas);
+  auto sync = [&] {
+    if (ctas == 1) __syncthreads();
+    else cluster_sync();
+  };
+  const Share rows(s.B, cta, ctas), mine(s.num_pages, cta * kPlanWarps + warp, ctas * kPlanWarps);
+  // rows of a warp at a time: long ones are spread over the warps
+  const int each = imax(1, imin(32, (rows.hi - rows.lo + kPlanWarps - 1) / kPlanWarps));
+  const int row0 = rows.lo + warp * each, row_step = each * kPlanWarps;
   grid_dependents_launch();
 
   // 1. what rows give back leaves the counts; the partial pages that rows will write into
-  for (int b = rows.lo + warp; b < rows.hi; b += kPlanWarps)
-    released(a, b, RowLens(a, b), lane, [&](int, int page) { add_refs(s, page, -1); });
-  for (int b = rows.lo + (int)threadIdx.x; b < rows.hi; b += kPlanThreads) {
-    const RowLens r(a, b);
-    if (!length_ok(s, s.lens[b]) || !length_ok(s, __ldg(a.new_lens + b))) report(s);
+  for (int b0 = row0; b0 < rows.hi; b0 += row_step) {
+    const int b = b0 + lane, end = imin(b0 + each, rows.hi);
+    const RowLens r(a, b, end);
+    if (!r.ok) report(s);
     int page = kNoMove;
     if (r.N > r.L && r.L % s.page_size != 0) {
       page = s.table[(size_t)b * s.max_pages + page_index(s, r.L)];
       if (page < 0 || page >= s.num_pages) {  // its tokens are nowhere: a new page, no copy
         report(s);
         page = kFreshPage;
+      } else {
+        a.writers[page] = 0;
+        a.lowest[page] = s.B;
       }
     }
-    a.write_page[b] = page;
+    if (b < end) a.write_page[b] = page;
+    released(a, b0, r, lane, [&](int, int, int page) { add_refs(s, page, -1); });
   }
-  cluster_sync();
+  sync();
 
-  // 2. pages that each row needs. Of the g rows that write into a page with r holders all
+  // 2. the rows that write into a page that others hold too; the free pages
+  for (int b = rows.lo + (int)threadIdx.x; b < rows.hi; b += kPlanThreads) {
+    const int page = a.write_page[b];
+    if (page >= 0 && __ldcg(s.refs + page) > 1) {
+      atomicAdd(a.writers + page, 1);
+      atomicMin(a.lowest + page, b);
+    }
+  }
+  int n_free = 0;
+  free_masks(s.refs, mine.lo, mine.hi, lane, [&](int, uint32_t m) {
+    n_free += __popc(m);
+    return true;
+  });
+  if (lane == 0) warp_free[warp] = n_free;
+  sync();
+
+  // 3. pages that each row needs. Of the g rows that write into a page with r holders all
   // take a copy if others hold it (r > g), else all but the lowest.
   unsigned long long need = 0, moves = 0;
   for (int b0 = rows.lo; b0 < rows.hi; b0 += kPlanThreads) {
     const int b = b0 + (int)threadIdx.x;
     unsigned long long n = 0, m = 0;
+    int page = kNoMove;
     if (b < rows.hi) {
-      const RowLens r(a, b);
-      const int page = __ldcg(a.write_page + b);
+      const RowLens r(a, b, rows.hi);
       const int grown = pages_of(s, r.N) - pages_of(s, r.L);
-      n = (unsigned long long)(grown > 0 ? grown : 0);
-      if (page == kFreshPage) {
-        ++n;
-      } else if (page >= 0) {
+      page = a.write_page[b];
+      if (page >= 0) {
         const int holders = __ldcg(s.refs + page);
-        if (holders > 1) {
-          int g = 0, lowest = b;
-          for (int x = 0; x < s.B; ++x)
-            if (__ldcg(a.write_page + x) == page) {
-              ++g;
-              lowest = imin(lowest, x);
-            }
-          m = holders > g || lowest != b;
-          n += m;
-        }
+        if (holders > 1) m = holders > __ldcg(a.writers + page) || __ldcg(a.lowest + page) != b;
       }
+      n = (unsigned long long)(grown > 0 ? grown : 0) + (page == kFreshPage) + m;
     }
-    unsigned long long n_all, m_all;
-    const unsigned long long n_at = block_scan(n, scan, n_all), m_at = block_scan(m, scan, m_all);
+    unsigned long long all;
+    const unsigned long long at = block_scan(n | m << 48, scan, all), low = (1ull << 48) - 1;
     if (b < rows.hi) {
-      a.row_rank[b] = (int)imin64((long long)(need + n_at), 0x7fffffff);
-      if (m) a.row_move[b] = (int)(moves + m_at);
-      else a.row_move[b] = __ldcg(a.write_page + b) == kFreshPage ? kFreshPage : kNoMove;
+      a.row_rank[b] = (int)imin64((long long)(need + (at & low)), 0x7fffffff);
+      a.row_move[b] = m ? (int)(moves + (at >> 48)) : page == kFreshPage ? kFreshPage : kNoMove;
     }
-    need += n_all;
-    moves += m_all;
+    need += all & low;
+    moves += all >> 48;
   }
-  // free pages of each warp's share of the pool
-  const Share mine(s.num_pages, cta * kPlanWarps + warp, ctas * kPlanWarps);
-  int n_free = 0;
-  for (int p = mine.lo + lane; p - lane < mine.hi; p += 32)
-    n_free += __popc(__ballot_sync(0xffffffffu, p < mine.hi && __ldcg(s.refs + p) == 0));
-  if (lane == 0) warp_free[warp] = n_free;
-  __syncthreads();
   if (warp == 0) {
     int f = warp_free[lane];
 #pragma unroll
@@ -190,9 +270,9 @@ __global__ void __launch_bounds__(kPlanThreads) resize_kernel(const ResizeArgs a
     move_counts.publish(moves, lane);
     frees.publish((unsigned long long)f, lane);
   }
-  cluster_sync();
+  sync();
 
-  // 3. all or nothing
+  // 4. all or nothing
   const unsigned long long need_all = needs.sum(), free_all = frees.sum();
   const bool lacking = need_all > free_all;
   if (cta == 0 && threadIdx.x == 0) {
@@ -200,56 +280,74 @@ __global__ void __launch_bounds__(kPlanThreads) resize_kernel(const ResizeArgs a
     *a.moves.count = lacking ? 0 : (int)move_counts.sum();
   }
   if (lacking) {
-    for (int b = rows.lo + warp; b < rows.hi; b += kPlanWarps)
-      released(a, b, RowLens(a, b), lane, [&](int, int page) { add_refs(s, page, 1); });
+    for (int b0 = row0; b0 < rows.hi; b0 += row_step)
+      released(a, b0, RowLens(a, b0 + lane, imin(b0 + each, rows.hi)), lane, [&](int, int, int page) { add_refs(s, page, 1); });
     return;
   }
   if (need_all > 0) {  // the lowest free pages, in order
-    unsigned long long rank = frees.before(cta);
+    const int need_n = (int)need_all;
+    int rank = (int)frees.before(cta);
     for (int w = 0; w < warp; ++w) rank += warp_free[w];
-    for (int p = mine.lo + lane; p - lane < mine.hi && rank < need_all; p += 32) {
-      const bool is_free = p < mine.hi && __ldcg(s.refs + p) == 0;
-      const uint32_t m = __ballot_sync(0xffffffffu, is_free);
-      const unsigned long long at = rank + __popc(m & ((1u << lane) - 1));
-      if (is_free && at < need_all) {
-        a.free_list[at] = p;
-        s.refs[p] = 1;
-      }
-      rank += __popc(m);
-    }
-    cluster_sync();
+    if (rank < need_n)
+      free_masks(s.refs, mine.lo, mine.hi, lane, [&](int p, uint32_t m) {
+        const int at = rank + __popc(m & ((1u << lane) - 1));
+        if ((m >> lane & 1) && at < need_n) {
+          a.free_list[at] = p + lane;
+          s.refs[p + lane] = 1;
+        }
+        rank += __popc(m);
+        return rank < need_n;
+      });
+    sync();
   }
 
-  // 4. the rows
+  // 5. the rows
   const int need0 = (int)needs.before(cta), move0 = (int)move_counts.before(cta);
-  for (int b = rows.lo + warp; b < rows.hi; b += kPlanWarps) {
-    const RowLens r(a, b);
-    int32_t* row = s.table + (size_t)b * s.max_pages;
-    released(a, b, r, lane, [&](int i, int) { row[i] = -1; });
-    const int move = a.row_move[b], fresh = move != kNoMove;
-    const int32_t* pages = a.free_list + need0 + a.row_rank[b];
-    for (int i = pages_of(s, r.L) + lane, j = fresh + lane, n = pages_of(s, r.N); i < n; i += 32, j += 32)
-      row[i] = __ldcg(pages + j);
-    if (lane == 0 && fresh) {
-      const int page = __ldcg(pages);
-      row[page_index(s, r.L)] = page;
-      if (move >= 0) {
-        const int from = a.write_page[b];
-        atomicAdd(s.refs + from, -1);
-        a.moves.src[move0 + move] = from;
-        a.moves.dst[move0 + move] = page;
-        a.moves.tokens[move0 + move] = r.L % s.page_size;
+  for (int b0 = row0; b0 < rows.hi; b0 += row_step) {
+    const int b = b0 + lane;
+    const RowLens r(a, b, imin(b0 + each, rows.hi));
+    released(a, b0, r, lane, [&](int row, int i, int) { s.table[(size_t)row * s.max_pages + i] = -1; });
+    int rank = 0, n0 = 0, n1 = 0;
+    if (r.N > r.L) {
+      const int move = a.row_move[b], fresh = move != kNoMove;
+      rank = need0 + a.row_rank[b];
+      int32_t* row = s.table + (size_t)b * s.max_pages;
+      if (fresh) {
+        const int page = __ldcg(a.free_list + rank);
+        row[page_index(s, r.L)] = page;
+        if (move >= 0) {
+          const int from = a.write_page[b];
+          atomicAdd(s.refs + from, -1);
+          a.moves.src[move0 + move] = from;
+          a.moves.dst[move0 + move] = page;
+          a.moves.tokens[move0 + move] = r.L % s.page_size;
+        }
+      }
+      rank += fresh;
+      n0 = pages_of(s, r.L);
+      n1 = pages_of(s, r.N);
+      if (n1 == n0 + 1) {  // a decode step
+        row[n0] = __ldcg(a.free_list + rank);
+        n1 = n0;
       }
     }
-    __syncwarp();
-    if (lane == 0 && r.N != r.L) s.lens[b] = r.N;
+#pragma unroll 1
+    for (uint32_t todo = __ballot_sync(0xffffffffu, n1 > n0); todo; todo &= todo - 1) {
+      const int who = __ffs(todo) - 1, first = __shfl_sync(0xffffffffu, n0, who);
+      const int count = __shfl_sync(0xffffffffu, n1, who) - first;
+      const int32_t* pages = a.free_list + __shfl_sync(0xffffffffu, rank, who);
+      int32_t* row = s.table + (size_t)(b0 + who) * s.max_pages + first;
+#pragma unroll 8
+      for (int i = lane; i < count; i += 32) row[i] = __ldcg(pages + i);
+    }
+    if (r.N != r.L) s.lens[b] = r.N;
   }
 }
 
 // ---------------------------------------------------------------- compact
 // With U used pages, the k-th highest used page from U on moves to the k-th lowest free page
 // below U: as many of the one kind as of the other.
-__global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs a) {
+__global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const CompactArgs a) {
   __shared__ Totals used, holes;
   __shared__ int warp_used[kPlanWarps], warp_holes[kPlanWarps];
   const PoolState& s = a.s;
@@ -270,24 +368,28 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs
     cluster_sync();
   };
   int n = 0;
-  for (int p = mine.lo + lane; p - lane < mine.hi; p += 32)
-    n += __popc(__ballot_sync(0xffffffffu, p < mine.hi && s.refs[p] != 0));
+  free_masks(s.refs, mine.lo, mine.hi, lane, [&](int p, uint32_t free) {
+    const int in = imax(0, imin(32, mine.hi - p));
+    n += in - __popc(free);
+    return true;
+  });
   cluster_started_wait();
   publish(used, warp_used, n);
   const int U = (int)used.sum();
   int rank = (int)used.before(cta), n_holes = 0;  // used pages before p
   for (int w = 0; w < warp; ++w) rank += warp_used[w];
-  for (int p = mine.lo + lane; p - lane < mine.hi; p += 32) {
-    const bool in = p < mine.hi, is_used = in && s.refs[p] != 0;
-    const uint32_t m = __ballot_sync(0xffffffffu, is_used);
-    const int u = rank + __popc(m & ((1u << lane) - 1));
-    const bool hole = in && !is_used && p < U;
+  free_masks(s.refs, mine.lo, mine.hi, lane, [&](int p0, uint32_t free) {
+    const int in = imax(0, imin(32, mine.hi - p0)), p = p0 + lane;
+    const bool inside = lane < in, is_used = inside && !(free >> lane & 1);
+    const int u = rank + lane - __popc(free & ((1u << lane) - 1));
+    const bool hole = inside && !is_used && p < U;
     if (is_used && p >= U) a.moves.src[U - 1 - u] = p;
-    else if (in) a.page_map[p] = is_used ? p : -1;
+    else if (inside) a.page_map[p] = is_used ? p : -1;
     if (hole) a.moves.dst[p - u] = p;
     n_holes += __popc(__ballot_sync(0xffffffffu, hole));
-    rank += __popc(m);
-  }
+    rank += in - __popc(free);
+    return true;
+  });
   publish(holes, warp_holes, n_holes);
   const int M = (int)holes.sum();
   if (cta == 0 && threadIdx.x == 0) {
@@ -305,7 +407,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs
 // ---------------------------------------------------------------- copy
 // Of the entries with one destination the first is copied; within one pool an entry whose
 // source is another's destination is not. The entries left out are reported.
-__global__ void __launch_bounds__(kPlanThreads) copy_plan_kernel(const CopyPlanArgs a) {
+__global__ void __launch_bounds__(kPlanThreads, 1) copy_plan_kernel(const CopyPlanArgs a) {
   grid_dependents_launch();
   const int first = cluster_rank() * kPlanThreads + threadIdx.x, step = cluster_size() * kPlanThreads;
   auto entry = [&](int i, int& src, int& dst) {  // false: nothing to copy
@@ -338,10 +440,10 @@ __global__ void __launch_bounds__(kPlanThreads) copy_plan_kernel(const CopyPlanA
   if (first == 0) *a.moves.count = a.n;
 }
 
-// CTAs of a plan: one per 8192 units of work (pages or entries), as a power of two.
+// CTAs of a plan: one per 16384 units of work (pages or entries), as a power of two.
 int plan_ctas(long long work) {
   int n = 1;
-  while (n < kPlanMaxCtas && (long long)n * 8192 < work) n *= 2;
+  while (n < kPlanMaxCtas && n * 16384LL < work) n *= 2;
   return n;
 }
 
@@ -363,27 +465,46 @@ cudaError_t launch_plan(void (*kernel)(const Args), const Args& a, int ctas, siz
 
 }  // namespace
 
-cudaError_t launch_fork(const ForkArgs& a, cudaStream_t st) {
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem((const void*)fork_kernel, kForkMaxRows * 4, done);
-  if (e != cudaSuccess) return e;
-  return launch_plan(fork_kernel, a, plan_ctas((long long)a.s.B * a.s.max_pages), (size_t)a.s.B * 4, st);
+cudaError_t launch_fork(const ForkArgs& a, int num_sms, cudaStream_t st) {
+  static std::atomic<uint64_t> done[3];
+  const long long items = (long long)a.s.B * fork_chunks(a.s.max_pages);
+  const size_t smem = (size_t)a.s.B * 4;
+  cudaError_t e;
+  if (items <= 4 * kPlanMaxCtas * kPlanWarps) {
+    if ((e = allow_smem((const void*)fork_kernel<kBoth>, kForkMaxRows * 4, done[0])) != cudaSuccess) return e;
+    return launch_plan(fork_kernel<kBoth>, a, plan_ctas(items * kForkChunk), smem, st);
+  }
+  if ((e = allow_smem((const void*)fork_kernel<kGather>, kForkMaxRows * 4, done[1])) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(num_sms > 0 ? num_sms : 1);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  if ((e = cudaLaunchKernelEx(&cfg, fork_kernel<kGather>, a)) != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, fork_kernel<kScatter>, a);
 }
 
 cudaError_t launch_resize(const ResizeArgs& a, const PageCopy& c, int num_sms, cudaStream_t st) {
-  const long long work = imin64(0x7fffffff, (long long)a.s.num_pages + 32LL * a.s.B);
+  const long long work = imin64(0x7fffffff, (long long)a.s.num_pages + 16LL * a.s.B);
   const cudaError_t e = launch_plan(resize_kernel, a, plan_ctas(work), 0, st);
-  return e == cudaSuccess ? launch_page_copy(c, nullptr, num_sms, st) : e;
+  return e == cudaSuccess ? launch_page_copy(c, num_sms, st) : e;
 }
 
 cudaError_t launch_compact(const CompactArgs& a, const PageCopy& c, int num_sms, cudaStream_t st) {
   const cudaError_t e = launch_plan(compact_kernel, a, plan_ctas(a.s.num_pages), 0, st);
-  return e == cudaSuccess ? launch_page_copy(c, &a, num_sms, st) : e;
+  return e == cudaSuccess ? launch_compact_copy(c, a, num_sms, st) : e;
 }
 
 cudaError_t launch_copy_pages(const CopyPlanArgs& a, const PageCopy& c, int num_sms, cudaStream_t st) {
+  if (a.n <= kCopyDirect) return launch_direct_copy(c, a, num_sms, st);
   const cudaError_t e = launch_plan(copy_plan_kernel, a, plan_ctas(a.n), 0, st);
-  return e == cudaSuccess ? launch_page_copy(c, nullptr, num_sms, st) : e;
+  return e == cudaSuccess ? launch_page_copy(c, num_sms, st) : e;
 }
 
 }  // namespace attn

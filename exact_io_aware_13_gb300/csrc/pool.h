@@ -30,14 +30,16 @@ struct PageCopy {
   void* to[3];
   int Hkv, page_size, d;
   bool e4m3;
+  int* status;
   PageMoves moves;
+  int runs, kv_pieces, exp_pieces;  // of a move; set by the launch
 };
 
 struct ForkArgs {
   PoolState s;
   const int32_t* parents;  // [B]
   int32_t* rows;           // workspace [B, max_pages]: the new rows
-  int32_t* lens;           // workspace [B]
+  int32_t *old_lens, *new_lens;  // workspace [B] each
 };
 struct ResizeArgs {
   PoolState s;
@@ -45,6 +47,7 @@ struct ResizeArgs {
   int window;
   int32_t* missing;
   int32_t *write_page, *row_rank, *row_move;  // workspace [B] each
+  int32_t *writers, *lowest;                  // workspace [num_pages] each
   int32_t* free_list;                         // workspace [min(num_pages, B * max_pages)]
   PageMoves moves;                            // [B]
 };
@@ -63,13 +66,16 @@ struct CopyPlanArgs {
 };
 // Rows of one fork: their counters fill a CTA's shared memory.
 constexpr int kForkMaxRows = 49152;
-cudaError_t launch_fork(const ForkArgs& a, cudaStream_t st);
+cudaError_t launch_fork(const ForkArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_resize(const ResizeArgs& a, const PageCopy& c, int num_sms, cudaStream_t st);
 cudaError_t launch_compact(const CompactArgs& a, const PageCopy& c, int num_sms, cudaStream_t st);
 cudaError_t launch_copy_pages(const CopyPlanArgs& a, const PageCopy& c, int num_sms, cudaStream_t st);
 // The copies of a list, behind the plan kernel that writes it; a compaction's table entries are
-// rewritten in the same launch.
-cudaError_t launch_page_copy(const PageCopy& c, const CompactArgs* compact, int num_sms, cudaStream_t st);
+// rewritten in the same launch. A caller's list of up to kCopyDirect pages needs no plan.
+constexpr int kCopyDirect = 256;
+cudaError_t launch_page_copy(const PageCopy& c, int num_sms, cudaStream_t st);
+cudaError_t launch_compact_copy(const PageCopy& c, const CompactArgs& compact, int num_sms, cudaStream_t st);
+cudaError_t launch_direct_copy(const PageCopy& c, const CopyPlanArgs& plan, int num_sms, cudaStream_t st);
 
 // Verification of drafted tokens.
 struct VerifyArgs {

@@ -483,7 +483,7 @@ attn_status attn_cache_fork(int32_t* page_table, int32_t* seq_lens, int32_t* pag
                             const int32_t* parents, int B, int max_pages_per_seq, int num_pages,
                             int page_size, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of attn_cache_fork: round256(4 B max_pages_per_seq) + round256(4 B). */
+/* Workspace bytes of attn_cache_fork: round256(4 B max_pages_per_seq) + 2 round256(4 B). */
 size_t attn_fork_workspace_size(int B, int max_pages_per_seq);
 
 /*
@@ -510,8 +510,8 @@ attn_status attn_cache_resize(const attn_paged_cache* cache, int32_t* page_table
                               size_t workspace_bytes, void* stream);
 
 /*
- * Workspace bytes of attn_cache_resize: 6 round256(4 B) + round256(4 min(num_pages, B
- * max_pages_per_seq)) + 256.
+ * Workspace bytes of attn_cache_resize: 6 round256(4 B) + 2 round256(4 num_pages) +
+ * round256(4 min(num_pages, B max_pages_per_seq)) + 256.
  */
 size_t attn_resize_workspace_size(int B, int max_pages_per_seq, int num_pages);
 

@@ -140,9 +140,9 @@ def test_verify_refusals(lib):
 def test_workspace_sizes(lib):
     r = lambda n: -(-n // 256) * 256  # noqa: E731
     for B, M, pages, n in ((0, 0, 0, 0), (1, 1, 1, 1), (100, 33, 5000, 777), (7, 1000, 123_457, 64)):
-        assert lib.attn_fork_workspace_size(B, M) == (r(4 * B * M) + r(4 * B) if B else 0)
+        assert lib.attn_fork_workspace_size(B, M) == (r(4 * B * M) + 2 * r(4 * B) if B else 0)
         assert lib.attn_resize_workspace_size(B, M, pages) == (
-            6 * r(4 * B) + r(4 * min(pages, B * M)) + 256)
+            6 * r(4 * B) + 2 * r(4 * pages) + r(4 * min(pages, B * M)) + 256)
         assert lib.attn_compact_workspace_size(pages) == 2 * r(4 * pages) + 256
         assert lib.attn_copy_workspace_size(pages, n) == r(4 * pages) + 2 * r(4 * n) + 256
     assert lib.attn_fork_workspace_size(-1, 5) == 0
