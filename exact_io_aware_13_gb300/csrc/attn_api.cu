@@ -1103,8 +1103,7 @@ attn_status attn_cache_compact(const attn_paged_cache* cache, int32_t* page_tabl
 }
 
 size_t attn_copy_workspace_size(int num_pages_to, int n) {
-  if (num_pages_to < 0 || n < 0) return 0;
-  return round256((size_t)num_pages_to * 4) + 2 * round256((size_t)n * 4) + 256;
+  return num_pages_to < 0 || n < 0 ? 0 : round256((size_t)num_pages_to * 4);
 }
 
 attn_status attn_cache_copy(const attn_paged_cache* from, const attn_paged_cache* to,
@@ -1115,7 +1114,7 @@ attn_status attn_cache_copy(const attn_paged_cache* from, const attn_paged_cache
   if (s == ATTN_OK) s = check_cache(to, 0, 0, 0, 0, &pt);
   if (s != ATTN_OK) return s;
   if (pf.e4m3 != pt.e4m3) return ATTN_ERR_ARG;
-  if (n < 0 || pf.Hkv != pt.Hkv || pf.page_size != pt.page_size || pf.d != pt.d) return ATTN_ERR_SHAPE;
+  if (n < 0 || n > kMaxCopyEntries || pf.Hkv != pt.Hkv || pf.page_size != pt.page_size || pf.d != pt.d) return ATTN_ERR_SHAPE;
   if (n == 0) return ATTN_OK;
   if (!src_pages || !dst_pages) return ATTN_ERR_ARG;
   if ((s = check_pool_tensors(pf)) != ATTN_OK || (s = check_pool_tensors(pt)) != ATTN_OK) return s;
@@ -1132,25 +1131,18 @@ attn_status attn_cache_copy(const attn_paged_cache* from, const attn_paged_cache
     return s;
   DeviceInfo* dev = nullptr;
   if ((s = current_device(&dev)) != ATTN_OK) return s;
-  CopyPlanArgs a{};
-  a.src = src_pages;
-  a.dst = dst_pages;
-  a.n = n;
-  a.num_pages_from = pf.num_pages;
-  a.num_pages_to = pt.num_pages;
+  CopyList l{};
+  l.src = src_pages;
+  l.dst = dst_pages;
+  l.n = n;
+  l.num_pages_from = pf.num_pages;
+  l.num_pages_to = pt.num_pages;
   // (one pool described with two sizes: the smaller one holds both pages)
-  a.same_pool = same;
-  if (same) a.num_pages_from = a.num_pages_to = std::min(pf.num_pages, pt.num_pages);
-  a.status = dev->status;
-  Carve ws{static_cast<uint8_t*>(workspace)};
-  a.owner = ws.ints(pt.num_pages);
-  a.moves.src = ws.ints(n);
-  a.moves.dst = ws.ints(n);
-  a.moves.count = ws.ints(1);
-  a.moves.most = n;
-  c.moves = a.moves;
-  c.status = dev->status;
-  return from_cuda(launch_copy_pages(a, c, dev->num_sms, static_cast<cudaStream_t>(stream)));
+  l.same_pool = same;
+  if (same) l.num_pages_from = l.num_pages_to = std::min(pf.num_pages, pt.num_pages);
+  l.owner = static_cast<int32_t*>(workspace);
+  c.status = l.status = dev->status;
+  return from_cuda(launch_copy_pages(l, c, dev->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 attn_status attn_verify_drafts(int prob_type, const void* target, long long target_stride,

@@ -404,42 +404,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const CompactA
   }
 }
 
-// ---------------------------------------------------------------- copy
-// Of the entries with one destination the first is copied; within one pool an entry whose
-// source is another's destination is not. The entries left out are reported.
-__global__ void __launch_bounds__(kPlanThreads, 1) copy_plan_kernel(const CopyPlanArgs a) {
-  grid_dependents_launch();
-  const int first = cluster_rank() * kPlanThreads + threadIdx.x, step = cluster_size() * kPlanThreads;
-  auto entry = [&](int i, int& src, int& dst) {  // false: nothing to copy
-    src = __ldg(a.src + i);
-    dst = __ldg(a.dst + i);
-    return src >= 0 && dst >= 0 && src < a.num_pages_from && dst < a.num_pages_to;
-  };
-  int src, dst;
-  for (int i = first; i < a.n; i += step)
-    if (entry(i, src, dst)) {
-      a.owner[dst] = 0x7fffffff;
-      if (a.same_pool) a.owner[src] = 0x7fffffff;
-    } else if (src >= a.num_pages_from || dst >= a.num_pages_to) {
-      atomicOr(a.status, DEV_BAD_INPUT);
-    }
-  cluster_sync();
-  for (int i = first; i < a.n; i += step)
-    if (entry(i, src, dst)) atomicMin(a.owner + dst, i);
-  cluster_sync();
-  for (int i = first; i < a.n; i += step) {
-    bool copied = entry(i, src, dst);
-    if (copied) {
-      copied = __ldcg(a.owner + dst) == i;
-      if (a.same_pool && src != dst && __ldcg(a.owner + src) != 0x7fffffff) copied = false;
-      if (!copied) atomicOr(a.status, DEV_BAD_INPUT);
-    }
-    a.moves.src[i] = copied && !(a.same_pool && src == dst) ? src : -1;
-    a.moves.dst[i] = dst;
-  }
-  if (first == 0) *a.moves.count = a.n;
-}
-
 // CTAs of a plan: one per 16384 units of work (pages or entries), as a power of two.
 int plan_ctas(long long work) {
   int n = 1;
@@ -499,12 +463,6 @@ cudaError_t launch_resize(const ResizeArgs& a, const PageCopy& c, int num_sms, c
 cudaError_t launch_compact(const CompactArgs& a, const PageCopy& c, int num_sms, cudaStream_t st) {
   const cudaError_t e = launch_plan(compact_kernel, a, plan_ctas(a.s.num_pages), 0, st);
   return e == cudaSuccess ? launch_compact_copy(c, a, num_sms, st) : e;
-}
-
-cudaError_t launch_copy_pages(const CopyPlanArgs& a, const PageCopy& c, int num_sms, cudaStream_t st) {
-  if (a.n <= kCopyDirect) return launch_direct_copy(c, a, num_sms, st);
-  const cudaError_t e = launch_plan(copy_plan_kernel, a, plan_ctas(a.n), 0, st);
-  return e == cudaSuccess ? launch_page_copy(c, num_sms, st) : e;
 }
 
 }  // namespace attn

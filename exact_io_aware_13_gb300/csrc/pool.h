@@ -56,12 +56,14 @@ struct CompactArgs {
   int32_t *used, *page_map;
   PageMoves moves;  // [num_pages]
 };
-struct CopyPlanArgs {
+constexpr int kMaxCopyEntries = 1 << 30;  // of a caller's list
+// A caller's list of page copies. Of the entries with one destination the first is copied; within
+// one pool an entry whose source is another's destination is not.
+struct CopyList {
   const int32_t *src, *dst;  // [n]
   int n, num_pages_from, num_pages_to;
   bool same_pool;
-  int32_t* owner;  // workspace [num_pages_to]
-  PageMoves moves;  // [n]
+  int32_t* owner;  // workspace [num_pages_to]: the first entry with that destination
   int* status;
 };
 // Rows of one fork: their counters fill a CTA's shared memory.
@@ -69,13 +71,11 @@ constexpr int kForkMaxRows = 49152;
 cudaError_t launch_fork(const ForkArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_resize(const ResizeArgs& a, const PageCopy& c, int num_sms, cudaStream_t st);
 cudaError_t launch_compact(const CompactArgs& a, const PageCopy& c, int num_sms, cudaStream_t st);
-cudaError_t launch_copy_pages(const CopyPlanArgs& a, const PageCopy& c, int num_sms, cudaStream_t st);
-// The copies of a list, behind the plan kernel that writes it; a compaction's table entries are
-// rewritten in the same launch. A caller's list of up to kCopyDirect pages needs no plan.
-constexpr int kCopyDirect = 256;
+cudaError_t launch_copy_pages(const CopyList& l, const PageCopy& c, int num_sms, cudaStream_t st);
+// The copies of a plan, behind the kernel that lists them; a compaction's table entries are
+// rewritten in the same launch.
 cudaError_t launch_page_copy(const PageCopy& c, int num_sms, cudaStream_t st);
 cudaError_t launch_compact_copy(const PageCopy& c, const CompactArgs& compact, int num_sms, cudaStream_t st);
-cudaError_t launch_direct_copy(const PageCopy& c, const CopyPlanArgs& plan, int num_sms, cudaStream_t st);
 
 // Verification of drafted tokens.
 struct VerifyArgs {

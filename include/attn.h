@@ -545,7 +545,7 @@ attn_status attn_cache_copy(const attn_paged_cache* from, const attn_paged_cache
                             const int32_t* src_pages, const int32_t* dst_pages, int n,
                             void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of attn_cache_copy: round256(4 num_pages of `to`) + 2 round256(4 n) + 256. */
+/* Workspace bytes of attn_cache_copy: round256(4 num_pages of `to`), whatever n. */
 size_t attn_copy_workspace_size(int num_pages_to, int n);
 
 /* Types of probabilities. */
