@@ -333,16 +333,22 @@ cudaError_t launch(const PageCopy& copy, const CompactArgs& compact, const CopyL
   c.runs = c.moves.tokens ? c.Hkv : 1;
   const long long tokens = c.moves.tokens ? c.page_size : (long long)c.Hkv * c.page_size;
   const long long kv = tokens * (c.e4m3 ? c.d : 2 * c.d);
-  const bool small = kv < kSmallBelow;
-  const int piece = small ? kSmallPiece : kPiece;
-  c.kv_pieces = (int)((kv + piece - 1) / piece);
-  c.exp_pieces = c.e4m3 ? (int)((tokens * 2 + piece - 1) / piece) : 0;
+  const long long exps = c.e4m3 ? tokens * 2 : 0, sms = num_sms > 0 ? num_sms : 1;
+  auto pieces = [&](int piece) {
+    c.kv_pieces = (int)((kv + piece - 1) / piece);
+    c.exp_pieces = (int)((exps + piece - 1) / piece);
+    return most * c.runs * (2 * c.kv_pieces + c.exp_pieces);
+  };
+  // Small pieces one per lane, unless there are few for a warp: then the ring's shorter way counts
+  // (24 pages of 4 KB 3.3 us, a piece per lane 5.0).
+  long long units = pieces(kPiece);
+  const bool small = kv < kSmallBelow && units > 16 * kCopyWarps * sms;
+  if (small) units = pieces(kSmallPiece);
   const auto kernel = small ? small_copy_kernel<kMode> : page_copy_kernel<kMode>;
   const int smem = small ? kSmallSmem : kCopySmem;
   static std::atomic<uint64_t> done[2];
   const cudaError_t e = allow_smem((const void*)kernel, smem, done[small]);
   if (e != cudaSuccess) return e;
-  const long long units = most * c.runs * (2 * c.kv_pieces + c.exp_pieces), sms = num_sms > 0 ? num_sms : 1;
   const int per_cta = small ? kCopyThreads : kCopyWarps;
   const long long ctas = (units + per_cta - 1) / per_cta + more_ctas;
   cudaLaunchConfig_t cfg{};
