@@ -126,25 +126,31 @@ struct RowLens {
 
 // Calls f(b, i, page) for the table entries that the warp's rows give back (lane l has row b0 + l):
 // those behind a row's new length (empty ones too), and with a window those wholly below it, from
-// the window's edge down to the next entry that holds no page. The warp takes its rows one by one.
-constexpr int kWalk = 4;  // words of a row in flight
+// the window's edge down to the next entry that holds no page. The warp takes its rows one by one;
+// `subs` warps share the long way of a row.
+constexpr int kWalk = 4;      // words of a row in flight
+constexpr int kFewPages = 4;  // pages of a row that its lane sees to alone
 template <class F>
-__device__ __forceinline__ void released(const ResizeArgs& a, int b0, const RowLens& r, int lane, F f) {
+__device__ __forceinline__ void released(const ResizeArgs& a, int b0, const RowLens& r, int lane, int sub, int subs,
+                                         F f) {
   const PoolState& s = a.s;
   const int n0 = pages_of(s, r.N), n1 = pages_of(s, r.L);
   int top = -1;  // the last entry wholly below the lowest position that stays visible
-  if (a.window > 0) {
+  if (a.window > 0 && sub == 0) {
     const int low = imin(r.L, r.N) - a.window + 1;
     if (low > 0) top = page_index(s, low) - 1;
     if (top >= 0 && s.table[(size_t)(b0 + lane) * s.max_pages + top] < 0) top = -1;  // the usual case
   }
+  const bool few = n1 - n0 <= kFewPages;  // by the row's own lane
+  if (few && sub == 0)
+    for (int i = n0; i < n1; ++i) f(b0 + lane, i, s.table[(size_t)(b0 + lane) * s.max_pages + i]);
 #pragma unroll 1
-  for (uint32_t todo = __ballot_sync(0xffffffffu, n1 > n0 || top >= 0); todo; todo &= todo - 1) {
+  for (uint32_t todo = __ballot_sync(0xffffffffu, !few || top >= 0); todo; todo &= todo - 1) {
     const int who = __ffs(todo) - 1, b = b0 + who;
     const int32_t* row = s.table + (size_t)b * s.max_pages;
-    const int end = __shfl_sync(0xffffffffu, n1, who);
+    const int end = __shfl_sync(0xffffffffu, few ? n0 : n1, who);
 #pragma unroll 8
-    for (int i = __shfl_sync(0xffffffffu, n0, who) + lane; i < end; i += 32) f(b, i, row[i]);
+    for (int i = __shfl_sync(0xffffffffu, n0, who) + lane + 32 * sub; i < end; i += 32 * subs) f(b, i, row[i]);
     bool more = true;
 #pragma unroll 1
     for (int t = __shfl_sync(0xffffffffu, top, who) - lane; more; t -= 32 * kWalk) {
@@ -194,9 +200,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const ResizeArg
     else cluster_sync();
   };
   const Share rows(s.B, cta, ctas), mine(s.num_pages, cta * kPlanWarps + warp, ctas * kPlanWarps);
-  // rows of a warp at a time: long ones are spread over the warps
-  const int each = imax(1, imin(32, (rows.hi - rows.lo + kPlanWarps - 1) / kPlanWarps));
-  const int row0 = rows.lo + warp * each, row_step = each * kPlanWarps;
+  // rows of a warp at a time, or warps of a row: long rows are spread over the warps
+  const int n_rows = rows.hi - rows.lo;
+  const int each = imax(1, imin(32, (n_rows + kPlanWarps - 1) / kPlanWarps));
+  const int subs = imax(1, kPlanWarps / imax(1, n_rows)), sub = warp % subs;
+  const int row0 = rows.lo + warp / subs * each, row_step = kPlanWarps / subs * each;
   grid_dependents_launch();
 
   // 1. what rows give back leaves the counts; the partial pages that rows will write into
@@ -205,7 +213,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const ResizeArg
     const RowLens r(a, b, end);
     if (!r.ok) report(s);
     int page = kNoMove;
-    if (r.N > r.L && r.L % s.page_size != 0) {
+    if (sub == 0 && r.N > r.L && r.L % s.page_size != 0) {
       page = s.table[(size_t)b * s.max_pages + page_index(s, r.L)];
       if (page < 0 || page >= s.num_pages) {  // its tokens are nowhere: a new page, no copy
         report(s);
@@ -215,8 +223,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const ResizeArg
         a.lowest[page] = s.B;
       }
     }
-    if (b < end) a.write_page[b] = page;
-    released(a, b0, r, lane, [&](int, int, int page) { add_refs(s, page, -1); });
+    if (sub == 0 && b < end) a.write_page[b] = page;
+    released(a, b0, r, lane, sub, subs, [&](int, int, int page) { add_refs(s, page, -1); });
   }
   sync();
 
@@ -281,7 +289,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const ResizeArg
   }
   if (lacking) {
     for (int b0 = row0; b0 < rows.hi; b0 += row_step)
-      released(a, b0, RowLens(a, b0 + lane, imin(b0 + each, rows.hi)), lane, [&](int, int, int page) { add_refs(s, page, 1); });
+      released(a, b0, RowLens(a, b0 + lane, imin(b0 + each, rows.hi)), lane, sub, subs,
+               [&](int, int, int page) { add_refs(s, page, 1); });
     return;
   }
   if (need_all > 0) {  // the lowest free pages, in order
@@ -306,13 +315,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const ResizeArg
   for (int b0 = row0; b0 < rows.hi; b0 += row_step) {
     const int b = b0 + lane;
     const RowLens r(a, b, imin(b0 + each, rows.hi));
-    released(a, b0, r, lane, [&](int row, int i, int) { s.table[(size_t)row * s.max_pages + i] = -1; });
+    released(a, b0, r, lane, sub, subs, [&](int row, int i, int) { s.table[(size_t)row * s.max_pages + i] = -1; });
     int rank = 0, n0 = 0, n1 = 0;
     if (r.N > r.L) {
       const int move = a.row_move[b], fresh = move != kNoMove;
       rank = need0 + a.row_rank[b];
       int32_t* row = s.table + (size_t)b * s.max_pages;
-      if (fresh) {
+      if (fresh && sub == 0) {
         const int page = __ldcg(a.free_list + rank);
         row[page_index(s, r.L)] = page;
         if (move >= 0) {
@@ -326,8 +335,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const ResizeArg
       rank += fresh;
       n0 = pages_of(s, r.L);
       n1 = pages_of(s, r.N);
-      if (n1 == n0 + 1) {  // a decode step
-        row[n0] = __ldcg(a.free_list + rank);
+      if (n1 - n0 <= kFewPages) {  // a decode step
+        for (int i = n0; i < n1; ++i) row[i] = __ldcg(a.free_list + rank + (i - n0));
         n1 = n0;
       }
     }
@@ -338,8 +347,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const ResizeArg
       const int32_t* pages = a.free_list + __shfl_sync(0xffffffffu, rank, who);
       int32_t* row = s.table + (size_t)(b0 + who) * s.max_pages + first;
 #pragma unroll 8
-      for (int i = lane; i < count; i += 32) row[i] = __ldcg(pages + i);
+      for (int i = lane + 32 * sub; i < count; i += 32 * subs) row[i] = __ldcg(pages + i);
     }
+  }
+  __syncthreads();  // (the row's other warps have read its length)
+  for (int b = rows.lo + (int)threadIdx.x; b < rows.hi; b += kPlanThreads) {
+    const RowLens r(a, b, rows.hi);
     if (r.N != r.L) s.lens[b] = r.N;
   }
 }
