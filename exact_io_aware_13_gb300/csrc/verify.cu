@@ -65,10 +65,14 @@ __device__ __forceinline__ bool some_weight(const Pair& p) { return p.hi > 0.f &
 // Two of them, for the elements of even and of odd index.
 struct Pair2 {
   uint64_t hi = 0, lo = 0;
-  __device__ __forceinline__ void add(uint64_t x, uint64_t err) {
+  __device__ __forceinline__ void add(uint64_t x) {
     const uint64_t s = add_f32x2(hi, x), t = sub_f32x2(s, hi);
-    lo = add_f32x2(lo, add_f32x2(add_f32x2(sub_f32x2(hi, sub_f32x2(s, t)), sub_f32x2(x, t)), err));
+    lo = add_f32x2(lo, add_f32x2(sub_f32x2(hi, sub_f32x2(s, t)), sub_f32x2(x, t)));
     hi = s;
+  }
+  __device__ __forceinline__ void add(uint64_t x, uint64_t err) {
+    lo = add_f32x2(lo, err);
+    add(x);
   }
   __device__ __forceinline__ Pair sum() const {
     Pair p, r;
@@ -145,16 +149,27 @@ struct Row {
   }
 };
 
+// A group without its element at byte `at`.
+template <class T>
+__device__ __forceinline__ uint4 cleared(const uint4& x, int at) {
+  const uint32_t mask = sizeof(T) == 4 ? 0u : at & 2 ? 0x0000FFFFu : 0xFFFF0000u;
+  uint4 r = x;
+  if (at / 4 == 0) r.x &= mask;
+  if (at / 4 == 1) r.y &= mask;
+  if (at / 4 == 2) r.z &= mask;
+  if (at / 4 == 3) r.w &= mask;
+  return r;
+}
+
 // Sum over whole groups [g0, g1), a lane's share of them, two elements per instruction and the
 // loads of kAhead groups in flight. fmaxf drops NaN; an infinity spoils the sum for good, which
 // the caller sees.
 template <class T, bool kQ>
 __device__ __forceinline__ Pair sum_groups(const Row<T>& row, int g0, int g1, int lane) {
-  constexpr int kVec = Row<T>::kVec, kAhead = kQ ? 2 : 4;
+  constexpr int kVec = Row<T>::kVec, kAhead = 2;
   const uint4* p = reinterpret_cast<const uint4*>(row.p - row.shift);
   const uint4* q = reinterpret_cast<const uint4*>(row.q - row.shift);
   const int skip_group = !kQ && row.skip >= 0 ? (row.skip + row.shift) / kVec : -1;
-  const int skip_at = !kQ ? (row.skip + row.shift) % kVec : 0;
   Pair2 sum;
 #pragma unroll 1
   for (int g = g0 + lane; g - lane < g1; g += 32 * kAhead) {
@@ -166,25 +181,23 @@ __device__ __forceinline__ Pair sum_groups(const Row<T>& row, int g0, int g1, in
         x[i] = __ldg(p + g + 32 * i);
         if constexpr (kQ) y[i] = __ldg(q + g + 32 * i);
       }
+      if (!kQ && g + 32 * i == skip_group) x[i] = cleared<T>(x[i], (row.skip + row.shift) % kVec * (int)sizeof(T));
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
 #pragma unroll
       for (int j = 0; j < kVec / 2; ++j) {
-        uint64_t err = 0;
         float u, v;
         if constexpr (kQ) {
           const uint64_t pv = Row<T>::two(x[i], j), qv = Row<T>::two(y[i], j), d = sub_f32x2(pv, qv);
           float eu, ev;
           f32x2_split(d, u, v);
           f32x2_split(sub_f32x2(sub_f32x2(pv, d), qv), eu, ev);
-          err = f32x2(u > 0.f ? eu : 0.f, v > 0.f ? ev : 0.f);
+          sum.add(f32x2(fmaxf(u, 0.f), fmaxf(v, 0.f)), f32x2(u > 0.f ? eu : 0.f, v > 0.f ? ev : 0.f));
         } else {
           f32x2_split(Row<T>::two(x[i], j), u, v);
-          if (g + 32 * i == skip_group && skip_at == 2 * j) u = 0.f;
-          if (g + 32 * i == skip_group && skip_at == 2 * j + 1) v = 0.f;
+          sum.add(f32x2(fmaxf(u, 0.f), fmaxf(v, 0.f)));
         }
-        sum.add(f32x2(fmaxf(u, 0.f), fmaxf(v, 0.f)), err);
       }
   }
   return sum.sum();
