@@ -349,8 +349,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const ResizeArg
 #pragma unroll 8
       for (int i = lane + 32 * sub; i < count; i += 32 * subs) row[i] = __ldcg(pages + i);
     }
+    if (subs == 1 && r.N != r.L) s.lens[b] = r.N;
   }
-  __syncthreads();  // (the row's other warps have read its length)
+  if (subs == 1) return;
+  __syncthreads();  // the row's other warps have read its length
   for (int b = rows.lo + (int)threadIdx.x; b < rows.hi; b += kPlanThreads) {
     const RowLens r(a, b, rows.hi);
     if (r.N != r.L) s.lens[b] = r.N;
@@ -417,12 +419,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const CompactA
   }
 }
 
-// CTAs of a plan: one per 16384 units of work (pages or entries), as a power of two.
-int plan_ctas(long long work) {
+// CTAs of a plan: one per `each` units of work, as a power of two.
+int plan_ctas(long long work, int each) {
   int n = 1;
-  while (n < kPlanMaxCtas && n * 16384LL < work) n *= 2;
+  while (n < kPlanMaxCtas && (long long)n * each < work) n *= 2;
   return n;
 }
+// A cluster's barriers cost a resize 2 us (64 rows, 4900 pages: 11.2 in one CTA, 12.9 in two); a
+// compaction has fewer of them and more to do per page (8700 pages: 189 in one CTA, 185 in four).
+constexpr int kResizeEach = 16384, kCompactEach = 4096, kForkEachCta = 16384;
 
 template <class Args>
 cudaError_t launch_plan(void (*kernel)(const Args), const Args& a, int ctas, size_t smem, cudaStream_t st) {
@@ -449,7 +454,7 @@ cudaError_t launch_fork(const ForkArgs& a, int num_sms, cudaStream_t st) {
   cudaError_t e;
   if (items <= 4 * kPlanMaxCtas * kPlanWarps) {
     if ((e = allow_smem((const void*)fork_kernel<kBoth>, kForkMaxRows * 4, done[0])) != cudaSuccess) return e;
-    return launch_plan(fork_kernel<kBoth>, a, plan_ctas(items * kForkChunk), smem, st);
+    return launch_plan(fork_kernel<kBoth>, a, plan_ctas(items * kForkChunk, kForkEachCta), smem, st);
   }
   if ((e = allow_smem((const void*)fork_kernel<kGather>, kForkMaxRows * 4, done[1])) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -469,12 +474,12 @@ cudaError_t launch_fork(const ForkArgs& a, int num_sms, cudaStream_t st) {
 
 cudaError_t launch_resize(const ResizeArgs& a, const PageCopy& c, int num_sms, cudaStream_t st) {
   const long long work = imin64(0x7fffffff, (long long)a.s.num_pages + 16LL * a.s.B);
-  const cudaError_t e = launch_plan(resize_kernel, a, plan_ctas(work), 0, st);
+  const cudaError_t e = launch_plan(resize_kernel, a, plan_ctas(work, kResizeEach), 0, st);
   return e == cudaSuccess ? launch_page_copy(c, num_sms, st) : e;
 }
 
 cudaError_t launch_compact(const CompactArgs& a, const PageCopy& c, int num_sms, cudaStream_t st) {
-  const cudaError_t e = launch_plan(compact_kernel, a, plan_ctas(a.s.num_pages), 0, st);
+  const cudaError_t e = launch_plan(compact_kernel, a, plan_ctas(a.s.num_pages, kCompactEach), 0, st);
   return e == cudaSuccess ? launch_compact_copy(c, a, num_sms, st) : e;
 }
 
