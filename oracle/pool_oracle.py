@@ -126,6 +126,7 @@ def verify(target, draft, tokens, offsets, accept_u, sample_u):
             x = int(tokens[t + 1])
             one = draft is None
             if not (0 <= x < V and np.isfinite(accept_u[t]) and np.isfinite(float(target[t, x])) and
+                    float(target[t, x]) > 0 and (one or np.isfinite(float(draft[t, x]))) and
                     Fraction(float(accept_u[t])) * (1 if one else Fraction(float(draft[t, x])))
                     < Fraction(float(target[t, x]))):
                 q = np.zeros(V) if one else draft[t]

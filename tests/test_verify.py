@@ -212,6 +212,18 @@ def test_weights_that_are_no_numbers():
     assert got == tuple(w.want())
 
 
+def test_drafts_whose_probabilities_are_no_numbers():
+    """Neither an infinite nor a NaN probability lets a draft stay, whatever its random number."""
+    inf, nan = float("inf"), float("nan")
+    for u in (0.0, 0.5):
+        for p, q in ((inf, 0.5), (nan, 0.5), (-inf, 0.5), (-0.25, -0.5), (0.0, 0.0), (0.5, nan), (0.5, inf),
+                     (0.5, -inf), (0.25, 0.0), (2.0 ** -149, 2.0 ** -149), (3e38, 3e38)):
+            w = Drafts([3, 2], 40, "fp32", seed=4)
+            w.tokens[:] = 9
+            w.target[:, 9], w.draft[:, 9], w.accept_u[:] = p, q, u
+            w.check()
+
+
 def test_tiny_weights_count():
     """Probabilities in fp32's subnormal range, residuals that cancel to their last bits."""
     w = Drafts([1, 2, 2], 400, "fp32", seed=6)
