@@ -24,6 +24,9 @@ namespace {
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyCtasPerSm = 4;
+// Pieces of a row whose sums are kept: of about 4096 tokens, which a CTA searches in 16 steps. One
+// piece per warp for 585 sequences over 256000 tokens (32000 each) takes 93 us, of 4096 64 us.
+constexpr int kMaxPieces = 256, kPieceTokens = 4096;
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -163,45 +166,60 @@ __device__ __forceinline__ uint4 cleared(const uint4& x, int at) {
   return r;
 }
 
-// Sum over whole groups [g0, g1), a lane's share of them, two elements per instruction and the
-// loads of kAhead groups in flight. fmaxf drops NaN; an infinity spoils the sum for good, which
-// the caller sees.
+// Sum over whole groups [g0, g1), a lane's share of them, two elements per instruction and kAhead
+// groups in flight. What is no positive finite number spoils the sum for good, or sets `odd`,
+// where it may not count (the residual max(p - q, 0) is p - min(p, q), whose rounding error needs
+// no test then): the caller sees to that.
 template <class T, bool kQ>
-__device__ __forceinline__ Pair sum_groups(const Row<T>& row, int g0, int g1, int lane) {
-  constexpr int kVec = Row<T>::kVec, kAhead = 2;
-  const uint4* p = reinterpret_cast<const uint4*>(row.p - row.shift);
-  const uint4* q = reinterpret_cast<const uint4*>(row.q - row.shift);
-  const int skip_group = !kQ && row.skip >= 0 ? (row.skip + row.shift) / kVec : -1;
+__device__ __forceinline__ Pair sum_groups(const Row<T>& row, int g0, int g1, int lane, bool& odd) {
+  constexpr int kVec = Row<T>::kVec, kAhead = kQ ? 2 : 3;
+  constexpr uint32_t kSigns = sizeof(T) == 4 ? 0x80000000u : 0x80008000u;
+  const uint4* p = reinterpret_cast<const uint4*>(row.p - row.shift) + lane;
+  const uint4* q = reinterpret_cast<const uint4*>(row.q - row.shift) + lane;
+  const int skip_group = !kQ && row.skip >= 0 ? (row.skip + row.shift) / kVec - lane : -32;
   Pair2 sum;
+  uint32_t bits = 0;
+  auto add = [&](uint4 x, const uint4& y, int g) {
+    if (!kQ) {
+      if (g == skip_group) x = cleared<T>(x, (row.skip + row.shift) % kVec * (int)sizeof(T));
+      bits |= x.x | x.y | x.z | x.w;
+    }
+#pragma unroll
+    for (int j = 0; j < kVec / 2; ++j) {
+      const uint64_t pv = Row<T>::two(x, j);
+      if constexpr (kQ) {
+        float pa, pb, qa, qb;
+        f32x2_split(pv, pa, pb);
+        f32x2_split(Row<T>::two(y, j), qa, qb);
+        const uint64_t qv = f32x2(fminf(pa, qa), fminf(pb, qb)), w = sub_f32x2(pv, qv);
+        sum.add(w, sub_f32x2(sub_f32x2(pv, w), qv));
+      } else {
+        sum.add(pv);
+      }
+    }
+  };
+  int g = g0;
 #pragma unroll 1
-  for (int g = g0 + lane; g - lane < g1; g += 32 * kAhead) {
+  for (; g + 32 * kAhead <= g1; g += 32 * kAhead) {
     uint4 x[kAhead], y[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      x[i] = y[i] = make_uint4(0, 0, 0, 0);  // (no weight)
-      if (g + 32 * i < g1) {
-        x[i] = __ldg(p + g + 32 * i);
-        if constexpr (kQ) y[i] = __ldg(q + g + 32 * i);
-      }
-      if (!kQ && g + 32 * i == skip_group) x[i] = cleared<T>(x[i], (row.skip + row.shift) % kVec * (int)sizeof(T));
+      x[i] = __ldg(p + g + 32 * i);
+      if constexpr (kQ) y[i] = __ldg(q + g + 32 * i);
     }
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-#pragma unroll
-      for (int j = 0; j < kVec / 2; ++j) {
-        float u, v;
-        if constexpr (kQ) {
-          const uint64_t pv = Row<T>::two(x[i], j), qv = Row<T>::two(y[i], j), d = sub_f32x2(pv, qv);
-          float eu, ev;
-          f32x2_split(d, u, v);
-          f32x2_split(sub_f32x2(sub_f32x2(pv, d), qv), eu, ev);
-          sum.add(f32x2(fmaxf(u, 0.f), fmaxf(v, 0.f)), f32x2(u > 0.f ? eu : 0.f, v > 0.f ? ev : 0.f));
-        } else {
-          f32x2_split(Row<T>::two(x[i], j), u, v);
-          sum.add(f32x2(fmaxf(u, 0.f), fmaxf(v, 0.f)));
-        }
-      }
+    for (int i = 0; i < kAhead; ++i) add(x[i], y[i], g + 32 * i);
   }
+#pragma unroll 1
+  for (; g < g1; g += 32) {
+    uint4 x = make_uint4(0, 0, 0, 0), y = x;  // (no weight)
+    if (g + lane < g1) {
+      x = __ldg(p + g);
+      if constexpr (kQ) y = __ldg(q + g);
+    }
+    add(x, y, g);
+  }
+  odd = bits & kSigns;
   return sum.sum();
 }
 
@@ -213,8 +231,9 @@ __device__ __forceinline__ Pair sum_piece(const Row<T>& row, int x0, int x1, int
   const int shift = row.shift;
   int g0 = (x0 + shift + kVec - 1) / kVec, g1 = (int)(((long long)x1 + shift) / kVec);
   if (!row.vec || g1 < g0) g0 = g1 = (x1 + shift) / kVec;
-  Pair sum = sum_groups<T, kQ>(row, g0, g1, lane);
-  if (!__all_sync(0xffffffffu, sum.hi < INFINITY)) {
+  bool odd;
+  Pair sum = sum_groups<T, kQ>(row, g0, g1, lane, odd);
+  if (!__all_sync(0xffffffffu, sum.hi < INFINITY && !odd)) {
     g0 = g1 = (x1 + shift) / kVec;
     sum = Pair{0.f, 0.f};
   }
@@ -228,7 +247,7 @@ __device__ __forceinline__ Pair sum_piece(const Row<T>& row, int x0, int x1, int
 template <class T>
 __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtasPerSm) verify_kernel(const VerifyArgs a) {
   __shared__ int s_kept;
-  __shared__ Pair sums[kPlanMaxCtas * kVerifyWarps];  // of every warp of the cluster
+  __shared__ Pair sums[kMaxPieces];  // of every piece of the row
   __shared__ Pair span_sums[kVerifyWarps];
   __shared__ int first_over, last_some;  // threads
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -297,24 +316,27 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtasPerSm) verify_kerne
     const Row<T> row(target + (size_t)t * a.target_stride,
                      residual && draft ? draft + (size_t)t * a.draft_stride : nullptr, a.V,
                      residual && !draft ? __ldg(a.tokens + t + 1) : -1);
-    const int pieces = pass == 0 ? warps : kVerifyWarps;
+    // a warp's share in pieces small enough to be searched
+    const int n_warps = pass == 0 ? warps : kVerifyWarps;
+    const int each = imax(1, imin(kMaxPieces, a.V / kPieceTokens) / n_warps), pieces = n_warps * each;
     const int per = row.per_piece(pieces);
-    const Pair s = row.q ? sum_piece<T, true>(row, row.at(me, per), row.at(me + 1, per), lane)
-                         : sum_piece<T, false>(row, row.at(me, per), row.at(me + 1, per), lane);
-    if (pass == 0) {
-      if (lane < (int)ctas)
-        store_peer(&sums[me], lane, (unsigned long long)__float_as_uint(s.lo) << 32 | __float_as_uint(s.hi));
-      cluster_sync();
-    } else {  // (its peers may be gone)
-      if (lane == 0) sums[me] = s;
-      __syncthreads();
+#pragma unroll 1
+    for (int i = me * each; i < (me + 1) * each; ++i) {
+      const Pair s = row.q ? sum_piece<T, true>(row, row.at(i, per), row.at(i + 1, per), lane)
+                           : sum_piece<T, false>(row, row.at(i, per), row.at(i + 1, per), lane);
+      if (pass > 0) {  // (its peers may be gone)
+        if (lane == 0) sums[i] = s;
+      } else if (lane < (int)ctas) {
+        store_peer(&sums[i], lane, (unsigned long long)__float_as_uint(s.lo) << 32 | __float_as_uint(s.hi));
+      }
     }
+    if (pass == 0) cluster_sync();
+    else __syncthreads();
     // every warp: the piece in which the running sum passes u times the total
-    constexpr int kEach = kPlanMaxCtas * kVerifyWarps / 32;
+    const int of_lane = (pieces + 31) / 32;
     Pair of{0.f, 0.f};
 #pragma unroll 1
-    for (int i = 0; i < kEach; ++i)
-      if (lane * kEach + i < pieces) of = of + sums[lane * kEach + i];
+    for (int i = lane * of_lane; i < imin((lane + 1) * of_lane, pieces); ++i) of = of + sums[i];
     Pair run = warp_scan(of, lane), before;
     const Pair total = shfl(run, 31);
     if (!some_weight(total)) {
@@ -330,17 +352,18 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtasPerSm) verify_kerne
       return;
     }
     const Pair threshold = u * total;
-    int piece = pick_lane(of, run, threshold, lane, before) * kEach, last = piece;
+    const int piece = pick_lane(of, run, threshold, lane, before) * of_lane;
+    int last = piece;
     Pair base = before;
 #pragma unroll 1
-    for (int i = piece; i < imin(piece + kEach, pieces); ++i) {  // among the lane's
+    for (int i = piece; i < imin(piece + of_lane, pieces); ++i) {  // among the lane's
       if (!(sums[i].hi > 0.f)) continue;
       last = i;
       base = before;
       before = before + sums[i];
       if (before > threshold) break;
     }
-    if (pass == 0 && last / kVerifyWarps != (int)cta) return;
+    if (pass == 0 && last / (kVerifyWarps * each) != (int)cta) return;
     // by the whole CTA: a contiguous span of the piece per thread, the running sums at its ends,
     // and the element where they enclose the threshold
     const int x0 = row.at(last, per), x1 = row.at(last + 1, per);
@@ -348,7 +371,11 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtasPerSm) verify_kerne
     const int at = imin(x0 + (int)threadIdx.x * span, x1), end = imin(at + span, x1);
     Pair sum{0.f, 0.f};
 #pragma unroll 4
-    for (int x = at; x < end; ++x) sum = sum + row.weight(x);
+    for (int x = at; x < end; ++x) {
+      const Pair w = row.weight(x);
+      sum.add(w.hi, w.lo);
+    }
+    sum = sum.normal();
     run = warp_scan(sum, lane);
     if (lane == 31) span_sums[warp] = run;
     __syncthreads();
@@ -367,10 +394,10 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtasPerSm) verify_kerne
 #pragma unroll 4
     for (int x = at; x < end; ++x) {
       const Pair w = row.weight(x);
-      before = before + w;
+      before.add(w.hi, w.lo);
       if (w.hi > 0.f) {
         token = x;
-        if (before > threshold) break;
+        if (before.normal() > threshold) break;
       }
     }
     a.next_tokens[b] = token;

@@ -131,6 +131,15 @@ def test_many_sequences():
     assert [(got[0][b], got[1][b]) for b in keep] == w2
 
 
+@pytest.mark.parametrize("kind,draft", [("bf16", True), ("fp32", False)])
+def test_long_pieces(kind, draft):
+    """So many sequences that one CTA has a whole vocabulary, in several pieces per warp."""
+    w = Drafts([1] * 300 + [3, 2, 1, 4], 70_003, kind, draft, seed=6)
+    got = w.run()
+    keep = list(range(0, 300, 43)) + [300, 301, 302, 303]
+    assert [(got[0][b], got[1][b]) for b in keep] == float64_want_of(w, keep)
+
+
 def float64_want_of(w, which):
     import copy
     out = []
@@ -138,7 +147,7 @@ def float64_want_of(w, which):
         one = copy.copy(w)
         r0, r1 = int(w.offsets[b]), int(w.offsets[b + 1])
         one.B, one.offsets = 1, np.array([0, r1 - r0], dtype=np.int32)
-        one.target, one.draft = w.target[r0:r1], w.draft[r0:r1]
+        one.target, one.draft = w.target[r0:r1], None if w.draft is None else w.draft[r0:r1]
         one.tokens, one.accept_u = w.tokens[r0:r1], w.accept_u[r0:r1]
         one.sample_u = w.sample_u[b:b + 1]
         a, t = float64_want(one)
@@ -189,7 +198,12 @@ def test_equal_distributions():
     w.accept_u[:] = 1.0                                       # u q < p fails: no residual is left
     w.check()
     assert w.run()[0] == [0, 0]
-    big = Drafts([2, 3], 40_000, "bf16", seed=2)
+    for V in (40_000, 200_001):
+        forced_rejection(V)
+
+
+def forced_rejection(V):
+    big = Drafts([2, 3], V, "bf16", seed=2)
     big.draft, big.accept_u[:] = big.target.clone(), 1.0
     accepted, token = big.run()
     assert accepted == [0, 0]
