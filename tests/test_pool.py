@@ -161,6 +161,107 @@ def test_fork_permutes_and_frees():
     assert ea.device_status() == 0
 
 
+def test_most_rows():
+    """As many rows as a fork takes, against array operations."""
+    ea, B, page = _ea(), 49152, 8
+    rng = np.random.default_rng(0)
+    lens = rng.integers(0, 3, B) * page                       # whole pages: nothing is copied
+    k = torch.zeros(B * 2 + 50, 1, page, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.full((B, 4), -1, dtype=torch.int32, device="cuda")
+    g_lens, refs = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(len(k), dtype=torch.int32,
+                                                                                device="cuda")
+    assert ea.cache_resize(k, k.clone(), table, g_lens, refs, i32(lens)).tolist() == [0]
+    want = np.full((B, 4), -1)
+    need, at = lens // page, np.concatenate([[0], np.cumsum(lens // page)])
+    for i in (0, 1):
+        want[need > i, i] = at[:-1][need > i] + i
+    assert np.array_equal(table.cpu().numpy(), want) and np.array_equal(g_lens.cpu().numpy(), lens)
+    assert int(refs.sum()) == int(need.sum()) == int(refs[:at[-1]].sum())
+    parents = rng.integers(-1, B, B)
+    ea.cache_fork(table, g_lens, refs, i32(parents), page_size=page)
+    took = np.where(parents[:, None] >= 0, want[parents], -1)
+    assert np.array_equal(table.cpu().numpy(), took)
+    assert np.array_equal(g_lens.cpu().numpy(), np.where(parents >= 0, lens[parents], 0))
+    assert np.array_equal(refs.cpu().numpy(), np.bincount(took[took >= 0], minlength=len(k)))
+    used, page_map = ea.cache_compact(k, k.clone(), table, g_lens, refs)
+    held = np.unique(took[took >= 0])
+    assert used.tolist() == [len(held)]
+    m = page_map.cpu().numpy()
+    assert np.array_equal(table.cpu().numpy(), np.where(took >= 0, m[took], -1))
+    assert np.array_equal(np.sort(m[held]), np.arange(len(held))) and int((m >= 0).sum()) == len(held)
+    assert ea.device_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_holders_outside_of_the_table(kind):
+    """A kept page that no row holds moves too, with its count, and is never handed out."""
+    ea = _ea()
+    w = PoolPair(2, 6, 20, page=8, kind=kind, seed=12)
+    w.resize(ea, [16, 40])
+    for p, n in ((17, 3), (19, 1), (3, 2)):
+        w.refs[p] += n
+        w.g_refs[p] += n
+    w.resize(ea, [48, 48])
+    w.check()
+    w.resize(ea, [0, 9])
+    used, moves = w.compact(ea)
+    w.check()
+    assert used == 4 and {m[0] for m in moves} == {17, 19}      # 2 and 3 (kept too), 17, 19
+    w.holders(extra=6)
+    assert ea.device_status() == 0
+
+
+def test_lengths_at_the_ends_of_their_type():
+    ea = _ea()
+    big, small = 2 ** 31 - 1, -2 ** 31
+    for lens, new in (([big, 3], [0, 3]), ([small, 3], [0, 3]), ([5, 3], [big, 3]), ([5, 3], [small, 3])):
+        w = PoolPair(2, 4, 12, page=8, seed=13)
+        w.resize(ea, [5, 3])
+        w.g_lens.copy_(i32(lens))
+        ea.cache_resize(*w.g_cache[:2], *w.state, i32(new), window=big)
+        assert ea.device_status() == BAD_INPUT
+        assert int(w.g_lens[1]) == 3
+    w = PoolPair(2, 4, 12, page=8, seed=13)
+    w.resize(ea, [5, 3])
+    w.fork(ea, [small, 0])
+    w.check()
+    w.resize(ea, [0, 32], window=big)
+    w.check()
+    assert ea.device_status() == 0
+
+
+def test_the_binding_refuses():
+    ea = _ea()
+    w, e = PoolPair(2, 3, 6, page=8), PoolPair(2, 3, 6, page=8, kind="e4m3")
+    k, v = w.g_cache[:2]
+    one = i32([0])
+    for bad in (dict(page_table=w.g_table[:, :2]), dict(page_table=w.g_table.long()), dict(seq_lens=i32([0])),
+                dict(page_refs=i32([0] * 5)), dict(new_lens=i32([1])), dict(new_lens=w.g_lens.cpu()),
+                dict(k_cache=k[:, :, :4]), dict(v_cache=v[:5]), dict(kv_exp=e.g_cache[2])):
+        args = dict(k_cache=k, v_cache=v, page_table=w.g_table, seq_lens=w.g_lens, page_refs=w.g_refs,
+                    new_lens=i32([1, 1]))
+        args.update(bad)
+        with pytest.raises(ValueError):
+            ea.cache_resize(**args)
+    for bad in (dict(kv_exp_to=e.g_cache[2]), dict(kv_exp=e.g_cache[2]), dict(src_pages=i32([0, 1])),
+                dict(dst_pages=one.float()), dict(k_to=PoolPair(1, 1, 6, page=16).g_cache[0])):
+        args = dict(k_cache=k, v_cache=v, k_to=k, v_to=v, src_pages=one, dst_pages=one)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            ea.cache_copy(**args)
+    with pytest.raises(ValueError, match="both be given"):
+        ea.cache_copy(*e.g_cache[:2], k, v, one, one, kv_exp=e.g_cache[2])
+    with pytest.raises(ea.AttnError):                         # a part of the pool itself
+        ea.cache_copy(k, v, k[1:], v[1:], one, one)
+    with pytest.raises(ea.AttnError):
+        ea.cache_resize(k, v, *w.state, i32([1, 1]), window=-1)
+    with pytest.raises(ea.AttnError):
+        ea.cache_fork(*w.state, i32([0, 1]), page_size=12)
+    with pytest.raises(ea.AttnError):
+        ea.cache_fork(*w.state, i32([0, 1]), page_size=8, workspace=torch.empty(8, device="cuda"))
+    w.check()
+
+
 # ------------------------------------------------------------------ copy
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("page,d,Hkv", [(8, 64, 1), (16, 128, 3), (64, 128, 8), (192, 64, 5)])

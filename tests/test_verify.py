@@ -189,6 +189,54 @@ def test_random_numbers_at_the_ends(kind):
     assert max(w.run()[1]) < 100
 
 
+def test_what_is_not_read():
+    """The rows of draft, random numbers and tokens that the rule does not name may hold anything."""
+    w = Drafts([4, 1, 0, 3], 300, "fp32", seed=12, spare=2)
+    want = w.run()
+    last = [int(o) - 1 for o in w.offsets[1:]] + [w.T - 2, w.T - 1]
+    w.draft[last] = float("nan")
+    w.accept_u[last] = float("nan")
+    w.target[w.T - 2:] = float("nan")
+    w.tokens[[int(o) for o in w.offsets[:-1]]] = -5
+    w.tokens[w.T - 2:] = 10 ** 9
+    w.sample_u[2] = float("nan")                              # of the sequence without rows
+    assert w.run() == want
+
+
+def test_more_sequences_than_a_grid_holds_at_once():
+    w = Drafts([1, 2, 0, 3] * 5000, 37, "fp16", seed=13)
+    got = w.run()
+    part = Drafts([1, 2, 0, 3] * 5000, 37, "fp16", seed=13)
+    part.B, T = 400, int(part.offsets[400])
+    part.offsets, part.lens, part.sample_u = part.offsets[:401], part.lens[:400], part.sample_u[:400]
+    part.T, part.target, part.draft = T, part.target[:T], part.draft[:T]
+    part.tokens, part.accept_u = part.tokens[:T], part.accept_u[:T]
+    want = part.want()
+    assert (got[0][:400], got[1][:400]) == tuple(want)
+    assert all(0 <= t < 37 for t, n in zip(got[1], np.diff(w.offsets)) if n)
+
+
+def test_the_binding_refuses():
+    ea = _ea()
+    w = Drafts([3, 2], 50, "fp32", seed=1)
+    good = dict(target=w.target.cuda(), tokens=w.tokens.cuda(), offsets=i32(w.offsets), accept_u=w.accept_u.cuda(),
+                sample_u=w.sample_u.cuda(), draft=w.draft.cuda(), seq_lens=w.lens.cuda())
+    for bad in (dict(target=good["target"].double()), dict(target=good["target"].t().contiguous().t()),
+                dict(draft=good["draft"].half()), dict(draft=good["draft"][:4]), dict(draft=good["draft"][:, :49]),
+                dict(tokens=good["tokens"].long()), dict(tokens=good["tokens"][:4]), dict(offsets=i32([])),
+                dict(accept_u=good["accept_u"].double()), dict(accept_u=good["accept_u"][:4]),
+                dict(sample_u=good["sample_u"][:1]), dict(seq_lens=i32([1])), dict(target=w.target),
+                dict(target=good["target"][0])):
+        with pytest.raises(ValueError):
+            ea.verify_drafts(**{**good, **bad})
+    out = i32([0, 0])
+    kw = {k: v for k, v in good.items() if k != "seq_lens"}
+    with pytest.raises(ValueError, match="needs seq_lens"):
+        ea.verify_drafts_into(accepted=out, next_tokens=out.clone(), kept_lens=out.clone(), **kw)
+    ea.verify_drafts(**good)
+    assert ea.device_status() == 0
+
+
 def test_equal_distributions():
     """p = q: every draft stays unless u = 1 - ... rounds; a forced rejection draws from p."""
     w = Drafts([5, 2], 700, "fp32", seed=2)
