@@ -6,7 +6,7 @@
 // plan reads the counts of all pages at most twice (4 bytes a page) and the table entries that
 // change; it is bound by the latency of its few steps, not by bytes: 512 beams of up to 1024 pages
 // forked in 9 us, 64 rows over 4900 pages grown by a token in 7 us (the copy kernel behind it not
-// counted), 160 rows over 99500 pages in 20 us, 8660 pages planned for compaction in 10 us.
+// counted), 160 rows over 99500 pages in 13 us, 8660 pages planned for compaction in 10 us.
 #include "paged.cuh"
 #include "pool.cuh"
 
@@ -28,7 +28,7 @@ __device__ __forceinline__ void add_refs(const PoolState& s, int page, int n) {
 // cluster (kBoth) for few entries, else in two launches over all SMs. A warp takes kForkChunk
 // entries of a row at a time, a lane's loads all in flight.
 enum ForkPhase { kGather = 1, kScatter = 2, kBoth = 3 };
-constexpr int kForkChunk = 256, kForkEach = kForkChunk / 32;
+constexpr int kForkChunk = 256, kChunkEach = kForkChunk / 32;
 __host__ __device__ constexpr int fork_chunks(int max_pages) {
   return max_pages > 0 ? (max_pages + kForkChunk - 1) / kForkChunk : 1;
 }
@@ -67,19 +67,19 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fork_kernel(const ForkArgs a)
       const int c = taken[b], p = parent_of(b);
       const int L = length(b), n = c != 1 ? pages_of(s, L) : 0;
       const int32_t* row = s.table + (size_t)b * s.max_pages;
-      int page[kForkEach];
+      int page[kChunkEach];
 #pragma unroll
-      for (int j = 0; j < kForkEach; ++j) page[j] = i0 + 32 * j < n ? row[i0 + 32 * j] : -1;
+      for (int j = 0; j < kChunkEach; ++j) page[j] = i0 + 32 * j < n ? row[i0 + 32 * j] : -1;
 #pragma unroll
-      for (int j = 0; j < kForkEach; ++j) add_refs(s, page[j], c - 1);
+      for (int j = 0; j < kChunkEach; ++j) add_refs(s, page[j], c - 1);
       if (p == b) continue;
       const int new_length = p < 0 ? 0 : length(p), m = pages_of(s, new_length);
       const int32_t* from = s.table + (size_t)(p < 0 ? 0 : p) * s.max_pages;
       int32_t* to = a.rows + (size_t)b * s.max_pages;
 #pragma unroll
-      for (int j = 0; j < kForkEach; ++j) page[j] = i0 + 32 * j < m ? from[i0 + 32 * j] : -1;
+      for (int j = 0; j < kChunkEach; ++j) page[j] = i0 + 32 * j < m ? from[i0 + 32 * j] : -1;
 #pragma unroll
-      for (int j = 0; j < kForkEach; ++j) {
+      for (int j = 0; j < kChunkEach; ++j) {
         if (page[j] >= s.num_pages) report(s);
         if (i0 + 32 * j < m) to[i0 + 32 * j] = page[j];
       }
@@ -98,11 +98,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fork_kernel(const ForkArgs a)
       const int L = __ldcg(a.new_lens + b), n = pages_of(s, L), old = pages_of(s, __ldcg(a.old_lens + b));
       int32_t* row = s.table + (size_t)b * s.max_pages;
       const int32_t* from = a.rows + (size_t)b * s.max_pages;
-      int page[kForkEach];
+      int page[kChunkEach];
 #pragma unroll
-      for (int j = 0; j < kForkEach; ++j) page[j] = i0 + 32 * j < n ? __ldcg(from + i0 + 32 * j) : -1;
+      for (int j = 0; j < kChunkEach; ++j) page[j] = i0 + 32 * j < n ? __ldcg(from + i0 + 32 * j) : -1;
 #pragma unroll
-      for (int j = 0; j < kForkEach; ++j)
+      for (int j = 0; j < kChunkEach; ++j)
         if (i0 + 32 * j < (n > old ? n : old)) row[i0 + 32 * j] = page[j];
       if (i0 == 0) s.lens[b] = L;
     }
@@ -151,7 +151,7 @@ __device__ __forceinline__ void released(const ResizeArgs& a, int b0, const RowL
     const int who = __ffs(todo) - 1, b = b0 + who;
     const int32_t* row = s.table + (size_t)b * s.max_pages;
     const int end = __shfl_sync(0xffffffffu, few ? n0 : n1, who);
-#pragma unroll 8
+#pragma unroll 4
     for (int i = __shfl_sync(0xffffffffu, n0, who) + lane + 32 * sub; i < end; i += 32 * subs) f(b, i, row[i]);
     bool more = true;
 #pragma unroll 1
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const ResizeArg
       const int count = __shfl_sync(0xffffffffu, n1, who) - first;
       const int32_t* pages = a.free_list + __shfl_sync(0xffffffffu, rank, who);
       int32_t* row = s.table + (size_t)(b0 + who) * s.max_pages + first;
-#pragma unroll 8
+#pragma unroll 4
       for (int i = lane + 32 * sub; i < count; i += 32 * subs) row[i] = __ldcg(pages + i);
     }
     if (subs == 1 && r.N != r.L) s.lens[b] = r.N;
@@ -421,18 +421,41 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const CompactA
   }
 }
 
-// CTAs of a plan: one per `each` units of work, as a power of two.
-int plan_ctas(long long work, int each) {
+// CTAs of a plan: one up to `one` units of work, else one per `each`, as a power of two.
+int plan_ctas(long long work, int one, int each) {
   int n = 1;
-  while (n < kPlanMaxCtas && (long long)n * each < work) n *= 2;
+  while (work > one && n < kPlanMaxCtas && (long long)n * each < work) n *= 2;
   return n;
 }
-// A cluster's barriers cost a resize 2 us (64 rows, 4900 pages: 11.2 in one CTA, 12.9 in two); a
-// compaction has fewer of them and more to do per page (8700 pages: 189 in one CTA, 185 in four).
-constexpr int kResizeEach = 16384, kCompactEach = 4096, kForkEachCta = 16384;
+// A cluster's four barriers cost a resize 1-2 us, its CTAs speed up what rows have to give back and
+// to take: 64 rows of a decode step over 8900 pages 9.8 us in one CTA, 10.9 in three or four; 160
+// rows that end, start and go on over 18000 pages 13.3 in eight, 16.7 in two; over 99500 pages with
+// a window 17.6 in sixteen, 25 in eight. A compaction has fewer barriers and more to do per page
+// (8900 pages 11.8 us in eight CTAs, 13.4 in two).
+constexpr int kResizeOne = 12288, kResizeEach = 4096;
+constexpr int kCompactOne = 2048, kCompactEach = 2048;
+constexpr int kForkOne = 16384, kForkEach = 16384;  // table entries
 
+// Whether clusters of more than the portable size can run this kernel, asked once per device.
+bool large_clusters(const void* kernel, cudaLaunchConfig_t cfg, std::atomic<uint64_t>& known,
+                    std::atomic<uint64_t>& yes) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
+  const uint64_t bit = 1ull << dev;
+  if (known.load(std::memory_order_acquire) & bit) return yes.load(std::memory_order_acquire) & bit;
+  int clusters = 0;
+  const bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                  cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0;
+  if (!ok) cudaGetLastError();
+  if (ok) yes.fetch_or(bit, std::memory_order_release);
+  known.fetch_or(bit, std::memory_order_release);
+  return ok;
+}
+
+// `state`: two words of the launch site's kernel for large_clusters.
 template <class Args>
-cudaError_t launch_plan(void (*kernel)(const Args), const Args& a, int ctas, size_t smem, cudaStream_t st) {
+cudaError_t launch_plan(void (*kernel)(const Args), const Args& a, int ctas, size_t smem, cudaStream_t st,
+                        std::atomic<uint64_t>* state) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kPlanThreads);
@@ -444,19 +467,23 @@ cudaError_t launch_plan(void (*kernel)(const Args), const Args& a, int ctas, siz
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (ctas > kPortableCtas && !large_clusters((const void*)kernel, cfg, state[0], state[1])) {
+    cfg.gridDim = dim3(kPortableCtas);
+    attr[0].val.clusterDim.x = kPortableCtas;
+  }
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace
 
 cudaError_t launch_fork(const ForkArgs& a, int num_sms, cudaStream_t st) {
-  static std::atomic<uint64_t> done[3];
+  static std::atomic<uint64_t> done[3], large[2];
   const long long items = (long long)a.s.B * fork_chunks(a.s.max_pages);
   const size_t smem = (size_t)a.s.B * 4;
   cudaError_t e;
-  if (items <= 4 * kPlanMaxCtas * kPlanWarps) {
+  if (items <= 4 * kPortableCtas * kPlanWarps) {
     if ((e = allow_smem((const void*)fork_kernel<kBoth>, kForkMaxRows * 4, done[0])) != cudaSuccess) return e;
-    return launch_plan(fork_kernel<kBoth>, a, plan_ctas(items * kForkChunk, kForkEachCta), smem, st);
+    return launch_plan(fork_kernel<kBoth>, a, plan_ctas(items * kForkChunk, kForkOne, kForkEach), smem, st, large);
   }
   if ((e = allow_smem((const void*)fork_kernel<kGather>, kForkMaxRows * 4, done[1])) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -476,12 +503,14 @@ cudaError_t launch_fork(const ForkArgs& a, int num_sms, cudaStream_t st) {
 
 cudaError_t launch_resize(const ResizeArgs& a, const PageCopy& c, int num_sms, cudaStream_t st) {
   const long long work = imin64(0x7fffffff, (long long)a.s.num_pages + 16LL * a.s.B);
-  const cudaError_t e = launch_plan(resize_kernel, a, plan_ctas(work, kResizeEach), 0, st);
+  static std::atomic<uint64_t> large[2];
+  const cudaError_t e = launch_plan(resize_kernel, a, plan_ctas(work, kResizeOne, kResizeEach), 0, st, large);
   return e == cudaSuccess ? launch_page_copy(c, num_sms, st) : e;
 }
 
 cudaError_t launch_compact(const CompactArgs& a, const PageCopy& c, int num_sms, cudaStream_t st) {
-  const cudaError_t e = launch_plan(compact_kernel, a, plan_ctas(a.s.num_pages, kCompactEach), 0, st);
+  static std::atomic<uint64_t> large[2];
+  const cudaError_t e = launch_plan(compact_kernel, a, plan_ctas(a.s.num_pages, kCompactOne, kCompactEach), 0, st, large);
   return e == cudaSuccess ? launch_compact_copy(c, a, num_sms, st) : e;
 }
 

@@ -427,7 +427,7 @@ cudaError_t launch_verify(const VerifyArgs& a, int num_sms, cudaStream_t st) {
   // CTAs per sequence: what the SMs hold at once, shared by the sequences, and a step of the
   // warps' vector loads each at least
   const long long held = (long long)num_sms * kVerifyCtasPerSm / a.B;
-  const int ctas = (int)imin64(imin64(held > 1 ? held : 1, kPlanMaxCtas), a.V / 4096 + 1);
+  const int ctas = (int)imin64(imin64(held > 1 ? held : 1, kPortableCtas), a.V / 4096 + 1);
   switch (a.type) {
     case ATTN_PROB_FP32: return launch<float>(a, ctas, st);
     case ATTN_PROB_BF16: return launch<__nv_bfloat16>(a, ctas, st);
