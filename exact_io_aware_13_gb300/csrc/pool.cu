@@ -11,6 +11,22 @@
 #include "pool.cuh"
 
 namespace attn {
+
+bool large_clusters(const void* kernel, cudaLaunchConfig_t cfg, std::atomic<uint64_t>& known,
+                    std::atomic<uint64_t>& yes) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
+  const uint64_t bit = 1ull << dev;
+  if (known.load(std::memory_order_acquire) & bit) return yes.load(std::memory_order_acquire) & bit;
+  int clusters = 0;
+  const bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                  cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0;
+  if (!ok) cudaGetLastError();
+  if (ok) yes.fetch_or(bit, std::memory_order_release);
+  known.fetch_or(bit, std::memory_order_release);
+  return ok;
+}
+
 namespace {
 
 __device__ __forceinline__ void report(const PoolState& s) { atomicOr(s.status, DEV_BAD_INPUT); }
@@ -435,22 +451,6 @@ int plan_ctas(long long work, int one, int each) {
 constexpr int kResizeOne = 12288, kResizeEach = 4096;
 constexpr int kCompactOne = 2048, kCompactEach = 2048;
 constexpr int kForkOne = 16384, kForkEach = 16384;  // table entries
-
-// Whether clusters of more than the portable size can run this kernel, asked once per device.
-bool large_clusters(const void* kernel, cudaLaunchConfig_t cfg, std::atomic<uint64_t>& known,
-                    std::atomic<uint64_t>& yes) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
-  const uint64_t bit = 1ull << dev;
-  if (known.load(std::memory_order_acquire) & bit) return yes.load(std::memory_order_acquire) & bit;
-  int clusters = 0;
-  const bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-                  cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0;
-  if (!ok) cudaGetLastError();
-  if (ok) yes.fetch_or(bit, std::memory_order_release);
-  known.fetch_or(bit, std::memory_order_release);
-  return ok;
-}
 
 // `state`: two words of the launch site's kernel for large_clusters.
 template <class Args>

@@ -66,6 +66,11 @@ struct CopyList {
   int32_t* owner;  // workspace [num_pages_to]: the first entry with that destination
   int* status;
 };
+// Whether clusters of more than the portable size can run this kernel, asked once per device.
+// known, yes: one bit per device, statics of the launch site's kernel.
+bool large_clusters(const void* kernel, cudaLaunchConfig_t cfg, std::atomic<uint64_t>& known,
+                    std::atomic<uint64_t>& yes);
+
 // Rows of one fork: their counters fill a CTA's shared memory.
 constexpr int kForkMaxRows = 49152;
 cudaError_t launch_fork(const ForkArgs& a, int num_sms, cudaStream_t st);

@@ -418,6 +418,11 @@ cudaError_t launch(const VerifyArgs& a, int ctas, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  static std::atomic<uint64_t> large[2];
+  if (ctas > kPortableCtas && !large_clusters((const void*)verify_kernel<T>, cfg, large[0], large[1])) {
+    cfg.gridDim = dim3((unsigned)a.B * kPortableCtas);
+    attr[0].val.clusterDim.x = kPortableCtas;
+  }
   return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a);
 }
 
@@ -425,9 +430,11 @@ cudaError_t launch(const VerifyArgs& a, int ctas, cudaStream_t st) {
 
 cudaError_t launch_verify(const VerifyArgs& a, int num_sms, cudaStream_t st) {
   // CTAs per sequence: what the SMs hold at once, shared by the sequences, and a step of the
-  // warps' vector loads each at least
+  // warps' vector loads each at least; more than eight only as sixteen (64 sequences over 256000
+  // tokens 21.4 us by eight CTAs each, 26.2 by nine; four sequences 11.1 by eight, 8.7 by sixteen)
   const long long held = (long long)num_sms * kVerifyCtasPerSm / a.B;
-  const int ctas = (int)imin64(imin64(held > 1 ? held : 1, kPortableCtas), a.V / 4096 + 1);
+  const int most = held >= kPlanMaxCtas ? kPlanMaxCtas : kPortableCtas;
+  const int ctas = (int)imin64(imin64(held > 1 ? held : 1, most), a.V / 4096 + 1);
   switch (a.type) {
     case ATTN_PROB_FP32: return launch<float>(a, ctas, st);
     case ATTN_PROB_BF16: return launch<__nv_bfloat16>(a, ctas, st);
