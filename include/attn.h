@@ -463,9 +463,11 @@ attn_status attn_decode_paged_e4m3(const attn_paged_cache* cache, const void* q,
  *   page_refs   [num_pages]: how many table entries hold the page, plus whatever else the
  *               caller counts as a holder (a prefix kept for later); a page with 0 is free
  * The tensors of one call must not overlap. Bad DEVICE inputs (a length outside [0,
- * max_pages_per_seq * page_size], an entry at or above num_pages that the call reads, a parent at
- * or above B) are skipped, never followed, and reported by attn_device_status as ATTN_ERR_DEVICE_INPUT;
- * the results of that call are then unspecified. The calls allocate nothing, take any B (0
+ * max_pages_per_seq * page_size], an entry at or above num_pages that the call reads, a parent
+ * at or above B) are skipped, never followed, and reported by attn_device_status as
+ * ATTN_ERR_DEVICE_INPUT; the results of that call are then unspecified. A roll-back into a page
+ * that the table has given up (a window's) is such an input for the call that grows the row
+ * again. The calls allocate nothing, take any B (0
  * included, attn_cache_fork up to 49152) and are deterministic. workspace: DEVICE memory of
  * the size that the call's size function gives, 256-byte aligned, not shared with a concurrent
  * call (two captured graphs that may run at the same time need one each).
