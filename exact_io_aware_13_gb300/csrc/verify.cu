@@ -68,7 +68,20 @@ __device__ __forceinline__ Pair operator*(float u, const Pair& a) {
   return p.normal();
 }
 __device__ __forceinline__ bool some_weight(const Pair& p) { return p.hi > 0.f && p.hi < INFINITY; }
-// Two of them, for the elements of even and of odd index.
+// u times the total weight, which a running sum has to pass. The product's low bits are held where
+// it is at least 2^-76 (48 bits, and fp32 goes down to 2^-149). Below that both sides of every
+// comparison are 2^96 times as large: exactly so, but for running sums that become infinite, which
+// pass as they should, and for products below 2^-172, which every weight there is passes anyway.
+struct Threshold {
+  float scale;
+  Pair at;
+  __device__ __forceinline__ Threshold(float u, const Pair& total)
+      : scale(u * total.hi < 0x1p-76f ? 0x1p96f : 1.f), at(u * scale * total) {}
+  __device__ __forceinline__ bool passed(const Pair& run) const {  // normal
+    return Pair{run.hi * scale, run.lo * scale} > at;
+  }
+};
+// Two pairs, for the elements of even and of odd index.
 struct Pair2 {
   uint64_t hi = 0, lo = 0;
   __device__ __forceinline__ void add(uint64_t x) {
@@ -103,10 +116,10 @@ __device__ __forceinline__ Pair warp_scan(Pair x, int lane) {
 
 // First lane whose running sum passes the threshold, the last with a sum at all if none does.
 // run: the inclusive prefix of mine. `before`: the running sum in front of that lane.
-__device__ __forceinline__ int pick_lane(const Pair& mine, const Pair& run, const Pair& threshold, int lane,
+__device__ __forceinline__ int pick_lane(const Pair& mine, const Pair& run, const Threshold& threshold, int lane,
                                          Pair& before) {
   const uint32_t some = __ballot_sync(0xffffffffu, mine.hi > 0.f);
-  const uint32_t over = some & __ballot_sync(0xffffffffu, run > threshold);
+  const uint32_t over = some & __ballot_sync(0xffffffffu, threshold.passed(run));
   const int who = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0;
   const Pair x = shfl(run, who > 0 ? who - 1 : 0);
   before = who > 0 ? x : Pair{0.f, 0.f};
@@ -352,7 +365,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtasPerSm) verify_kerne
       }
       return;
     }
-    const Pair threshold = u * total;
+    const Threshold threshold(u, total);
     const int piece = pick_lane(of, run, threshold, lane, before) * of_lane;
     int last = piece;
     Pair base = before;
@@ -362,7 +375,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtasPerSm) verify_kerne
       last = i;
       base = before;
       before = before + sums[i];
-      if (before > threshold) break;
+      if (threshold.passed(before)) break;
     }
     if (pass == 0 && last / (kVerifyWarps * each) != (int)cta) return;
     // by the whole CTA: a contiguous span of the piece per thread, the running sums at its ends,
@@ -386,7 +399,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtasPerSm) verify_kerne
     before = Pair{__shfl_up_sync(0xffffffffu, run.hi, 1), __shfl_up_sync(0xffffffffu, run.lo, 1)};
     if (lane == 0) before = base;
     if (sum.hi > 0.f) {
-      if (run > threshold) atomicMin(&first_over, (int)threadIdx.x);
+      if (threshold.passed(run)) atomicMin(&first_over, (int)threadIdx.x);
       else atomicMax(&last_some, (int)threadIdx.x);
     }
     __syncthreads();
@@ -398,7 +411,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtasPerSm) verify_kerne
       before.add(w.hi, w.lo);
       if (w.hi > 0.f) {
         token = x;
-        if (before.normal() > threshold) break;
+        if (threshold.passed(before.normal())) break;
       }
     }
     a.next_tokens[b] = token;
