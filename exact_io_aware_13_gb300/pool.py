@@ -7,9 +7,13 @@ Three int32 tensors hold the state and are changed in place: page_table [B, max_
 loop with drafted tokens runs without a host round trip:
 
     missing = cache_resize(k_cache, v_cache, table, lens, refs, lens + n_new)
-    cache_write(...); o, _ = prefill_paged(...)            # score the drafts
-    accepted, token, kept = verify_drafts(probs, tokens, offsets, u, u2, draft=q, seq_lens=lens)
+    rows = offsets * (missing == 0)                        # no rows where the pool is full
+    cache_write(...); o, _ = prefill_paged(...)            # of rows: score the drafts
+    accepted, token, kept = verify_drafts(probs, tokens, rows, u, u2, draft=q, seq_lens=lens)
     cache_resize(k_cache, v_cache, table, lens, refs, kept)  # roll back
+
+Without `rows`, or a look at `missing`, the calls behind a refused cache_resize take the last cached
+tokens for the new ones: they are overwritten, in shared pages too, and rolled back.
 
 Wrong tensors raise ValueError, a refusal of the library AttnError. workspace (default: made for
 the call) is a tensor of the bytes that the call's size function gives, 256-byte aligned, not
@@ -65,7 +69,8 @@ def cache_resize(k_cache, v_cache, page_table, seq_lens, page_refs, new_lens, *,
     """Take every row to new_lens[b] tokens (int32 [B]): pages for new tokens (a partly filled
     page that others hold too is copied first), pages behind the new length given back, and with
     a sliding window of `window` tokens (0: none) those that it has passed. Returns how many
-    free pages lack (int32 [1]); if that is not 0 nothing has changed."""
+    free pages lack (int32 [1]); if that is not 0 nothing has changed, seq_lens neither, and the
+    new tokens must not be written (see the loop above)."""
     out = _lib.binding().cache_resize(k_cache, v_cache, page_table, seq_lens, page_refs, new_lens,
                                       kv_exp, window, stream, None, None)
     if out.__class__ is int:

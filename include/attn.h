@@ -503,7 +503,12 @@ size_t attn_fork_workspace_size(int B, int max_pages_per_seq);
  *   3. Rows take the pages for their new tokens. Free pages (those given back in step 1 are
  *      among them) are handed out in ascending order, rows in order, a row's copied page first.
  * If the pages do not suffice nothing is changed, and *missing (DEVICE int32) says how many
- * lack; else it is 0. Only the cache's sizes, kind, k, v and kv_exp are used (cache->page_table
+ * lack; else it is 0. seq_lens do not count the new tokens then: attn_cache_write,
+ * attn_prefill_paged and attn_verify_drafts would take the last cached tokens for the rows of the
+ * chunk, the first overwriting them, in shared pages too. A caller that goes on without reading
+ * *missing gives those calls offsets that are all zero if *missing is not 0 (offsets times
+ * (*missing == 0)): no rows, nothing written, kept_lens equal to seq_lens.
+ * Only the cache's sizes, kind, k, v and kv_exp are used (cache->page_table
  * is not read). What new pages hold behind the copied tokens stays.
  */
 attn_status attn_cache_resize(const attn_paged_cache* cache, int32_t* page_table,
