@@ -149,11 +149,13 @@ struct Pieces {
     const int s = kMode == kShort ? src[move] : __ldcg(src + move), d = kMode == kShort ? dst[move] : __ldcg(dst + move);
     if (s < 0) return x;
     if constexpr (kMode == kOwned) {
-      if (!is_entry(given, s, d) || (given.same_pool && s == d)) return x;
-      if (__ldcg(given.owner + d) != move || (given.same_pool && __ldcg(given.owner + s) < given.n)) {
+      if (!is_entry(given, s, d)) return x;
+      const bool itself = given.same_pool && s == d;
+      if (__ldcg(given.owner + d) != move || (given.same_pool && !itself && __ldcg(given.owner + s) < given.n)) {
         atomicOr(given.status, DEV_BAD_INPUT);
         return x;
       }
+      if (itself) return x;
     }
     const int run = c.runs > 1 ? rest / per_run : 0, part = rest - run * per_run;
     const int which = part < c.kv_pieces ? 0 : part < 2 * c.kv_pieces ? 1 : 2;
@@ -338,7 +340,8 @@ cudaError_t launch(const PageCopy& copy, const CompactArgs& compact, const CopyL
   const long long kv = tokens * (c.e4m3 ? c.d : 2 * c.d);
   const long long exps = c.e4m3 ? tokens * 2 : 0, sms = num_sms > 0 ? num_sms : 1;
   auto pieces = [&](int piece) {
-    c.kv_pieces = (int)((kv + piece - 1) / piece);
+    // (the entries of pages without bytes are checked too, each by a piece of none)
+    c.kv_pieces = kMode == kOwned && kv == 0 ? 1 : (int)((kv + piece - 1) / piece);
     c.exp_pieces = (int)((exps + piece - 1) / piece);
     return most * c.runs * (2 * c.kv_pieces + c.exp_pieces);
   };

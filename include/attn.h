@@ -545,7 +545,8 @@ size_t attn_compact_workspace_size(int num_pages);
  * page is skipped. `to` may be the same pool as `from`; pools that overlap in any other way are
  * refused (ATTN_ERR_ARG). Every source is read as it was before the call: of the entries with one
  * destination only the first is copied, and within one pool none whose source is another entry's
- * destination; the entries left out, and pages outside the pools, are reported
+ * destination (an entry that copies a page to itself is good, if it is the first with that
+ * destination); the entries left out, and pages outside the pools, are reported
  * (ATTN_ERR_DEVICE_INPUT) while the others are copied. Counts and tables are the caller's.
  */
 attn_status attn_cache_copy(const attn_paged_cache* from, const attn_paged_cache* to,
