@@ -1119,7 +1119,9 @@ attn_status attn_cache_copy(const attn_paged_cache* from, const attn_paged_cache
   if (!src_pages || !dst_pages) return ATTN_ERR_ARG;
   if ((s = check_pool_tensors(pf)) != ATTN_OK || (s = check_pool_tensors(pt)) != ATTN_OK) return s;
   PageCopy c = page_copy(pf, pt);
-  const bool same = pf.k_cache == pt.k_cache && pf.v_cache == pt.v_cache && pf.kv_exp == pt.kv_exp;
+  // (pools without bytes, whose pointers tell nothing, are two)
+  const bool same = pool_bytes(pf, 0) > 0 && pf.k_cache == pt.k_cache && pf.v_cache == pt.v_cache &&
+                    pf.kv_exp == pt.kv_exp;
   for (int i = 0; i < 3; ++i)
     for (int j = 0; j < 3; ++j) {
       const uintptr_t x = reinterpret_cast<uintptr_t>(c.from[i]), y = reinterpret_cast<uintptr_t>(c.to[j]);

@@ -89,8 +89,8 @@ def test_rules(name, same, n):
 @pytest.mark.parametrize("n", PADDED)
 @pytest.mark.parametrize("same", [True, False])
 def test_rules_of_pages_without_bytes(same, n):
-    """Pools without heads: there is nothing to copy, and the entries left out are reported."""
-    for name in ("plain", "repeated"):
+    """Pools without heads count as two: there is nothing to copy, and the entries left out are reported."""
+    for name in ("plain", "repeated", "to itself twice", "chain"):
         check(*LISTS[name], same, n, Hkv=0)
 
 
