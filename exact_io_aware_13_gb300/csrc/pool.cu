@@ -12,15 +12,24 @@
 
 namespace attn {
 
-bool large_clusters(const void* kernel, cudaLaunchConfig_t cfg, std::atomic<uint64_t>& known,
+bool large_clusters(const void* kernel, const cudaLaunchConfig_t& cfg, std::atomic<uint64_t>& known,
                     std::atomic<uint64_t>& yes) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
   const uint64_t bit = 1ull << dev;
   if (known.load(std::memory_order_acquire) & bit) return yes.load(std::memory_order_acquire) & bit;
+  // (the answer is kept, so the question is one of sizes that do not change from call to call)
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kPlanMaxCtas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t ask = cfg;
+  ask.gridDim = dim3(kPlanMaxCtas);
+  ask.attrs = attr;
+  ask.numAttrs = 1;
   int clusters = 0;
   const bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-                  cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0;
+                  cudaOccupancyMaxActiveClusters(&clusters, kernel, &ask) == cudaSuccess && clusters > 0;
   if (!ok) cudaGetLastError();
   if (ok) yes.fetch_or(bit, std::memory_order_release);
   known.fetch_or(bit, std::memory_order_release);
@@ -437,12 +446,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const CompactA
   }
 }
 
-// CTAs of a plan: one up to `one` units of work, else one per `each`, as a power of two.
-int plan_ctas(long long work, int one, int each) {
-  int n = 1;
-  while (work > one && n < kPlanMaxCtas && (long long)n * each < work) n *= 2;
-  return n;
-}
 // A cluster's four barriers cost a resize 1-2 us, its CTAs speed up what rows have to give back and
 // to take: 64 rows of a decode step over 8900 pages 9.8 us in one CTA, 10.9 in three or four; 160
 // rows that end, start and go on over 18000 pages 13.3 in eight, 16.7 in two; over 99500 pages with

@@ -10,8 +10,6 @@ namespace attn {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanMaxCtas = 16;     // the largest cluster there is
-constexpr int kPortableCtas = 8;     // the largest that every device of this kind schedules
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;

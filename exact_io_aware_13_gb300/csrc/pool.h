@@ -4,6 +4,7 @@
 
 #include "attn.h"
 #include "paged.h"
+#include "pool_rules.h"
 
 namespace attn {
 
@@ -66,9 +67,10 @@ struct CopyList {
   int32_t* owner;  // workspace [num_pages_to]: the first entry with that destination
   int* status;
 };
-// Whether clusters of more than the portable size can run this kernel, asked once per device.
-// known, yes: one bit per device, statics of the launch site's kernel.
-bool large_clusters(const void* kernel, cudaLaunchConfig_t cfg, std::atomic<uint64_t>& known,
+// Whether clusters of kPlanMaxCtas, the only size above the portable one in use, can run this
+// kernel with cfg's block and shared memory: asked once per device. known, yes: one bit per device,
+// statics of the launch site's kernel.
+bool large_clusters(const void* kernel, const cudaLaunchConfig_t& cfg, std::atomic<uint64_t>& known,
                     std::atomic<uint64_t>& yes);
 
 // Rows of one fork: their counters fill a CTA's shared memory.

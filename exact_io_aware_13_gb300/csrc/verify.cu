@@ -24,7 +24,6 @@ namespace {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kVerifyCtasPerSm = 4;
 // Pieces of a row whose sums are kept: of about 4096 tokens, which a CTA searches in 16 steps. One
 // piece per warp for 585 sequences over 256000 tokens (32000 each) takes 93 us, of 4096 64 us.
 constexpr int kMaxPieces = 256, kPieceTokens = 4096;
@@ -442,12 +441,7 @@ cudaError_t launch(const VerifyArgs& a, int ctas, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_verify(const VerifyArgs& a, int num_sms, cudaStream_t st) {
-  // CTAs per sequence: what the SMs hold at once, shared by the sequences, and a step of the
-  // warps' vector loads each at least; more than eight only as sixteen (64 sequences over 256000
-  // tokens 21.4 us by eight CTAs each, 26.2 by nine; four sequences 11.1 by eight, 8.7 by sixteen)
-  const long long held = (long long)num_sms * kVerifyCtasPerSm / a.B;
-  const int most = held >= kPlanMaxCtas ? kPlanMaxCtas : kPortableCtas;
-  const int ctas = (int)imin64(imin64(held > 1 ? held : 1, most), a.V / 4096 + 1);
+  const int ctas = verify_ctas(num_sms, a.B, a.V);
   switch (a.type) {
     case ATTN_PROB_FP32: return launch<float>(a, ctas, st);
     case ATTN_PROB_BF16: return launch<__nv_bfloat16>(a, ctas, st);
