@@ -205,14 +205,14 @@ __device__ __forceinline__ int moves_of(const PageCopy& c, const CompactArgs& co
 }
 
 // Small pages: a piece per lane. The 32 loads of a batch complete on one barrier; the next batch is
-// on its way while a batch is stored.
+// on its way while a batch is stored. (Not for short lists, which have few pieces.)
 template <CopyMode kMode>
 __global__ void __launch_bounds__(kCopyThreads) small_copy_kernel(const PageCopy c, const CompactArgs compact,
                                                                  const CopyList given) {
+  static_assert(kMode != kShort, "");
   extern __shared__ __align__(128) uint8_t ring_smem[];
   __shared__ __align__(8) uint64_t full[kCopyWarps * 2];
   __shared__ int abort_flag;
-  __shared__ int list[kMode == kShort ? 2 * kShortList : 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t bar = smem_u32(full + warp * 2);
   const uint32_t slot = smem_u32(ring_smem) + (warp * 64 + lane) * kSmallPiece;  // + 32 * kSmallPiece: odd batches
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kCopyThreads) small_copy_kernel(const PageCopy
   fence_barrier_init();
   __syncthreads();
   const int *src, *dst;
-  const int moves = moves_of<kMode>(c, compact, given, list, src, dst);
+  const int moves = moves_of<kMode>(c, compact, given, nullptr, src, dst);
   if (moves == 0) return;
   const WaitCtx wait{&abort_flag, c.status};
   const Pieces<kSmallPiece, kMode> pieces(c, given, src, dst, moves);
@@ -348,9 +348,15 @@ cudaError_t launch(const PageCopy& copy, const CompactArgs& compact, const CopyL
   // Small pieces one per lane, unless there are few for a warp: then the ring's shorter way counts
   // (24 pages of 4 KB 3.3 us, a piece per lane 5.0).
   long long units = pieces(kPiece);
-  const bool small = kv < kSmallBelow && units > 16 * kCopyWarps * sms;
-  if (small) units = pieces(kSmallPiece);
-  const auto kernel = small ? small_copy_kernel<kMode> : page_copy_kernel<kMode>;
+  bool small = false;
+  auto kernel = page_copy_kernel<kMode>;
+  if constexpr (kMode != kShort) {
+    small = kv < kSmallBelow && units > 16 * kCopyWarps * sms;
+    if (small) {
+      units = pieces(kSmallPiece);
+      kernel = small_copy_kernel<kMode>;
+    }
+  }
   const int smem = small ? kSmallSmem : kCopySmem;
   static std::atomic<uint64_t> done[2];
   const cudaError_t e = allow_smem((const void*)kernel, smem, done[small]);
