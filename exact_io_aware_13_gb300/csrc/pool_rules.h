@@ -17,18 +17,18 @@ constexpr int plan_ctas(long long work, int one, int each) {
 }
 
 // CTAs per sequence of a verification: what the SMs hold at once, shared by the sequences, and a step
-// of the warps' vector loads each at least. Clusters of sixteen only for up to a 24th of the CTAs that
-// the SMs hold (25 sequences: they do not pack as closely as small ones, and do not all start at once)
-// and from sixteen steps on; nothing between eight and sixteen. Microseconds by eight and by sixteen:
-// 256000 fp32 tokens 13.0 and 9.1 for 4 sequences, 18.7 and 13.5 for 24, 22.7 and 24.8 for 38; 100000
-// bf16 tokens 7.6 and 6.9, 8.9 and 9.7, 10.0 and 14.0; 50257 bf16 tokens 6.6 and 6.4, 7.6 and 8.9, 8.2 and
-// 12.8 (by thirteen 6.4 for 4 sequences, 8.9 for 38); 64 sequences over 256000 bf16 tokens 21.4 by eight,
-// 26.2 by nine.
+// of the warps' vector loads each at least; nothing between eight and sixteen. Clusters of sixteen do
+// not fill the SMs: 33 of them start at once, so they are left to 32 sequences (19 CTAs held for each),
+// and to rows of sixteen steps. Microseconds by sixteen and by eight: 32 sequences over 256000 fp32 tokens
+// 15.1 and 20.9, 34 of them 21.6 and 22.0, of bf16 12.6 and 13.4, then 15.6 and 13.8; over 100000 bf16 tokens
+// 4 sequences 6.9 and 7.6, 32 9.9 and 9.0, 34 12.9 and 8.9; over 50257 bf16 tokens 4 sequences 6.4 and 6.6, 24 8.9
+// and 7.6, 38 12.8 and 8.2 (by thirteen 6.4, -, 8.9). 64 sequences over 256000 bf16 tokens 21.4 by eight, 26.2
+// by nine.
 constexpr int verify_ctas(int num_sms, int B, int V) {
   const long long held = (long long)num_sms * kVerifyCtasPerSm / B, steps = (long long)V / kVerifyEach + 1;
   const long long ctas = steps < held ? steps : held > 1 ? held : 1;
   if (ctas <= kPortableCtas) return (int)ctas;
-  return steps >= kPlanMaxCtas && held >= 24 ? kPlanMaxCtas : kPortableCtas;
+  return steps >= kPlanMaxCtas && held >= 19 ? kPlanMaxCtas : kPortableCtas;
 }
 
 }  // namespace attn
