@@ -5,8 +5,9 @@
 // order, rows take them in order, and counters are sums, so no order of atomics shows. Each
 // plan reads the counts of all pages at most twice (4 bytes a page) and the table entries that
 // change; it is bound by the latency of its few steps, not by bytes: 512 beams of up to 1024 pages
-// forked in 9 us, 64 rows over 4900 pages grown by a token in 7 us (the copy kernel behind it not
-// counted), 160 rows over 99500 pages in 13 us, 8660 pages planned for compaction in 10 us.
+// forked in 9 us, 64 rows over 4900 pages grown by a token in 8 us (the copy kernel behind it, 1 us
+// where there is nothing to copy, not counted), 160 rows over 99500 pages with a window in 17 us, 8660 pages
+// planned for compaction in 6 us.
 #include "paged.cuh"
 #include "pool.cuh"
 
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const CompactA
 // A cluster's four barriers cost a resize 1-2 us, its CTAs speed up what rows have to give back and
 // to take: 64 rows of a decode step over 8900 pages 9.8 us in one CTA, 10.9 in three or four; 160
 // rows that end, start and go on over 18000 pages 13.3 in eight, 16.7 in two; over 99500 pages with
-// a window 17.6 in sixteen, 25 in eight. A compaction has fewer barriers and more to do per page
+// a window 17.8 in sixteen, 25 in eight. A compaction has fewer barriers and more to do per page
 // (8900 pages 11.8 us in eight CTAs, 13.4 in two).
 constexpr int kResizeOne = 12288, kResizeEach = 4096;
 constexpr int kCompactOne = 2048, kCompactEach = 2048;

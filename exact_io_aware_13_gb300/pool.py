@@ -128,7 +128,8 @@ def verify_drafts(target, tokens, offsets, accept_u, sample_u, *, draft=None, se
     numbers. target and draft (fp32, bf16 or fp16 [T, V], contiguous along V) are the
     probabilities of the token after each packed row of the scored chunks; tokens int32 [T], a
     sequence's first row being the token before its drafts; without draft the tokens count as
-    drawn with certainty. Returns (accepted, next_tokens), int32 [B], and with seq_lens the
+    drawn with certainty. Rows may be padded; target and draft alike, or their loads take elements
+    one by one. Returns (accepted, next_tokens), int32 [B], and with seq_lens the
     lengths that cache_resize rolls back to."""
     out = _lib.binding().verify_drafts(target, tokens, offsets, accept_u, sample_u, draft, seq_lens,
                                        stream, None, None, None)

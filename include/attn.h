@@ -582,7 +582,9 @@ enum { ATTN_PROB_FP32 = 0, ATTN_PROB_BF16 = 1, ATTN_PROB_FP16 = 2 };
  * exceeds sample_u[b] times the total weight (the last with any weight if rounding leaves
  * none). Rows need not sum to one; what is not a positive finite number has no weight, and a
  * draft without a positive finite target probability or a finite draft probability does not stay.
- * Sums are held to about 48 bits. A sequence without rows gets 0 and -1; one whose row has no weight
+ * Sums are held as pairs of fp32 numbers: where sample_u[b] times the total lies closer than 2^-32 of
+ * the total to the border between two tokens (V up to 2^20) the token may be either. A sequence
+ * without rows gets 0 and -1; one whose row has no weight, or weights that sum to more than fp32 holds,
  * gets -1 and is reported (ATTN_ERR_DEVICE_INPUT), as are offsets that break the rule and a draft
  * outside [0, V), which does not stay.
  * With seq_lens (int32 [B], the cached tokens with all rows of the chunk; else NULL)
