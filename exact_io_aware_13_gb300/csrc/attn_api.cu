@@ -1139,9 +1139,7 @@ attn_status attn_cache_copy(const attn_paged_cache* from, const attn_paged_cache
   l.n = n;
   l.num_pages_from = pf.num_pages;
   l.num_pages_to = pt.num_pages;
-  // (one pool described with two sizes: the smaller one holds both pages)
   l.same_pool = same;
-  if (same) l.num_pages_from = l.num_pages_to = std::min(pf.num_pages, pt.num_pages);
   l.owner = static_cast<int32_t*>(workspace);
   c.status = l.status = dev->status;
   return from_cuda(launch_copy_pages(l, c, dev->num_sms, static_cast<cudaStream_t>(stream)));

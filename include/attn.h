@@ -542,9 +542,8 @@ size_t attn_compact_workspace_size(int num_pages);
  * Copies page src_pages[i] of one pool to page dst_pages[i] of another (int32 [n]), K, V and
  * scales, for i = 0 .. n - 1: to another engine's pool, or out of the way and back. Both caches
  * agree in kind, Hkv, page_size and d; their page tables are not read. An entry with a negative
- * page is skipped. `to` may be the same pool as `from` (pools without bytes count as two); pools
- * that overlap in any other way are
- * refused (ATTN_ERR_ARG). Every source is read as it was before the call: of the entries with one
+ * page is skipped. `to` may be the same pool as `from`, described with other num_pages too (pools
+ * without bytes count as two); pools that overlap in any other way are refused (ATTN_ERR_ARG). Every source is read as it was before the call: of the entries with one
  * destination only the first is copied, and within one pool none whose source is another entry's
  * destination (an entry that copies a page to itself is good, if it is the first with that
  * destination); the entries left out, and pages outside the pools, are reported

@@ -103,3 +103,25 @@ def test_random_lists(entries, same, kind):
     for _ in range(3):
         check(rng.integers(-3, 41, entries).tolist(), rng.integers(-3, 51, entries).tolist(), same, 0, kind,
               Hkv=2)
+
+
+@pytest.mark.parametrize("n", PADDED)
+@pytest.mark.parametrize("pages_from,pages_to", [(40, 25), (25, 40)])
+def test_one_pool_in_two_sizes(pages_from, pages_to, n):
+    """A pool beside its own front: every page that the one or the other has can be copied."""
+    ea = _ea()
+    for src, dst in (([39, 1, 30, 24], [5, 2, 24, 6]), ([3, 1, 24], [39, 30, 20]), ([39, 5], [25, 39]),
+                     ([30, 2], [3, 30])):
+        if n:
+            at = np.sort(np.random.default_rng(n).permutation(n)[:len(src)])
+            s, d = np.full(n, -1), np.full(n, 3)
+            s[at], d[at] = src, dst
+            src, dst = s.tolist(), d.tolist()
+        a = PoolPair(1, 1, 40, page=8, Hkv=1, kind="e4m3", seed=1)
+        copies, bad = rules(src, dst, pages_from, pages_to, True)
+        P.copy_pages(a.cache, a.cache, copies)
+        k, v, exp = a.g_cache
+        ea.cache_copy(k[:pages_from], v[:pages_from], k[:pages_to], v[:pages_to], i32(src), i32(dst),
+                      kv_exp=exp[:pages_from], kv_exp_to=exp[:pages_to])
+        assert ea.device_status() == (BAD_INPUT if bad else 0)
+        a.check()
